@@ -333,6 +333,148 @@ int bcq_dequant_gemv(const lutgemm_shape* s, int32_t m, const void* d_bits,
 int lutgemm_stream_read(const void* d_src, size_t bytes, uint32_t* d_sink, size_t sink_count,
                         int nontemporal, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Serving operators beside the weight products
+ *
+ * What a decoder layer does between its products when it generates: the norms
+ * and the position rotation of queries and keys with the append to the paged
+ * key/value cache, the attention of the new tokens over that cache, and
+ * low-rank adapters added to a projection's output.
+ *
+ * Conventions on top of those at the head of this file: strides are counted in
+ * elements; a strided array's innermost dimension is contiguous; element types
+ * are those of lutgemm_type. Indices, lengths and page numbers are device data,
+ * which the host cannot check: what each call does with a value outside its
+ * range is stated there, and no such value makes a kernel access memory outside
+ * the arrays described. All argument checks run before any HIP call; on error
+ * nothing is launched. */
+typedef enum lutgemm_type { LUTGEMM_F16 = 0, LUTGEMM_BF16 = 1 } lutgemm_type;
+
+/* Per-head norms of queries and keys, rotation by position, and the append of
+ * keys and values to a paged cache, in one pass over a fused QKV output.
+ *
+ * For token t and each of its heads x [head_dim] (queries, then keys):
+ *   n = x * w / sqrt(mean(x^2) + eps)       (n = x without a norm weight w)
+ *   pairs (a, b) = (n[i], n[i + R/2])       i < R/2, R = rotary  (interleaved = 0)
+ *                = (n[2i], n[2i + 1])                            (interleaved = 1)
+ *   a' = a cos_i - b sin_i, b' = b cos_i + a sin_i; entries from R on are kept,
+ * with cos_i = table[p][i], sin_i = table[p][R/2 + i], p = positions[t]. fp32
+ * throughout, rounded once at the end. Values are copied.
+ *   d_qkv    [tokens][heads + 2 kv_heads][head_dim], rows qkv_token apart:
+ *            queries, keys, values
+ *   d_positions int64 [tokens]; a position outside [0, positions) makes the
+ *            token's queries and keys NaN (not read when rotary is 0)
+ *   d_table  fp32 [positions][rotary], contiguous (ignored when rotary is 0)
+ *   d_q_weight, d_k_weight  [head_dim] of the same type, or both NULL
+ *   d_q      [tokens][heads][head_dim], row t at t * q_token; may be the query
+ *            part of d_qkv itself
+ *   d_k, d_v  cache pages [pages][page_size][kv_heads][head_dim] with strides
+ *            (k_page, k_slot, k_head) and (v_page, v_slot, v_head)
+ *   d_slots  int64 [tokens]: the token's key and value go to slot
+ *            slots[t] % page_size of page slots[t] / page_size; a slot outside
+ *            [0, pages * page_size) writes neither. Two tokens with one slot
+ *            leave either one's key and either one's value there.
+ * With d_slots NULL there is no cache: d_k is [tokens][kv_heads][head_dim] with
+ * token stride k_page and head stride k_head, d_v is not used and the values stay
+ * where they are (pages, page_size, k_slot and the v strides are ignored).
+ * Shape rules: 0 <= tokens < 2^24, heads and kv_heads from 1 to 65536, head_dim a
+ * multiple of 16 up to 256, rotary a multiple of 16 up to head_dim (0: none),
+ * page_size >= 1, eps >= 0 and finite; strides non-negative multiples of 8. Alignment: d_qkv, d_q, d_k, d_v,
+ * weights and table 16 bytes, positions and slots 8. */
+typedef struct lutgemm_heads {
+  int32_t type, heads, kv_heads, head_dim;
+  int32_t rotary, interleaved, page_size;
+  float eps;
+  int64_t tokens, positions, pages;
+  int64_t qkv_token, q_token;
+  int64_t k_page, k_slot, k_head;
+  int64_t v_page, v_slot, v_head;
+} lutgemm_heads;
+int lutgemm_qk_norm_rotate(const lutgemm_heads* h, const void* d_qkv, const int64_t* d_positions,
+                           const float* d_table, const void* d_q_weight, const void* d_k_weight,
+                           void* d_q, void* d_k, void* d_v, const int64_t* d_slots, void* stream);
+
+/* Attention of new tokens over a paged key/value cache.
+ *
+ * Sequence s holds n = kv_lens[s] keys, the last len of which belong to its new
+ * tokens, the query rows q_starts[s] .. q_starts[s + 1] - 1 (len of them). Row t
+ * of the sequence stands at p = n - len + t and sees the keys j <= p, and with a
+ * window > 0 only j > p - window:
+ *   out = sum_j softmax_j(scale * q . k_j) v_j     over the keys that it sees,
+ * zero for a row that sees none (p < 0). Query head h reads key head
+ * h / (heads / kv_heads). Scores, softmax and sums are fp32; the softmax weights
+ * are rounded to the element type for the matrix product with the values; the
+ * output is rounded once.
+ *   d_q, d_out  [tokens][heads][head_dim], strides (q_token, q_head), (o_token, o_head)
+ *   d_k, d_v    pages [pages][page_size][kv_heads][head_dim], strides as in lutgemm_heads
+ *   d_table     int32 [seqs][table_width], rows table_stride apart: key j of sequence
+ *               s is in page table[s][j / page_size]; entries past a sequence's
+ *               last key are not read
+ *   d_kv_lens   int32 [seqs]
+ *   d_q_starts  int32 [seqs + 1], non-decreasing, or NULL: one new token for each
+ *               sequence (tokens == seqs). Output rows before q_starts[0] and from
+ *               q_starts[seqs] on are left as they were.
+ * A page number outside [0, pages) among those that a row's keys need, or a
+ * kv_lens[s] larger than table_width * page_size, makes the rows of that sequence
+ * that meet it NaN; a negative kv_lens[s] counts as 0. Slots past a sequence's last
+ * key are not read, whatever they hold. A NaN or infinity among a sequence's
+ * values can reach the rows whose masks exclude it; NaN and infinity among its
+ * keys do not.
+ * max_q and max_kv say how many new tokens and keys the host expects one sequence
+ * to have at most; the launch is chosen by them, results are right without them
+ * being so. Results for the same sizes, max_q and max_kv are bitwise reproducible.
+ *   d_workspace  at least lutgemm_paged_attention_workspace bytes (may be NULL when
+ *               that is 0); its contents need no preparation and are free again
+ *               when the call has completed on `stream`; calls that overlap in time
+ *               must not share one.
+ * Shape rules: head_dim 64 or 128; kv_heads >= 1 divides heads; page_size a power
+ * of two from 16 to 65536; pages >= 1; 0 <= seqs < 2^20, 0 <= tokens < 2^24, heads
+ * <= 1024, table_width >= 1 with table_width * page_size < 2^31; scale > 0 and
+ * finite; window >= 0; strides non-negative multiples of 8, slot strides below 2^24.
+ * Alignment: d_q, d_k, d_v, d_out and d_workspace 16 bytes, the int32 arrays 4. */
+typedef struct lutgemm_attention {
+  int32_t type, heads, kv_heads, head_dim;
+  int32_t page_size, seqs, table_width, window;
+  float scale;
+  int32_t reserved;
+  int64_t tokens, pages, table_stride, max_q, max_kv;
+  int64_t q_token, q_head, o_token, o_head;
+  int64_t k_page, k_slot, k_head;
+  int64_t v_page, v_slot, v_head;
+} lutgemm_attention;
+int lutgemm_paged_attention_workspace(const lutgemm_attention* a, size_t* bytes);
+int lutgemm_paged_attention(const lutgemm_attention* a, const void* d_q, const void* d_k,
+                            const void* d_v, const int32_t* d_table, const int32_t* d_kv_lens,
+                            const int32_t* d_q_starts, void* d_out, void* d_workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* Low-rank adapters of many requests, added to a projection's output:
+ *   out_i = y_i + scales[a] * B[a] (A[a] x_i),  a = ids[i],
+ * and out_i = y_i where ids[i] is outside [0, adapters): a row without an adapter.
+ *   d_x    [rows][K], rows x_row apart      d_y, d_out  [rows][N], rows y_row and
+ *   out_row apart; d_out may be d_y (with the same stride), not otherwise overlap it
+ *   d_a    [adapters][rank][K], contiguous  d_b  [adapters][N][rank], contiguous
+ *   d_scales  fp32 [adapters], or NULL: 1   d_ids  int32 [rows], in any order
+ * Sums are fp32. A x is kept to about 2^-21 of its largest entry in fp16 (a power of
+ * two per row and a pair of fp16 numbers per entry) and to 2^-16 of each entry in
+ * bf16 (a pair of bf16 numbers); out is rounded once. A row's result does not depend
+ * on the other rows' ids.
+ *   d_workspace  at least lutgemm_adapters_workspace bytes; as for attention.
+ * Shape rules: 0 <= rows <= 65535, K a multiple of 8 below 2^24, N below 2^23, rank a
+ * multiple of 8 from 8 to 128, 0 <= adapters <= 4096 (0: out = y); x_row a multiple
+ * of 8. Alignment: d_x, d_a, d_b and d_workspace 16 bytes, d_ids and d_scales 4,
+ * d_y and d_out 2. */
+typedef struct lutgemm_adapters {
+  int32_t type, rows, K, N;
+  int32_t rank, adapters;
+  int64_t x_row, y_row, out_row;
+} lutgemm_adapters;
+int lutgemm_adapters_workspace(const lutgemm_adapters* l, size_t* bytes);
+int lutgemm_adapters_add(const lutgemm_adapters* l, const void* d_x, const void* d_y,
+                         const void* d_a, const void* d_b, const float* d_scales,
+                         const int32_t* d_ids, void* d_out, void* d_workspace,
+                         size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

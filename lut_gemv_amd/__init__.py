@@ -8,6 +8,8 @@ the device is not gfx950, calls raise.
 Names follow the C ABI: :func:`bcq_pack`, :func:`bcq_pack_uniform`,
 :func:`lutgemm_run`, plus the size queries. :class:`PackedBCQ` bundles a
 packed weight held in device memory with a reusable workspace.
+:func:`qk_norm_rotate`, :func:`paged_attention` and :func:`adapters_add` (from
+``serving.py``) are what a decoder layer does between its products.
 """
 from __future__ import annotations
 
@@ -23,7 +25,7 @@ __all__ = [
     "bcq_pack", "bcq_pack_uniform", "lutgemm_run", "bcq_dequant_gemv", "footprint_bits",
     "search_group_sizes", "bcq_quantize", "stream_read", "lutgemm_run_noalloc",
     "noalloc_scratch_bytes", "query_plan", "TABLES", "trace_attach", "use_traced_library",
-    "PackedBCQ", "STATUS",
+    "PackedBCQ", "STATUS", "rotary_table", "qk_norm_rotate", "paged_attention", "adapters_add",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -121,6 +123,16 @@ def lib() -> ctypes.CDLL:
     L.lutgemm_stream_read.argtypes = [_P, _SZ, _P, _SZ, ctypes.c_int, _P]
     L.lutgemm_trace_attach.restype = ctypes.c_int
     L.lutgemm_trace_attach.argtypes = [_P, _SZ]
+    L.lutgemm_qk_norm_rotate.restype = ctypes.c_int
+    L.lutgemm_qk_norm_rotate.argtypes = [_P] * 11
+    L.lutgemm_paged_attention_workspace.restype = ctypes.c_int
+    L.lutgemm_paged_attention_workspace.argtypes = [_P, _SZP]
+    L.lutgemm_paged_attention.restype = ctypes.c_int
+    L.lutgemm_paged_attention.argtypes = [_P] * 9 + [_SZ, _P]
+    L.lutgemm_adapters_workspace.restype = ctypes.c_int
+    L.lutgemm_adapters_workspace.argtypes = [_P, _SZP]
+    L.lutgemm_adapters_add.restype = ctypes.c_int
+    L.lutgemm_adapters_add.argtypes = [_P] * 9 + [_SZ, _P]
     L.lutgemm_query_plan.restype = ctypes.c_int
     L.lutgemm_query_plan.argtypes = [_SHP, ctypes.c_int32, ctypes.c_int32, _SZ,
                                      ctypes.POINTER(_Plan)]
@@ -401,14 +413,19 @@ class PackedBCQ:
                                 or out.device != x.device or not out.is_contiguous()):
             raise ValueError(f"out must be a contiguous fp16 [{x.shape[0]}][{self.N}] tensor on {x.device}")
 
-    def __call__(self, x, out=None):
-        """y = W_hat x for fp16 x [m][K] on the device; returns fp16 y [m][N]."""
+    def __call__(self, x, out=None, adapters=None, ids=None):
+        """y = W_hat x for fp16 x [m][K] on the device; returns fp16 y [m][N].
+
+        With ``adapters`` = (a, b, scales) and ``ids`` int32 [m], the rows' low-rank
+        adapters are added to y (:func:`adapters_add`)."""
         import torch
         self._check_io(x, out)
         x = x.contiguous()
         m = x.shape[0]
         if out is None:
             out = torch.empty((m, self.N), dtype=torch.float16, device=x.device)
+        if (adapters is None) != (ids is None):
+            raise ValueError("adapters and ids go together")
         strm = torch.cuda.current_stream(x.device)
         ws, ws_bytes = self.workspace(m, strm)
         stream = strm.cuda_stream
@@ -416,6 +433,9 @@ class PackedBCQ:
                     self.d_offset.data_ptr() if self.d_offset is not None else None,
                     x.data_ptr(), out.data_ptr(),
                     ws.data_ptr() if ws is not None else None, ws_bytes, stream)
+        if adapters is not None:
+            a, b, scales = adapters
+            adapters_add(out, x, a, b, ids, scales, out=out)
         return out
 
     def dequant(self, x, out=None):
@@ -431,3 +451,6 @@ class PackedBCQ:
                          self.d_offset.data_ptr() if self.d_offset is not None else None,
                          x.data_ptr(), out.data_ptr(), stream)
         return out
+
+
+from .serving import adapters_add, paged_attention, qk_norm_rotate, rotary_table  # noqa: E402

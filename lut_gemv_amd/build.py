@@ -73,7 +73,8 @@ def build(verbose: bool = False, extra_hip_flags=(), trace: bool = True) -> str:
     tmp = tempfile.mkdtemp(prefix="lutgemm_build_")
     try:
         common = [os.path.join(tmp, f) for f in ("pack.o", "dequant.o", "footprint.o",
-                                                  "quantize.o", "probe.o")]
+                                                  "quantize.o", "probe.o", "heads.o",
+                                                  "attention.o", "adapters.o")]
         jobs = [
             [CXX, *CXX_FLAGS, *incs, "-c", os.path.join(CSRC, "pack.cpp"), "-o", common[0]],
             [HIPCC, *HIP_FLAGS, *extra_hip_flags, *incs, "-c", "-Rpass-analysis=kernel-resource-usage",
@@ -83,6 +84,12 @@ def build(verbose: bool = False, extra_hip_flags=(), trace: bool = True) -> str:
             [HIPCC, *HIP_FLAGS, *extra_hip_flags, *incs, "-c",
              os.path.join(CSRC, "probe.hip"), "-o", common[4]],
         ]
+        # the serving operators
+        for name, obj in (("heads.hip", common[5]), ("attention.hip", common[6]),
+                          ("adapters.hip", common[7])):
+            jobs.append([HIPCC, *HIP_FLAGS, *extra_hip_flags, *incs, "-c",
+                         "-Rpass-analysis=kernel-resource-usage",
+                         os.path.join(CSRC, name), "-o", obj])
         variants = {LIB_PATH: ([], "")}
         if trace:
             variants[TRACE_LIB_PATH] = (["-DLUTGEMM_PHASE_TRACE"], "_trace")

@@ -1,0 +1,253 @@
+// heads.hip -- per-head norms of queries and keys, rotation by position, and the
+// append of keys and values to the paged cache, in one pass over a fused QKV
+// output (lutgemm_qk_norm_rotate; the formulas are in lutgemm.h).
+//
+// Memory bounds it: every element is read once and written once, with a few fp32
+// operations between. A thread owns sixteen entries of a head as two 16-byte words,
+// chosen so that both halves of each rotated pair are its own (entries 8u .. 8u+7
+// and R/2 + 8u .. for pairs of halves, 16u .. 16u+15 for neighbours); the only
+// exchange between lanes is the norm's sum over a head, 2 to 4 lane swaps. A
+// workgroup serves one token, so its angles are read once and kept in registers
+// for all the heads it walks.
+#include "serve.h"
+
+namespace lutgemm {
+namespace {
+
+using namespace serve;
+
+struct HeadsParams {
+  const uint16_t* qkv;
+  const int64_t* positions;
+  const float* table;
+  const uint16_t* q_weight;
+  const uint16_t* k_weight;
+  uint16_t* q;
+  uint16_t* k;
+  uint16_t* v;
+  const int64_t* slots;
+  int64_t n_positions, n_slots;
+  int64_t qkv_token, q_token;
+  int64_t k_page, k_slot, k_head, v_page, v_slot, v_head;
+  int32_t heads, kv_heads, dim, rotary, interleaved, page_size;
+  int32_t lanes_log2;  // lanes of a head: the power of two from dim / 16 up
+  int32_t walk;        // head groups that one workgroup serves
+  float eps;
+};
+
+constexpr int kThreads = 256;
+
+template <class T>
+__device__ __forceinline__ void load16(const uint16_t* p, int c0, int c1, float (&a)[8],
+                                       float (&b)[8]) {
+  const u4v w0 = *(const u4v*)(p + c0), w1 = *(const u4v*)(p + c1);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const f2v x = T::unpack(w0[i]), y = T::unpack(w1[i]);
+    a[2 * i] = x.x;
+    a[2 * i + 1] = x.y;
+    b[2 * i] = y.x;
+    b[2 * i + 1] = y.y;
+  }
+}
+
+// The rotation of a thread's sixteen entries. Pairs of halves: (a[i], b[i]);
+// neighbours: the entries a[0..7], b[0..7] in order, two by two.
+__device__ __forceinline__ void turn(float (&a)[8], float (&b)[8], const float (&cs)[8],
+                                     const float (&sn)[8], bool interleaved) {
+  if (interleaved) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float x = a[2 * i], y = a[2 * i + 1];
+      a[2 * i] = x * cs[i] - y * sn[i];
+      a[2 * i + 1] = y * cs[i] + x * sn[i];
+      const float z = b[2 * i], w = b[2 * i + 1];
+      b[2 * i] = z * cs[4 + i] - w * sn[4 + i];
+      b[2 * i + 1] = w * cs[4 + i] + z * sn[4 + i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float x = a[i], y = b[i];
+      a[i] = x * cs[i] - y * sn[i];
+      b[i] = y * cs[i] + x * sn[i];
+    }
+  }
+}
+
+template <class T>
+__global__ __launch_bounds__(kThreads) void heads_kernel(HeadsParams p) {
+  const int64_t t = blockIdx.x;
+  const int lanes = 1 << p.lanes_log2;
+  const int u = threadIdx.x & (lanes - 1);            // which sixteen entries of the head
+  const int per_group = kThreads >> p.lanes_log2;     // heads served together
+  const int all = p.heads + 2 * p.kv_heads;
+  const bool active = u < p.dim / 16;
+  const bool turned = u < p.rotary / 16;
+  const bool halves = turned && !p.interleaved;
+  const int c0 = halves ? 8 * u : 16 * u;
+  const int c1 = halves ? 8 * u + p.rotary / 2 : 16 * u + 8;
+
+  int64_t slot = p.slots ? p.slots[t] : 0;
+  const bool kept = !p.slots || (slot >= 0 && slot < p.n_slots);
+  int64_t page = t, in_page = 0;
+  if (p.slots && kept) {
+    page = slot / p.page_size;
+    in_page = slot - page * p.page_size;
+  }
+  float cs[8], sn[8];
+  if (turned) {
+    const int64_t pos = p.positions[t];
+    const bool known = pos >= 0 && pos < p.n_positions;
+    const float* row = p.table + (known ? pos : 0) * p.rotary + 8 * u;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const f4v c = *(const f4v*)(row + 4 * i), s = *(const f4v*)(row + p.rotary / 2 + 4 * i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        cs[4 * i + j] = known ? c[j] : __builtin_nanf("");
+        sn[4 * i + j] = known ? s[j] : __builtin_nanf("");
+      }
+    }
+  }
+  const uint16_t* src = p.qkv + t * p.qkv_token;
+  for (int g = 0; g < p.walk; ++g) {
+    const int h = ((int)blockIdx.y * p.walk + g) * per_group + (int)(threadIdx.x >> p.lanes_log2);
+    // whole head groups step together, so every lane of a head is here or none is
+    if (h >= all) break;
+    const bool is_q = h < p.heads, is_v = h >= p.heads + p.kv_heads;
+    if ((is_v && !p.slots) || (!is_q && !kept)) continue;
+    const uint16_t* in = src + (int64_t)h * p.dim;
+    uint16_t* out = is_q ? p.q + t * p.q_token + (int64_t)h * p.dim
+                  : is_v ? p.v + page * p.v_page + in_page * p.v_slot +
+                               (int64_t)(h - p.heads - p.kv_heads) * p.v_head
+                         : p.k + page * p.k_page + in_page * p.k_slot +
+                               (int64_t)(h - p.heads) * p.k_head;
+    if (is_v) {
+      if (active) {
+        *(u4v*)(out + c0) = *(const u4v*)(in + c0);
+        *(u4v*)(out + c1) = *(const u4v*)(in + c1);
+      }
+      continue;
+    }
+    float a[8] = {}, b[8] = {};
+    if (active) load16<T>(in, c0, c1, a, b);
+    const uint16_t* w = is_q ? p.q_weight : p.k_weight;
+    if (w) {
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum += a[i] * a[i] + b[i] * b[i];
+      for (int d = 1; d < lanes; d <<= 1) sum += __shfl_xor(sum, d, 64);
+      const float r = 1.0f / sqrtf(sum / (float)p.dim + p.eps);
+      if (active) {
+        float wa[8], wb[8];
+        load16<T>(w, c0, c1, wa, wb);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          a[i] *= r * wa[i];
+          b[i] *= r * wb[i];
+        }
+      }
+    }
+    if (turned) turn(a, b, cs, sn, p.interleaved);
+    if (active) {
+      u4v w0, w1;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        w0[i] = T::pack(a[2 * i], a[2 * i + 1]);
+        w1[i] = T::pack(b[2 * i], b[2 * i + 1]);
+      }
+      *(u4v*)(out + c0) = w0;
+      *(u4v*)(out + c1) = w1;
+    }
+  }
+}
+
+int check_heads(const lutgemm_heads* h, bool paged) {
+  if (!h) return LUTGEMM_ERR_NULL;
+  if (h->type != LUTGEMM_F16 && h->type != LUTGEMM_BF16) return LUTGEMM_ERR_SHAPE;
+  if (h->heads < 1 || h->kv_heads < 1 || h->heads > (1 << 16) || h->kv_heads > (1 << 16))
+    return LUTGEMM_ERR_SHAPE;
+  if (h->head_dim < 16 || h->head_dim > 256 || h->head_dim % 16) return LUTGEMM_ERR_SHAPE;
+  if (h->rotary < 0 || h->rotary > h->head_dim || h->rotary % 16) return LUTGEMM_ERR_SHAPE;
+  if (h->interleaved != 0 && h->interleaved != 1) return LUTGEMM_ERR_SHAPE;
+  if (!(h->eps >= 0.0f) || !isfinite(h->eps)) return LUTGEMM_ERR_VALUE;
+  if (h->tokens < 0 || h->tokens >= (1 << 24)) return LUTGEMM_ERR_SHAPE;
+  if (h->rotary && (h->positions < 1 || h->positions >= ((int64_t)1 << 40)))
+    return LUTGEMM_ERR_SHAPE;
+  if (!stride_ok(h->qkv_token) || !stride_ok(h->q_token) || !stride_ok(h->k_page) ||
+      !stride_ok(h->k_head))
+    return LUTGEMM_ERR_SHAPE;
+  if (paged) {
+    if (h->page_size < 1 || h->pages < 0 || h->pages >= ((int64_t)1 << 31)) return LUTGEMM_ERR_SHAPE;
+    if (!stride_ok(h->k_slot) || !stride_ok(h->v_page) || !stride_ok(h->v_slot) ||
+        !stride_ok(h->v_head))
+      return LUTGEMM_ERR_SHAPE;
+  }
+  return LUTGEMM_OK;
+}
+
+}  // namespace
+}  // namespace lutgemm
+
+using namespace lutgemm;
+
+extern "C" int lutgemm_qk_norm_rotate(const lutgemm_heads* h, const void* d_qkv,
+                                      const int64_t* d_positions, const float* d_table,
+                                      const void* d_q_weight, const void* d_k_weight, void* d_q,
+                                      void* d_k, void* d_v, const int64_t* d_slots, void* stream) {
+  try {
+    int st = check_heads(h, d_slots != nullptr);
+    if (st) return st;
+    if (h->tokens == 0) return LUTGEMM_OK;
+    if (!d_qkv || !d_q || !d_k || (d_slots && !d_v)) return LUTGEMM_ERR_NULL;
+    if (h->rotary && (!d_positions || !d_table)) return LUTGEMM_ERR_NULL;
+    if ((d_q_weight == nullptr) != (d_k_weight == nullptr)) return LUTGEMM_ERR_NULL;
+    if (!aligned(d_qkv, 16) || !aligned(d_q, 16) || !aligned(d_k, 16) || !aligned(d_v, 16) ||
+        !aligned(d_table, 16) || !aligned(d_q_weight, 16) || !aligned(d_k_weight, 16) ||
+        !aligned(d_positions, 8) || !aligned(d_slots, 8))
+      return LUTGEMM_ERR_ALIGN;
+    int cus = 0;
+    st = serve::check_device(&cus);
+    if (st) return st;
+    HeadsParams p{};
+    p.qkv = (const uint16_t*)d_qkv;
+    p.positions = d_positions;
+    p.table = d_table;
+    p.q_weight = (const uint16_t*)d_q_weight;
+    p.k_weight = (const uint16_t*)d_k_weight;
+    p.q = (uint16_t*)d_q;
+    p.k = (uint16_t*)d_k;
+    p.v = (uint16_t*)d_v;
+    p.slots = d_slots;
+    p.n_positions = h->positions;
+    p.n_slots = h->pages * h->page_size;
+    p.qkv_token = h->qkv_token;
+    p.q_token = h->q_token;
+    p.k_page = h->k_page;
+    p.k_slot = h->k_slot;
+    p.k_head = h->k_head;
+    p.v_page = h->v_page;
+    p.v_slot = h->v_slot;
+    p.v_head = h->v_head;
+    p.heads = h->heads;
+    p.kv_heads = h->kv_heads;
+    p.dim = h->head_dim;
+    p.rotary = h->rotary;
+    p.interleaved = h->interleaved;
+    p.page_size = h->page_size;
+    p.eps = h->eps;
+    while ((16 << p.lanes_log2) < h->head_dim) ++p.lanes_log2;
+    const int per_group = kThreads >> p.lanes_log2;
+    const int all = h->heads + h->kv_heads * (d_slots ? 2 : 1);
+    const int groups = (all + per_group - 1) / per_group;
+    // few tokens: a workgroup for each group of heads; many: one walks them all
+    p.walk = (int64_t)h->tokens * groups <= 8 * (int64_t)cus ? 1 : groups;
+    const dim3 grid((unsigned)h->tokens, (unsigned)((groups + p.walk - 1) / p.walk));
+    return serve::launch(h->type == LUTGEMM_F16 ? heads_kernel<serve::F16>
+                                                : heads_kernel<serve::BF16>,
+                         grid, kThreads, p, (hipStream_t)stream);
+  } catch (...) {
+    return LUTGEMM_ERR_INTERNAL;
+  }
+}

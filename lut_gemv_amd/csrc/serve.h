@@ -1,0 +1,132 @@
+// Shared by the serving operators (heads.hip, attention.hip, adapters.hip): the
+// element types with their matrix-core instructions, and the host's device check.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+#include <stdlib.h>
+#include <string.h>
+
+#include <atomic>
+
+#include "lutgemm.h"
+
+namespace lutgemm {
+namespace serve {
+
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+typedef __bf16 b8 __attribute__((ext_vector_type(8)));
+typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+typedef short s4v __attribute__((ext_vector_type(4)));
+typedef uint32_t u2v __attribute__((ext_vector_type(2)));
+typedef uint32_t u4v __attribute__((ext_vector_type(4)));
+typedef float f2v __attribute__((ext_vector_type(2)));
+typedef float f4v __attribute__((ext_vector_type(4)));
+typedef float f16v __attribute__((ext_vector_type(16)));
+
+// An element type: operands of the matrix cores travel as 16-byte words of eight
+// elements. Operand layouts (row or column i, eight consecutive k per lane):
+//   32x32x16: i = lane % 32, k = 8 (lane / 32) + j; result entry r of a lane is row
+//             8 (r / 4) + 4 (lane / 32) + r % 4, column lane % 32
+//   16x16x32: i = lane % 16, k = 8 (lane / 16) + j; result entry r of a lane is row
+//             4 (lane / 16) + r, column lane % 16
+struct F16 {
+  static constexpr bool kHalf = true;
+  static __device__ __forceinline__ f16v mfma32(u4v a, u4v b, f16v c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, a),
+                                                  __builtin_bit_cast(h8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ f4v mfma16(u4v a, u4v b, f4v c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, a),
+                                                  __builtin_bit_cast(h8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {  // to nearest even
+    const h2 v = {(_Float16)a, (_Float16)b};
+    return __builtin_bit_cast(uint32_t, v);
+  }
+  static __device__ __forceinline__ f2v unpack(uint32_t w) {
+    const h2 v = __builtin_bit_cast(h2, w);
+    return f2v{(float)v.x, (float)v.y};
+  }
+  static __device__ __forceinline__ uint16_t one(float a) {
+    return __builtin_bit_cast(uint16_t, (_Float16)a);
+  }
+  static __device__ __forceinline__ float wide(uint16_t a) {
+    return (float)__builtin_bit_cast(_Float16, a);
+  }
+};
+
+struct BF16 {
+  static constexpr bool kHalf = false;
+  static __device__ __forceinline__ f16v mfma32(u4v a, u4v b, f16v c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b8, a),
+                                                   __builtin_bit_cast(b8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ f4v mfma16(u4v a, u4v b, f4v c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b8, a),
+                                                   __builtin_bit_cast(b8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    const b2 v = {(__bf16)a, (__bf16)b};
+    return __builtin_bit_cast(uint32_t, v);
+  }
+  static __device__ __forceinline__ f2v unpack(uint32_t w) {
+    return f2v{__builtin_bit_cast(float, w << 16), __builtin_bit_cast(float, w & 0xFFFF0000u)};
+  }
+  static __device__ __forceinline__ uint16_t one(float a) {
+    return __builtin_bit_cast(uint16_t, (__bf16)a);
+  }
+  static __device__ __forceinline__ float wide(uint16_t a) {
+    return __builtin_bit_cast(float, (uint32_t)a << 16);
+  }
+};
+
+// Four elements of a column of LDS: the sixteen lanes of a group give the addresses
+// of a 4 x 16 block (lane i: row i / 4, columns 4 (i % 4) ..), and lane i receives
+// column i, rows 0 .. 3.
+__device__ __forceinline__ u2v read_column(const void* lds) {
+  return __builtin_bit_cast(
+      u2v, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4v*)(lds)));
+}
+
+// ------------------------------------------------------------------ host side
+
+// The current device must be gfx950 (LUTGEMM_FAKE_ARCH, a debugging aid, replaces
+// the reported name and bypasses the per-device cache). *cus: its compute units.
+inline int check_device(int* cus) {
+  static std::atomic<int> known_cus[64];  // > 0: gfx950 with so many; < 0: another
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess) return LUTGEMM_ERR_HIP;
+  const char* fake = getenv("LUTGEMM_FAKE_ARCH");
+  const bool cached = dev >= 0 && dev < 64 && !(fake && *fake);
+  int n = cached ? known_cus[dev].load(std::memory_order_relaxed) : 0;
+  if (n == 0) {
+    hipDeviceProp_t prop;
+    if (hipGetDeviceProperties(&prop, dev) != hipSuccess) return LUTGEMM_ERR_HIP;
+    if (prop.multiProcessorCount <= 0) return LUTGEMM_ERR_HIP;
+    const bool ours = strncmp((fake && *fake) ? fake : prop.gcnArchName, "gfx950", 6) == 0;
+    n = ours ? prop.multiProcessorCount : -1;
+    if (cached) known_cus[dev].store(n, std::memory_order_relaxed);
+  }
+  *cus = n;
+  return n > 0 ? LUTGEMM_OK : LUTGEMM_ERR_UNSUPPORTED;
+}
+
+inline bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+inline bool stride_ok(int64_t s) { return s >= 0 && s % 8 == 0 && s < ((int64_t)1 << 40); }
+
+template <class P>
+int launch(void (*kernel)(P), dim3 grid, int threads, const P& p, hipStream_t stream) {
+  P copy = p;
+  void* args[] = {&copy};
+  if (hipLaunchKernel((const void*)kernel, grid, dim3((unsigned)threads), args, 0, stream) !=
+      hipSuccess)
+    return LUTGEMM_ERR_HIP;
+  return LUTGEMM_OK;
+}
+
+}  // namespace serve
+}  // namespace lutgemm

@@ -1,0 +1,550 @@
+"""The operators beside the weight products on the GPU, against their plain fp64
+forms (oracle/serving.py) with bounds counted there: paged attention, head norms
+with rotation and cache append, low-rank adapters; then a run of them together
+as a decoder layer uses them."""
+import sys
+
+import numpy as np
+import pytest
+
+from oracle import serving as plain
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+import lut_gemv_amd as lg  # noqa: E402
+
+DEV = "cuda:0"
+F16, BF16 = torch.float16, torch.bfloat16
+U = {F16: 2.0 ** -11, BF16: 2.0 ** -8}
+NAN = float("nan")
+
+
+def _say(msg):
+    print(f"[serving] {msg}", flush=True)
+    sys.stdout.flush()
+
+
+def _np(t):
+    return t.detach().cpu().double().numpy()
+
+
+def _inside(got, want, bound, what):
+    got = _np(got)
+    assert np.isfinite(got).all(), f"{what}: not finite"
+    worst = float((np.abs(got - want) / np.maximum(bound, 1e-300)).max()) if got.size else 0.0
+    _say(f"{what}: worst err/bound {worst:.3f}")
+    assert worst <= 1.0, what
+
+
+def _normal(shape, dtype, seed, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(shape, generator=g) * scale).to(dtype).to(DEV)
+
+
+# ---------------------------------------------------------------- paged attention
+
+class Batch:
+    """Sequences in a paged cache whose unused slots and pages hold NaN."""
+
+    def __init__(self, dtype, heads, kv_heads, dim, page, lens, news, seed=0, order="nhd",
+                 scale=1.0, lead=0, tail=0):
+        self.dtype, self.lens, self.news = dtype, lens, news
+        self.page, self.heads, self.kv_heads, self.dim = page, heads, kv_heads, dim
+        self.lead = lead
+        need = [-(-n // page) for n in lens]
+        pages, width = sum(need) + 2, max(max(need), 1) + 1
+        rng = np.random.default_rng(seed)
+        ids = rng.permutation(pages)
+        shape = (pages, page, kv_heads, dim)
+        k, v = (torch.full(shape, NAN, dtype=dtype) for _ in range(2))
+        table = torch.full((len(lens), width), -7, dtype=torch.int32)
+        g = torch.Generator().manual_seed(seed)
+        self.k, self.v, at = [], [], 0
+        for i, n in enumerate(lens):
+            kn = (torch.randn((n, kv_heads, dim), generator=g) * scale).to(dtype)
+            vn = torch.randn((n, kv_heads, dim), generator=g).to(dtype)
+            for j in range(need[i]):
+                page_id = int(ids[at])
+                at += 1
+                table[i, j] = page_id
+                part = slice(j * page, min(n, (j + 1) * page))
+                k[page_id, :part.stop - part.start] = kn[part]
+                v[page_id, :part.stop - part.start] = vn[part]
+            self.k.append(kn)
+            self.v.append(vn)
+        tokens = lead + sum(news) + tail
+        self.q = _normal((tokens, heads, dim), dtype, seed + 1, scale)
+        if order == "hnd":   # heads outside slots
+            k, v = (t.transpose(1, 2).contiguous().transpose(1, 2) for t in (k, v))
+            self.k_pages = k.to(DEV).transpose(1, 2).contiguous().transpose(1, 2)
+            self.v_pages = v.to(DEV).transpose(1, 2).contiguous().transpose(1, 2)
+        else:
+            self.k_pages, self.v_pages = k.to(DEV), v.to(DEV)
+        self.table = table.to(DEV)
+        self.kv_lens = torch.tensor(lens, dtype=torch.int32, device=DEV)
+        starts = np.concatenate([[0], np.cumsum(news)]) + lead
+        self.starts = torch.tensor(starts, dtype=torch.int32, device=DEV)
+
+    def call(self, **kw):
+        return lg.paged_attention(self.q, self.k_pages, self.v_pages, self.table, self.kv_lens,
+                                  kw.pop("q_starts", self.starts), **kw)
+
+    def check(self, got, what, scale=None, window=0, only=None):
+        scale = self.dim ** -0.5 if scale is None else scale
+        q = _np(self.q)
+        at = self.lead
+        for i, (n, new) in enumerate(zip(self.lens, self.news)):
+            rows = slice(at, at + new)
+            at += new
+            if only is not None and i not in only:
+                continue
+            want, bound = plain.attention(q[rows], _np(self.k[i]), _np(self.v[i]), new, n, scale,
+                                          window, U[self.dtype])
+            _inside(got[rows], want, bound, f"{what} seq {i} ({new} of {n})")
+
+
+DECODE_LENS = [0, 1, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 129, 300]
+
+
+@pytest.mark.parametrize("heads,kv_heads,dim", [(4, 4, 128), (16, 2, 128), (14, 2, 64), (3, 1, 64),
+                                                (32, 2, 64), (24, 1, 128)])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_attention_single_tokens(dtype, heads, kv_heads, dim):
+    """One new token a sequence, keys from none to a few tiles, with and without starts."""
+    b = Batch(dtype, heads, kv_heads, dim, 16, DECODE_LENS, [1] * len(DECODE_LENS), seed=heads)
+    got = b.call(q_starts=None)
+    b.check(got, f"decode {heads}/{kv_heads}x{dim}")
+    assert torch.equal(got[0], torch.zeros_like(got[0]))
+    same = b.call(max_q=1)
+    b.check(same, "decode with starts")
+
+
+@pytest.mark.parametrize("page", [16, 32, 128, 1024])
+@pytest.mark.parametrize("window", [0, 1, 40, 700])
+def test_attention_split_long_and_windows(page, window):
+    """Keys split over workgroups, pages that end inside a tile, and windows."""
+    lens = [2111, 1, 777, 1536, 0, 4097]
+    b = Batch(F16, 8, 2, 128, page, lens, [1] * 6, seed=page + window)
+    b.check(b.call(q_starts=None, window=window), f"page {page} window {window}", window=window)
+
+
+@pytest.mark.parametrize("heads,kv_heads,dim", [(4, 4, 128), (8, 2, 64), (5, 1, 128)])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("window", [0, 33])
+def test_attention_chunks(dtype, heads, kv_heads, dim, window):
+    """Chunks of one to a few tiles beside single tokens and sequences with no new
+    token; one whose rows stand before its first key."""
+    lens = [300, 5, 64, 129, 700, 1, 40, 513, 20]
+    news = [130, 5, 64, 1, 3, 1, 0, 257, 33]
+    b = Batch(dtype, heads, kv_heads, dim, 16, lens, news, seed=3 * heads + window)
+    got = b.call(window=window)
+    b.check(got, f"chunks {heads}/{kv_heads}x{dim} window {window}", window=window)
+    b.check(b.call(window=window, max_q=1, max_kv=64), "with wrong hints", window=window)
+    b.check(b.call(window=window, max_q=257, max_kv=700), "with right hints", window=window)
+
+
+def test_attention_one_long_chunk_split():
+    """Few row tiles on a long key axis: the 128-row kernel's parts are joined."""
+    b = Batch(BF16, 4, 1, 128, 64, [5000], [40], seed=5)
+    b.check(b.call(), "40 of 5000")
+    b = Batch(F16, 8, 8, 64, 32, [3000, 2500, 90], [17, 1, 90], seed=6)
+    b.check(b.call(), "17 of 3000 beside one of 2500")
+
+
+def test_attention_large_and_small_scores():
+    """Scores of some hundreds, where one key takes all the weight, and a small scale."""
+    b = Batch(F16, 8, 2, 128, 16, [900, 33], [20, 1], seed=7, scale=4.0)
+    b.check(b.call(), "scores near +-180", scale=None)
+    b.check(b.call(scale=1e-4), "scale 1e-4", scale=1e-4)
+
+
+def test_attention_rising_scores():
+    """Every key scores higher than the one before: the running maximum moves all along."""
+    b = Batch(F16, 4, 4, 64, 16, [640, 640], [1, 64], seed=8)
+    for i in range(2):
+        ramp = torch.linspace(-2, 2, 640)[:, None, None] * torch.ones((640, 4, 64))
+        b.k[i] = ramp.to(F16)
+        for j in range(40):
+            b.k_pages[int(b.table[i, j])] = b.k[i][16 * j:16 * j + 16].to(DEV)
+    b.q.fill_(1.0)
+    b.check(b.call(scale=0.5), "rising", scale=0.5)
+
+
+def test_attention_strides_and_rows_left_alone():
+    """Heads outside slots in the cache, queries inside a fused product's rows, an output
+    with gaps, rows before the first and after the last sequence left as they were."""
+    b = Batch(F16, 6, 2, 64, 32, [100, 50, 333], [20, 1, 40], seed=9, order="hnd", lead=3, tail=4)
+    assert b.k_pages.stride(2) > b.k_pages.stride(1)
+    fused = _normal((b.q.shape[0], 10, 64), F16, 10)
+    fused[:, :6] = b.q
+    b.q = fused[:, :6]
+    wide = torch.full((b.q.shape[0], 7, 72), 5.0, dtype=F16, device=DEV)
+    out = wide[:, :6, :64]
+    assert b.call(out=out) is out
+    b.check(out, "strided")
+    assert (wide[:3] == 5).all() and (wide[-4:] == 5).all()
+    assert (wide[:, 6:] == 5).all() and (wide[:, :, 64:] == 5).all()
+
+
+@pytest.mark.parametrize("news", [[1, 1, 1, 1], [20, 1, 30, 9]])
+def test_attention_bad_pages_and_lengths(news):
+    """A page number outside the cache or more keys than the table holds make that
+    sequence's rows NaN and no others; negative lengths count as none."""
+    b = Batch(F16, 4, 2, 128, 16, [70, 80, 90, 60], news, seed=11)
+    b.table[0, 2] = 10 ** 6
+    b.kv_lens[2] = 100000
+    b.table[2] = 0
+    got = b.call()
+    at = np.concatenate([[0], np.cumsum(news)])
+    # rows of sequence 0 that see a key of its third page
+    assert torch.isnan(got[at[0 + 1] - 1]).all()
+    assert torch.isnan(got[at[2]:at[3]]).all()
+    b.check(got, "the others", only=[1, 3])
+    b.table[0, 2] = -1
+    b.kv_lens[3] = -5
+    got = b.call()
+    assert torch.isnan(got[at[1] - 1]).all()
+    assert (got[at[3]:] == 0).all()
+
+
+def test_attention_non_finite_keys_stay_behind_the_mask():
+    """NaN and infinity among the keys reach exactly the rows that see them."""
+    b = Batch(F16, 2, 1, 64, 16, [200], [100], seed=12)
+    bad = 150
+    b.k_pages[int(b.table[0, bad // 16]), bad % 16, 0, 5] = float("nan")
+    got = b.call()
+    row = bad - 100
+    assert torch.isfinite(got[:row]).all() and torch.isnan(got[row:]).all()
+
+
+def test_attention_far_pages():
+    """Pages more than 2^32 bytes, and 2^31 elements, into the cache."""
+    pages = (1 << 31) // (64 * 8 * 128) + 40
+    k = torch.zeros((pages, 64, 8, 128), dtype=F16, device=DEV)
+    v = torch.zeros((pages, 64, 8, 128), dtype=F16, device=DEV)
+    assert k.numel() > 1 << 31
+    b = Batch(F16, 16, 8, 128, 64, [200, 130], [1, 30], seed=13)
+    far = {}
+    for i in range(2):
+        for j in range(-(-b.lens[i] // 64)):
+            near = int(b.table[i, j])
+            far[near] = pages - 1 - near
+            k[far[near]], v[far[near]] = b.k_pages[near], b.v_pages[near]
+            b.table[i, j] = far[near]
+    b.k_pages, b.v_pages = k, v
+    b.check(b.call(), "far pages")
+
+
+def test_attention_repeats_and_graphs():
+    """The same bits from every call, from two captured graphs replayed in turn and at
+    once on two streams, with eager work between."""
+    b = Batch(F16, 16, 2, 128, 16, [2000, 30, 900], [1, 1, 1], seed=14)
+    c = Batch(BF16, 8, 2, 128, 32, [1500, 700], [33, 2], seed=15)
+    want_b, want_c = b.call(max_q=1), c.call()
+    assert torch.equal(want_b, b.call(max_q=1)) and torch.equal(want_c, c.call())
+    graphs = []
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for batch, kw in ((b, dict(max_q=1)), (c, {})):
+        out = torch.zeros_like(batch.q)
+        with torch.cuda.stream(side):
+            batch.call(out=out, **kw)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            batch.call(out=out, **kw)
+        graphs.append((g, out))
+    other = torch.cuda.Stream()
+    for r in range(4):
+        for _, out in graphs:
+            out.fill_(3)
+        junk = torch.randn(1 << 16, device=DEV).sum()
+        torch.cuda.synchronize()
+        if r % 2:
+            graphs[0][0].replay()
+            with torch.cuda.stream(other):
+                graphs[1][0].replay()
+        else:
+            graphs[1][0].replay()
+            graphs[0][0].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(graphs[0][1], want_b) and torch.equal(graphs[1][1], want_c), r
+        assert torch.isfinite(junk)
+
+
+def test_attention_nothing_to_do():
+    b = Batch(F16, 4, 2, 64, 16, [10], [1], seed=16)
+    empty = lg.paged_attention(b.q[:0], b.k_pages, b.v_pages, b.table[:0], b.kv_lens[:0])
+    assert empty.shape == (0, 4, 64)
+    none = torch.zeros(2, dtype=torch.int32, device=DEV)
+    out = torch.full_like(b.q, 9.0)
+    lg.paged_attention(b.q, b.k_pages, b.v_pages, b.table, b.kv_lens, none, out=out)
+    torch.cuda.synchronize()
+    assert (out == 9).all()
+
+
+# ------------------------------------------------- norms, rotation, cache append
+
+def _heads_case(dtype, tokens, heads, kv, dim, rotary, interleaved, norm, seed=0, limit=1000):
+    qkv = _normal((tokens, (heads + 2 * kv) * dim), dtype, seed)
+    table = lg.rotary_table(limit, rotary, device=DEV) if rotary else None
+    g = torch.Generator().manual_seed(seed + 1)
+    positions = torch.randint(limit, (tokens,), generator=g).to(DEV)
+    w = [_normal((dim,), dtype, seed + 2 + i) for i in range(2)] if norm else [None, None]
+    return qkv, table, positions, w
+
+
+def _heads_want(qkv, table, positions, w, heads, kv, dim, interleaved, eps, u):
+    x = _np(qkv).reshape(qkv.shape[0], heads + 2 * kv, dim)
+    t = _np(table)[positions.cpu().numpy()] if table is not None else np.zeros((len(x), 0))
+    c, s = t[:, :t.shape[1] // 2], t[:, t.shape[1] // 2:]
+    return [plain.heads(part, None if wt is None else _np(wt), eps, c, s, interleaved, u)
+            for part, wt in ((x[:, :heads], w[0]), (x[:, heads:heads + kv], w[1]))] \
+        + [x[:, heads + kv:]]
+
+
+@pytest.mark.parametrize("heads,kv,dim,rotary", [(4, 2, 128, 128), (3, 1, 64, 32), (5, 5, 96, 96),
+                                                 (1, 1, 16, 16), (2, 2, 256, 64), (7, 1, 80, 0),
+                                                 (40, 8, 128, 64)])
+@pytest.mark.parametrize("dtype,interleaved,norm", [(F16, False, True), (BF16, True, True),
+                                                    (F16, True, False), (BF16, False, False)])
+@pytest.mark.parametrize("tokens", [1, 37])
+def test_heads_into_the_cache(dtype, interleaved, norm, heads, kv, dim, rotary, tokens):
+    qkv, table, positions, w = _heads_case(dtype, tokens, heads, kv, dim, rotary, interleaved, norm,
+                                           seed=heads + dim)
+    pages, page = 6, 8
+    k_pages = torch.full((pages, page, kv, dim), 7.0, dtype=dtype, device=DEV)
+    v_pages = torch.full((pages, kv, page, dim), 7.0, dtype=dtype, device=DEV).transpose(1, 2)
+    slots = torch.from_numpy(np.random.default_rng(1).permutation(pages * page)[:tokens].copy()).to(DEV)
+    if tokens > 4:
+        slots[3], slots[4] = -1, pages * page
+    q = lg.qk_norm_rotate(qkv, heads, kv, positions, table, *w, eps=1e-5, interleaved=interleaved,
+                          k_pages=k_pages, v_pages=v_pages, slots=slots)
+    (qw, qb), (kw, kb), vw = _heads_want(qkv, table, positions, w, heads, kv, dim, interleaved,
+                                         1e-5, U[dtype])
+    _inside(q, qw, qb, "queries")
+    used = np.zeros(pages * page, bool)
+    for t, slot in enumerate(slots.tolist()):
+        if 0 <= slot < pages * page:
+            used[slot] = True
+            _inside(k_pages[slot // page, slot % page], kw[t], kb[t], f"key {t}") if t < 3 else None
+            assert np.abs(_np(k_pages[slot // page, slot % page]) - kw[t]).max() <= kb[t].max()
+            assert np.array_equal(_np(v_pages[slot // page, slot % page]), vw[t])
+    for slot in np.flatnonzero(~used):
+        assert (k_pages[slot // page, slot % page] == 7).all()
+        assert (v_pages[slot // page, slot % page] == 7).all()
+
+
+def test_heads_without_a_cache_and_in_place():
+    qkv, table, positions, w = _heads_case(F16, 50, 6, 2, 128, 128, False, True, seed=20)
+    (qw, qb), (kw, kb), _ = _heads_want(qkv, table, positions, w, 6, 2, 128, False, 1e-6, U[F16])
+    q, k = lg.qk_norm_rotate(qkv, 6, 2, positions, table, *w)
+    _inside(q, qw, qb, "queries")
+    _inside(k, kw, kb, "keys")
+    # a fused row with room on both sides, the queries written over themselves
+    wide = torch.full((50, 10 * 128 + 64), 3.0, dtype=F16, device=DEV)
+    inner = wide[:, 32:32 + 10 * 128]
+    inner.copy_(qkv)
+    out = inner[:, :6 * 128].unflatten(1, (6, 128))
+    q2, k2 = lg.qk_norm_rotate(inner, 6, 2, positions, table, *w, out=out)
+    assert torch.equal(q2, q) and torch.equal(k2, k) and q2.data_ptr() == inner.data_ptr()
+    assert torch.equal(inner[:, 6 * 128:], qkv[:, 6 * 128:])
+    assert (wide[:, :32] == 3).all() and (wide[:, -32:] == 3).all()
+
+
+def test_heads_positions_outside_the_table():
+    qkv, table, positions, _ = _heads_case(F16, 6, 2, 1, 64, 32, False, False, seed=21)
+    positions[1], positions[4] = -1, 1000
+    q, k = lg.qk_norm_rotate(qkv, 2, 1, positions, table)
+    for t in range(6):
+        assert torch.isnan(q[t, :, :32]).all() == (t in (1, 4))
+        assert torch.isfinite(q[t, :, 32:]).all()
+        assert torch.isnan(k[t, :, :32]).all() == (t in (1, 4))
+
+
+def test_heads_many_tokens_and_tiny_values():
+    """A workgroup that walks all heads, and rows of zeros and of the smallest numbers."""
+    qkv, table, positions, w = _heads_case(BF16, 3000, 20, 4, 64, 64, True, True, seed=22)
+    qkv[7] = 0
+    qkv[8] = 1e-30
+    q, k = lg.qk_norm_rotate(qkv, 20, 4, positions, table, *w, interleaved=True)
+    (qw, qb), (kw, kb), _ = _heads_want(qkv, table, positions, w, 20, 4, 64, True, 1e-6, U[BF16])
+    _inside(q, qw, qb, "queries")
+    _inside(k, kw, kb, "keys")
+
+
+def test_rotary_table_is_rounded_from_64_bits():
+    t = lg.rotary_table(70000, 64, 10000.0, device="cpu").double().numpy()
+    p = np.arange(70000)[:, None] * 10000.0 ** (-np.arange(0, 64, 2) / 64)
+    assert np.abs(t - np.concatenate([np.cos(p), np.sin(p)], 1)).max() <= 2.0 ** -24
+
+
+# ------------------------------------------------------------- low-rank adapters
+
+def _adapters_case(dtype, rows, K, N, rank, count, ids, seed=0):
+    x, y = _normal((rows, K), dtype, seed), _normal((rows, N), dtype, seed + 1)
+    a = _normal((count, rank, K), dtype, seed + 2, max(K, 1) ** -0.5)
+    b = _normal((count, N, rank), dtype, seed + 3, rank ** -0.5)
+    scales = torch.linspace(0.5, 2.0, max(count, 1))[:count].to(DEV)
+    return y, x, a, b, torch.tensor(ids, dtype=torch.int32, device=DEV), scales
+
+
+def _adapters_check(got, y, x, a, b, ids, scales, what):
+    pair = {F16: 2.0 ** -21, BF16: 2.0 ** -16}[x.dtype]
+    want, bound = plain.adapters(_np(y), _np(x), _np(a), _np(b), ids.tolist(),
+                                 None if scales is None else _np(scales), U[x.dtype], pair)
+    _inside(got, want, bound, what)
+    for i, l in enumerate(ids.tolist()):
+        if not 0 <= l < a.shape[0]:
+            assert torch.equal(got[i], y[i])
+
+
+def _ids(rows, count, seed, none=0.2):
+    rng = np.random.default_rng(seed)
+    ids = rng.integers(0, max(count, 1), rows)
+    ids[rng.random(rows) < none] = rng.choice([-1, count, -2 ** 31, 2 ** 31 - 1])
+    return ids.tolist()
+
+
+@pytest.mark.parametrize("rows,count", [(1, 1), (1, 3), (16, 1), (17, 1), (17, 5), (64, 3), (64, 64),
+                                        (65, 1), (65, 70), (200, 4)])
+@pytest.mark.parametrize("dtype,K,N,rank", [(F16, 520, 260, 16), (BF16, 1032, 129, 8),
+                                            (F16, 8, 5, 40), (BF16, 2056, 640, 128)])
+def test_adapters(dtype, K, N, rank, rows, count):
+    """Every grouping (one row to a lane, sorted above 64 rows), odd and narrow sizes."""
+    case = _adapters_case(dtype, rows, K, N, rank, count, _ids(rows, count, rows + count), seed=rows)
+    got = lg.adapters_add(*case)
+    _adapters_check(got, *case, f"{rows} rows, {count} adapters, {K}->{N}, rank {rank}")
+    assert torch.equal(got, lg.adapters_add(*case))   # the same bits again
+
+
+def test_adapters_rows_do_not_depend_on_others():
+    """A row alone, in a full batch and in a sorted batch gives the same bits when the
+    work is split alike, and the same value in any case."""
+    ids = _ids(130, 7, 1)
+    y, x, a, b, d_ids, s = _adapters_case(F16, 130, 512, 200, 16, 7, ids, seed=30)
+    whole = lg.adapters_add(y, x, a, b, d_ids, s)
+    for i in (0, 5, 129):
+        one = lg.adapters_add(y[i:i + 1], x[i:i + 1], a, b, d_ids[i:i + 1].contiguous(), s)
+        assert torch.equal(one[0], whole[i])
+
+
+def test_adapters_in_place_strided_and_plain_scales():
+    ids = _ids(40, 3, 2)
+    y, x, a, b, d_ids, s = _adapters_case(F16, 40, 256, 136, 24, 3, ids, seed=31)
+    wide_x = _normal((40, 300 + 4), F16, 32)
+    wide_x[:, 16:272] = x
+    wide_y = torch.full((40, 150), 2.0, dtype=F16, device=DEV)
+    wide_y[:, 3:139] = y
+    part = wide_y[:, 3:139]
+    got = lg.adapters_add(part, wide_x[:, 16:272], a, b, d_ids, None, out=part)
+    assert got is part
+    _adapters_check(got, y, x, a, b, d_ids, None, "in place, odd offsets")
+    assert (wide_y[:, :3] == 2).all() and (wide_y[:, 139:] == 2).all()
+    y2 = y.clone()
+    lg.adapters_add(y2, x, a, b, d_ids, s, out=y2)
+    assert torch.equal(y2, lg.adapters_add(y, x, a, b, d_ids, s))
+
+
+def test_adapters_large_and_tiny_inner_values():
+    """Inner values past fp16's range and below its normal numbers."""
+    for scale, back in ((300.0, 1e-4), (1e-4, 100.0)):
+        y, x, a, b, ids, s = _adapters_case(F16, 9, 1024, 64, 16, 2, [0, 1] * 4 + [0], seed=33)
+        x = (x.float() * scale).to(F16)
+        a = (a.float() * min(scale, 30.0)).to(F16)
+        s = s * (back / scale / 30)
+        got = lg.adapters_add(y, x, a, b, ids, s)
+        _adapters_check(got, y, x, a, b, ids, s, f"inner values scaled by {scale}")
+
+
+def test_adapters_nothing_to_add():
+    y, x, a, b, ids, s = _adapters_case(F16, 70, 64, 32, 8, 2, [-1] * 70, seed=34)
+    assert torch.equal(lg.adapters_add(y, x, a, b, ids, s), y)
+    none = lg.adapters_add(y, x, a[:0], b[:0], ids, s[:0])
+    assert torch.equal(none, y)
+    assert lg.adapters_add(y[:0], x[:0], a, b, ids[:0], s).shape == (0, 32)
+    flat = lg.adapters_add(y, x[:, :0], a[:, :, :0].contiguous(), b, torch.zeros_like(ids), s)
+    assert torch.equal(flat, y)
+
+
+def test_adapters_graph_and_streams():
+    case = _adapters_case(BF16, 100, 1024, 512, 32, 9, _ids(100, 9, 3), seed=35)
+    want = lg.adapters_add(*case)
+    outs = [torch.zeros_like(want) for _ in range(2)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graphs = []
+    for out in outs:
+        with torch.cuda.stream(side):
+            lg.adapters_add(*case, out=out)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            lg.adapters_add(*case, out=out)
+        graphs.append(g)
+    other = torch.cuda.Stream()
+    for r in range(3):
+        for out in outs:
+            out.fill_(0)
+        torch.randn(1 << 16, device=DEV).sum()
+        torch.cuda.synchronize()
+        graphs[0].replay()
+        with torch.cuda.stream(other):
+            graphs[1].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], want) and torch.equal(outs[1], want), r
+
+
+# ------------------------------------------------------------------ used together
+
+def test_packed_product_with_adapters():
+    """PackedBCQ's product with its rows' adapters is the product, then the adapters."""
+    import workloads
+    w = workloads.random_bcq(528, 1024, 3, 128, m=5, seed=40, sigma=0.02)
+    pw = lg.PackedBCQ.from_bcq(w.bits, w.alpha, None, w.g, device=DEV)
+    x = torch.from_numpy(w.x).to(DEV)
+    _, _, a, b, ids, s = _adapters_case(F16, 5, 1024, 528, 16, 3, [2, -1, 0, 2, 1], seed=41)
+    y = pw(x)
+    got = pw(x, adapters=(a, b, s), ids=ids)
+    assert torch.equal(got, lg.adapters_add(y, x, a, b, ids, s))
+    assert torch.equal(got[1], y[1]) and not torch.equal(got[0], y[0])
+
+
+@pytest.mark.parametrize("norm", [False, True])
+def test_a_prompt_in_chunks_then_tokens(norm):
+    """Two requests through projection, adapters, norms, rotation, cache and attention,
+    their prompts in chunks and then token by token: each step's attention is that of
+    the fp64 form on the cache as it stands."""
+    import workloads
+    heads, kv, dim, page, K = 4, 2, 64, 16, 256
+    N = (heads + 2 * kv) * dim
+    w = workloads.random_bcq(N, K, 3, 128, seed=50, sigma=0.06)
+    pw = lg.PackedBCQ.from_bcq(w.bits, w.alpha, None, w.g, device=DEV)
+    _, _, a, b, _, s = _adapters_case(F16, 1, K, N, 16, 2, [0], seed=51)
+    weights = [_normal((dim,), F16, 52), _normal((dim,), F16, 53)] if norm else [None, None]
+    rope = lg.rotary_table(256, dim, device=DEV)
+    k_pages = torch.full((12, page, kv, dim), NAN, dtype=F16, device=DEV)
+    v_pages = torch.full((12, page, kv, dim), NAN, dtype=F16, device=DEV)
+    table = torch.tensor([[3, 9, 1, 7, 0], [2, 11, 5, 8, 10]], dtype=torch.int32, device=DEV)
+    have = [0, 0]
+    for step, news in enumerate([(40, 19), (11, 1), (1, 1), (1, 1)]):
+        req = np.repeat([0, 1], news)
+        pos = np.concatenate([np.arange(h, h + n) for h, n in zip(have, news)])
+        have = [h + n for h, n in zip(have, news)]
+        x = _normal((len(req), K), F16, 60 + step)
+        ids = torch.tensor(np.where(req == 0, 1, -1), dtype=torch.int32, device=DEV)
+        qkv = pw(x, adapters=(a, b, s), ids=ids)
+        d_req, d_pos = torch.from_numpy(req).to(DEV), torch.from_numpy(pos).to(DEV)
+        slots = table[d_req, d_pos // page].long() * page + d_pos % page
+        q = lg.qk_norm_rotate(qkv, heads, kv, d_pos, rope, *weights, k_pages=k_pages,
+                              v_pages=v_pages, slots=slots)
+        starts = torch.tensor([0, news[0], sum(news)], dtype=torch.int32, device=DEV)
+        lens = torch.tensor(have, dtype=torch.int32, device=DEV)
+        o = lg.paged_attention(q, k_pages, v_pages, table, lens, starts, max_q=max(news))
+        for r in range(2):
+            rows = slice(int(starts[r]), int(starts[r + 1]))
+            ks, vs = (t[table[r].long()].flatten(0, 1)[:have[r]] for t in (k_pages, v_pages))
+            want, bound = plain.attention(_np(q[rows]), _np(ks), _np(vs), news[r], have[r],
+                                          dim ** -0.5, 0, U[F16])
+            _inside(o[rows], want, bound, f"step {step} request {r}")

@@ -1,0 +1,222 @@
+"""The operators beside the weight products, host side: every argument error is
+reported before any HIP call, the descriptors' layout is the header's, and the
+plain forms agree with torch's own attention. No GPU."""
+import ctypes
+import os
+import shutil
+import struct
+import subprocess
+
+import numpy as np
+import pytest
+
+import lut_gemv_amd as lg
+from lut_gemv_amd import serving
+from oracle import serving as plain
+
+torch = pytest.importorskip("torch")
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+A = 0x100000     # a fake, aligned device address: never dereferenced
+NULL, SHAPE, VALUE, BUFFER, ALIGN = 1, 2, 3, 4, 5
+
+
+# ------------------------------------------------------------- attention refusals
+
+ATT = dict(type=0, heads=8, kv_heads=2, head_dim=128, page_size=16, seqs=3, table_width=10, window=0,
+           scale=0.1, reserved=0, tokens=30, pages=20, table_stride=10, max_q=10, max_kv=160,
+           q_token=1024, q_head=128, o_token=1024, o_head=128, k_page=4096, k_slot=256, k_head=128,
+           v_page=4096, v_slot=256, v_head=128)
+
+
+def _attention(ws=None, wsb=0, q=A, k=A, v=A, table=A, lens=A, starts=A, out=A, **change):
+    d = serving._ATTENTION.pack(*{**ATT, **change}.values())
+    return lg.lib().lutgemm_paged_attention(d, q, k, v, table, lens, starts, out, ws, wsb, None)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(type=2), SHAPE), (dict(type=-1), SHAPE), (dict(head_dim=96), SHAPE), (dict(head_dim=0), SHAPE),
+    (dict(heads=0), SHAPE), (dict(heads=7), SHAPE), (dict(heads=2048), SHAPE), (dict(kv_heads=0), SHAPE),
+    (dict(page_size=8), SHAPE), (dict(page_size=48), SHAPE), (dict(page_size=1 << 17), SHAPE),
+    (dict(seqs=-1), SHAPE), (dict(seqs=1 << 20), SHAPE), (dict(tokens=-1), SHAPE),
+    (dict(tokens=1 << 24), SHAPE), (dict(table_width=0), SHAPE), (dict(table_width=1 << 27), SHAPE),
+    (dict(table_stride=-1), SHAPE), (dict(pages=0), SHAPE), (dict(pages=1 << 31), SHAPE),
+    (dict(window=-1), SHAPE), (dict(max_q=-1), SHAPE), (dict(max_kv=-1), SHAPE),
+    (dict(scale=0.0), VALUE), (dict(scale=-1.0), VALUE), (dict(scale=float("nan")), VALUE),
+    (dict(scale=float("inf")), VALUE), (dict(q_token=1020), SHAPE), (dict(q_head=-8), SHAPE),
+    (dict(o_head=4), SHAPE), (dict(k_slot=1 << 24), SHAPE), (dict(v_page=12), SHAPE),
+    (dict(q=None), NULL), (dict(k=None), NULL), (dict(v=None), NULL), (dict(table=None), NULL),
+    (dict(lens=None), NULL), (dict(out=None), NULL), (dict(q=A + 8), ALIGN), (dict(k=A + 2), ALIGN),
+    (dict(v=A + 8), ALIGN), (dict(out=A + 8), ALIGN), (dict(table=A + 2), ALIGN),
+    (dict(lens=A + 1), ALIGN), (dict(starts=A + 2), ALIGN), (dict(starts=None), SHAPE),
+])
+def test_attention_refusals(change, status):
+    assert _attention(**change) == status
+
+
+def test_attention_empty_calls_and_workspace():
+    assert _attention(tokens=0) == 0 and _attention(tokens=0, seqs=0, starts=None) == 0
+    L = lg.lib()
+    assert L.lutgemm_paged_attention(None, A, A, A, A, A, A, A, None, 0, None) == NULL
+    n = ctypes.c_size_t()
+    long = dict(seqs=1, tokens=1, max_q=1, max_kv=65536, table_width=4096)
+    d = serving._ATTENTION.pack(*{**ATT, **long}.values())
+    assert L.lutgemm_paged_attention_workspace(d, ctypes.byref(n)) == 0 and n.value > 0
+    assert L.lutgemm_paged_attention_workspace(d, None) == NULL
+    assert _attention(**long) == NULL
+    assert _attention(ws=A, wsb=n.value - 1, **long) == BUFFER
+    assert _attention(ws=A + 4, wsb=n.value, **long) == ALIGN
+
+
+# ----------------------------------------------------------------- heads refusals
+
+HEADS = dict(type=1, heads=4, kv_heads=2, head_dim=64, rotary=64, interleaved=0, page_size=16, eps=1e-6,
+             tokens=5, positions=100, pages=9, qkv_token=512, q_token=256, k_page=2048, k_slot=128,
+             k_head=64, v_page=2048, v_slot=128, v_head=64)
+
+
+def _heads(qkv=A, at=A, table=A, qw=A, kw=A, q=A, k=A, v=A, slots=A, **change):
+    d = serving._HEADS.pack(*{**HEADS, **change}.values())
+    return lg.lib().lutgemm_qk_norm_rotate(d, qkv, at, table, qw, kw, q, k, v, slots, None)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(type=3), SHAPE), (dict(heads=0), SHAPE), (dict(kv_heads=0), SHAPE), (dict(heads=70000), SHAPE),
+    (dict(head_dim=8), SHAPE), (dict(head_dim=72), SHAPE), (dict(head_dim=272), SHAPE),
+    (dict(rotary=80), SHAPE), (dict(rotary=8), SHAPE), (dict(rotary=-16), SHAPE),
+    (dict(interleaved=2), SHAPE), (dict(page_size=0), SHAPE), (dict(eps=-1.0), VALUE),
+    (dict(eps=float("nan")), VALUE), (dict(eps=float("inf")), VALUE), (dict(tokens=-1), SHAPE),
+    (dict(tokens=1 << 24), SHAPE), (dict(positions=0), SHAPE), (dict(pages=-1), SHAPE),
+    (dict(qkv_token=4), SHAPE), (dict(q_token=-8), SHAPE), (dict(k_slot=1), SHAPE),
+    (dict(v_head=12), SHAPE), (dict(qkv=None), NULL), (dict(q=None), NULL), (dict(k=None), NULL),
+    (dict(v=None), NULL), (dict(at=None), NULL), (dict(table=None), NULL), (dict(qw=None), NULL),
+    (dict(kw=None), NULL), (dict(qkv=A + 2), ALIGN), (dict(q=A + 8), ALIGN), (dict(k=A + 8), ALIGN),
+    (dict(v=A + 8), ALIGN), (dict(table=A + 4), ALIGN), (dict(qw=A + 2), ALIGN), (dict(at=A + 4), ALIGN),
+    (dict(slots=A + 4), ALIGN),
+])
+def test_heads_refusals(change, status):
+    assert _heads(**change) == status
+
+
+def test_heads_empty_call():
+    assert _heads(tokens=0) == 0
+    assert lg.lib().lutgemm_qk_norm_rotate(None, A, A, A, A, A, A, A, A, A, None) == NULL
+
+
+# -------------------------------------------------------------- adapters refusals
+
+ADD = dict(type=0, rows=20, K=64, N=40, rank=16, adapters=3, x_row=64, y_row=40, out_row=40)
+
+
+def _adapters(x=A, y=A, a=A, b=A, s=A, ids=A, out=2 * A, ws=A, wsb=1 << 20, **change):
+    d = serving._ADAPTERS.pack(*{**ADD, **change}.values())
+    return lg.lib().lutgemm_adapters_add(d, x, y, a, b, s, ids, out, ws, wsb, None)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(type=2), SHAPE), (dict(rows=-1), SHAPE), (dict(rows=65536), SHAPE), (dict(K=12), SHAPE),
+    (dict(K=-8), SHAPE), (dict(K=1 << 24), SHAPE), (dict(N=-1), SHAPE), (dict(N=1 << 23), SHAPE),
+    (dict(rank=0), SHAPE), (dict(rank=12), SHAPE), (dict(rank=136), SHAPE), (dict(adapters=-1), SHAPE),
+    (dict(adapters=4097), SHAPE), (dict(x_row=60), SHAPE), (dict(y_row=-1), SHAPE),
+    (dict(out_row=-1), SHAPE), (dict(x=None), NULL), (dict(y=None), NULL), (dict(a=None), NULL),
+    (dict(b=None), NULL), (dict(ids=None), NULL), (dict(out=None), NULL), (dict(ws=None), NULL),
+    (dict(wsb=16), BUFFER), (dict(ws=A + 8), ALIGN), (dict(x=A + 8), ALIGN), (dict(a=A + 2), ALIGN),
+    (dict(b=A + 4), ALIGN), (dict(s=A + 2), ALIGN), (dict(ids=A + 2), ALIGN), (dict(y=A + 1), ALIGN),
+    (dict(out=A + 1), ALIGN), (dict(out=A, out_row=48), SHAPE),
+])
+def test_adapters_refusals(change, status):
+    assert _adapters(**change) == status
+
+
+def test_adapters_empty_calls():
+    assert _adapters(rows=0) == 0 and _adapters(N=0) == 0
+    assert lg.lib().lutgemm_adapters_add(None, A, A, A, A, A, A, A, A, 0, None) == NULL
+    assert lg.lib().lutgemm_adapters_workspace(serving._ADAPTERS.pack(*ADD.values()), None) == NULL
+
+
+# ------------------------------------------------------------- the binding's checks
+
+def test_binding_refuses_cpu_tensors_and_types():
+    h = torch.zeros((2, 256), dtype=torch.float16)
+    with pytest.raises(ValueError, match="GPU"):
+        lg.qk_norm_rotate(h, 2, 1)
+    with pytest.raises(ValueError, match="fp16 or bf16"):
+        lg.qk_norm_rotate(h.float(), 2, 1)
+    with pytest.raises(ValueError, match="GPU"):
+        lg.paged_attention(h.view(2, 2, 128), h, h, h, h)
+    with pytest.raises(ValueError, match="GPU"):
+        lg.adapters_add(h, h, h, h, h)
+    with pytest.raises(ValueError):
+        lg.rotary_table(0, 64)
+    with pytest.raises(ValueError):
+        lg.rotary_table(8, 7)
+
+
+def test_packed_call_needs_adapters_and_ids_together():
+    import workloads
+    w = workloads.random_bcq(32, 512, 2, 128, seed=1)
+    pw = lg.PackedBCQ.from_bcq(w.bits, w.alpha, None, w.g, device="cpu")
+    x = torch.zeros((2, 512), dtype=torch.float16)
+    for kw in (dict(adapters=(x, x, None)), dict(ids=x)):
+        with pytest.raises(ValueError, match="together"):
+            pw(x, **kw)
+
+
+def test_descriptors_match_the_header(tmp_path):
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        pytest.skip("no C compiler")
+    src = tmp_path / "sizes.c"
+    src.write_text('''
+#include <stdio.h>
+#include "lutgemm.h"
+int main(void) {
+  printf("%zu %zu %zu %zu %zu %zu\\n", sizeof(lutgemm_heads), offsetof(lutgemm_heads, v_head),
+         sizeof(lutgemm_attention), offsetof(lutgemm_attention, v_head), sizeof(lutgemm_adapters),
+         offsetof(lutgemm_adapters, out_row));
+  return 0;
+}
+''')
+    exe = tmp_path / "sizes"
+    subprocess.run([cc, "-std=c99", f"-I{os.path.join(ROOT, 'include')}", str(src), "-o", str(exe)],
+                   check=True)
+    got = [int(v) for v in subprocess.run([str(exe)], capture_output=True, text=True).stdout.split()]
+    want = []
+    for s in (serving._HEADS, serving._ATTENTION, serving._ADAPTERS):
+        want += [s.size, s.size - 8]
+    assert got == want and struct.calcsize("@i") == 4
+
+
+# ----------------------------------------------------------------- the plain forms
+
+def test_plain_attention_is_softmax_attention():
+    rng = np.random.default_rng(0)
+    q, k, v = (rng.standard_normal(s) for s in ((3, 4, 8), (7, 2, 8), (7, 2, 8)))
+    out, _ = plain.attention(q, k, v, 3, 7, 0.3, 0, 2.0 ** -11)
+    tq, tk, tv = (torch.from_numpy(t).transpose(0, 1) for t in (q, k, v))
+    tk, tv = (t.repeat_interleave(2, 0) for t in (tk, tv))
+    mask = torch.tril(torch.ones(7, 7, dtype=torch.bool))[-3:]
+    ref = torch.nn.functional.scaled_dot_product_attention(tq, tk, tv, attn_mask=mask, scale=0.3)
+    assert np.allclose(out, ref.transpose(0, 1).numpy(), atol=1e-12)
+    early, _ = plain.attention(q, k[:1], v[:1], 3, 1, 0.3, 0, 2.0 ** -11)
+    assert (early[:2] == 0).all() and np.allclose(early[2], v[0].repeat(2, 0))
+
+
+def test_plain_heads_turn_pairs():
+    x = np.random.default_rng(1).standard_normal((2, 3, 6))
+    th = np.array([[0.5, 1.0], [0.1, -0.4]])
+    for interleaved in (False, True):
+        out, _ = plain.heads(x, None, 0.0, np.cos(th), np.sin(th), interleaved, 2.0 ** -11)
+        a, b = (x[..., [0, 2]], x[..., [1, 3]]) if interleaved else (x[..., :2], x[..., 2:4])
+        z = (a + 1j * b) * np.exp(1j * th)[:, None]
+        got = (out[..., [0, 2]] + 1j * out[..., [1, 3]]) if interleaved \
+            else out[..., :2] + 1j * out[..., 2:4]
+        assert np.allclose(got, z) and np.array_equal(out[..., 4:], x[..., 4:])
+
+
+def test_plain_adapters():
+    rng = np.random.default_rng(2)
+    y, x, a, b = (rng.standard_normal(s) for s in ((3, 5), (3, 8), (2, 4, 8), (2, 5, 4)))
+    out, _ = plain.adapters(y, x, a, b, [1, -1, 0], [2.0, 3.0], 2.0 ** -11, 2.0 ** -21)
+    assert np.allclose(out[0], y[0] + 3 * b[1] @ a[1] @ x[0]) and np.array_equal(out[1], y[1])
+    assert np.allclose(out[2], y[2] + 2 * b[0] @ a[0] @ x[2])
