@@ -5,7 +5,8 @@ Host code (the packer) is compiled with g++, device code with hipcc, and the
 two are linked into one shared library next to this file. The same sources
 built with ``-DLUTGEMM_PHASE_TRACE`` give ``liblutgemm_trace.so``, the variant
 whose kernels stamp their phase boundaries (``lutgemm_trace_attach``; read by
-``python -m lut_gemv_amd.phases``).
+``python -m lut_gemv_amd.phases``). ``_binding.so`` takes the serving operators'
+torch tensors to the library; it is built against the installed torch.
 """
 from __future__ import annotations
 
@@ -13,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 import tempfile
 from concurrent.futures import ThreadPoolExecutor
 
@@ -23,6 +25,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "liblutgemm.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 TRACE_LIB_PATH = os.path.join(PKG, "liblutgemm_trace.so")
+BINDING_PATH = os.path.join(PKG, "_binding.so")
 
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 HIPCC = os.environ.get("HIPCC", os.path.join(ROCM, "bin", "hipcc"))
@@ -62,6 +65,20 @@ def _run(cmd, verbose):
     if verbose and r.stdout.strip():
         print(r.stdout, flush=True)
     return r.stdout
+
+
+def _binding_job(out: str):
+    """The compiler call for the torch binding (host code only)."""
+    import torch
+    from torch.utils import cpp_extension
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    incs = [sysconfig.get_paths()["include"], *cpp_extension.include_paths(),
+            os.path.join(ROCM, "include")]
+    return [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1",
+            "-DUSE_ROCM=1", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            f"-I{INCLUDE}", *(a for i in incs for a in ("-isystem", i)),
+            os.path.join(CSRC, "binding.cpp"), f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10",
+            "-lc10_hip", "-o", out]
 
 
 def build(verbose: bool = False, extra_hip_flags=(), trace: bool = True) -> str:
@@ -106,6 +123,7 @@ def build(verbose: bool = False, extra_hip_flags=(), trace: bool = True) -> str:
                 jobs.append([HIPCC, *HIP_FLAGS, *extra_hip_flags, *defs, *incs, f"-DLUTGEMM_Q={q}",
                              "-c", "-Rpass-analysis=kernel-resource-usage",
                              os.path.join(CSRC, "lutgemv_q.hip"), "-o", o])
+        jobs.append(_binding_job(os.path.join(tmp, "_binding.so")))
         workers = max(1, min(len(jobs), int(os.environ.get("MAX_JOBS", os.cpu_count() or 1))))
         with ThreadPoolExecutor(max_workers=workers) as ex:
             outs = [f.result() for f in [ex.submit(_run, j, False) for j in jobs]]
@@ -119,6 +137,8 @@ def build(verbose: bool = False, extra_hip_flags=(), trace: bool = True) -> str:
             _run([HIPCC, "-shared", "-fPIC", f"--offload-arch={ARCH}", *ob,
                   "-pthread", "-o", out_tmp], verbose)
             os.replace(out_tmp, path)
+        shutil.copyfile(os.path.join(tmp, "_binding.so"), BINDING_PATH + ".tmp")
+        os.replace(BINDING_PATH + ".tmp", BINDING_PATH)
     finally:
         shutil.rmtree(tmp, ignore_errors=True)
     return LIB_PATH

@@ -11,7 +11,6 @@ import numpy as np
 import pytest
 
 import lut_gemv_amd as lg
-from lut_gemv_amd import serving
 from oracle import serving as plain
 
 torch = pytest.importorskip("torch")
@@ -19,6 +18,10 @@ torch = pytest.importorskip("torch")
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 A = 0x100000     # a fake, aligned device address: never dereferenced
 NULL, SHAPE, VALUE, BUFFER, ALIGN = 1, 2, 3, 4, 5
+# the header's descriptors
+_HEADS = struct.Struct("@7if11q")
+_ATTENTION = struct.Struct("@8ifi15q")
+_ADAPTERS = struct.Struct("@6i3q")
 
 
 # ------------------------------------------------------------- attention refusals
@@ -30,7 +33,7 @@ ATT = dict(type=0, heads=8, kv_heads=2, head_dim=128, page_size=16, seqs=3, tabl
 
 
 def _attention(ws=None, wsb=0, q=A, k=A, v=A, table=A, lens=A, starts=A, out=A, **change):
-    d = serving._ATTENTION.pack(*{**ATT, **change}.values())
+    d = _ATTENTION.pack(*{**ATT, **change}.values())
     return lg.lib().lutgemm_paged_attention(d, q, k, v, table, lens, starts, out, ws, wsb, None)
 
 
@@ -60,7 +63,7 @@ def test_attention_empty_calls_and_workspace():
     assert L.lutgemm_paged_attention(None, A, A, A, A, A, A, A, None, 0, None) == NULL
     n = ctypes.c_size_t()
     long = dict(seqs=1, tokens=1, max_q=1, max_kv=65536, table_width=4096)
-    d = serving._ATTENTION.pack(*{**ATT, **long}.values())
+    d = _ATTENTION.pack(*{**ATT, **long}.values())
     assert L.lutgemm_paged_attention_workspace(d, ctypes.byref(n)) == 0 and n.value > 0
     assert L.lutgemm_paged_attention_workspace(d, None) == NULL
     assert _attention(**long) == NULL
@@ -76,7 +79,7 @@ HEADS = dict(type=1, heads=4, kv_heads=2, head_dim=64, rotary=64, interleaved=0,
 
 
 def _heads(qkv=A, at=A, table=A, qw=A, kw=A, q=A, k=A, v=A, slots=A, **change):
-    d = serving._HEADS.pack(*{**HEADS, **change}.values())
+    d = _HEADS.pack(*{**HEADS, **change}.values())
     return lg.lib().lutgemm_qk_norm_rotate(d, qkv, at, table, qw, kw, q, k, v, slots, None)
 
 
@@ -109,7 +112,7 @@ ADD = dict(type=0, rows=20, K=64, N=40, rank=16, adapters=3, x_row=64, y_row=40,
 
 
 def _adapters(x=A, y=A, a=A, b=A, s=A, ids=A, out=2 * A, ws=A, wsb=1 << 20, **change):
-    d = serving._ADAPTERS.pack(*{**ADD, **change}.values())
+    d = _ADAPTERS.pack(*{**ADD, **change}.values())
     return lg.lib().lutgemm_adapters_add(d, x, y, a, b, s, ids, out, ws, wsb, None)
 
 
@@ -131,7 +134,7 @@ def test_adapters_refusals(change, status):
 def test_adapters_empty_calls():
     assert _adapters(rows=0) == 0 and _adapters(N=0) == 0
     assert lg.lib().lutgemm_adapters_add(None, A, A, A, A, A, A, A, A, 0, None) == NULL
-    assert lg.lib().lutgemm_adapters_workspace(serving._ADAPTERS.pack(*ADD.values()), None) == NULL
+    assert lg.lib().lutgemm_adapters_workspace(_ADAPTERS.pack(*ADD.values()), None) == NULL
 
 
 # ------------------------------------------------------------- the binding's checks
@@ -182,7 +185,7 @@ int main(void) {
                    check=True)
     got = [int(v) for v in subprocess.run([str(exe)], capture_output=True, text=True).stdout.split()]
     want = []
-    for s in (serving._HEADS, serving._ATTENTION, serving._ADAPTERS):
+    for s in (_HEADS, _ATTENTION, _ADAPTERS):
         want += [s.size, s.size - 8]
     assert got == want and struct.calcsize("@i") == 4
 
