@@ -11,10 +11,11 @@
 // is raised only when a score passes it by more than 8: until then weights stay below
 // 2^8, inside fp16's range, and the accumulators need no rescaling.
 //
-// Two kernels, chosen per sequence by its rows (tokens x group):
-//   few_kernel   up to 16 rows, memory-bound: each wave streams its own 32-key tiles
-//   many_kernel  more rows: 128 rows x 64 keys per step, keys and values through LDS
-// Both split a long key axis over workgroups; combine_kernel joins the parts.
+// Two bodies, chosen per sequence by its rows (tokens x group):
+//   few_rows   up to 16 rows, memory-bound: each wave streams its own 32-key tiles
+//   many_rows  more rows: 128 rows x 64 keys per step, keys and values through LDS
+// in a kernel each, and in one together for a batch that has both. Both split a long key
+// axis over workgroups; the combine kernels join the parts.
 #include "serve.h"
 
 namespace lutgemm {
@@ -24,6 +25,7 @@ using namespace serve;
 
 constexpr int kThreads = 256;
 constexpr int kFewRows = 16;
+constexpr int kFewWaves = 8;
 constexpr int kManyRows = 128;
 constexpr int kSplitKeys = 128;   // a part of the key axis is a multiple of this
 constexpr int kMaxSplits = 128;
@@ -43,9 +45,10 @@ struct AttnParams {
   int64_t k_page, k_head, v_page, v_head;
   int32_t k_slot, v_slot;
   int32_t tokens, seqs, heads, kv_heads, group, pages, page_log2, table_keys, window;
-  int32_t splits, chunk;
-  int32_t few_rows;  // sequences of up to so many rows are few_kernel's
-  int32_t tiles;     // row tiles of many_kernel, an upper bound
+  int32_t splits[2], chunk[2];  // of few_rows and of many_rows
+  int32_t few_rows;             // sequences of up to so many rows are few_rows'
+  int32_t tiles;                // row tiles of many_rows, an upper bound
+  int32_t few_blocks;           // mixed_kernel: the workgroups of its first kind
   float scale2;      // scale * log2(e)
 };
 
@@ -78,6 +81,7 @@ struct Span {
   int lo, hi, chunk, parts;
 };
 
+template <int Kind>  // 0: few_rows', 1: many_rows'
 __device__ __forceinline__ Span span_of(const AttnParams& p, const Seq& q, int r0, int r1) {
   Span a;
   const int first = q.n - q.len + r0 / p.group, last = q.n - q.len + (r1 - 1) / p.group;
@@ -86,19 +90,30 @@ __device__ __forceinline__ Span span_of(const AttnParams& p, const Seq& q, int r
   a.lo = lo < 0 ? 0 : lo & ~63;
   const int keys = a.hi > a.lo ? a.hi - a.lo : 0;
   // a sequence longer than the launch was made for takes longer parts
-  const int need = (keys + p.splits - 1) / p.splits;
-  a.chunk = need > p.chunk ? (need + kSplitKeys - 1) / kSplitKeys * kSplitKeys : p.chunk;
+  const int need = (keys + p.splits[Kind] - 1) / p.splits[Kind];
+  a.chunk = need > p.chunk[Kind] ? (need + kSplitKeys - 1) / kSplitKeys * kSplitKeys
+                                 : p.chunk[Kind];
   a.parts = keys > a.chunk ? (keys + a.chunk - 1) / a.chunk : 1;
   return a;
 }
 
-// Where the sixteen keys from key 16 * blk on lie in their page: the page's number
-// and the element offset of the first of them.
-__device__ __forceinline__ int page_of(const AttnParams& p, const int32_t* row, int blk, bool* bad) {
-  const int id = row[blk >> (p.page_log2 - 4)];
+// A row of the page table, read by scalar loads: they do not wait in turn behind the
+// keys and values under way.
+typedef const __attribute__((address_space(4))) int32_t* TableRow;
+
+__device__ __forceinline__ TableRow table_row(const AttnParams& p, int s) {
+  return (TableRow)(p.table + s * p.table_stride);
+}
+
+// The page of the sixteen keys from key 16 * blk on, and the slot of the first of them.
+__device__ __forceinline__ int page_of(const AttnParams& p, int id, bool* bad) {
   const bool out = (uint32_t)id >= (uint32_t)p.pages;
   *bad |= out;
   return out ? 0 : id;
+}
+
+__device__ __forceinline__ int table_at(const AttnParams& p, int blk) {
+  return blk >> (p.page_log2 - 4);
 }
 
 __device__ __forceinline__ int slot_of(const AttnParams& p, int blk) {
@@ -122,66 +137,91 @@ __device__ __forceinline__ int v_word(int row, int word) {
   return row * (2 * D) + (((word >> 1) ^ turn) << 5) + ((word & 1) << 4);
 }
 
+// 16 bytes a lane from memory to LDS, in lane order from `to` on (the same for the
+// wave). Buffer loads: while loads of the flat kind to LDS are under way the compiler
+// lets no LDS read overtake another.
+__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t from, uint32_t offset, char* to) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void*)to, 16,
+                                           offset, 0, 0, 0);
+}
+
+// The sixteen rows from `base` on, of `slot` elements' distance and D elements each.
+template <int D>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t sixteen_rows(const uint16_t* base, int slot) {
+  return __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, 30 * slot + 2 * D, 0x00027000);
+}
+
+// This wave's loads have arrived, in LDS too.
+__device__ __forceinline__ void wait_for_loads() { __builtin_amdgcn_s_waitcnt(0x0F70); }
+
 // ------------------------------------------------------------------- few rows
 //
-// Bound by reading the cache. The four waves of a workgroup take turns at 32-key
-// tiles of its part and keep their own softmax; a tile's keys go straight from
-// memory to the operand registers, its values through the wave's own 32 rows of LDS,
-// so the loop has no barrier. The next tile's loads are in flight while a tile is
-// computed: with two workgroups on a compute unit 128 KB per unit.
+// Bound by reading the cache. The eight waves of a workgroup take turns at 32-key
+// tiles of its part and keep their own softmax. A tile's keys and values pass through
+// the wave's own 64 rows of LDS, so the loop has no barrier; the next tile's loads
+// follow at once into the registers that this frees and are in flight while the tile is
+// computed, 128 KB per compute unit. Loads cover whole
+// rows of the cache: keys loaded in the matrix operand's own layout (64 bytes of each
+// of 16 rows at a time) needed no LDS and were slower.
 
+// One tile's 32 keys and values in registers as they lie in memory: a load covers
+// whole rows, 64 / (D / 8) of them.
 template <int D>
 struct FewTile {
-  u4v k[2][D / 32];
-  u4v v[2][D / 32];
+  u4v k[D / 16], v[D / 16];
 };
 
-template <class T, int D>
-__device__ __forceinline__ void few_load(const AttnParams& p, FewTile<D>& t, const int32_t* table,
+template <int D>
+__device__ __forceinline__ void few_load(const AttnParams& p, FewTile<D>& t, const int (&ids)[2],
                                          int kvh, int kt, int n, int lane, bool* bad) {
+  constexpr int words = D / 8, rows = 64 / words, each = 16 / rows;
   const int last = (n - 1) >> 4;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int blk = min_of(2 * kt + i, last), most = n - 1 - 16 * blk;
-    const int id = uniform(page_of(p, table, blk, bad));
-    const int slot = slot_of(p, blk);
+    const int id = page_of(p, ids[i], bad), slot = slot_of(p, blk);
     const uint16_t* kb = p.k + (int64_t)id * p.k_page + (int64_t)slot * p.k_slot + kvh * p.k_head;
     const uint16_t* vb = p.v + (int64_t)id * p.v_page + (int64_t)slot * p.v_slot + kvh * p.v_head;
-    const uint32_t ko = (uint32_t)min_of(lane & 15, most) * (uint32_t)p.k_slot + 8 * (lane >> 4);
 #pragma unroll
-    for (int ks = 0; ks < D / 32; ++ks) t.k[i][ks] = *(const u4v*)(kb + ko + 32 * ks);
-    constexpr int words = D / 8, rows = 64 / words;  // rows of values that one load covers
-#pragma unroll
-    for (int j = 0; j < D / 32; ++j) {
-      const int row = min_of(rows * j + lane / words, most);
-      t.v[i][j] = *(const u4v*)(vb + (uint32_t)row * (uint32_t)p.v_slot + 8 * (lane % words));
+    for (int j = 0; j < each; ++j) {
+      const uint32_t row = (uint32_t)min_of(rows * j + lane / words, most);
+      const uint32_t col = 8 * (lane % words);
+      t.k[each * i + j] =
+          __builtin_nontemporal_load((const u4v*)(kb + row * (uint32_t)p.k_slot + col));
+      t.v[each * i + j] =
+          __builtin_nontemporal_load((const u4v*)(vb + row * (uint32_t)p.v_slot + col));
     }
   }
 }
 
-template <class T, int D>
-__global__ __launch_bounds__(kThreads, 2) void few_kernel(AttnParams p) {
-  constexpr int kPitch = D + 4;
-  constexpr int kOut = 4 * kFewRows * kPitch * 4, kVal = 4 * 32 * D * 2;
-  __shared__ __attribute__((aligned(16))) char mem[kOut > kVal ? kOut : kVal];
-  __shared__ float wave_m[4][kFewRows], wave_l[4][kFewRows];
-  __shared__ int any_bad;
+// W waves; region(w): the LDS of wave w, 64 rows of D elements.
+template <int W>
+struct FewShared {
+  float m[W][kFewRows], l[W][kFewRows];
+  int any_bad;
+};
 
-  const int s = blockIdx.x / p.kv_heads, kvh = blockIdx.x % p.kv_heads, split = blockIdx.y;
+template <class T, int D, int W, class Region>
+__device__ __forceinline__ void few_rows(const AttnParams& p, int block, Region region,
+                                         FewShared<W>& shared) {
+  constexpr int kPitch = D + 4;
+  static_assert(kFewRows * kPitch * 4 <= 64 * D * 2, "a wave's sums fit its region");
+  const int part = block / p.kv_heads, kvh = block % p.kv_heads;
+  const int s = part / p.splits[0], split = part % p.splits[0];
   const Seq seq = sequence(p, s);
   const int rows = seq.len * p.group;
   if (rows > p.few_rows) return;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int c = lane >> 4;
-  const int32_t* table = p.table + s * p.table_stride;
+  const TableRow table = table_row(p, s);
 
   for (int r0 = 0; r0 < rows; r0 += kFewRows) {
     const int r1 = min_of(r0 + kFewRows, rows);
-    const Span span = span_of(p, seq, r0, r1);
+    const Span span = span_of<0>(p, seq, r0, r1);
     if (split >= span.parts) continue;
     const int from = span.lo + split * span.chunk;
     const int to = min_of(span.hi, from + span.chunk);
-    if (threadIdx.x == 0) any_bad = seq.bad;
+    if (threadIdx.x == 0) shared.any_bad = seq.bad;
     __syncthreads();
 
     // this lane's row: its query operand and the keys [row_lo, row_hi) it sees
@@ -202,21 +242,42 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(AttnParams p) {
     for (int d = 0; d < D / 16; ++d) o[d] = f4v{0.f, 0.f, 0.f, 0.f};
     float m = -INFINITY, l = 0.f;
     bool bad = false;
-    char* vals = mem + wave * (32 * D * 2);
-
-    auto step = [&](const FewTile<D>& t, int kt) {
-      f4v sc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    char* keys = region(wave);
+    char* vals = keys + 32 * D * 2;
+    FewTile<D> t;
+    int ids[2];
+    const int end = (to + 31) >> 5, end_blk = (span.hi - 1) >> 4;
+    auto next_ids = [&](int kt) {
 #pragma unroll
-      for (int ks = 0; ks < D / 32; ++ks) {
-        sc[0] = T::mfma16(t.k[0][ks], q[ks], sc[0]);
-        sc[1] = T::mfma16(t.k[1][ks], q[ks], sc[1]);
-      }
+      for (int i = 0; i < 2; ++i) ids[i] = table[table_at(p, min_of(2 * kt + i, end_blk))];
+    };
+    int kt = (from >> 5) + wave;
+    if (kt < end) {
+      next_ids(kt);
+      few_load<D>(p, t, ids, kvh, kt, span.hi, lane, &bad);
+      next_ids(kt + W);
+    }
+    for (; kt < end; kt += W) {
       constexpr int words = D / 8, vr = 64 / words;
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int j = 0; j < D / 16; ++j) {
+        *(u4v*)(keys + k_word<D>(vr * j + lane / words, lane % words)) = t.k[j];
+        *(u4v*)(vals + v_word<D>(vr * j + lane / words, lane % words)) = t.v[j];
+      }
+      if (kt + W < end) {
+        few_load<D>(p, t, ids, kvh, kt + W, span.hi, lane, &bad);
+        next_ids(kt + 2 * W);
+      }
+      // the wave's own stores to LDS are complete and visible to its other lanes
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      f4v sc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
-        for (int j = 0; j < D / 32; ++j)
-          *(u4v*)(vals + v_word<D>(16 * i + vr * j + lane / words, lane % words)) = t.v[i][j];
+      for (int ks = 0; ks < D / 32; ++ks)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          sc[i] = T::mfma16(*(const u4v*)(keys + k_word<D>(16 * i + (lane & 15), 4 * ks + c)), q[ks],
+                            sc[i]);
       float top = -INFINITY;
 #pragma unroll
       for (int i = 0; i < 2; ++i)
@@ -253,9 +314,6 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(AttnParams p) {
       w[1] = T::pack(sc[0][2], sc[0][3]);
       w[2] = T::pack(sc[1][0], sc[1][1]);
       w[3] = T::pack(sc[1][2], sc[1][3]);
-      // the wave's own stores to LDS are complete and visible to its other lanes
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
       const int row = 4 * c + ((lane & 15) >> 2), col = lane & 3;  // col: 8-byte words
 #pragma unroll
       for (int d = 0; d < D / 16; ++d) {
@@ -266,68 +324,46 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(AttnParams p) {
       // the next tile's stores come after these reads
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
-    };
-
-    const int end = (to + 31) >> 5;
-    int kt = (from >> 5) + wave;
-    if (kt < end) {
-      FewTile<D> t0, t1;
-      few_load<T, D>(p, t0, table, kvh, kt, seq.n, lane, &bad);
-      while (true) {
-        if (kt + 4 < end) few_load<T, D>(p, t1, table, kvh, kt + 4, seq.n, lane, &bad);
-        step(t0, kt);
-        kt += 4;
-        if (kt >= end) break;
-        if (kt + 4 < end) few_load<T, D>(p, t0, table, kvh, kt + 4, seq.n, lane, &bad);
-        step(t1, kt);
-        kt += 4;
-        if (kt >= end) break;
-      }
     }
-    // join the four waves
+    // join the waves
     l += __shfl_xor(l, 16, 64);
     l += __shfl_xor(l, 32, 64);
-    if (bad && lane == 0) any_bad = 1;
+    if (bad && lane == 0) shared.any_bad = 1;
     if (c == 0) {
-      wave_m[wave][lane] = m;
-      wave_l[wave][lane] = l;
+      shared.m[wave][lane] = m;
+      shared.l[wave][lane] = l;
     }
     __syncthreads();
-    float* sums = (float*)mem;
+    float* sums = (float*)region(wave);
 #pragma unroll
     for (int d = 0; d < D / 16; ++d)
-      *(f4v*)(sums + (wave * kFewRows + (lane & 15)) * kPitch + 16 * d + 4 * c) = o[d];
+      *(f4v*)(sums + (lane & 15) * kPitch + 16 * d + 4 * c) = o[d];
     __syncthreads();
-    const int jr = threadIdx.x >> 4, jc = (threadIdx.x & 15) * (D / 16);
+    constexpr int E = kFewRows * D / (64 * W);  // outputs of a thread
+    const int jr = threadIdx.x / (D / E), jc = threadIdx.x % (D / E) * E;
     if (r0 + jr < r1) {
-      float top = -INFINITY, total = 0.f, f[4];
+      float top = -INFINITY, total = 0.f, f[W], sum[E] = {};
 #pragma unroll
-      for (int w = 0; w < 4; ++w) top = fmaxf(top, wave_m[w][jr]);
+      for (int w = 0; w < W; ++w) top = fmaxf(top, shared.m[w][jr]);
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        f[w] = wave_m[w][jr] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(wave_m[w][jr] - top);
-        total += wave_l[w][jr] * f[w];
+      for (int w = 0; w < W; ++w) {
+        f[w] = shared.m[w][jr] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(shared.m[w][jr] - top);
+        total += shared.l[w][jr] * f[w];
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          sum[e] += ((const float*)region(w))[jr * kPitch + jc + e] * f[w];
       }
-      float sum[D / 16];
-#pragma unroll
-      for (int e = 0; e < D / 16; ++e) {
-        sum[e] = 0.f;
-#pragma unroll
-        for (int w = 0; w < 4; ++w)
-          sum[e] += sums[(w * kFewRows + jr) * kPitch + jc + e] * f[w];
-      }
-      if (any_bad) total = __builtin_nanf("");
+      if (shared.any_bad) total = __builtin_nanf("");
       const int token = seq.begin + (r0 + jr) / p.group, hd = kvh * p.group + (r0 + jr) % p.group;
       if (span.parts == 1) {
         const float inv = total == 0.f ? 0.f : 1.f / total;
         uint32_t* to32 = (uint32_t*)(p.out + (int64_t)token * p.o_token + hd * p.o_head + jc);
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e) to32[e] = T::pack(sum[2 * e] * inv, sum[2 * e + 1] * inv);
+        for (int e = 0; e < E / 2; ++e) to32[e] = T::pack(sum[2 * e] * inv, sum[2 * e + 1] * inv);
       } else {
         const int64_t at = ((int64_t)split * p.tokens + token) * p.heads + hd;
 #pragma unroll
-        for (int e = 0; e < D / 16; e += 4)
-          *(f4v*)(p.part_o + at * D + jc + e) = f4v{sum[e], sum[e + 1], sum[e + 2], sum[e + 3]};
+        for (int e = 0; e < E; ++e) p.part_o[at * D + jc + e] = sum[e];
         if (jc == 0) *(f2v*)(p.part_ml + 2 * at) = f2v{top, total};
       }
     }
@@ -335,23 +371,32 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(AttnParams p) {
   }
 }
 
+template <class T, int D>
+__global__ __launch_bounds__(64 * kFewWaves, 2) void few_kernel(AttnParams p) {
+  __shared__ __attribute__((aligned(16))) char mem[kFewWaves * 64 * D * 2];
+  __shared__ FewShared<kFewWaves> shared;
+  few_rows<T, D, kFewWaves>(p, blockIdx.x, [&](int w) { return mem + w * (64 * D * 2); }, shared);
+}
+
 // ------------------------------------------------------------------ many rows
 //
-// Bound by the matrix cores and the softmax between them. A wave owns 32 rows; the
-// four share 64 keys and values in LDS, in two buffers: the next tile's loads are
-// issued before a tile is computed and stored to the other buffer after it, one
-// barrier a tile. Two workgroups share a compute unit, so one's products run beside
-// the other's exponentials.
+// Bound by the matrix cores, the exponentials beside them and the power both draw:
+// 2048 tokens x 32 heads on 16384 keys take 490 us, 1050 TFLOP/s, at a clock that the
+// card lowers from 2.0 to 1.7 GHz meanwhile (a large library product in bf16 reaches 1200).
+// A wave owns 32 rows; the four share 64 keys and values in LDS, in two buffers that
+// loads fill without passing registers, one barrier a tile. (Through registers, with
+// the operands' LDS reads waiting on them: 605 us.) The scores of one block of 32 keys are computed
+// beside the exponentials of the block before it, which costs 32 registers and saves
+// a third of the cycles; two workgroups share a compute unit. The buffers are arrays of
+// their own, so that the compiler sees that a load into one and a read of the other
+// need not wait for each other.
 
 template <class T, int D>
-__global__ __launch_bounds__(kThreads, 2) void many_kernel(AttnParams p) {
-  constexpr int kTile = 64 * D * 2;
-  __shared__ __attribute__((aligned(16))) char keys[2][kTile];
-  __shared__ __attribute__((aligned(16))) char vals[2][kTile];
-  __shared__ int any_bad;
-
-  const int kvh = blockIdx.x % p.kv_heads, split = blockIdx.y;
-  const int tile = p.tiles - 1 - (int)(blockIdx.x / p.kv_heads);  // the longest rows first
+__device__ __forceinline__ void many_rows(const AttnParams& p, int block, char* keys0, char* vals0,
+                                          char* keys1, char* vals1, int& any_bad) {
+  const int kvh = block % p.kv_heads;
+  const int nth = block / p.kv_heads % p.tiles, split = block / p.kv_heads / p.tiles;
+  const int tile = p.tiles - 1 - nth;  // the longest rows first
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int h = lane >> 5;
 
@@ -373,7 +418,7 @@ __global__ __launch_bounds__(kThreads, 2) void many_kernel(AttnParams p) {
   const int r0 = (tile - (int)((int64_t)seq.begin * p.group / kManyRows) - s) * kManyRows;
   if (r0 < 0 || r0 >= rows) return;
   const int r1 = min_of(r0 + kManyRows, rows);
-  const Span span = span_of(p, seq, r0, r1);
+  const Span span = span_of<1>(p, seq, r0, r1);
   if (split >= span.parts) return;
   const int from = span.lo + split * span.chunk;
   const int to = min_of(span.hi, from + span.chunk);
@@ -389,9 +434,8 @@ __global__ __launch_bounds__(kThreads, 2) void many_kernel(AttnParams p) {
   const int row_lo = p.window > 0 ? pos - p.window + 1 : 0;
   const int first = uniform(seq.n - seq.len + min_of(w0, r1 - 1) / p.group);
   const int last = uniform(seq.n - seq.len + min_of(w0 + 31, r1 - 1) / p.group);
-  // keys that some row sees [wave_lo, wave_hi), and that every row sees [all_lo, all_hi)
-  const int wave_hi = w0 < r1 ? last + 1 : 0, all_hi = first + 1;
-  const int wave_lo = p.window > 0 ? first - p.window + 1 : 0;
+  // the keys that every row of the wave sees
+  const int all_hi = first + 1;
   const int all_lo = p.window > 0 ? last - p.window + 1 : 0;
   u4v q[D / 16];
   {
@@ -404,113 +448,168 @@ __global__ __launch_bounds__(kThreads, 2) void many_kernel(AttnParams p) {
   for (int d = 0; d < D / 32; ++d)
 #pragma unroll
     for (int e = 0; e < 16; ++e) o[d][e] = 0.f;
-  float m = -INFINITY, l = 0.f;
+  float m = -INFINITY, l = 0.f, base = 0.f;
   bool bad = false;
 
-  // a thread's share of a tile: one 16-byte word of each of kLoads row groups
-  constexpr int kWords = D / 8, kRowsEach = kThreads / kWords, kLoads = 64 / kRowsEach;
-  const int my_row = threadIdx.x / kWords, my_word = threadIdx.x % kWords;
-  u4v kr[kLoads], vr[kLoads];
-  const int end_blk = (seq.n - 1) >> 4;
-  auto load = [&](int kt) {
+  // A wave brings sixteen of a tile's keys and values, straight from memory to LDS:
+  // a load places 1 KB of whole rows there in lane order, so each lane reads the word
+  // whose place in the LDS layout its own is.
+  constexpr int kWords = D / 8, kRowsEach = 64 / kWords, kLoads = 16 / kRowsEach;
+  const int end_blk = (span.hi - 1) >> 4;
+  // lane i: the page of this wave's values of tile ids_from + i - 1, lanes' keys being two
+  // blocks of sixteen further on
+  int k_ids = 0, v_ids = 0, ids_from = 0;
+  auto block_at = [&](int blk) { return min_of(blk < 0 ? 0 : blk, end_blk); };
+  auto read_ids = [&](int kt) {
+    ids_from = kt - 1;
+    k_ids = table[table_at(p, block_at(4 * (ids_from + lane) + 2 + wave))];
+    v_ids = table[table_at(p, block_at(4 * (ids_from + lane) + wave))];
+    asm volatile("" : "+v"(k_ids), "+v"(v_ids));  // they arrive here, not behind later loads
+  };
+  auto load = [&](int blk, int id, const uint16_t* cache, int64_t page_step, int64_t head_step,
+                  int slot_step, char* to, auto word_of) {
+    const int page = page_of(p, id, &bad);
+    const __amdgpu_buffer_rsrc_t rows = sixteen_rows<D>(
+        cache + page * page_step + (int64_t)slot_of(p, blk) * slot_step + kvh * head_step, slot_step);
+    const int most = span.hi - 1 - 16 * blk;
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int row = kRowsEach * i + my_row;
-      const int blk = uniform(min_of(4 * kt + (row >> 4), end_blk));
-      const int id = uniform(page_of(p, table, blk, &bad));
-      const int slot = slot_of(p, blk);
-      const uint32_t in_blk = (uint32_t)min_of(row & 15, seq.n - 1 - 16 * blk);
-      const uint16_t* kb = p.k + (int64_t)id * p.k_page + (int64_t)slot * p.k_slot + kvh * p.k_head;
-      const uint16_t* vb = p.v + (int64_t)id * p.v_page + (int64_t)slot * p.v_slot + kvh * p.v_head;
-      kr[i] = *(const u4v*)(kb + in_blk * (uint32_t)p.k_slot + 8 * my_word);
-      vr[i] = *(const u4v*)(vb + in_blk * (uint32_t)p.v_slot + 8 * my_word);
+    for (int j = 0; j < kLoads; ++j) {
+      const int row = kRowsEach * j + lane / kWords, place = lane % kWords;
+      const uint32_t word = (uint32_t)(word_of(row, place) - row * 2 * D);
+      load_to_lds(rows, 2 * __umul24(min_of(row, most), slot_step) + word,
+                  to + (16 * wave + kRowsEach * j) * 2 * D);
     }
   };
-  auto store = [&](int buf) {
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int row = kRowsEach * i + my_row;
-      *(u4v*)(keys[buf] + k_word<D>(row, my_word)) = kr[i];
-      *(u4v*)(vals[buf] + v_word<D>(row, my_word)) = vr[i];
-    }
+  auto load_keys = [&](int kt, char* to) {
+    if (kt - ids_from >= 64) read_ids(kt);
+    load(block_at(4 * kt + 2 + wave), __builtin_amdgcn_readlane(k_ids, kt - ids_from), p.k, p.k_page,
+         p.k_head, p.k_slot, to, [](int r, int w) { return k_word<D>(r, w); });
   };
-  auto step = [&](int buf, int kt) {
-    const int k0 = 64 * kt;
-    f16v sc[2];
+  auto load_values = [&](int kt, char* to) {
+    load(block_at(4 * kt + wave), __builtin_amdgcn_readlane(v_ids, kt - ids_from), p.v, p.v_page,
+         p.v_head, p.v_slot, to, [](int r, int w) { return v_word<D>(r, w); });
+  };
+  constexpr int kSteps = D / 16;
+  // S^T of 32 keys in LDS
+  auto scores = [&](const char* keys) {
+    f16v sc;
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
+    for (int e = 0; e < 16; ++e) sc[e] = 0.f;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) sc[b][e] = 0.f;
+    for (int ks = 0; ks < kSteps; ++ks)
+      sc = T::mfma32(*(const u4v*)(keys + k_word<D>(lane & 31, 2 * ks + h)), q[ks], sc);
+    return sc;
+  };
+  // of the keys from k0 on: hidden ones out, and the running maximum
+  auto settle = [&](f16v& sc, int k0) {
+    if (k0 + 32 > all_hi || k0 < all_lo) {
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        const u4v a = *(const u4v*)(keys[buf] + k_word<D>(32 * b + (lane & 31), 2 * ks + h));
-        sc[b] = T::mfma32(a, q[ks], sc[b]);
+      for (int e = 0; e < 16; ++e) {
+        const int key = k0 + 8 * (e >> 2) + 4 * h + (e & 3);
+        if (key >= row_hi || key < row_lo) sc[e] = -INFINITY;
       }
-    }
-    if (k0 + 64 > all_hi || k0 < all_lo) {
-#pragma unroll
-      for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int key = k0 + 32 * b + 8 * (e >> 2) + 4 * h + (e & 3);
-          if (key >= row_hi || key < row_lo) sc[b][e] = -INFINITY;
-        }
     }
     float top = -INFINITY;
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) top = fmaxf(top, sc[b][e]);
+    for (int e = 0; e < 16; ++e) top = fmaxf(top, sc[e]);
     top *= p.scale2;
     if (__any(top > m + kRaise)) {
       top = fmaxf(top, __shfl_xor(top, 32, 64));
       const float raised = fmaxf(m, top);
       const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - raised);
       m = raised;
+      base = m == -INFINITY ? 0.f : m;
       l *= f;
 #pragma unroll
       for (int d = 0; d < D / 32; ++d)
 #pragma unroll
         for (int e = 0; e < 16; ++e) o[d][e] *= f;
     }
-    const float base = m == -INFINITY ? 0.f : m;
-#pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        sc[b][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[b][e], p.scale2, -base));
-        l += sc[b][e];
-      }
+  };
+  // the weights of 32 keys and their products with the values in LDS
+  auto weigh = [&](const f16v& sc, const char* vals) {
     const int vrow = 4 * h + ((lane & 15) >> 2), col = lane & 3, half = (lane >> 4) & 1;
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+    for (int g = 0; g < 2; ++g) {
+      u4v w;
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        u4v w;
+      for (int e = 0; e < 4; ++e) {
+        float x[2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = T::pack(sc[b][8 * u + 2 * e], sc[b][8 * u + 2 * e + 1]);
-        const int row = 32 * b + 16 * u + vrow;
-#pragma unroll
-        for (int d = 0; d < D / 32; ++d) {
-          const int word = 4 * d + 2 * half + (col >> 1);
-          const u2v x = read_column(vals[buf] + v_word<D>(row, word) + 8 * (col & 1));
-          const u2v y = read_column(vals[buf] + v_word<D>(row + 8, word) + 8 * (col & 1));
-          o[d] = T::mfma32(u4v{x.x, x.y, y.x, y.y}, w, o[d]);
+        for (int i = 0; i < 2; ++i) {
+          x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[8 * g + 2 * e + i], p.scale2, -base));
+          l += x[i];
         }
+        w[e] = T::pack(x[0], x[1]);
       }
+#pragma unroll
+      for (int d = 0; d < D / 32; ++d) {
+        const int row = 16 * g + vrow, word = 4 * d + 2 * half + (col >> 1);
+        const u2v x = read_column(vals + v_word<D>(row, word) + 8 * (col & 1));
+        const u2v y = read_column(vals + v_word<D>(row + 8, word) + 8 * (col & 1));
+        o[d] = T::mfma32(u4v{x.x, x.y, y.x, y.y}, w, o[d]);
+      }
+    }
   };
 
   const int begin = from >> 6, end = (to + 63) >> 6;
+  constexpr int kHalf = 32 * D * 2;
   if (begin < end) {
-    load(begin);
-    store(0);
+    read_ids(begin);
+    load_keys(begin - 1, keys1);
+    load_keys(begin, keys0);
+    load_values(begin, vals0);
+    // the queries have arrived before the loop: a wait for them in it would be one
+    // for the loads under way as well
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) asm volatile("" : "+v"(q[ks]));
+    wait_for_loads();
     __syncthreads();
-    for (int kt = begin; kt < end; ++kt) {
-      const int buf = (kt - begin) & 1;
-      if (kt + 1 < end) load(kt + 1);
-      if (64 * kt < wave_hi && 64 * kt + 64 > wave_lo) step(buf, kt);
-      if (kt + 1 < end) store(buf ^ 1);
+    if (w0 < r1) {
+      f16v s0, s1;
+      // Two steps of 32 keys, in each the weights of one block and the scores of the
+      // next: independent, so the products of one run beside the exponentials of the
+      // other. LDS holds the values of blocks 2 kt and 2 kt + 1 and the keys of the
+      // blocks after them.
+      auto turn = [&](int kt, char* keys, char* next_keys, char* vals, char* next_vals) {
+        load_keys(kt + 1, next_keys);
+        load_values(kt + 1, next_vals);
+        __builtin_amdgcn_sched_barrier(0);
+        s1 = scores(keys);
+        weigh(s0, vals);
+        settle(s1, 64 * kt + 32);
+        s0 = scores(keys + kHalf);
+        weigh(s1, vals + kHalf);
+        settle(s0, 64 * kt + 64);
+        wait_for_loads();
+        __syncthreads();
+      };
+      auto last = [&](int kt, char* keys, char* vals) {
+        s1 = scores(keys);
+        weigh(s0, vals);
+        settle(s1, 64 * kt + 32);
+        weigh(s1, vals + kHalf);
+      };
+      s0 = scores(keys1 + kHalf);
+      settle(s0, 64 * begin);
       __syncthreads();
+      int kt = begin;
+      for (; kt + 2 < end; kt += 2) {
+        turn(kt, keys0, keys1, vals0, vals1);
+        turn(kt + 1, keys1, keys0, vals1, vals0);
+      }
+      const bool two = kt + 1 < end;
+      if (two) turn(kt, keys0, keys1, vals0, vals1);
+      last(end - 1, two ? keys1 : keys0, two ? vals1 : vals0);
+    } else {  // a wave without rows only loads
+      __syncthreads();
+      for (int kt = begin; kt + 1 < end; ++kt) {
+        const bool even = ((kt - begin) & 1) == 0;
+        load_keys(kt + 1, even ? keys1 : keys0);
+        load_values(kt + 1, even ? vals1 : vals0);
+        wait_for_loads();
+        __syncthreads();
+      }
     }
   } else {
     __syncthreads();
@@ -543,12 +642,98 @@ __global__ __launch_bounds__(kThreads, 2) void many_kernel(AttnParams p) {
   }
 }
 
+template <class T, int D>
+__global__ __launch_bounds__(kThreads, 2) void many_kernel(AttnParams p) {
+  constexpr int kTile = 64 * D * 2;
+  __shared__ __attribute__((aligned(16))) char keys0[kTile], vals0[kTile], keys1[kTile], vals1[kTile];
+  __shared__ int any_bad;
+  many_rows<T, D>(p, blockIdx.x, keys0, vals0, keys1, vals1, any_bad);
+}
+
+// A batch with sequences of both kinds in one launch: the reading of the one runs
+// beside the products of the other.
+template <class T, int D>
+__global__ __launch_bounds__(kThreads, 2) void mixed_kernel(AttnParams p) {
+  constexpr int kTile = 64 * D * 2;
+  __shared__ __attribute__((aligned(16))) char keys0[kTile], vals0[kTile], keys1[kTile], vals1[kTile];
+  __shared__ FewShared<kThreads / 64> shared;
+  if ((int)blockIdx.x < p.few_blocks)
+    few_rows<T, D, kThreads / 64>(
+        p, blockIdx.x,
+        [&](int w) { return w == 0 ? keys0 : w == 1 ? vals0 : w == 2 ? keys1 : vals1; }, shared);
+  else
+    many_rows<T, D>(p, blockIdx.x - p.few_blocks, keys0, vals0, keys1, vals1, shared.any_bad);
+}
+
 // -------------------------------------------------------------- joining parts
 //
-// One wave for each row that was split: the parts' sums brought to one maximum.
+// One wave for each row that was split: the parts' sums brought to one maximum. The
+// lanes read the parts' maxima together, and four parts' sums are under way at a time.
 
 template <class T, int D>
-__global__ __launch_bounds__(kThreads) void combine_kernel(AttnParams p) {
+__device__ __forceinline__ void combine_row(const AttnParams& p, int parts, int token, int head) {
+  constexpr int E = D / 64;
+  typedef float fE __attribute__((ext_vector_type(E)));
+  const int lane = threadIdx.x & 63;
+  const int64_t row = (int64_t)token * p.heads + head, step = (int64_t)p.tokens * p.heads;
+  const float* from = p.part_o + row * D + lane * E;
+  float top = -INFINITY, total = 0.f;
+  fE sum = {};
+  for (int j0 = 0; j0 < parts; j0 += 64) {
+    const bool here = j0 + lane < parts;
+    f2v ml = f2v{-INFINITY, 0.f};
+    if (here) ml = *(const f2v*)(p.part_ml + 2 * (row + (j0 + lane) * step));
+    float most = ml.x;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) most = fmaxf(most, __shfl_xor(most, d, 64));
+    const float raised = fmaxf(top, most);
+    const float old = top == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(top - raised);
+    const float f = ml.x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ml.x - raised);
+    top = raised;
+    float l = ml.y != ml.y ? ml.y : ml.y * f;  // NaN marks a part that met a bad page
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) l += __shfl_xor(l, d, 64);
+    total = total * old + l;
+    sum *= old;
+    const int n = min_of(parts - j0, 64);
+    for (int j = 0; j < n; j += 4) {
+      fE o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = *(const fE*)(from + (j0 + min_of(j + i, n - 1)) * step * D);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float w = j + i < n ? __shfl(f, j + i, 64) : 0.f;
+        sum += o[i] * w;
+      }
+    }
+  }
+  const float inv = total == 0.f ? 0.f : 1.f / total;
+  uint16_t* dst = p.out + (int64_t)token * p.o_token + head * p.o_head + lane * E;
+  if constexpr (D == 128)
+    *(uint32_t*)dst = T::pack(sum[0] * inv, sum[1] * inv);
+  else
+    *dst = T::one(sum[0] * inv);
+}
+
+// few_rows' rows: four of one sequence and key head at a time.
+template <class T, int D>
+__global__ __launch_bounds__(kThreads) void combine_few_kernel(AttnParams p) {
+  const int s = blockIdx.x / p.kv_heads, kvh = blockIdx.x % p.kv_heads;
+  const Seq seq = sequence(p, s);
+  const int rows = seq.len * p.group;
+  if (rows > p.few_rows) return;
+  const int wave = uniform(threadIdx.x >> 6);
+  for (int r = blockIdx.y * 4 + wave; r < rows; r += 4 * gridDim.y) {
+    const int r0 = r / kFewRows * kFewRows;
+    const Span span = span_of<0>(p, seq, r0, min_of(r0 + kFewRows, rows));
+    if (span.parts > 1)
+      combine_row<T, D>(p, span.parts, seq.begin + r / p.group, kvh * p.group + r % p.group);
+  }
+}
+
+// many_rows' rows: one wave each.
+template <class T, int D>
+__global__ __launch_bounds__(kThreads) void combine_many_kernel(AttnParams p) {
   const int lane = threadIdx.x & 63;
   const int64_t row = (int64_t)blockIdx.x * 4 + uniform(threadIdx.x >> 6);
   if (row >= (int64_t)p.tokens * p.heads) return;
@@ -566,30 +751,11 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(AttnParams p) {
     if (s >= p.seqs) return;
   }
   const Seq seq = sequence(p, s);
-  if (token < seq.begin || token >= seq.begin + seq.len) return;
   const int rows = seq.len * p.group;
-  const int tile = rows <= p.few_rows ? kFewRows : kManyRows;
-  const int r0 = ((token - seq.begin) * p.group + head % p.group) / tile * tile;
-  const Span span = span_of(p, seq, r0, min_of(r0 + tile, rows));
-  if (span.parts == 1) return;
-  const int64_t step = (int64_t)p.tokens * p.heads;
-  float top = -INFINITY;
-  for (int j = 0; j < span.parts; ++j) top = fmaxf(top, p.part_ml[2 * (row + j * step)]);
-  float total = 0.f, sum[D / 64] = {};
-  for (int j = 0; j < span.parts; ++j) {
-    const float m = p.part_ml[2 * (row + j * step)], l = p.part_ml[2 * (row + j * step) + 1];
-    const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - top);
-    total += l != l ? l : l * f;
-#pragma unroll
-    for (int e = 0; e < D / 64; ++e)
-      sum[e] += f * p.part_o[(row + j * step) * D + lane * (D / 64) + e];
-  }
-  const float inv = total == 0.f ? 0.f : 1.f / total;
-  uint16_t* dst = p.out + (int64_t)token * p.o_token + head * p.o_head + lane * (D / 64);
-  if constexpr (D == 128)
-    *(uint32_t*)dst = T::pack(sum[0] * inv, sum[1] * inv);
-  else
-    *dst = T::one(sum[0] * inv);
+  if (token < seq.begin || token >= seq.begin + seq.len || rows <= p.few_rows) return;
+  const int r0 = ((token - seq.begin) * p.group + head % p.group) / kManyRows * kManyRows;
+  const Span span = span_of<1>(p, seq, r0, min_of(r0 + kManyRows, rows));
+  if (span.parts > 1) combine_row<T, D>(p, span.parts, token, head);
 }
 
 // ------------------------------------------------------------------ host side
@@ -621,17 +787,28 @@ int check_attention(const lutgemm_attention* a) {
 
 struct AttnPlan {
   bool few, many;
-  int splits, chunk;
+  int splits[2], chunk[2];
   int64_t tiles;
   size_t ws_bytes;
 };
 
-// Which kernels run and how many parts the longest key axis is cut into: enough to
-// fill the card twice over, of at least kSplitKeys keys (few rows) or 512 (many).
+// Parts of a key axis of up to `keys` keys for `base` workgroups to fill the card
+// with `fill` of them, none shorter than `least`.
+void split_keys(int64_t keys, int64_t base, int64_t fill, int64_t least, int* splits, int* chunk) {
+  int64_t n = (fill + base - 1) / base;
+  const int64_t most = (keys + least - 1) / least;
+  if (n > most) n = most;
+  if (n > kMaxSplits) n = kMaxSplits;
+  if (n < 1) n = 1;
+  const int64_t each = ((keys + n - 1) / n + kSplitKeys - 1) / kSplitKeys * kSplitKeys;
+  *splits = (int)((keys + each - 1) / each);
+  *chunk = (int)each;
+}
+
+// Which kernels run and how many parts the longest key axis is cut into.
 AttnPlan plan(const lutgemm_attention* a) {
   AttnPlan r{};
   if (a->tokens == 0 || a->seqs == 0) return r;  // nothing runs
-  constexpr int64_t kFill = 512;  // workgroups: two on each of 256 compute units
   const int64_t group = a->heads / a->kv_heads;
   const int64_t table_keys = (int64_t)a->table_width * a->page_size;
   int64_t max_q = a->max_q < a->tokens ? a->max_q : a->tokens;
@@ -643,35 +820,41 @@ AttnPlan plan(const lutgemm_attention* a) {
   r.many = max_q * group > kFewRows;
   r.few = !r.many || a->seqs > 1;
   r.tiles = a->tokens * group / kManyRows + a->seqs;
-  const int64_t base = (r.many ? a->tokens * group / kManyRows + 1 : a->seqs) * a->kv_heads;
-  const int64_t least = r.many ? 512 : kSplitKeys;
-  int64_t splits = (kFill + base - 1) / base;
-  const int64_t most = (keys + least - 1) / least;
-  if (splits > most) splits = most;
-  if (splits > kMaxSplits) splits = kMaxSplits;
-  if (splits < 1) splits = 1;
-  int64_t chunk = (keys + splits - 1) / splits;
-  chunk = (chunk + kSplitKeys - 1) / kSplitKeys * kSplitKeys;
-  r.splits = (int)((keys + chunk - 1) / chunk);
-  r.chunk = (int)chunk;
-  if (r.splits > 1)
-    r.ws_bytes = (size_t)r.splits * (size_t)a->tokens * (size_t)a->heads *
+  // Workgroups to fill the card with: few_kernel's are one to a compute unit, and four
+  // rounds of them even out sequences of different lengths (48 of 800 .. 8000 keys: 164 us;
+  // one round 181, two 181, twelve 181); beside many_kernel's two rounds are enough.
+  split_keys(keys, (int64_t)a->seqs * a->kv_heads, r.many ? 512 : 1024, 512, &r.splits[0],
+             &r.chunk[0]);
+  split_keys(keys, (a->tokens * group / kManyRows + (a->seqs + 1) / 2) * a->kv_heads, 512, 512,
+             &r.splits[1], &r.chunk[1]);
+  if (!r.few) r.splits[0] = 1;
+  if (!r.many) r.splits[1] = 1;
+  const int most = r.splits[0] > r.splits[1] ? r.splits[0] : r.splits[1];
+  if (most > 1)
+    r.ws_bytes = (size_t)most * (size_t)a->tokens * (size_t)a->heads *
                  (size_t)(a->head_dim + 2) * sizeof(float);
   return r;
 }
 
 template <class T, int D>
 int run_attention(const AttnPlan& r, const AttnParams& p, hipStream_t stream) {
-  int st = LUTGEMM_OK;
-  if (r.many)
-    st = launch(many_kernel<T, D>, dim3((unsigned)(r.tiles * p.kv_heads), (unsigned)r.splits),
-                kThreads, p, stream);
-  if (!st && r.few)
-    st = launch(few_kernel<T, D>, dim3((unsigned)(p.seqs * p.kv_heads), (unsigned)r.splits),
-                kThreads, p, stream);
-  if (!st && r.splits > 1)
-    st = launch(combine_kernel<T, D>,
+  const int64_t few = (int64_t)p.seqs * r.splits[0] * p.kv_heads;
+  const int64_t many = r.tiles * p.kv_heads * r.splits[1];
+  int st;
+  if (r.few && r.many)
+    st = launch(mixed_kernel<T, D>, dim3((unsigned)(few + many)), kThreads, p, stream);
+  else if (r.many)
+    st = launch(many_kernel<T, D>, dim3((unsigned)many), kThreads, p, stream);
+  else
+    st = launch(few_kernel<T, D>, dim3((unsigned)few), 64 * kFewWaves, p, stream);
+  if (!st && r.many && r.splits[1] > 1)
+    st = launch(combine_many_kernel<T, D>,
                 dim3((unsigned)(((int64_t)p.tokens * p.heads + 3) / 4)), kThreads, p, stream);
+  if (!st && r.few && r.splits[0] > 1)
+    st = launch(combine_few_kernel<T, D>,
+                dim3((unsigned)(p.seqs * p.kv_heads),
+                     (unsigned)(r.many || p.group >= kFewRows ? kFewRows / 4 : (p.group + 3) / 4)),
+                kThreads, p, stream);
   return st;
 }
 
@@ -705,8 +888,9 @@ extern "C" int lutgemm_paged_attention(const lutgemm_attention* a, const void* d
     const AttnPlan r = plan(a);
     // a launch has fewer than 2^32 threads along each axis of its grid
     constexpr int64_t kMost = (int64_t)1 << 24;
-    if (r.tiles * a->kv_heads >= kMost || (int64_t)a->seqs * a->kv_heads >= kMost ||
-        (r.splits > 1 && a->tokens * a->heads / 4 + 1 >= kMost))
+    const int64_t few = (int64_t)a->seqs * r.splits[0] * a->kv_heads;
+    if (r.tiles * a->kv_heads * r.splits[1] + few >= kMost / 2 ||
+        (r.splits[1] > 1 && a->tokens * a->heads / 4 + 1 >= kMost))
       return LUTGEMM_ERR_SHAPE;
     if (r.ws_bytes) {
       if (!d_workspace) return LUTGEMM_ERR_NULL;
@@ -726,7 +910,7 @@ extern "C" int lutgemm_paged_attention(const lutgemm_attention* a, const void* d
     p.out = (uint16_t*)d_out;
     p.part_o = (float*)d_workspace;
     p.part_ml = r.ws_bytes ? (float*)d_workspace +
-                                 (size_t)r.splits * a->tokens * a->heads * a->head_dim
+                                 r.ws_bytes / sizeof(float) / (a->head_dim + 2) * a->head_dim
                            : nullptr;
     p.table_stride = a->table_stride;
     p.q_token = a->q_token;
@@ -748,8 +932,11 @@ extern "C" int lutgemm_paged_attention(const lutgemm_attention* a, const void* d
     for (p.page_log2 = 4; (1 << p.page_log2) < a->page_size;) ++p.page_log2;
     p.table_keys = a->table_width * a->page_size;
     p.window = a->window;
-    p.splits = r.splits;
-    p.chunk = r.chunk;
+    for (int i = 0; i < 2; ++i) {
+      p.splits[i] = r.splits[i];
+      p.chunk[i] = r.chunk[i];
+    }
+    p.few_blocks = (int32_t)few;
     p.few_rows = !r.many ? 0x7FFFFFFF : r.few ? kFewRows : 0;
     p.tiles = (int32_t)r.tiles;
     p.scale2 = a->scale * 1.4426950408889634f;
