@@ -460,9 +460,9 @@ int lutgemm_paged_attention(const lutgemm_attention* a, const void* d_q, const v
  * bf16 (a pair of bf16 numbers); out is rounded once. A row's result does not depend
  * on the other rows' ids.
  *   d_workspace  at least lutgemm_adapters_workspace bytes; as for attention.
- * Shape rules: 0 <= rows <= 65535, K a multiple of 8 below 2^24, N below 2^23, rank a
+ * Shape rules: 0 <= rows <= 65535, K a multiple of 8 below 2^23, N below 2^23, rank a
  * multiple of 8 from 8 to 128, 0 <= adapters <= 4096 (0: out = y); x_row a multiple
- * of 8. Alignment: d_x, d_a, d_b and d_workspace 16 bytes, d_ids and d_scales 4,
+ * of 8; x, y and out less than 2 GiB each from their first element to the last. Alignment: d_x, d_a, d_b and d_workspace 16 bytes, d_ids and d_scales 4,
  * d_y and d_out 2. */
 typedef struct lutgemm_adapters {
   int32_t type, rows, K, N;

@@ -2,15 +2,18 @@
 // (lutgemm_adapters_add; the formula is in lutgemm.h).
 //
 // Two products on the matrix cores, t = A[a] x and out = y + s B[a] t, over tiles of
-// up to 16 rows that share an adapter. Memory bounds both: a decode step reads each
-// adapter it uses once, a prompt reads x and y. Rows come in any order; up to 64 of
-// them every workgroup sorts for itself (one row per lane, no extra launch), above
-// that one workgroup sorts them first (sort_kernel).
+// up to 16 or 32 rows that share an adapter. Memory and the latency of a few dependent
+// reads bound both: a decode step reads each adapter it uses once, a prompt reads x and y.
+// Rows come in any order; up to 64 of them every wave sorts for itself (one row per lane, no
+// extra launch), above that one workgroup sorts them first (sort_kernel).
 //
 // shrink_kernel splits K over workgroups and waves; its parts are summed when
 // expand_kernel reads them, in a fixed order. t is rounded for the second product to
 // a pair of numbers, high + low, of the element type: the pair's error is far below
 // the rounding of the output, for two small matrix products in place of one.
+//
+// 61 rows of 24 adapters of rank 64, K = 11008, N = 4096 (46 MB): 16.7 us, 2.8 TB/s;
+// 4096 rows, K = N = 8192, rank 32 (206 MB): 74 us, 2.8 TB/s.
 #include "serve.h"
 
 namespace lutgemm {
@@ -19,12 +22,14 @@ namespace {
 using namespace serve;
 
 constexpr int kThreads = 256;
-constexpr int kTileRows = 16;
+constexpr int kTileRows = 16;    // of a set of rows
 constexpr int kLaneRows = 64;    // up to so many rows are sorted by each wave itself
 constexpr int kStepK = 128;      // K that a wave reads before the next wave's share
 constexpr int kSortThreads = 1024;
 constexpr int kMaxAdapters = 4096;
-constexpr int kTileCols = 64;    // output columns of a wave
+constexpr int kTileCols = 64;    // output columns of a wave at a time
+constexpr int kTurns = 2;        // expand_kernel: how many times
+constexpr int kFusedWaves = 16;
 
 struct AdapterParams {
   const uint16_t* x;
@@ -37,74 +42,128 @@ struct AdapterParams {
   float* part;       // [split][row][rank]
   int32_t* order;    // rows sorted by adapter (above kLaneRows rows)
   int32_t* tiles;    // [tile][3]: adapter (-1: none, -2: no such tile), start, count
-  int64_t x_row, y_row, out_row;
+  int32_t x_row, y_row, out_row;
+  uint32_t x_bytes, y_bytes, out_bytes;
   int32_t rows, K, N, rank, adapters, splits, split_k, n_tiles;
-  int32_t wide;      // y and out rows can be read 16 bytes at a time
+  int32_t wide;      // y and out can be read 16 bytes at a time, and N is a multiple of 8
   int32_t in_place;
+  int32_t id_bits;   // of the numbers 0 .. adapters
+  int32_t tile_rows;
 };
 
+// R sets of sixteen rows.
+template <int R>
 struct Tile {
   int adapter;  // -1: rows without one; -2: no such tile
   int count;
-  int row;      // of this lane's column (lane % 16); one of the tile's rows in any case
+  int row[R];   // of this lane's columns (16 set + lane % 16); one of the tile's rows in any case
+
+  __device__ __forceinline__ bool has(int set) const {
+    return 16 * set + (int)(threadIdx.x & 15) < count;
+  }
 };
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// Buffers with 32-bit offsets: few instructions an address, and words past the end
+// read as zeros and are not written. All of an address is in the vector offset, the
+// one that is checked against the buffer's size; buffers are below 2 GiB, so kNowhere
+// and a few words from it are past the end of each.
+constexpr uint32_t kNowhere = 0x80000000u;
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, (int)bytes, 0x00027000);
+}
+__device__ __forceinline__ u4v load16(__amdgpu_buffer_rsrc_t b, uint32_t at) {
+  return __builtin_bit_cast(u4v, __builtin_amdgcn_raw_buffer_load_b128(b, at, 0, 0));
+}
+
+__device__ __forceinline__ int at_most(int v, int most) { return v < most ? v : most; }
 
 __device__ __forceinline__ int id_of(const AdapterParams& p, int row) {
   const int id = p.ids[row];
   return (uint32_t)id < (uint32_t)p.adapters ? id : -1;
 }
 
-// Tile `g` of the rows grouped by adapter. Up to 64 rows: a row's rank among those of
-// its adapter makes every sixteenth of them the head of a tile.
-__device__ __forceinline__ Tile find_tile(const AdapterParams& p, int g) {
+// The lanes whose `v`, a number of so many bits, is this lane's.
+__device__ __forceinline__ uint64_t lanes_with(int v, int bits) {
+  uint64_t same = ~(uint64_t)0;
+  for (int b = 0; b < bits; ++b) {
+    const bool one = (v >> b) & 1;
+    const uint64_t ones = __ballot(one);
+    same &= one ? ones : ~ones;
+  }
+  return same;
+}
+
+// Tile `g` of the rows grouped by adapter, sixteen rows to a tile; up to 64 rows each
+// wave finds it from the ids, one to a lane.
+template <int R>
+__device__ __forceinline__ Tile<R> find_tile(const AdapterParams& p, int g) {
   const int lane = threadIdx.x & 63;
-  Tile t;
-  if (p.rows > kLaneRows) {
+  Tile<R> t;
+  if (R > 1 || p.rows > kLaneRows) {
     t.adapter = uniform(p.tiles[3 * g]);
     const int start = uniform(p.tiles[3 * g + 1]);
     t.count = uniform(p.tiles[3 * g + 2]);
-    const int col = lane & 15;
-    t.row = t.adapter == -2 ? 0 : p.order[start + (col < t.count ? col : 0)];
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+      t.row[j] = t.adapter == -2 ? 0 : p.order[start + (t.has(j) ? 16 * j + (lane & 15) : 0)];
     return t;
   }
   const bool here = lane < p.rows;
-  const int id = here ? id_of(p, lane) : -2;
-  int rank = 0;
-  for (int j = 0; j < p.rows; ++j)
-    rank += __builtin_amdgcn_readlane(id, j) == id && j < lane ? 1 : 0;
+  const int id = here ? id_of(p, lane) : -1;
+  const uint64_t same = lanes_with(id < 0 ? p.adapters : id, p.id_bits) & __ballot(here);
+  const int rank = __popcll(same & (((uint64_t)1 << lane) - 1));
+  // every sixteenth row of an adapter heads a tile
   const uint64_t heads = __ballot(here && rank % kTileRows == 0);
   t.adapter = -2;
   t.count = 0;
-  t.row = 0;
+  t.row[0] = 0;
   if (g >= __popcll(heads)) return t;
   const int before = __builtin_amdgcn_mbcnt_hi((uint32_t)(heads >> 32),
                                                __builtin_amdgcn_mbcnt_lo((uint32_t)heads, 0));
-  const uint64_t mine = __ballot(((heads >> lane) & 1) && before == g);
-  const int head = __builtin_ctzll(mine);
+  const int head = __builtin_ctzll(__ballot(((heads >> lane) & 1) && before == g));
   t.adapter = __builtin_amdgcn_readlane(id, head);
-  const int first = __builtin_amdgcn_readlane(rank, head);
-  const bool member = here && id == t.adapter && rank >= first && rank < first + kTileRows;
+  const int place = rank - __builtin_amdgcn_readlane(rank, head);
+  const bool member = here && id == t.adapter && place >= 0 && place < kTileRows;
   t.count = __popcll(__ballot(member));
-  const int placed = __builtin_amdgcn_ds_permute(4 * (member ? rank - first : 63), lane);
-  const int col = lane & 15;
-  t.row = __shfl(placed, col < t.count ? col : 0, 64);
+  // row number to the lane of its column; the others' go to a lane that is not read
+  const int placed = __builtin_amdgcn_ds_permute(4 * (member ? place : 63), lane);
+  t.row[0] = __shfl(placed, t.has(0) ? lane & 15 : 0, 64);
   return t;
 }
 
 // ---------------------------------------------------------------------- sorting
 
+// One workgroup counts the rows of each adapter, places the adapters one after the
+// other, describes the tiles and puts the rows in order. Rows of one adapter often stand
+// together, so a wave adds its rows to a counter at once: 4096 rows of 8 adapters take 8.4
+// us in place of 11.7 with an atomic for each.
 __global__ __launch_bounds__(kSortThreads) void sort_kernel(AdapterParams p) {
   __shared__ int count[kMaxAdapters + 1], row_at[kMaxAdapters + 1], tile_at[kMaxAdapters + 2];
-  __shared__ int sums[2][kSortThreads];
+  __shared__ int sums[2][kSortThreads / 64];
+  fetch(p);
   const int bins = p.adapters + 1, tid = threadIdx.x;  // the last bin: rows without one
+  const int lane = tid & 63, wave = tid >> 6;
+  // the bin of a row, -1 past the last row
+  auto bin_of = [&](int row) {
+    if (row >= p.rows) return -1;
+    const int id = id_of(p, row);
+    return id < 0 ? p.adapters : id;
+  };
+  // counters[bin] raised by the wave's rows of each bin; *at: this row's place in its bin
+  auto add = [&](int* counters, int bin, int* at) {
+    const uint64_t same = lanes_with(bin < 0 ? 0 : bin, p.id_bits) & __ballot(bin >= 0);
+    const int first = bin >= 0 ? __builtin_ctzll(same) : lane;
+    int old = 0;
+    if (bin >= 0 && lane == first) old = atomicAdd(&counters[bin], __popcll(same));
+    *at = __shfl(old, first, 64) + __popcll(same & (((uint64_t)1 << lane) - 1));
+  };
   for (int i = tid; i < bins; i += kSortThreads) count[i] = 0;
   __syncthreads();
-  for (int i = tid; i < p.rows; i += kSortThreads) {
-    const int id = id_of(p, i);
-    atomicAdd(&count[id < 0 ? p.adapters : id], 1);
-  }
+  int at;
+  for (int i = wave * 64; i < p.rows; i += kSortThreads) add(count, bin_of(i + lane), &at);
   __syncthreads();
   // running sums of rows and of tiles over the bins, a few bins to a thread
   const int each = (bins + kSortThreads - 1) / kSortThreads;
@@ -112,26 +171,33 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(AdapterParams p) {
   int rows = 0, tiles = 0;
   for (int i = b0; i < b1; ++i) {
     rows += count[i];
-    tiles += (count[i] + kTileRows - 1) / kTileRows;
+    tiles += (count[i] + p.tile_rows - 1) / p.tile_rows;
   }
-  sums[0][tid] = rows;
-  sums[1][tid] = tiles;
+  int row = rows, tile = tiles;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int x = __shfl_up(row, d, 64), y = __shfl_up(tile, d, 64);
+    row += lane >= d ? x : 0;
+    tile += lane >= d ? y : 0;
+  }
+  if (lane == 63) {
+    sums[0][wave] = row;
+    sums[1][wave] = tile;
+  }
   __syncthreads();
-  for (int d = 1; d < kSortThreads; d <<= 1) {
-    const int x = tid >= d ? sums[0][tid - d] : 0, y = tid >= d ? sums[1][tid - d] : 0;
-    __syncthreads();
-    sums[0][tid] += x;
-    sums[1][tid] += y;
-    __syncthreads();
+  row -= rows;
+  tile -= tiles;
+  for (int w = 0; w < wave; ++w) {
+    row += sums[0][w];
+    tile += sums[1][w];
   }
-  int row = sums[0][tid] - rows, tile = sums[1][tid] - tiles;
   for (int i = b0; i < b1; ++i) {
     row_at[i] = row;
     tile_at[i] = tile;
     row += count[i];
-    tile += (count[i] + kTileRows - 1) / kTileRows;
+    tile += (count[i] + p.tile_rows - 1) / p.tile_rows;
   }
-  if (tid == 0) tile_at[bins] = sums[1][kSortThreads - 1];
+  if (b0 < bins && b1 == bins) tile_at[bins] = tile;
   __syncthreads();
   for (int t = tid; t < p.n_tiles; t += kSortThreads) {
     int* to = p.tiles + 3 * t;
@@ -140,224 +206,397 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(AdapterParams p) {
       to[1] = to[2] = 0;
       continue;
     }
-    int lo = 0, hi = bins;  // the last bin that begins at or before t and has a tile there
+    int lo = 0, hi = bins;  // the last bin that begins at or before t, which has a tile there
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (tile_at[mid] <= t) lo = mid; else hi = mid;
     }
-    const int at = (t - tile_at[lo]) * kTileRows;
+    const int in_bin = (t - tile_at[lo]) * p.tile_rows;
     to[0] = lo == p.adapters ? -1 : lo;
-    to[1] = row_at[lo] + at;
-    to[2] = count[lo] - at < kTileRows ? count[lo] - at : kTileRows;
+    to[1] = row_at[lo] + in_bin;
+    to[2] = count[lo] - in_bin < p.tile_rows ? count[lo] - in_bin : p.tile_rows;
   }
   __syncthreads();
   // the order within a bin changes from run to run; no row's result depends on it
-  for (int i = tid; i < p.rows; i += kSortThreads) {
-    const int id = id_of(p, i);
-    p.order[atomicAdd(&row_at[id < 0 ? p.adapters : id], 1)] = i;
+  for (int i = wave * 64; i < p.rows; i += kSortThreads) {
+    const int bin = bin_of(i + lane);
+    add(row_at, bin, &at);
+    if (bin >= 0) p.order[at] = i + lane;
   }
 }
 
 // ------------------------------------------------------------------ t = A[a] x
 //
 // NB blocks of 16 ranks. Both operands come straight from memory in their layout
-// (eight consecutive k per lane), so nothing is staged; the four waves take turns at
-// 128 k each and join their sums through LDS.
+// (eight consecutive k per lane), so nothing is staged; W waves take turns at 128 k
+// each. Entry e of acc[i]: rank 16 i + 4 (lane / 16) + e of the row of column lane % 16.
 
-template <class T, int NB>
-__global__ __launch_bounds__(kThreads) void shrink_kernel(AdapterParams p) {
-  __shared__ float sums[4][NB][64][4];
-  const Tile t = find_tile(p, blockIdx.x);
-  if (t.adapter < 0) return;
-  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  const int c = lane >> 4, col = lane & 15;
-  const int from = blockIdx.y * p.split_k;
-  const int to = from + p.split_k < p.K ? from + p.split_k : p.K;
-  const uint16_t* x = p.x + t.row * p.x_row + 8 * c;
-  const uint16_t* a = p.a + (int64_t)t.adapter * p.rank * p.K + 8 * c;
-  int64_t a_row[NB];
+template <class T, int NB, int R>
+__device__ __forceinline__ void shrink(const AdapterParams& p, const Tile<R>& t, int from, int to,
+                                       int stride, f4v (&acc)[R][NB]) {
+  const int lane = threadIdx.x & 63, c = lane >> 4, col = lane & 15;
+  const __amdgpu_buffer_rsrc_t x = buffer(p.x, p.x_bytes);
+  const __amdgpu_buffer_rsrc_t a =
+      buffer(p.a + (int64_t)t.adapter * p.rank * p.K, 2u * (uint32_t)p.rank * (uint32_t)p.K);
+  // columns and ranks past the last read nothing
+  uint32_t x_at[R], a_at[NB];
+#pragma unroll
+  for (int j = 0; j < R; ++j)
+    x_at[j] = t.has(j) ? 2 * (uint32_t)t.row[j] * (uint32_t)p.x_row + 16 * c : kNowhere;
 #pragma unroll
   for (int i = 0; i < NB; ++i) {
-    const int r = 16 * i + col;
-    a_row[i] = (int64_t)(r < p.rank ? r : p.rank - 1) * p.K;
+    a_at[i] = 2 * (uint32_t)(16 * i + col) * (uint32_t)p.K + 16 * c;
+    if (16 * i + col >= p.rank) a_at[i] = kNowhere;
   }
-  f4v acc[NB];
 #pragma unroll
-  for (int i = 0; i < NB; ++i) acc[i] = f4v{0.f, 0.f, 0.f, 0.f};
-  for (int k0 = from + kStepK * wave; k0 < to; k0 += 4 * kStepK) {
-    u4v xw[kStepK / 32], aw[kStepK / 32][NB];
+  for (int j = 0; j < R; ++j)
 #pragma unroll
-    for (int s = 0; s < kStepK / 32; ++s) {
-      const bool in = k0 + 32 * s + 8 * c < to;
-      xw[s] = in ? *(const u4v*)(x + k0 + 32 * s) : u4v{0, 0, 0, 0};
+    for (int i = 0; i < NB; ++i) acc[j][i] = f4v{0.f, 0.f, 0.f, 0.f};
+  constexpr int kWords = kStepK / 32;
+  for (int k0 = from; k0 < to; k0 += stride) {
+    u4v xw[kWords][R], aw[kWords][NB];
+    uint32_t x_k[R], a_k[NB];
 #pragma unroll
-      for (int i = 0; i < NB; ++i)
-        aw[s][i] = in ? *(const u4v*)(a + a_row[i] + k0 + 32 * s) : u4v{0, 0, 0, 0};
+    for (int j = 0; j < R; ++j) x_k[j] = x_at[j] == kNowhere ? kNowhere : x_at[j] + 2 * k0;
+#pragma unroll
+    for (int i = 0; i < NB; ++i) a_k[i] = a_at[i] == kNowhere ? kNowhere : a_at[i] + 2 * k0;
+    if (k0 + kStepK <= to) {
+#pragma unroll
+      for (int s = 0; s < kWords; ++s) {
+#pragma unroll
+        for (int j = 0; j < R; ++j) xw[s][j] = load16(x, x_k[j] + 64 * s);
+#pragma unroll
+        for (int i = 0; i < NB; ++i) aw[s][i] = load16(a, a_k[i] + 64 * s);
+      }
+    } else {
+#pragma unroll
+      for (int s = 0; s < kWords; ++s) {
+        const bool in = k0 + 32 * s + 8 * c < to;
+#pragma unroll
+        for (int j = 0; j < R; ++j) xw[s][j] = load16(x, in ? x_k[j] + 64 * s : kNowhere);
+#pragma unroll
+        for (int i = 0; i < NB; ++i) aw[s][i] = load16(a, in ? a_k[i] + 64 * s : kNowhere);
+      }
     }
 #pragma unroll
-    for (int s = 0; s < kStepK / 32; ++s)
+    for (int s = 0; s < kWords; ++s)
 #pragma unroll
-      for (int i = 0; i < NB; ++i) acc[i] = T::mfma16(aw[s][i], xw[s], acc[i]);
+      for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int j = 0; j < R; ++j) acc[j][i] = T::mfma16(aw[s][i], xw[s][j], acc[j][i]);
   }
+}
+
+template <class T, int NB, int R>
+__global__ __launch_bounds__(kThreads) void shrink_kernel(AdapterParams p) {
+  __shared__ float sums[4][R * NB][64][4];
+  fetch(p);
+  const Tile<R> t = find_tile<R>(p, blockIdx.x);
+  if (t.adapter < 0) return;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int from = blockIdx.y * p.split_k;
+  const int to = from + p.split_k < p.K ? from + p.split_k : p.K;
+  f4v acc[R][NB];
+  shrink<T, NB, R>(p, t, from + kStepK * wave, to, 4 * kStepK, acc);
 #pragma unroll
-  for (int i = 0; i < NB; ++i) *(f4v*)sums[wave][i][lane] = acc[i];
+  for (int j = 0; j < R; ++j)
+#pragma unroll
+    for (int i = 0; i < NB; ++i) *(f4v*)sums[wave][j * NB + i][lane] = acc[j][i];
   __syncthreads();
-  // entry e of lane l: rank 16 i + 4 (l / 16) + e of the row of column l % 16
-  for (int i = wave; i < NB; i += 4) {
-    const int r = 16 * i + 4 * c;
-    f4v v = *(f4v*)sums[0][i][lane];
+  for (int e = wave; e < R * NB; e += 4) {
+    const int j = e / NB, r = 16 * (e % NB) + 4 * (lane >> 4);
+    f4v v = *(f4v*)sums[0][e][lane];
 #pragma unroll
-    for (int w = 1; w < 4; ++w) v += *(f4v*)sums[w][i][lane];
-    if (col < t.count && r < p.rank)
-      *(f4v*)(p.part + ((int64_t)blockIdx.y * p.rows + t.row) * p.rank + r) = v;
+    for (int w = 1; w < 4; ++w) v += *(f4v*)sums[w][e][lane];
+    int row = t.row[0];
+#pragma unroll
+    for (int i = 1; i < R; ++i) row = j == i ? t.row[i] : row;
+    if (t.has(j) && r < p.rank)
+      *(f4v*)(p.part + ((int64_t)blockIdx.y * p.rows + row) * p.rank + r) = v;
   }
 }
 
 // ------------------------------------------------------------- out = y + s B[a] t
 //
-// A wave serves 64 output columns. Row i of the four column blocks' operands is
+// 64 output columns to a wave at a time. Row i of the four column blocks' operands is
 // output column 16 (i / 4) + 4 block + i % 4, so a lane's results are sixteen
-// consecutive columns of its row: 32 bytes of y and out.
+// consecutive columns of its row: 32 bytes of y and out. y and B are read before t is needed.
 
-template <class T, int NB>
-__global__ __launch_bounds__(kThreads) void expand_kernel(AdapterParams p) {
-  constexpr int kSteps = (NB + 1) / 2;  // products of 32 ranks
-  const Tile t = find_tile(p, blockIdx.x);
-  if (t.adapter == -2 || (t.adapter == -1 && p.in_place)) return;
-  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  const int c = lane >> 4, col = lane & 15;
-  const int n0 = ((int)blockIdx.y * 4 + wave) * kTileCols;
-  if (n0 >= p.N) return;
-  f4v acc[4];
+template <class T, int NB, int R>
+struct Columns {
+  static constexpr int kSteps = (NB + 1) / 2;  // products of 32 ranks
+  u4v b[kSteps][4], y[R][2];
+
+  __device__ __forceinline__ void load(const AdapterParams& p, const Tile<R>& t, int n0) {
+    const int lane = threadIdx.x & 63, c = lane >> 4, col = lane & 15;
+    const int n = n0 + 16 * c;
+    const __amdgpu_buffer_rsrc_t from = buffer(p.y, p.y_bytes);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) acc[i] = f4v{0.f, 0.f, 0.f, 0.f};
-  float scale = 0.f;
-  if (t.adapter >= 0) {
-    const uint16_t* b = p.b + (int64_t)t.adapter * p.N * p.rank + 8 * c;
-    u4v bw[kSteps][4];
+    for (int j = 0; j < R; ++j) {
+      const uint32_t at = 2 * ((uint32_t)t.row[j] * (uint32_t)p.y_row + n);
+      if (p.wide) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          y[j][i] = load16(from, t.has(j) && n + 8 * i < p.N ? at + 16 * i : kNowhere);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t e0 = __builtin_amdgcn_raw_buffer_load_b16(
+              from, t.has(j) && n + 2 * i < p.N ? at + 4 * i : kNowhere, 0, 0);
+          const uint32_t e1 = __builtin_amdgcn_raw_buffer_load_b16(
+              from, t.has(j) && n + 2 * i + 1 < p.N ? at + 4 * i + 2 : kNowhere, 0, 0);
+          y[j][i / 4][i % 4] = (e0 & 0xFFFF) | (e1 << 16);
+        }
+      }
+    }
+    if (t.adapter < 0) return;
+    const __amdgpu_buffer_rsrc_t rows =
+        buffer(p.b + (int64_t)t.adapter * p.N * p.rank, 2u * (uint32_t)p.N * (uint32_t)p.rank);
+    const uint32_t b_at =
+        2 * (uint32_t)(n0 + 16 * (col >> 2) + (col & 3)) * (uint32_t)p.rank + 16 * c;
 #pragma unroll
     for (int s = 0; s < kSteps; ++s)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int n = n0 + 16 * (col >> 2) + 4 * i + (col & 3);
-        bw[s][i] = 32 * s + 8 * c < p.rank
-                       ? *(const u4v*)(b + (int64_t)(n < p.N ? n : p.N - 1) * p.rank + 32 * s)
-                       : u4v{0, 0, 0, 0};
-      }
-    // this row's t, eight ranks per step, the parts summed in order
-    float v[kSteps][8];
-    float top = 0.f;
+      for (int i = 0; i < 4; ++i)
+        b[s][i] = load16(rows, 32 * s + 8 * c < p.rank ? b_at + 64 * s + 8 * i * (uint32_t)p.rank
+                                                       : kNowhere);
+  }
+};
+
+// t of sixteen rows, from fp32 in LDS to pairs high + low of the element type in operand
+// layout. fp16: the row's largest entry is brought to [512, 1024) by a power of two, so
+// neither half overflows and the low half keeps its digits; `factor` undoes it.
+template <class T, int NB>
+struct Inner {
+  static constexpr int kSteps = (NB + 1) / 2;
+  u4v hi[kSteps], lo[kSteps];
+  float factor;
+
+  __device__ __forceinline__ void read(const AdapterParams& p, int adapter, bool here,
+                                       const float* inner) {
+    const int lane = threadIdx.x & 63, c = lane >> 4;
+    float v[kSteps][8], top = 0.f;
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
+    for (int s = 0; s < kSteps; ++s)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[s][e] = 0.f;
-      if (32 * s + 8 * c < p.rank) {
-        const float* from = p.part + (int64_t)t.row * p.rank + 32 * s + 8 * c;
-        for (int j = 0; j < p.splits; ++j) {
-          const f4v lo = *(const f4v*)from, hi = *(const f4v*)(from + 4);
-          from += (int64_t)p.rows * p.rank;
+      for (int e = 0; e < 8; e += 4) {
+        const bool in = 32 * s + 8 * c < p.rank && here;
+        const f4v w = *(const f4v*)(inner + at_most(32 * s + 8 * c, p.rank - 8) + e);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            v[s][e] += lo[e];
-            v[s][4 + e] += hi[e];
-          }
+        for (int i = 0; i < 4; ++i) {
+          v[s][e + i] = in ? w[i] : 0.f;
+          top = fmaxf(top, fabsf(v[s][e + i]));
         }
       }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[s][e]));
-    }
-    scale = p.scales ? p.scales[t.adapter] : 1.f;
-    float down = 1.f;
+    factor = p.scales ? p.scales[adapter] : 1.f;
     if (T::kHalf) {
-      // fp16: the row's largest entry brought to [512, 1024) by a power of two, so
-      // neither half of a pair overflows and the low half keeps its digits
       top = fmaxf(top, __shfl_xor(top, 16, 64));
       top = fmaxf(top, __shfl_xor(top, 32, 64));
       const bool plain = !(top > 0.f) || top == INFINITY;
       const int e = plain ? 0 : 10 - __builtin_amdgcn_frexp_expf(top);
-      down = __builtin_amdgcn_ldexpf(1.f, -e);
+      factor *= __builtin_amdgcn_ldexpf(1.f, -e);
 #pragma unroll
       for (int s = 0; s < kSteps; ++s)
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[s][i] = __builtin_amdgcn_ldexpf(v[s][i], e);
     }
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      u4v hi, lo;
+    for (int s = 0; s < kSteps; ++s)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        hi[i] = T::pack(v[s][2 * i], v[s][2 * i + 1]);
-        const f2v h = T::unpack(hi[i]);
+        hi[s][i] = T::pack(v[s][2 * i], v[s][2 * i + 1]);
+        const f2v h = T::unpack(hi[s][i]);
         const float l0 = v[s][2 * i] - h.x, l1 = v[s][2 * i + 1] - h.y;
         // of an infinity or NaN the high half says all
-        lo[i] = T::pack(fabsf(h.x) < INFINITY ? l0 : 0.f, fabsf(h.y) < INFINITY ? l1 : 0.f);
+        lo[s][i] = T::pack(fabsf(h.x) < INFINITY ? l0 : 0.f, fabsf(h.y) < INFINITY ? l1 : 0.f);
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        acc[i] = T::mfma16(bw[s][i], hi, acc[i]);
-        acc[i] = T::mfma16(bw[s][i], lo, acc[i]);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[i][e] = acc[i][e] * down * scale;
   }
-  if (col >= t.count) return;
+};
+
+template <class T, int NB, int R>
+__device__ __forceinline__ void expand(const AdapterParams& p, const Tile<R>& t,
+                                       const Columns<T, NB, R>& w, const Inner<T, NB> (&v)[R],
+                                       int n0) {
+  const int lane = threadIdx.x & 63, c = lane >> 4;
   const int n = n0 + 16 * c;
-  const uint16_t* y = p.y + t.row * p.y_row + n;
-  uint16_t* out = p.out + t.row * p.out_row + n;
-  if (p.wide && n + 16 <= p.N) {
+  const __amdgpu_buffer_rsrc_t to = buffer(p.out, p.out_bytes);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      u4v w = *(const u4v*)(y + 8 * i);
-      if (t.adapter >= 0) {
+  for (int j = 0; j < R; ++j) {
+    f4v acc[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const f2v f = T::unpack(w[e]);
-          const int at = 2 * i + e / 2, el = 2 * (e % 2);
-          w[e] = T::pack(f.x + acc[at][el], f.y + acc[at][el + 1]);
+    for (int i = 0; i < 4; ++i) acc[i] = f4v{0.f, 0.f, 0.f, 0.f};
+    u4v r[2] = {w.y[j][0], w.y[j][1]};
+    if (t.adapter >= 0) {
+#pragma unroll
+      for (int s = 0; s < Inner<T, NB>::kSteps; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          acc[i] = T::mfma16(w.b[s][i], v[j].hi[s], acc[i]);
+          acc[i] = T::mfma16(w.b[s][i], v[j].lo[s], acc[i]);
         }
-      }
-      *(u4v*)(out + 8 * i) = w;
-    }
-  } else {
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (n + i < p.N)
-        out[i] = t.adapter >= 0 ? T::one(T::wide(y[i]) + acc[i / 4][i % 4]) : y[i];
+      for (int i = 0; i < 8; ++i) {
+        const f2v f = T::unpack(r[i / 4][i % 4]);
+        r[i / 4][i % 4] = T::pack(f.x + acc[i / 2][2 * (i % 2)] * v[j].factor,
+                                  f.y + acc[i / 2][2 * (i % 2) + 1] * v[j].factor);
+      }
+    }
+    const uint32_t at = 2 * ((uint32_t)t.row[j] * (uint32_t)p.out_row + n);
+    if (p.wide) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        __builtin_amdgcn_raw_buffer_store_b128(
+            r[i], to, t.has(j) && n + 8 * i < p.N ? at + 16 * i : kNowhere, 0, 0);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        __builtin_amdgcn_raw_buffer_store_b16((short)(r[i / 8][i / 2 % 4] >> (16 * (i % 2))), to,
+                                              t.has(j) && n + i < p.N ? at + 2 * i : kNowhere, 0,
+                                              0);
+    }
   }
 }
 
+// Two turns of 64 columns to a wave; the workgroup sums the parts of t once.
+template <class T, int NB, int R>
+__global__ __launch_bounds__(kThreads) void expand_kernel(AdapterParams p) {
+  constexpr int kPitch = 16 * NB + 4;
+  __shared__ __attribute__((aligned(16))) float inner[16 * R * kPitch];
+  __shared__ int row_of[16 * R];
+  fetch(p);
+  const Tile<R> t = find_tile<R>(p, blockIdx.x);
+  if (t.adapter == -2 || (t.adapter == -1 && p.in_place)) return;
+  const int wave = uniform(threadIdx.x >> 6), col = threadIdx.x & 15;
+  const int n0 = ((int)blockIdx.y * 4 + wave) * kTurns * kTileCols;
+  Columns<T, NB, R> w;
+  if (n0 < p.N) w.load(p, t, n0);
+  Inner<T, NB> v[R];
+  if (t.adapter >= 0) {
+    if (threadIdx.x < 16) {
+#pragma unroll
+      for (int j = 0; j < R; ++j) row_of[16 * j + col] = t.row[j];
+    }
+    __syncthreads();
+    const int words = p.rank / 4;
+    for (int e = threadIdx.x; e < 16 * R * words; e += kThreads) {
+      const int at = e / words, r = e % words * 4;
+      const float* from = p.part + (int64_t)row_of[at] * p.rank + r;
+      const int64_t step = (int64_t)p.rows * p.rank;
+      f4v sum = f4v{0.f, 0.f, 0.f, 0.f};
+      for (int j = 0; j < p.splits; j += 4) {
+        f4v x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = *(const f4v*)(from + at_most(j + i, p.splits - 1) * step);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (j + i < p.splits) sum += x[i];
+      }
+      *(f4v*)(inner + at * kPitch + r) = sum;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+      v[j].read(p, t.adapter, t.has(j), inner + (16 * j + col) * kPitch);
+  }
+#pragma unroll
+  for (int i = 0; i < kTurns; ++i) {
+    const int at = n0 + i * kTileCols;
+    if (at >= p.N) return;
+    if (i) w.load(p, t, at);
+    expand<T, NB, R>(p, t, w, v, at);
+  }
+}
+
+// ------------------------------------------------------------ both in one launch
+//
+// For few rows with small adapters: sixteen waves compute t of a tile over all of K, in
+// every workgroup again for its 1024 output columns. Reading A again for each of them costs less
+// than a second launch and the way of t through memory.
+
+template <class T, int NB>
+__global__ __launch_bounds__(64 * kFusedWaves) void fused_kernel(AdapterParams p) {
+  constexpr int kPitch = 16 * NB + 4;
+  __shared__ __attribute__((aligned(16))) float sums[kFusedWaves * NB * 256];
+  __shared__ __attribute__((aligned(16))) float inner[16 * kPitch];
+  fetch(p);
+  const Tile<1> t = find_tile<1>(p, blockIdx.x);
+  if (t.adapter == -2 || (t.adapter == -1 && p.in_place)) return;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int n0 = ((int)blockIdx.y * kFusedWaves + wave) * kTileCols;
+  Columns<T, NB, 1> w;
+  if (n0 < p.N) w.load(p, t, n0);
+  Inner<T, NB> v[1];
+  if (t.adapter >= 0) {
+    f4v acc[1][NB];
+    shrink<T, NB, 1>(p, t, kStepK * wave, p.K, kFusedWaves * kStepK, acc);
+#pragma unroll
+    for (int i = 0; i < NB; ++i) *(f4v*)(sums + ((wave * NB + i) * 64 + lane) * 4) = acc[0][i];
+    __syncthreads();
+    if (threadIdx.x < NB * 256) {
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < kFusedWaves; ++i) sum += sums[i * NB * 256 + threadIdx.x];
+      const int l = threadIdx.x / 4 % 64, r = threadIdx.x / 256 * 16 + 4 * (l >> 4) + threadIdx.x % 4;
+      inner[(l & 15) * kPitch + r] = sum;
+    }
+    __syncthreads();
+    v[0].read(p, t.adapter, t.has(0), inner + (lane & 15) * kPitch);
+  }
+  if (n0 < p.N) expand<T, NB, 1>(p, t, w, v, n0);
+}
+
 // ------------------------------------------------------------------- host side
+
+constexpr int64_t kMostBytes = 0x7FFFFF00;
+
+// Bytes from the first element of `rows` rows of n elements to the last.
+int64_t extent(int64_t rows, int64_t stride, int64_t n) {
+  if (rows < 1 || n < 1) return 0;
+  return stride > kMostBytes ? kMostBytes + 1 : 2 * ((rows - 1) * stride + n);
+}
 
 int check_adapters(const lutgemm_adapters* l) {
   if (!l) return LUTGEMM_ERR_NULL;
   if (l->type != LUTGEMM_F16 && l->type != LUTGEMM_BF16) return LUTGEMM_ERR_SHAPE;
   if (l->rows < 0 || l->rows > 65535) return LUTGEMM_ERR_SHAPE;
-  if (l->K < 0 || l->K % 8 || l->K >= (1 << 24) || l->N < 0 || l->N >= (1 << 23))
+  if (l->K < 0 || l->K % 8 || l->K >= (1 << 23) || l->N < 0 || l->N >= (1 << 23))
     return LUTGEMM_ERR_SHAPE;
   if (l->rank < 8 || l->rank > 128 || l->rank % 8) return LUTGEMM_ERR_SHAPE;
   if (l->adapters < 0 || l->adapters > kMaxAdapters) return LUTGEMM_ERR_SHAPE;
-  constexpr int64_t far = (int64_t)1 << 40;
-  if (!stride_ok(l->x_row) || l->y_row < 0 || l->y_row >= far || l->out_row < 0 || l->out_row >= far)
+  // the kernels address x, y and out with 32-bit offsets
+  if (!stride_ok(l->x_row) || l->y_row < 0 || l->out_row < 0) return LUTGEMM_ERR_SHAPE;
+  if (extent(l->rows, l->x_row, l->K) > kMostBytes || extent(l->rows, l->y_row, l->N) > kMostBytes ||
+      extent(l->rows, l->out_row, l->N) > kMostBytes)
     return LUTGEMM_ERR_SHAPE;
   return LUTGEMM_OK;
 }
 
 struct AdapterPlan {
-  int tiles, splits, split_k;
+  bool fused;
+  int tile_rows, tiles, splits, split_k;
   size_t part_at, ws_bytes;
 };
 
 AdapterPlan plan(const lutgemm_adapters* l) {
   AdapterPlan r{};
   const int groups = l->adapters + 1 < l->rows ? l->adapters + 1 : l->rows;
-  r.tiles = l->rows / kTileRows + groups;
+  // many rows to an adapter: two sets of sixteen in a tile share A and B (2048 rows of 3
+  // adapters of rank 64: 44 us against 55 to 72; 1000 rows of 10, rank 16: 25.5 against 27.7)
+  r.tile_rows = l->rows > kLaneRows && l->rows >= 32 * (l->adapters + 1) ? 32 : 16;
+  r.tiles = l->rows / r.tile_rows + groups;
   if (r.tiles > l->rows) r.tiles = l->rows;
-  // enough workgroups to use every compute unit, each wave with a full step at least
-  constexpr int kFill = 256;
-  int splits = r.tiles > 0 ? (kFill + r.tiles - 1) / r.tiles : 1;
+  // fused_kernel reads A again for every 1024 columns. A compute unit gets about 25 GB/s, so
+  // up to 128 KB a workgroup and 16 MB in all that is the faster way (one row, K = N = 4096,
+  // rank 16: 8.3 us against 9.0; 32 rows of 16 adapters, N = 12288: 10.1 against 9.8)
+  const int64_t a_bytes = (int64_t)l->K * l->rank * 2;
+  const int64_t blocks = (int64_t)r.tiles * ((l->N + 1023) / 1024);
+  r.fused = l->rows <= kLaneRows && l->rank <= 32 && a_bytes <= 128 << 10 &&
+            a_bytes * blocks <= 16 << 20;
+  if (r.fused) return r;
+  // enough workgroups to use every compute unit, twice with the larger tiles, each wave
+  // with a full step at least
+  const int fill = r.tile_rows == 32 ? 512 : 256;
+  int splits = r.tiles > 0 ? (fill + r.tiles - 1) / r.tiles : 1;
   const int most = (l->K + 4 * kStepK - 1) / (4 * kStepK);
   if (splits > most) splits = most;
   if (splits > 16) splits = 16;
@@ -371,18 +610,33 @@ AdapterPlan plan(const lutgemm_adapters* l) {
   return r;
 }
 
+template <class T, int NB, int R>
+int run_tiles(const AdapterPlan& r, const AdapterParams& p, hipStream_t stream) {
+  int st = LUTGEMM_OK;
+  if (r.splits > 0 && p.adapters > 0)
+    st = launch(shrink_kernel<T, NB, R>, dim3((unsigned)r.tiles, (unsigned)r.splits), kThreads, p,
+                stream);
+  constexpr int cols = 4 * kTurns * kTileCols;
+  if (!st)
+    st = launch(expand_kernel<T, NB, R>,
+                dim3((unsigned)r.tiles, (unsigned)((p.N + cols - 1) / cols)), kThreads, p, stream);
+  return st;
+}
+
 template <class T, int NB>
 int run_adapters(const AdapterPlan& r, const AdapterParams& p, hipStream_t stream) {
-  int st = LUTGEMM_OK;
-  if (p.rows > kLaneRows) st = launch(sort_kernel, dim3(1), kSortThreads, p, stream);
-  if (!st && r.splits > 0 && p.adapters > 0)
-    st = launch(shrink_kernel<T, NB>, dim3((unsigned)r.tiles, (unsigned)r.splits), kThreads, p,
-                stream);
-  if (!st)
-    st = launch(expand_kernel<T, NB>,
-                dim3((unsigned)r.tiles, (unsigned)((p.N + 4 * kTileCols - 1) / (4 * kTileCols))),
-                kThreads, p, stream);
-  return st;
+  if constexpr (NB <= 2)
+    if (r.fused) {
+      constexpr int cols = kFusedWaves * kTileCols;
+      return launch(fused_kernel<T, NB>,
+                    dim3((unsigned)r.tiles, (unsigned)((p.N + cols - 1) / cols)),
+                    64 * kFusedWaves, p, stream);
+    }
+  if (p.rows > kLaneRows) {
+    const int st = launch(sort_kernel, dim3(1), kSortThreads, p, stream);
+    if (st) return st;
+  }
+  return r.tile_rows == 32 ? run_tiles<T, NB, 2>(r, p, stream) : run_tiles<T, NB, 1>(r, p, stream);
 }
 
 template <class T>
@@ -442,9 +696,12 @@ extern "C" int lutgemm_adapters_add(const lutgemm_adapters* l, const void* d_x, 
       p.tiles = p.order + l->rows;
     }
     p.part = (float*)((char*)d_workspace + r.part_at);
-    p.x_row = l->x_row;
-    p.y_row = l->y_row;
-    p.out_row = l->out_row;
+    p.x_row = (int32_t)l->x_row;
+    p.y_row = (int32_t)l->y_row;
+    p.out_row = (int32_t)l->out_row;
+    p.x_bytes = (uint32_t)extent(l->rows, l->x_row, l->K);
+    p.y_bytes = (uint32_t)extent(l->rows, l->y_row, l->N);
+    p.out_bytes = (uint32_t)extent(l->rows, l->out_row, l->N);
     p.rows = l->rows;
     p.K = l->K;
     p.N = l->N;
@@ -453,8 +710,11 @@ extern "C" int lutgemm_adapters_add(const lutgemm_adapters* l, const void* d_x, 
     p.splits = r.splits;
     p.split_k = r.split_k;
     p.n_tiles = r.tiles;
-    p.wide = aligned(d_y, 16) && aligned(d_out, 16) && l->y_row % 8 == 0 && l->out_row % 8 == 0;
+    p.tile_rows = r.tile_rows;
+    p.wide = aligned(d_y, 16) && aligned(d_out, 16) && l->y_row % 8 == 0 && l->out_row % 8 == 0 &&
+             l->N % 8 == 0;
     p.in_place = d_y == d_out;
+    while ((p.adapters >> p.id_bits) != 0) ++p.id_bits;
     return l->type == LUTGEMM_F16 ? run_adapters<serve::F16>(r, p, (hipStream_t)stream)
                                   : run_adapters<serve::BF16>(r, p, (hipStream_t)stream);
   } catch (...) {

@@ -3,12 +3,15 @@
 // output (lutgemm_qk_norm_rotate; the formulas are in lutgemm.h).
 //
 // Memory bounds it: every element is read once and written once, with a few fp32
-// operations between. A thread owns sixteen entries of a head as two 16-byte words,
-// chosen so that both halves of each rotated pair are its own (entries 8u .. 8u+7
-// and R/2 + 8u .. for pairs of halves, 16u .. 16u+15 for neighbours); the only
-// exchange between lanes is the norm's sum over a head, 2 to 4 lane swaps. A
-// workgroup serves one token, so its angles are read once and kept in registers
-// for all the heads it walks.
+// operations between. 8192 tokens of 64 + 2 x 8 heads of 128 (336 MB) take 63 us, 5.3
+// TB/s, what a plain copy of the same bytes takes. A thread owns sixteen entries of a head as two
+// 16-byte words, chosen so that both halves of each rotated pair are its own (entries 8u ..
+// 8u+7 and R/2 + 8u .. for pairs of halves, 16u .. 16u+15 for neighbours); the only
+// exchange between lanes is the norm's sum over a head. A workgroup serves one token, so
+// its slot and angles are looked up once for all the heads that it walks; reading several
+// heads ahead (64 to 66 us) or a workgroup for each group of heads (87 us) did not gain.
+#include <type_traits>
+
 #include "serve.h"
 
 namespace lutgemm {
@@ -32,22 +35,19 @@ struct HeadsParams {
   int32_t heads, kv_heads, dim, rotary, interleaved, page_size;
   int32_t lanes_log2;  // lanes of a head: the power of two from dim / 16 up
   int32_t walk;        // head groups that one workgroup serves
-  float eps;
+  int32_t all;         // heads served: of queries, keys and, into a cache, values
+  float eps, inv_dim;
 };
 
 constexpr int kThreads = 256;
 
 template <class T>
-__device__ __forceinline__ void load16(const uint16_t* p, int c0, int c1, float (&a)[8],
-                                       float (&b)[8]) {
-  const u4v w0 = *(const u4v*)(p + c0), w1 = *(const u4v*)(p + c1);
+__device__ __forceinline__ void unpack16(u4v w, float (&a)[8]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const f2v x = T::unpack(w0[i]), y = T::unpack(w1[i]);
+    const f2v x = T::unpack(w[i]);
     a[2 * i] = x.x;
     a[2 * i + 1] = x.y;
-    b[2 * i] = y.x;
-    b[2 * i + 1] = y.y;
   }
 }
 
@@ -75,29 +75,58 @@ __device__ __forceinline__ void turn(float (&a)[8], float (&b)[8], const float (
   }
 }
 
+// A value summed over aligned groups of 1 << log2 lanes, up to sixteen, without LDS.
+__device__ __forceinline__ float sum_lanes(float v, int log2) {
+  auto moved = [&](auto control) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v),
+                                                                 decltype(control)::value, 0xF, 0xF,
+                                                                 true));
+  };
+  if (log2 > 0) v += moved(std::integral_constant<int, 0xB1>{});   // lanes 1, 0, 3, 2 of each four
+  if (log2 > 1) v += moved(std::integral_constant<int, 0x4E>{});   // lanes 2, 3, 0, 1
+  if (log2 > 2) v += moved(std::integral_constant<int, 0x141>{});  // eight lanes mirrored
+  if (log2 > 3) v += moved(std::integral_constant<int, 0x140>{});  // sixteen mirrored
+  return v;
+}
+
 template <class T>
 __global__ __launch_bounds__(kThreads) void heads_kernel(HeadsParams p) {
+  fetch(p);
   const int64_t t = blockIdx.x;
   const int lanes = 1 << p.lanes_log2;
   const int u = threadIdx.x & (lanes - 1);            // which sixteen entries of the head
   const int per_group = kThreads >> p.lanes_log2;     // heads served together
-  const int all = p.heads + 2 * p.kv_heads;
   const bool active = u < p.dim / 16;
   const bool turned = u < p.rotary / 16;
   const bool halves = turned && !p.interleaved;
-  const int c0 = halves ? 8 * u : 16 * u;
-  const int c1 = halves ? 8 * u + p.rotary / 2 : 16 * u + 8;
+  const uint32_t c0 = !active ? 0 : halves ? 8 * u : 16 * u;
+  const uint32_t c1 = !active ? 8 : halves ? 8 * u + p.rotary / 2 : 16 * u + 8;
+  const uint16_t* src = p.qkv + t * p.qkv_token;
+  const int64_t slot = p.slots ? p.slots[t] : 0;
+  const int64_t pos = p.rotary ? p.positions[t] : 0;
+  const int first = (int)blockIdx.y * p.walk * per_group + (int)(threadIdx.x >> p.lanes_log2);
 
-  int64_t slot = p.slots ? p.slots[t] : 0;
+  // the first head's words are on their way while the slot and the angles are looked up
+  auto head_at = [&](int h) { return src + (uint32_t)min(h, p.all - 1) * (uint32_t)p.dim; };
+  u4v w0 = *(const u4v*)(head_at(first) + c0), w1 = *(const u4v*)(head_at(first) + c1);
+  u4v qw0 = {}, qw1 = {}, kw0 = {}, kw1 = {};
+  if (p.q_weight) {
+    qw0 = *(const u4v*)(p.q_weight + c0);
+    qw1 = *(const u4v*)(p.q_weight + c1);
+    kw0 = *(const u4v*)(p.k_weight + c0);
+    kw1 = *(const u4v*)(p.k_weight + c1);
+  }
   const bool kept = !p.slots || (slot >= 0 && slot < p.n_slots);
   int64_t page = t, in_page = 0;
   if (p.slots && kept) {
-    page = slot / p.page_size;
+    page = (p.n_slots >> 32) ? slot / p.page_size : (uint32_t)slot / (uint32_t)p.page_size;
     in_page = slot - page * p.page_size;
   }
+  uint16_t* const q_to = p.q + t * p.q_token;
+  uint16_t* const k_to = p.k + page * p.k_page + in_page * p.k_slot;
+  uint16_t* const v_to = p.v + page * p.v_page + in_page * p.v_slot;
   float cs[8], sn[8];
   if (turned) {
-    const int64_t pos = p.positions[t];
     const bool known = pos >= 0 && pos < p.n_positions;
     const float* row = p.table + (known ? pos : 0) * p.rotary + 8 * u;
 #pragma unroll
@@ -110,56 +139,49 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(HeadsParams p) {
       }
     }
   }
-  const uint16_t* src = p.qkv + t * p.qkv_token;
+  // whole heads step together, so every lane of a head is here or none is
   for (int g = 0; g < p.walk; ++g) {
-    const int h = ((int)blockIdx.y * p.walk + g) * per_group + (int)(threadIdx.x >> p.lanes_log2);
-    // whole head groups step together, so every lane of a head is here or none is
-    if (h >= all) break;
-    const bool is_q = h < p.heads, is_v = h >= p.heads + p.kv_heads;
-    if ((is_v && !p.slots) || (!is_q && !kept)) continue;
-    const uint16_t* in = src + (int64_t)h * p.dim;
-    uint16_t* out = is_q ? p.q + t * p.q_token + (int64_t)h * p.dim
-                  : is_v ? p.v + page * p.v_page + in_page * p.v_slot +
-                               (int64_t)(h - p.heads - p.kv_heads) * p.v_head
-                         : p.k + page * p.k_page + in_page * p.k_slot +
-                               (int64_t)(h - p.heads) * p.k_head;
-    if (is_v) {
-      if (active) {
-        *(u4v*)(out + c0) = *(const u4v*)(in + c0);
-        *(u4v*)(out + c1) = *(const u4v*)(in + c1);
-      }
-      continue;
+    const int h = first + g * per_group;
+    if (h >= p.all) break;
+    if (g) {
+      w0 = *(const u4v*)(head_at(h) + c0);
+      w1 = *(const u4v*)(head_at(h) + c1);
     }
-    float a[8] = {}, b[8] = {};
-    if (active) load16<T>(in, c0, c1, a, b);
-    const uint16_t* w = is_q ? p.q_weight : p.k_weight;
-    if (w) {
-      float sum = 0.f;
+    const bool is_q = h < p.heads, is_v = h >= p.heads + p.kv_heads;
+    if (!is_v) {
+      float a[8], b[8];
+      unpack16<T>(w0, a);
+      unpack16<T>(w1, b);
+      if (p.q_weight) {
+        float wa[8], wb[8], sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum += a[i] * a[i] + b[i] * b[i];
-      for (int d = 1; d < lanes; d <<= 1) sum += __shfl_xor(sum, d, 64);
-      const float r = 1.0f / sqrtf(sum / (float)p.dim + p.eps);
-      if (active) {
-        float wa[8], wb[8];
-        load16<T>(w, c0, c1, wa, wb);
+        for (int i = 0; i < 8; ++i) {
+          sum = __builtin_fmaf(a[i], a[i], sum);
+          sum = __builtin_fmaf(b[i], b[i], sum);
+        }
+        sum = sum_lanes(active ? sum : 0.f, p.lanes_log2);
+        const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(sum, p.inv_dim, p.eps));
+        unpack16<T>(is_q ? qw0 : kw0, wa);
+        unpack16<T>(is_q ? qw1 : kw1, wb);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           a[i] *= r * wa[i];
           b[i] *= r * wb[i];
         }
       }
-    }
-    if (turned) turn(a, b, cs, sn, p.interleaved);
-    if (active) {
-      u4v w0, w1;
+      if (turned) turn(a, b, cs, sn, p.interleaved);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         w0[i] = T::pack(a[2 * i], a[2 * i + 1]);
         w1[i] = T::pack(b[2 * i], b[2 * i + 1]);
       }
-      *(u4v*)(out + c0) = w0;
-      *(u4v*)(out + c1) = w1;
     }
+    if (!active || (!is_q && !kept)) continue;
+    uint16_t* to = is_q ? q_to + (uint32_t)h * (uint32_t)p.dim
+                 : is_v ? v_to + (int64_t)(h - p.heads - p.kv_heads) * p.v_head
+                        : k_to + (int64_t)(h - p.heads) * p.k_head;
+    *(u4v*)(to + c0) = w0;
+    *(u4v*)(to + c1) = w1;
   }
 }
 
@@ -237,12 +259,14 @@ extern "C" int lutgemm_qk_norm_rotate(const lutgemm_heads* h, const void* d_qkv,
     p.interleaved = h->interleaved;
     p.page_size = h->page_size;
     p.eps = h->eps;
+    p.inv_dim = 1.0f / (float)h->head_dim;
     while ((16 << p.lanes_log2) < h->head_dim) ++p.lanes_log2;
     const int per_group = kThreads >> p.lanes_log2;
     const int all = h->heads + h->kv_heads * (d_slots ? 2 : 1);
     const int groups = (all + per_group - 1) / per_group;
     // few tokens: a workgroup for each group of heads; many: one walks them all
     p.walk = (int64_t)h->tokens * groups <= 8 * (int64_t)cus ? 1 : groups;
+    p.all = all;
     const dim3 grid((unsigned)h->tokens, (unsigned)((groups + p.walk - 1) / p.walk));
     return serve::launch(h->type == LUTGEMM_F16 ? heads_kernel<serve::F16>
                                                 : heads_kernel<serve::BF16>,

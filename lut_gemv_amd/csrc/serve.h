@@ -91,6 +91,16 @@ __device__ __forceinline__ u2v read_column(const void* lds) {
       u2v, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4v*)(lds)));
 }
 
+// A kernel's parameters, asked for together at its start: they lie in host memory, and
+// fields first read where they are needed cost a trip there each.
+template <class P>
+__device__ __forceinline__ void fetch(const P& p) {
+  constexpr int n = sizeof(P) / 4;
+  const uint32_t* w = (const uint32_t*)&p;
+#pragma unroll
+  for (int i = 0; i < n; ++i) asm volatile("" ::"s"(w[i]));
+}
+
 // ------------------------------------------------------------------ host side
 
 // The current device must be gfx950 (LUTGEMM_FAKE_ARCH, a debugging aid, replaces

@@ -108,7 +108,7 @@ def test_heads_empty_call():
 
 # -------------------------------------------------------------- adapters refusals
 
-ADD = dict(type=0, rows=20, K=64, N=40, rank=16, adapters=3, x_row=64, y_row=40, out_row=40)
+ADD = dict(type=0, rows=80, K=64, N=40, rank=16, adapters=3, x_row=64, y_row=40, out_row=40)
 
 
 def _adapters(x=A, y=A, a=A, b=A, s=A, ids=A, out=2 * A, ws=A, wsb=1 << 20, **change):
@@ -118,10 +118,11 @@ def _adapters(x=A, y=A, a=A, b=A, s=A, ids=A, out=2 * A, ws=A, wsb=1 << 20, **ch
 
 @pytest.mark.parametrize("change,status", [
     (dict(type=2), SHAPE), (dict(rows=-1), SHAPE), (dict(rows=65536), SHAPE), (dict(K=12), SHAPE),
-    (dict(K=-8), SHAPE), (dict(K=1 << 24), SHAPE), (dict(N=-1), SHAPE), (dict(N=1 << 23), SHAPE),
+    (dict(K=-8), SHAPE), (dict(K=1 << 23), SHAPE), (dict(N=-1), SHAPE), (dict(N=1 << 23), SHAPE),
     (dict(rank=0), SHAPE), (dict(rank=12), SHAPE), (dict(rank=136), SHAPE), (dict(adapters=-1), SHAPE),
     (dict(adapters=4097), SHAPE), (dict(x_row=60), SHAPE), (dict(y_row=-1), SHAPE),
-    (dict(out_row=-1), SHAPE), (dict(x=None), NULL), (dict(y=None), NULL), (dict(a=None), NULL),
+    (dict(out_row=-1), SHAPE), (dict(x_row=1 << 26), SHAPE), (dict(y_row=1 << 40), SHAPE),
+    (dict(out_row=57 << 20), SHAPE), (dict(x=None), NULL), (dict(y=None), NULL), (dict(a=None), NULL),
     (dict(b=None), NULL), (dict(ids=None), NULL), (dict(out=None), NULL), (dict(ws=None), NULL),
     (dict(wsb=16), BUFFER), (dict(ws=A + 8), ALIGN), (dict(x=A + 8), ALIGN), (dict(a=A + 2), ALIGN),
     (dict(b=A + 4), ALIGN), (dict(s=A + 2), ALIGN), (dict(ids=A + 2), ALIGN), (dict(y=A + 1), ALIGN),
