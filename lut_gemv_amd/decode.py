@@ -15,11 +15,17 @@ What is modelled and what is not:
   * every projection of a layer is one product with its own weights, chained
     so that each product reads the output of an earlier one (the data
     dependence of a real decode step);
-  * attention over the key/value cache, normalisations, activation functions
-    and residual additions are not part of the kernel and are left out: the
-    output projection reads the first d entries of the fused QKV output in
-    place of the attention output, and the down projection reads the up half
-    of the fused gate/up output in place of the gated activation;
+  * with ``context`` > 0 every layer has a paged key/value cache of that many
+    keys for each sequence: the fused QKV output is rotated (the LLaMA shapes) and
+    its keys and values appended by one call, the attention of the new token runs
+    over the cache, and the output projection reads its result. By default
+    there is no cache, and the output projection reads the first d entries of the
+    QKV output in place of the attention output;
+  * with ``adapters`` > 0 every projection has that many low-rank adapters, and
+    sequence i uses adapter i modulo their number;
+  * activation functions, layer norms and residual additions are left out: the
+    down projection reads the up half of the fused gate/up output in place of the
+    gated activation;
   * scales are drawn so that one product keeps the activations' root mean
     square roughly unchanged (|N(0, sigma)| with sigma = 1/sqrt(q K)), so a
     deep chain stays finite in fp16.
@@ -39,7 +45,8 @@ from typing import Dict, List, Optional, Tuple
 
 import numpy as np
 
-from . import PackedBCQ, packed_sizes
+from . import (PackedBCQ, adapters_add, packed_sizes, paged_attention, qk_norm_rotate,
+               rotary_table)
 
 __all__ = ["MODELS", "Projection", "DecodeStack", "weight_bytes_per_step", "main"]
 
@@ -76,6 +83,9 @@ MODELS: Dict[str, Tuple[int, List[Projection], str]] = {
     "llama65b": (80, _llama(8192, 22016), "down"),
 }
 
+HEAD_DIM = 128                     # of every model's attention heads
+ROTATED = {"llama7b", "llama65b"}  # models that rotate queries and keys by position
+
 
 def weight_bytes_per_step(model: str, q: int = 3, g: int = 128,
                            layers: Optional[int] = None) -> int:
@@ -94,7 +104,8 @@ class DecodeStack:
 
     def __init__(self, model: str, layers: Optional[int] = None, q: int = 3, g: int = 128,
                  m: int = 1, seed: int = 0, device: str = "cuda:0", keep_logical: bool = False,
-                 log=None):
+                 log=None, context: int = 0, page_size: int = 64, adapters: int = 0,
+                 rank: int = 16):
         import torch
         import workloads
 
@@ -105,6 +116,9 @@ class DecodeStack:
         self.layers = full_layers if layers is None else int(layers)
         if self.layers < 1:
             raise ValueError("layers must be >= 1")
+        self.context, self.adapters = int(context), int(adapters)
+        if self.context < 0 or self.adapters < 0:
+            raise ValueError("context and adapters must be >= 0")
         self.projs, self.out_name, self.device = projs, out_name, device
         self.logical = {}
         protos = {}
@@ -136,18 +150,79 @@ class DecodeStack:
         self.x = torch.from_numpy(x0).to(device)
         self.outs = {p.name: torch.empty((self.m, p.N), dtype=torch.float16, device=device)
                      for p in projs}
+        self.caches = []      # per layer: key pages, value pages
+        if self.context:
+            self._make_caches(d_model, page_size, seed)
+        self.lora = []        # per layer: projection name -> (a, b)
+        if self.adapters:
+            self._make_adapters(rank, seed)
         self.graph = None
         self.graph_kernel = None
+
+    def _make_caches(self, d_model: int, page_size: int, seed: int):
+        """A paged cache a layer that holds `context` keys of every sequence, their pages
+        in any order, with room for the token that a step appends."""
+        import torch
+        gen = torch.Generator(device=self.device).manual_seed(seed)
+        self.heads = d_model // HEAD_DIM
+        each = -(-(self.context + 1) // page_size)
+        shape = (self.m * each, page_size, self.heads, HEAD_DIM)
+        for _ in range(self.layers):
+            self.caches.append(tuple(
+                torch.randn(shape, generator=gen, device=self.device).to(torch.float16)
+                for _ in range(2)))
+        order = torch.randperm(self.m * each, generator=gen, device=self.device)
+        table = order.view(self.m, each)
+        self.page_table = table.to(torch.int32)
+        at = self.context
+        self.positions = torch.full((self.m,), at, dtype=torch.int64, device=self.device)
+        self.slots = (table[:, at // page_size] * page_size + at % page_size).contiguous()
+        self.kv_lens = torch.full((self.m,), at + 1, dtype=torch.int32, device=self.device)
+        self.rotary = (rotary_table(at + 1, HEAD_DIM, device=self.device)
+                       if self.model in ROTATED else None)
+        self.queries = torch.empty((self.m, self.heads, HEAD_DIM), dtype=torch.float16,
+                                   device=self.device)
+        self.attended = torch.empty((self.m, d_model), dtype=torch.float16, device=self.device)
+
+    def _make_adapters(self, rank: int, seed: int):
+        import torch
+        gen = torch.Generator(device=self.device).manual_seed(seed + 1)
+        for _ in range(self.layers):
+            lw = {}
+            for p in self.projs:
+                a, b = (torch.randn(shape, generator=gen, device=self.device)
+                        for shape in ((self.adapters, rank, p.K), (self.adapters, p.N, rank)))
+                lw[p.name] = ((a * p.K ** -0.5).to(torch.float16),
+                              (b * (0.1 * rank ** -0.5)).to(torch.float16))
+            self.lora.append(lw)
+        self.ids = (torch.arange(self.m, device=self.device) % self.adapters).to(torch.int32)
 
     # ------------------------------------------------------------ sizes
     def bytes_per_step(self) -> int:
         """Packed weight bytes every decode step reads (bits + scales, all layers)."""
         return weight_bytes_per_step(self.model, self.q, self.g, self.layers)
 
+    def cache_bytes_per_step(self) -> int:
+        """Bytes of keys and values that one decode step's attention reads (all layers)."""
+        if not self.context:
+            return 0
+        return self.layers * self.m * (self.context + 1) * 2 * self.heads * HEAD_DIM * 2
+
     # ------------------------------------------------------------ one token
     def _src(self, p: Projection, x_layer):
+        if p.src == "qkv" and self.context:
+            return self.attended
         t = x_layer if p.src == "x" else self.outs[p.src]
         return t[:, p.src_off:p.src_off + p.K] if t.shape[1] != p.K else t
+
+    def _attend(self, layer: int):
+        """Layer's attention of the new tokens, from the QKV output to `attended`."""
+        k_pages, v_pages = self.caches[layer]
+        qk_norm_rotate(self.outs["qkv"], self.heads, self.heads, self.positions, self.rotary,
+                       k_pages=k_pages, v_pages=v_pages, slots=self.slots, out=self.queries)
+        paged_attention(self.queries, k_pages, v_pages, self.page_table, self.kv_lens,
+                        max_kv=self.context + 1,
+                        out=self.attended.view(self.m, self.heads, HEAD_DIM))
 
     def token(self, kernel: str = "lut"):
         """Run every product of every layer once, in order, on the current stream.
@@ -160,12 +235,17 @@ class DecodeStack:
                 if src.shape[1] != p.K or not src.is_contiguous():
                     src = src.contiguous()
                 w = lw[p.name]
+                out = self.outs[p.name]
                 if kernel == "lut":
-                    w(src, out=self.outs[p.name])
+                    w(src, out=out)
                 elif kernel == "dequant":
-                    w.dequant(src, out=self.outs[p.name])
+                    w.dequant(src, out=out)
                 else:
                     raise ValueError(f"unknown kernel {kernel!r}")
+                if self.adapters:
+                    adapters_add(out, src, *self.lora[l][p.name], self.ids, out=out)
+                if p.name == "qkv" and self.context:
+                    self._attend(l)
             # the next layer reads this output in place: its first product runs
             # before this buffer is written again
             x_layer = self.outs[self.out_name]
@@ -264,6 +344,11 @@ def main(argv=None) -> int:
     ap.add_argument("--tokens", type=int, default=20)
     ap.add_argument("--warmup", type=int, default=5)
     ap.add_argument("--kernel", default="both", choices=["lut", "dequant", "both"])
+    ap.add_argument("--context", type=int, default=0,
+                    help="keys of each sequence in the cache; 0: no attention")
+    ap.add_argument("--page-size", type=int, default=64)
+    ap.add_argument("--adapters", type=int, default=0, help="low-rank adapters of every projection")
+    ap.add_argument("--rank", type=int, default=16)
     ap.add_argument("--breakdown", action="store_true",
                     help="also time each projection on its own (us per GEMV)")
     a = ap.parse_args(argv)
@@ -274,7 +359,8 @@ def main(argv=None) -> int:
         return 2
     t0 = time.perf_counter()
     st = DecodeStack(a.model, a.layers, a.q, a.g, a.m,
-                     log=lambda msg: print(f"[decode] {msg}", flush=True))
+                     log=lambda msg: print(f"[decode] {msg}", flush=True), context=a.context,
+                     page_size=a.page_size, adapters=a.adapters, rank=a.rank)
     torch.cuda.synchronize()
     setup_s = time.perf_counter() - t0
     print(f"[decode] {a.model}: {st.layers} layers, {st.bytes_per_step() / 1e9:.2f} GB packed "
@@ -300,6 +386,10 @@ def main(argv=None) -> int:
     line = {"model": a.model, "layers": st.layers, "q": a.q, "g": a.g, "m": a.m,
             "weight_bytes_per_step": st.bytes_per_step(), "gemvs_per_step":
             st.layers * len(st.projs), "tokens": a.tokens, "results": res}
+    if a.context:
+        line.update(context=a.context, cache_bytes_per_step=st.cache_bytes_per_step())
+    if a.adapters:
+        line.update(adapters=a.adapters, rank=a.rank)
     if "lut" in res and "dequant" in res:
         line["dequant_over_lut"] = res["dequant"]["ms_per_step"] / res["lut"]["ms_per_step"]
     print(json.dumps(line), flush=True)

@@ -548,3 +548,41 @@ def test_a_prompt_in_chunks_then_tokens(norm):
             want, bound = plain.attention(_np(q[rows]), _np(ks), _np(vs), news[r], have[r],
                                           dim ** -0.5, 0, U[F16])
             _inside(o[rows], want, bound, f"step {step} request {r}")
+
+
+@pytest.mark.parametrize("model,adapters", [("llama7b", 0), ("llama7b", 2)])
+def test_decode_stack_with_a_cache(model, adapters):
+    """A decode step with attention (and adapters): each layer's attention is that of the
+    fp64 form on its cache as the step left it, every captured replay equals the
+    eager step, and the products without them are the driver's own as before."""
+    from lut_gemv_amd import decode
+    st = decode.DecodeStack(model, layers=2, q=2, g=128, m=3, device=DEV, context=150, page_size=32,
+                            adapters=adapters)
+    eager = st.token().clone()
+    torch.cuda.synchronize()
+    assert torch.isfinite(eager).all()
+    heads = st.heads
+    for layer in (0, 1):
+        st.token()
+        k_pages, v_pages = st.caches[layer]
+        if layer == 1:   # the last layer's queries and output are the ones that are left
+            for i in range(st.m):
+                rows = st.page_table[i].long()
+                ks, vs = (t[rows].flatten(0, 1)[:151] for t in (k_pages, v_pages))
+                want, bound = plain.attention(_np(st.queries[i:i + 1]), _np(ks), _np(vs), 1, 151,
+                                              128 ** -0.5, 0, U[F16])
+                _inside(st.attended.view(3, heads, 128)[i:i + 1], want, bound, f"sequence {i}")
+                qkv = _np(st.outs["qkv"][i]).reshape(3 * heads, 128)
+                assert np.array_equal(_np(vs[150]), qkv[2 * heads:])
+                angle = _np(st.rotary[150])
+                want, bound = plain.heads(qkv[None, heads:2 * heads], None, 0.0, angle[None, :64],
+                                          angle[None, 64:], False, U[F16])
+                _inside(ks[150:151], want, bound, f"key of sequence {i}")
+    g = st.capture()
+    for r in range(3):
+        st.outs[st.out_name].fill_(0)
+        torch.randn(1 << 16, device=DEV).sum()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(st.outs[st.out_name], eager), f"replay {r}"

@@ -166,6 +166,13 @@ def test_packed_call_needs_adapters_and_ids_together():
             pw(x, **kw)
 
 
+def test_decode_stack_arguments():
+    from lut_gemv_amd import decode
+    for kw in (dict(context=-1), dict(adapters=-1)):
+        with pytest.raises(ValueError):
+            decode.DecodeStack("llama7b", layers=1, device="cpu", **kw)
+
+
 def test_descriptors_match_the_header(tmp_path):
     cc = shutil.which("gcc") or shutil.which("cc")
     if cc is None:
