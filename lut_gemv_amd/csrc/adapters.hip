@@ -12,8 +12,8 @@
 // a pair of numbers, high + low, of the element type: the pair's error is far below
 // the rounding of the output, for two small matrix products in place of one.
 //
-// 61 rows of 24 adapters of rank 64, K = 11008, N = 4096 (46 MB): 16.7 us, 2.8 TB/s;
-// 4096 rows, K = N = 8192, rank 32 (206 MB): 74 us, 2.8 TB/s.
+// 61 rows of 24 adapters of rank 64, K = 11008, N = 4096 (49 MB): 16.5 us, 2.9 TB/s;
+// 4096 rows of 8, K = N = 8192, rank 32 (210 MB): 63 us, 3.3 TB/s, of them 8 sorting.
 #include "serve.h"
 
 namespace lutgemm {
@@ -24,7 +24,6 @@ using namespace serve;
 constexpr int kThreads = 256;
 constexpr int kTileRows = 16;    // of a set of rows
 constexpr int kLaneRows = 64;    // up to so many rows are sorted by each wave itself
-constexpr int kStepK = 128;      // K that a wave reads before the next wave's share
 constexpr int kSortThreads = 1024;
 constexpr int kMaxAdapters = 4096;
 constexpr int kTileCols = 64;    // output columns of a wave at a time
@@ -148,9 +147,8 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(AdapterParams p) {
   const int lane = tid & 63, wave = tid >> 6;
   // the bin of a row, -1 past the last row
   auto bin_of = [&](int row) {
-    if (row >= p.rows) return -1;
-    const int id = id_of(p, row);
-    return id < 0 ? p.adapters : id;
+    const int id = id_of(p, at_most(row, p.rows - 1));
+    return row >= p.rows ? -1 : id < 0 ? p.adapters : id;
   };
   // counters[bin] raised by the wave's rows of each bin; *at: this row's place in its bin
   auto add = [&](int* counters, int bin, int* at) {
@@ -162,8 +160,20 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(AdapterParams p) {
   };
   for (int i = tid; i < bins; i += kSortThreads) count[i] = 0;
   __syncthreads();
+  // four rows of a thread are read before the first is counted
+  constexpr int kBatch = 4;
+  auto each_row = [&](auto use) {
+    for (int i = wave * 64; i < p.rows; i += kBatch * kSortThreads) {
+      int bin[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) bin[j] = bin_of(i + j * kSortThreads + lane);
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        if (i + j * kSortThreads < p.rows) use(i + j * kSortThreads + lane, bin[j]);
+    }
+  };
   int at;
-  for (int i = wave * 64; i < p.rows; i += kSortThreads) add(count, bin_of(i + lane), &at);
+  each_row([&](int, int bin) { add(count, bin, &at); });
   __syncthreads();
   // running sums of rows and of tiles over the bins, a few bins to a thread
   const int each = (bins + kSortThreads - 1) / kSortThreads;
@@ -218,78 +228,121 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(AdapterParams p) {
   }
   __syncthreads();
   // the order within a bin changes from run to run; no row's result depends on it
-  for (int i = wave * 64; i < p.rows; i += kSortThreads) {
-    const int bin = bin_of(i + lane);
+  each_row([&](int row, int bin) {
     add(row_at, bin, &at);
-    if (bin >= 0) p.order[at] = i + lane;
-  }
+    if (bin >= 0) p.order[at] = row;
+  });
 }
 
 // ------------------------------------------------------------------ t = A[a] x
 //
-// NB blocks of 16 ranks. Both operands come straight from memory in their layout
-// (eight consecutive k per lane), so nothing is staged; W waves take turns at 128 k
-// each. Entry e of acc[i]: rank 16 i + 4 (lane / 16) + e of the row of column lane % 16.
+// NB blocks of 16 ranks, R sets of 16 rows; W waves take turns at kStep k each. A wave brings
+// whole rows of its step to its own LDS and reads both operands from there (eight
+// consecutive k per lane). Read from memory in the operands' own layout, 64 bytes of each
+// of sixteen rows at a time, every line is asked for twice, and a compute unit waits for
+// its lines (one row, K = 4096, rank 16, in one workgroup: 8.3 us, so 5.6; 4096 rows, rank 32: 26
+// us, so 20). Entry e of acc[j][i]: rank 16 i + 4 (lane / 16) + e of the row of column
+// lane % 16 of set j.
+
+template <int NB, int R>
+struct Stage {
+  static constexpr int kStep = NB == 8 ? 64 : 128;    // k of a step
+  static constexpr int kWords = kStep / 8;            // 16-byte words of a row
+  static constexpr int kRows = 64 / kWords;           // rows of one load
+  static constexpr int kBytes = (NB + R) * 16 * kStep * 2;
+  // the place of a word in its row of LDS, so that the rows read together differ in banks
+  static __device__ __forceinline__ int place(int row, int word) {
+    return word ^ (kWords == 16 ? row & 15 : (row >> 1) & 7);
+  }
+};
 
 template <class T, int NB, int R>
 __device__ __forceinline__ void shrink(const AdapterParams& p, const Tile<R>& t, int from, int to,
-                                       int stride, f4v (&acc)[R][NB]) {
+                                       int stride, char* lds, f4v (&acc)[R][NB]) {
+  using S = Stage<NB, R>;
   const int lane = threadIdx.x & 63, c = lane >> 4, col = lane & 15;
   const __amdgpu_buffer_rsrc_t x = buffer(p.x, p.x_bytes);
   const __amdgpu_buffer_rsrc_t a =
       buffer(p.a + (int64_t)t.adapter * p.rank * p.K, 2u * (uint32_t)p.rank * (uint32_t)p.K);
-  // columns and ranks past the last read nothing
-  uint32_t x_at[R], a_at[NB];
-#pragma unroll
-  for (int j = 0; j < R; ++j)
-    x_at[j] = t.has(j) ? 2 * (uint32_t)t.row[j] * (uint32_t)p.x_row + 16 * c : kNowhere;
-#pragma unroll
-  for (int i = 0; i < NB; ++i) {
-    a_at[i] = 2 * (uint32_t)(16 * i + col) * (uint32_t)p.K + 16 * c;
-    if (16 * i + col >= p.rank) a_at[i] = kNowhere;
-  }
 #pragma unroll
   for (int j = 0; j < R; ++j)
 #pragma unroll
     for (int i = 0; i < NB; ++i) acc[j][i] = f4v{0.f, 0.f, 0.f, 0.f};
-  constexpr int kWords = kStepK / 32;
-  for (int k0 = from; k0 < to; k0 += stride) {
-    u4v xw[kWords][R], aw[kWords][NB];
-    uint32_t x_k[R], a_k[NB];
+  char* const a_lds = lds + R * 16 * S::kStep * 2;
+  // this lane's row of each load and the word that belongs in its place
+  constexpr int kLoads = 16 / S::kRows;
+  uint32_t x_at[R][kLoads], a_at[kLoads];
 #pragma unroll
-    for (int j = 0; j < R; ++j) x_k[j] = x_at[j] == kNowhere ? kNowhere : x_at[j] + 2 * k0;
+  for (int l = 0; l < kLoads; ++l) {
+    const int row = S::kRows * l + lane / S::kWords;
+    const uint32_t word = 16 * S::place(row, lane % S::kWords);
+    a_at[l] = 2 * (uint32_t)row * (uint32_t)p.K + word;
 #pragma unroll
-    for (int i = 0; i < NB; ++i) a_k[i] = a_at[i] == kNowhere ? kNowhere : a_at[i] + 2 * k0;
-    if (k0 + kStepK <= to) {
+    for (int j = 0; j < R; ++j)
+      x_at[j][l] = 2 * (uint32_t)__shfl(t.row[j], row, 64) * (uint32_t)p.x_row + word;
+  }
+  const uint32_t a_block = 32 * (uint32_t)p.K;
+  int k0 = from;
+  for (; k0 + S::kStep <= to; k0 += stride) {
+    // rows past the tile's last are those of its first again, or not read; ranks past the
+    // last are the last rows' again: both only reach entries that are not used
 #pragma unroll
-      for (int s = 0; s < kWords; ++s) {
+    for (int j = 0; j < R; ++j)
 #pragma unroll
-        for (int j = 0; j < R; ++j) xw[s][j] = load16(x, x_k[j] + 64 * s);
+      for (int l = 0; l < kLoads; ++l)
+        if (16 * j + S::kRows * l < t.count)
+          load_to_lds(x, x_at[j][l] + 2 * k0, lds + (16 * j + S::kRows * l) * S::kStep * 2);
 #pragma unroll
-        for (int i = 0; i < NB; ++i) aw[s][i] = load16(a, a_k[i] + 64 * s);
-      }
-    } else {
+    for (int i = 0; i < NB; ++i)
 #pragma unroll
-      for (int s = 0; s < kWords; ++s) {
-        const bool in = k0 + 32 * s + 8 * c < to;
+      for (int l = 0; l < kLoads; ++l)
+        if (16 * i + S::kRows * l < p.rank)
+          load_to_lds(a, a_at[l] + i * a_block + 2 * k0,
+                      a_lds + (16 * i + S::kRows * l) * S::kStep * 2);
+    wait_for_loads();
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
 #pragma unroll
-        for (int j = 0; j < R; ++j) xw[s][j] = load16(x, in ? x_k[j] + 64 * s : kNowhere);
+    for (int s = 0; s < S::kStep / 32; ++s) {
+      const int word = 16 * S::place(col, 4 * s + c);
+      u4v xw[R];
 #pragma unroll
-        for (int i = 0; i < NB; ++i) aw[s][i] = load16(a, in ? a_k[i] + 64 * s : kNowhere);
+      for (int j = 0; j < R; ++j) xw[j] = *(const u4v*)(lds + (16 * j + col) * S::kStep * 2 + word);
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        const u4v aw = *(const u4v*)(a_lds + (16 * i + col) * S::kStep * 2 + word);
+#pragma unroll
+        for (int j = 0; j < R; ++j) acc[j][i] = T::mfma16(aw, xw[j], acc[j][i]);
       }
     }
+    // the next step's loads come after these reads
+    wait_for_lds();
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+  // the end of K, less than a step, straight to the operands
+  for (; k0 < to; k0 += 32) {
+    const bool in = k0 + 8 * c < to;
+    const uint32_t at = 2 * k0 + 16 * c;
+    u4v xw[R];
 #pragma unroll
-    for (int s = 0; s < kWords; ++s)
+    for (int j = 0; j < R; ++j)
+      xw[j] = load16(x, in && t.has(j) ? 2 * (uint32_t)t.row[j] * (uint32_t)p.x_row + at : kNowhere);
 #pragma unroll
-      for (int i = 0; i < NB; ++i)
+    for (int i = 0; i < NB; ++i) {
+      const u4v aw = load16(
+          a, in && 16 * i + col < p.rank ? 2 * (uint32_t)(16 * i + col) * (uint32_t)p.K + at : kNowhere);
 #pragma unroll
-        for (int j = 0; j < R; ++j) acc[j][i] = T::mfma16(aw[s][i], xw[s][j], acc[j][i]);
+      for (int j = 0; j < R; ++j) acc[j][i] = T::mfma16(aw, xw[j], acc[j][i]);
+    }
   }
 }
 
 template <class T, int NB, int R>
 __global__ __launch_bounds__(kThreads) void shrink_kernel(AdapterParams p) {
-  __shared__ float sums[4][R * NB][64][4];
+  using S = Stage<NB, R>;
+  __shared__ __attribute__((aligned(16))) char stage[4 * S::kBytes];
+  static_assert(S::kBytes >= R * NB * 1024, "the waves' sums fit their stage");
   fetch(p);
   const Tile<R> t = find_tile<R>(p, blockIdx.x);
   if (t.adapter < 0) return;
@@ -297,7 +350,9 @@ __global__ __launch_bounds__(kThreads) void shrink_kernel(AdapterParams p) {
   const int from = blockIdx.y * p.split_k;
   const int to = from + p.split_k < p.K ? from + p.split_k : p.K;
   f4v acc[R][NB];
-  shrink<T, NB, R>(p, t, from + kStepK * wave, to, 4 * kStepK, acc);
+  shrink<T, NB, R>(p, t, from + S::kStep * wave, to, 4 * S::kStep, stage + wave * S::kBytes, acc);
+  __syncthreads();
+  float(*sums)[R * NB][64][4] = (float(*)[R * NB][64][4])stage;
 #pragma unroll
   for (int j = 0; j < R; ++j)
 #pragma unroll
@@ -318,9 +373,10 @@ __global__ __launch_bounds__(kThreads) void shrink_kernel(AdapterParams p) {
 
 // ------------------------------------------------------------- out = y + s B[a] t
 //
-// 64 output columns to a wave at a time. Row i of the four column blocks' operands is
-// output column 16 (i / 4) + 4 block + i % 4, so a lane's results are sixteen
-// consecutive columns of its row: 32 bytes of y and out. y and B are read before t is needed.
+// 64 output columns to a wave at a time. Row i of column block k's operand is output
+// column 32 (k / 2) + 8 (i / 4) + 4 (k % 2) + i % 4, so a lane's results are twice eight
+// consecutive columns of its row, and four lanes' together 64 bytes of y and out. y and B are
+// read before t is needed.
 
 template <class T, int NB, int R>
 struct Columns {
@@ -329,37 +385,40 @@ struct Columns {
 
   __device__ __forceinline__ void load(const AdapterParams& p, const Tile<R>& t, int n0) {
     const int lane = threadIdx.x & 63, c = lane >> 4, col = lane & 15;
-    const int n = n0 + 16 * c;
+    const int n = n0 + 8 * c;
     const __amdgpu_buffer_rsrc_t from = buffer(p.y, p.y_bytes);
 #pragma unroll
     for (int j = 0; j < R; ++j) {
       const uint32_t at = 2 * ((uint32_t)t.row[j] * (uint32_t)p.y_row + n);
-      if (p.wide) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          y[j][i] = load16(from, t.has(j) && n + 8 * i < p.N ? at + 16 * i : kNowhere);
-      } else {
+      for (int i = 0; i < 2; ++i) {
+        if (p.wide) {
+          y[j][i] = load16(from, t.has(j) && n + 32 * i < p.N ? at + 64 * i : kNowhere);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t e0 = __builtin_amdgcn_raw_buffer_load_b16(
-              from, t.has(j) && n + 2 * i < p.N ? at + 4 * i : kNowhere, 0, 0);
-          const uint32_t e1 = __builtin_amdgcn_raw_buffer_load_b16(
-              from, t.has(j) && n + 2 * i + 1 < p.N ? at + 4 * i + 2 : kNowhere, 0, 0);
-          y[j][i / 4][i % 4] = (e0 & 0xFFFF) | (e1 << 16);
+          for (int e = 0; e < 4; ++e) {
+            const int m = n + 32 * i + 2 * e;
+            const uint32_t to = at + 64 * i + 4 * e;
+            const uint32_t e0 = __builtin_amdgcn_raw_buffer_load_b16(
+                from, t.has(j) && m < p.N ? to : kNowhere, 0, 0);
+            const uint32_t e1 = __builtin_amdgcn_raw_buffer_load_b16(
+                from, t.has(j) && m + 1 < p.N ? to + 2 : kNowhere, 0, 0);
+            y[j][i][e] = (e0 & 0xFFFF) | (e1 << 16);
+          }
         }
       }
     }
     if (t.adapter < 0) return;
     const __amdgpu_buffer_rsrc_t rows =
         buffer(p.b + (int64_t)t.adapter * p.N * p.rank, 2u * (uint32_t)p.N * (uint32_t)p.rank);
-    const uint32_t b_at =
-        2 * (uint32_t)(n0 + 16 * (col >> 2) + (col & 3)) * (uint32_t)p.rank + 16 * c;
+    const uint32_t b_at = 2 * (uint32_t)(n0 + 8 * (col >> 2) + (col & 3)) * (uint32_t)p.rank + 16 * c;
 #pragma unroll
     for (int s = 0; s < kSteps; ++s)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        b[s][i] = load16(rows, 32 * s + 8 * c < p.rank ? b_at + 64 * s + 8 * i * (uint32_t)p.rank
-                                                       : kNowhere);
+        b[s][i] = load16(rows, 32 * s + 8 * c < p.rank
+                                   ? b_at + 64 * s + (32 * (i / 2) + 4 * (i % 2)) * 2 * (uint32_t)p.rank
+                                   : kNowhere);
   }
 };
 
@@ -418,7 +477,7 @@ __device__ __forceinline__ void expand(const AdapterParams& p, const Tile<R>& t,
                                        const Columns<T, NB, R>& w, const Inner<T, NB> (&v)[R],
                                        int n0) {
   const int lane = threadIdx.x & 63, c = lane >> 4;
-  const int n = n0 + 16 * c;
+  const int n = n0 + 8 * c;
   const __amdgpu_buffer_rsrc_t to = buffer(p.out, p.out_bytes);
 #pragma unroll
   for (int j = 0; j < R; ++j) {
@@ -442,32 +501,35 @@ __device__ __forceinline__ void expand(const AdapterParams& p, const Tile<R>& t,
       }
     }
     const uint32_t at = 2 * ((uint32_t)t.row[j] * (uint32_t)p.out_row + n);
-    if (p.wide) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 2; ++i) {
+      if (p.wide) {
         __builtin_amdgcn_raw_buffer_store_b128(
-            r[i], to, t.has(j) && n + 8 * i < p.N ? at + 16 * i : kNowhere, 0, 0);
-    } else {
+            r[i], to, t.has(j) && n + 32 * i < p.N ? at + 64 * i : kNowhere, 0, 0);
+      } else {
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        __builtin_amdgcn_raw_buffer_store_b16((short)(r[i / 8][i / 2 % 4] >> (16 * (i % 2))), to,
-                                              t.has(j) && n + i < p.N ? at + 2 * i : kNowhere, 0,
-                                              0);
+        for (int e = 0; e < 8; ++e)
+          __builtin_amdgcn_raw_buffer_store_b16(
+              (short)(r[i][e / 2] >> (16 * (e % 2))), to,
+              t.has(j) && n + 32 * i + e < p.N ? at + 64 * i + 2 * e : kNowhere, 0, 0);
+      }
     }
   }
 }
 
-// Two turns of 64 columns to a wave; the workgroup sums the parts of t once.
+// Two turns of 64 columns to a wave; the workgroup sums the parts of t once. Workgroups
+// go to the eight XCDs in turn, the column blocks first: an XCD's L2 then holds its own
+// columns' part of B (4096 rows, N = 8192: 39 us with the tiles first, so 35).
 template <class T, int NB, int R>
 __global__ __launch_bounds__(kThreads) void expand_kernel(AdapterParams p) {
   constexpr int kPitch = 16 * NB + 4;
   __shared__ __attribute__((aligned(16))) float inner[16 * R * kPitch];
   __shared__ int row_of[16 * R];
   fetch(p);
-  const Tile<R> t = find_tile<R>(p, blockIdx.x);
+  const Tile<R> t = find_tile<R>(p, blockIdx.y);
   if (t.adapter == -2 || (t.adapter == -1 && p.in_place)) return;
   const int wave = uniform(threadIdx.x >> 6), col = threadIdx.x & 15;
-  const int n0 = ((int)blockIdx.y * 4 + wave) * kTurns * kTileCols;
+  const int n0 = ((int)blockIdx.x * 4 + wave) * kTurns * kTileCols;
   Columns<T, NB, R> w;
   if (n0 < p.N) w.load(p, t, n0);
   Inner<T, NB> v[R];
@@ -513,22 +575,26 @@ __global__ __launch_bounds__(kThreads) void expand_kernel(AdapterParams p) {
 // every workgroup again for its 1024 output columns. Reading A again for each of them costs less
 // than a second launch and the way of t through memory.
 
-template <class T, int NB>
+template <class T>
 __global__ __launch_bounds__(64 * kFusedWaves) void fused_kernel(AdapterParams p) {
-  constexpr int kPitch = 16 * NB + 4;
-  __shared__ __attribute__((aligned(16))) float sums[kFusedWaves * NB * 256];
+  constexpr int NB = 1, kPitch = 16 * NB + 4;
+  using S = Stage<NB, 1>;
+  __shared__ __attribute__((aligned(16))) char stage[kFusedWaves * S::kBytes];
   __shared__ __attribute__((aligned(16))) float inner[16 * kPitch];
   fetch(p);
-  const Tile<1> t = find_tile<1>(p, blockIdx.x);
+  const Tile<1> t = find_tile<1>(p, blockIdx.y);
   if (t.adapter == -2 || (t.adapter == -1 && p.in_place)) return;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  const int n0 = ((int)blockIdx.y * kFusedWaves + wave) * kTileCols;
+  const int n0 = ((int)blockIdx.x * kFusedWaves + wave) * kTileCols;
   Columns<T, NB, 1> w;
   if (n0 < p.N) w.load(p, t, n0);
   Inner<T, NB> v[1];
   if (t.adapter >= 0) {
     f4v acc[1][NB];
-    shrink<T, NB, 1>(p, t, kStepK * wave, p.K, kFusedWaves * kStepK, acc);
+    shrink<T, NB, 1>(p, t, S::kStep * wave, p.K, kFusedWaves * S::kStep, stage + wave * S::kBytes,
+                     acc);
+    __syncthreads();
+    float* sums = (float*)stage;
 #pragma unroll
     for (int i = 0; i < NB; ++i) *(f4v*)(sums + ((wave * NB + i) * 64 + lane) * 4) = acc[0][i];
     __syncthreads();
@@ -580,23 +646,24 @@ struct AdapterPlan {
 AdapterPlan plan(const lutgemm_adapters* l) {
   AdapterPlan r{};
   const int groups = l->adapters + 1 < l->rows ? l->adapters + 1 : l->rows;
-  // many rows to an adapter: two sets of sixteen in a tile share A and B (2048 rows of 3
-  // adapters of rank 64: 44 us against 55 to 72; 1000 rows of 10, rank 16: 25.5 against 27.7)
+  // many rows to an adapter: two sets of sixteen in a tile share A and B (4096 rows of 8
+  // adapters of rank 32: 63 us against 66; 1000 rows of 10, rank 16: 24.3 against 25.3)
   r.tile_rows = l->rows > kLaneRows && l->rows >= 32 * (l->adapters + 1) ? 32 : 16;
   r.tiles = l->rows / r.tile_rows + groups;
   if (r.tiles > l->rows) r.tiles = l->rows;
-  // fused_kernel reads A again for every 1024 columns. A compute unit gets about 25 GB/s, so
-  // up to 128 KB a workgroup and 16 MB in all that is the faster way (one row, K = N = 4096,
-  // rank 16: 8.3 us against 9.0; 32 rows of 16 adapters, N = 12288: 10.1 against 9.8)
+  // fused_kernel reads A again for every 1024 columns: with ranks up to 16, up to 128 KB a
+  // workgroup and 64 MB in all it is the faster way (K = N = 4096, one row: 5.6 us against 8.4; 32
+  // rows of 16 adapters, N = 12288, 30 MB: 8.3 against 9.9)
   const int64_t a_bytes = (int64_t)l->K * l->rank * 2;
   const int64_t blocks = (int64_t)r.tiles * ((l->N + 1023) / 1024);
-  r.fused = l->rows <= kLaneRows && l->rank <= 32 && a_bytes <= 128 << 10 &&
-            a_bytes * blocks <= 16 << 20;
+  r.fused = l->rows <= kLaneRows && l->rank <= 16 && a_bytes <= 128 << 10 &&
+            a_bytes * blocks <= 64 << 20;
   if (r.fused) return r;
   // enough workgroups to use every compute unit, twice with the larger tiles, each wave
   // with a full step at least
   const int fill = r.tile_rows == 32 ? 512 : 256;
   int splits = r.tiles > 0 ? (fill + r.tiles - 1) / r.tiles : 1;
+  constexpr int kStepK = 128;
   const int most = (l->K + 4 * kStepK - 1) / (4 * kStepK);
   if (splits > most) splits = most;
   if (splits > 16) splits = 16;
@@ -619,17 +686,17 @@ int run_tiles(const AdapterPlan& r, const AdapterParams& p, hipStream_t stream) 
   constexpr int cols = 4 * kTurns * kTileCols;
   if (!st)
     st = launch(expand_kernel<T, NB, R>,
-                dim3((unsigned)r.tiles, (unsigned)((p.N + cols - 1) / cols)), kThreads, p, stream);
+                dim3((unsigned)((p.N + cols - 1) / cols), (unsigned)r.tiles), kThreads, p, stream);
   return st;
 }
 
 template <class T, int NB>
 int run_adapters(const AdapterPlan& r, const AdapterParams& p, hipStream_t stream) {
-  if constexpr (NB <= 2)
+  if constexpr (NB == 1)
     if (r.fused) {
       constexpr int cols = kFusedWaves * kTileCols;
-      return launch(fused_kernel<T, NB>,
-                    dim3((unsigned)r.tiles, (unsigned)((p.N + cols - 1) / cols)),
+      return launch(fused_kernel<T>,
+                    dim3((unsigned)((p.N + cols - 1) / cols), (unsigned)r.tiles),
                     64 * kFusedWaves, p, stream);
     }
   if (p.rows > kLaneRows) {

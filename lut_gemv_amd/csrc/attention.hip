@@ -137,22 +137,11 @@ __device__ __forceinline__ int v_word(int row, int word) {
   return row * (2 * D) + (((word >> 1) ^ turn) << 5) + ((word & 1) << 4);
 }
 
-// 16 bytes a lane from memory to LDS, in lane order from `to` on (the same for the
-// wave). Buffer loads: while loads of the flat kind to LDS are under way the compiler
-// lets no LDS read overtake another.
-__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t from, uint32_t offset, char* to) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void*)to, 16,
-                                           offset, 0, 0, 0);
-}
-
 // The sixteen rows from `base` on, of `slot` elements' distance and D elements each.
 template <int D>
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t sixteen_rows(const uint16_t* base, int slot) {
   return __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, 30 * slot + 2 * D, 0x00027000);
 }
-
-// This wave's loads have arrived, in LDS too.
-__device__ __forceinline__ void wait_for_loads() { __builtin_amdgcn_s_waitcnt(0x0F70); }
 
 // ------------------------------------------------------------------- few rows
 //

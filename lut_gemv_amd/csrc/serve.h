@@ -91,6 +91,20 @@ __device__ __forceinline__ u2v read_column(const void* lds) {
       u2v, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4v*)(lds)));
 }
 
+// 16 bytes a lane from memory to LDS, in lane order from `to` on (the same for the
+// wave). Buffer loads: while loads of the flat kind to LDS are under way the compiler
+// lets no LDS read overtake another.
+__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t from, uint32_t offset, char* to) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void*)to, 16,
+                                           offset, 0, 0, 0);
+}
+
+// This wave's loads have arrived, in LDS too.
+__device__ __forceinline__ void wait_for_loads() { __builtin_amdgcn_s_waitcnt(0x0F70); }
+
+// This wave's LDS reads have returned.
+__device__ __forceinline__ void wait_for_lds() { __builtin_amdgcn_s_waitcnt(0xC07F); }
+
 // A kernel's parameters, asked for together at its start: they lie in host memory, and
 // fields first read where they are needed cost a trip there each.
 template <class P>
