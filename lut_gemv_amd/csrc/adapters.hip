@@ -631,6 +631,7 @@ int check_adapters(const lutgemm_adapters* l) {
   if (l->adapters < 0 || l->adapters > kMaxAdapters) return LUTGEMM_ERR_SHAPE;
   // the kernels address x, y and out with 32-bit offsets
   if (!stride_ok(l->x_row) || l->y_row < 0 || l->out_row < 0) return LUTGEMM_ERR_SHAPE;
+  if (l->rows > 1 && l->out_row < l->N) return LUTGEMM_ERR_SHAPE;  // output rows that overlap
   if (extent(l->rows, l->x_row, l->K) > kMostBytes || extent(l->rows, l->y_row, l->N) > kMostBytes ||
       extent(l->rows, l->out_row, l->N) > kMostBytes)
     return LUTGEMM_ERR_SHAPE;

@@ -10,6 +10,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
 #include <c10/hip/HIPGuard.h>
 #include <c10/hip/HIPStream.h>
@@ -68,6 +69,14 @@ int type_of(const at::Tensor& t, const char* what) {
   refuse(std::string(what) + " must be fp16 or bf16");
 }
 
+// The operators have no gradients: a graph that would silently end here is refused.
+void no_gradient(std::initializer_list<const at::Tensor*> inputs) {
+  if (!at::GradMode::is_enabled()) return;
+  for (const at::Tensor* t : inputs)
+    if (t->requires_grad())
+      refuse("the operator has no gradient: call it under torch.no_grad() or on detached tensors");
+}
+
 void on_gpu(const at::Tensor& t, const char* what) {
   if (!t.is_cuda()) refuse(std::string(what) + " must be on a GPU");
 }
@@ -117,6 +126,7 @@ PyObject* heads(PyObject* const* a) {
   h.type = type_of(qkv, "qkv");
   on_gpu(qkv, "qkv");
   like(qkv, qkv, 2, "qkv");
+  no_gradient({&qkv});
   h.heads = small(whole(a[1]), "heads");
   h.kv_heads = small(whole(a[2]), "kv_heads");
   const int64_t parts = (int64_t)h.heads + 2 * (int64_t)h.kv_heads;
@@ -144,7 +154,8 @@ PyObject* heads(PyObject* const* a) {
     kw = flat(tensor(a[6], "k_weight"), qkv.scalar_type(), qkv, {dim}, "k_weight");
   }
   h.eps = (float)real(a[7]);
-  h.interleaved = PyObject_IsTrue(a[8]) == 1;
+  h.interleaved = PyObject_IsTrue(a[8]);
+  if (h.interleaved < 0) throw Raised{};
   at::Tensor out;
   if (a[12] == Py_None) {
     out = at::empty({tokens, h.heads, dim}, qkv.options());
@@ -206,6 +217,7 @@ PyObject* attention(PyObject* const* a) {
   like(q, q, 3, "q");
   like(k, q, 4, "k_pages");
   like(v, q, 4, "v_pages");
+  no_gradient({&q, &k, &v});
   const int64_t tokens = q.size(0), heads = q.size(1), dim = q.size(2);
   if (k.size(3) != dim || k.sizes() != v.sizes())
     refuse("k_pages and v_pages must both be [pages][page_size][kv_heads][" + std::to_string(dim) +
@@ -276,6 +288,7 @@ PyObject* adapters(PyObject* const* a) {
   const int64_t rows = x.size(0), K = x.size(1), N = y.size(1);
   if (y.size(0) != rows) refuse("x and y must have the same rows");
   const at::Tensor& first = tensor(a[2], "a");
+  no_gradient({&x, &y, &first, &tensor(a[3], "b")});
   if (first.dim() != 3) refuse("a must be [adapters][rank][K]");
   const int64_t count = first.size(0), rank = first.size(1);
   const void* pa = flat(first, x.scalar_type(), x, {count, rank, K}, "a");

@@ -200,10 +200,19 @@ int check_heads(const lutgemm_heads* h, bool paged) {
   if (!stride_ok(h->qkv_token) || !stride_ok(h->q_token) || !stride_ok(h->k_page) ||
       !stride_ok(h->k_head))
     return LUTGEMM_ERR_SHAPE;
+  const int64_t dim = h->head_dim;
+  if (!serve::apart({{h->tokens, h->q_token}}, h->heads * dim)) return LUTGEMM_ERR_SHAPE;
+  if (!paged && !serve::apart({{h->tokens, h->k_page}, {h->kv_heads, h->k_head}}, dim))
+    return LUTGEMM_ERR_SHAPE;
   if (paged) {
     if (h->page_size < 1 || h->pages < 0 || h->pages >= ((int64_t)1 << 31)) return LUTGEMM_ERR_SHAPE;
     if (!stride_ok(h->k_slot) || !stride_ok(h->v_page) || !stride_ok(h->v_slot) ||
         !stride_ok(h->v_head))
+      return LUTGEMM_ERR_SHAPE;
+    if (!serve::apart({{h->pages, h->k_page}, {h->page_size, h->k_slot}, {h->kv_heads, h->k_head}},
+                      dim) ||
+        !serve::apart({{h->pages, h->v_page}, {h->page_size, h->v_slot}, {h->kv_heads, h->v_head}},
+                      dim))
       return LUTGEMM_ERR_SHAPE;
   }
   return LUTGEMM_OK;

@@ -24,6 +24,7 @@ typedef uint32_t u2v __attribute__((ext_vector_type(2)));
 typedef uint32_t u4v __attribute__((ext_vector_type(4)));
 typedef float f2v __attribute__((ext_vector_type(2)));
 typedef float f4v __attribute__((ext_vector_type(4)));
+typedef uint16_t us2v __attribute__((ext_vector_type(2)));
 typedef float f16v __attribute__((ext_vector_type(16)));
 
 // An element type: operands of the matrix cores travel as 16-byte words of eight
@@ -34,6 +35,7 @@ typedef float f16v __attribute__((ext_vector_type(16)));
 //             4 (lane / 16) + r, column lane % 16
 struct F16 {
   static constexpr bool kHalf = true;
+  static constexpr uint32_t kExponent = 0x7C00;  // all ones: infinity or NaN
   static __device__ __forceinline__ f16v mfma32(u4v a, u4v b, f16v c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, a),
                                                   __builtin_bit_cast(h8, b), c, 0, 0, 0);
@@ -60,6 +62,7 @@ struct F16 {
 
 struct BF16 {
   static constexpr bool kHalf = false;
+  static constexpr uint32_t kExponent = 0x7F80;
   static __device__ __forceinline__ f16v mfma32(u4v a, u4v b, f16v c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b8, a),
                                                    __builtin_bit_cast(b8, b), c, 0, 0, 0);
@@ -82,6 +85,36 @@ struct BF16 {
     return __builtin_bit_cast(float, (uint32_t)a << 16);
   }
 };
+
+// Whether one of these words' elements, two to a word, is an infinity or NaN: their
+// magnitudes are the largest.
+template <class T, int N>
+__device__ __forceinline__ bool any_non_finite(const u4v (&words)[N]) {
+  us2v most = {0, 0};
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      most = __builtin_elementwise_max(most, __builtin_bit_cast(us2v, words[j][e] & 0x7FFF7FFFu));
+  return most.x >= T::kExponent || most.y >= T::kExponent;
+}
+
+// The words with zeros in place of infinities and NaN.
+template <class T>
+__device__ __forceinline__ u4v finite(u4v words) {
+  constexpr uint32_t lo = T::kExponent, hi = T::kExponent << 16;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    words[e] &= ((words[e] & lo) == lo ? 0xFFFF0000u : ~0u) &
+                ((words[e] & hi) == hi ? 0xFFFFu : ~0u);
+  return words;
+}
+
+// `sum` with the infinity or NaN that an element may be.
+template <class T>
+__device__ __forceinline__ float with_non_finite(float sum, uint16_t element) {
+  return (element & T::kExponent) == T::kExponent ? sum + T::wide(element) : sum;
+}
 
 // Four elements of a column of LDS: the sixteen lanes of a group give the addresses
 // of a 4 x 16 block (lane i: row i / 4, columns 4 (i % 4) ..), and lane i receives
@@ -142,14 +175,37 @@ inline bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)
 
 inline bool stride_ok(int64_t s) { return s >= 0 && s % 8 == 0 && s < ((int64_t)1 << 40); }
 
+// One axis of an output: its length (below 2^32) and its stride in elements.
+struct Axis {
+  int64_t n, stride;
+};
+
+// Whether rows of `width` elements, addressed along N axes, lie apart from each other:
+// with the axes taken from the smallest stride up, each steps over all that is inside.
+template <int N>
+bool apart(Axis (&&axes)[N], int64_t width) {
+  __int128 inside = width;
+  for (int i = 0; i < N; ++i) {
+    int least = -1;
+    for (int j = 0; j < N; ++j)
+      if (axes[j].n > 1 && (least < 0 || axes[j].stride < axes[least].stride)) least = j;
+    if (least < 0) return true;
+    if (axes[least].stride < inside) return false;
+    inside += (__int128)(axes[least].n - 1) * axes[least].stride;
+    axes[least].n = 1;
+  }
+  return true;
+}
+
 template <class P>
 int launch(void (*kernel)(P), dim3 grid, int threads, const P& p, hipStream_t stream) {
   P copy = p;
   void* args[] = {&copy};
-  if (hipLaunchKernel((const void*)kernel, grid, dim3((unsigned)threads), args, 0, stream) !=
+  if (hipLaunchKernel((const void*)kernel, grid, dim3((unsigned)threads), args, 0, stream) ==
       hipSuccess)
-    return LUTGEMM_ERR_HIP;
-  return LUTGEMM_OK;
+    return LUTGEMM_OK;
+  (void)hipGetLastError();  // it is reported here, not by a later call
+  return LUTGEMM_ERR_HIP;
 }
 
 }  // namespace serve
