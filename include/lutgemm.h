@@ -379,8 +379,9 @@ typedef enum lutgemm_type { LUTGEMM_F16 = 0, LUTGEMM_BF16 = 1 } lutgemm_type;
  * where they are (pages, page_size, k_slot and the v strides are ignored).
  * Shape rules: 0 <= tokens < 2^24, heads and kv_heads from 1 to 65536, head_dim a
  * multiple of 16 up to 256, rotary a multiple of 16 up to head_dim (0: none),
- * page_size >= 1, eps >= 0 and finite; strides non-negative multiples of 8. Alignment: d_qkv, d_q, d_k, d_v,
- * weights and table 16 bytes, positions and slots 8. */
+ * page_size >= 1, eps >= 0 and finite; strides non-negative multiples of 8, and the
+ * strides of what is written keep its rows apart, one axis inside the other.
+ * Alignment: d_qkv, d_q, d_k, d_v, weights and table 16 bytes, positions and slots 8. */
 typedef struct lutgemm_heads {
   int32_t type, heads, kv_heads, head_dim;
   int32_t rotary, interleaved, page_size;
@@ -414,12 +415,11 @@ int lutgemm_qk_norm_rotate(const lutgemm_heads* h, const void* d_qkv, const int6
  *   d_q_starts  int32 [seqs + 1], non-decreasing, or NULL: one new token for each
  *               sequence (tokens == seqs). Output rows before q_starts[0] and from
  *               q_starts[seqs] on are left as they were.
- * A page number outside [0, pages) among those that a row's keys need, or a
- * kv_lens[s] larger than table_width * page_size, makes the rows of that sequence
- * that meet it NaN; a negative kv_lens[s] counts as 0. Slots past a sequence's last
- * key are not read, whatever they hold. A NaN or infinity among a sequence's
- * values can reach the rows whose masks exclude it; NaN and infinity among its
- * keys do not.
+ * A page number outside [0, pages) makes the rows NaN that need a key of it, and may
+ * make other rows of the sequence NaN; a kv_lens[s] larger than table_width *
+ * page_size makes all rows of the sequence NaN; a negative one counts as 0. Slots past
+ * a sequence's last key are not read, whatever they hold. A NaN or infinity among a
+ * sequence's keys or values reaches the rows that see it and no others.
  * max_q and max_kv say how many new tokens and keys the host expects one sequence
  * to have at most; the launch is chosen by them, results are right without them
  * being so. Results for the same sizes, max_q and max_kv are bitwise reproducible.
@@ -429,8 +429,11 @@ int lutgemm_qk_norm_rotate(const lutgemm_heads* h, const void* d_qkv, const int6
  *               must not share one.
  * Shape rules: head_dim 64 or 128; kv_heads >= 1 divides heads; page_size a power
  * of two from 16 to 65536; pages >= 1; 0 <= seqs < 2^20, 0 <= tokens < 2^24, heads
- * <= 1024, table_width >= 1 with table_width * page_size < 2^31; scale > 0 and
- * finite; window >= 0; strides non-negative multiples of 8, slot strides below 2^24.
+ * <= 1024, table_width >= 1 with table_width * page_size <= 2^30; scale > 0 and
+ * finite; window >= 0; strides non-negative multiples of 8, slot strides below 2^24,
+ * and the output's keep its rows apart, one axis inside the other. Calls too large for one grid (from about
+ * tokens * heads = 2^30 or seqs * kv_heads = 2^22 on) are refused with
+ * LUTGEMM_ERR_SHAPE.
  * Alignment: d_q, d_k, d_v, d_out and d_workspace 16 bytes, the int32 arrays 4. */
 typedef struct lutgemm_attention {
   int32_t type, heads, kv_heads, head_dim;
@@ -462,8 +465,9 @@ int lutgemm_paged_attention(const lutgemm_attention* a, const void* d_q, const v
  *   d_workspace  at least lutgemm_adapters_workspace bytes; as for attention.
  * Shape rules: 0 <= rows <= 65535, K a multiple of 8 below 2^23, N below 2^23, rank a
  * multiple of 8 from 8 to 128, 0 <= adapters <= 4096 (0: out = y); x_row a multiple
- * of 8; x, y and out less than 2 GiB each from their first element to the last. Alignment: d_x, d_a, d_b and d_workspace 16 bytes, d_ids and d_scales 4,
- * d_y and d_out 2. */
+ * of 8, out_row >= N; x, y and out less than 2 GiB each from their first element to the
+ * last. Alignment: d_x, d_a, d_b and d_workspace 16 bytes, d_ids and d_scales 4, d_y
+ * and d_out 2. */
 typedef struct lutgemm_adapters {
   int32_t type, rows, K, N;
   int32_t rank, adapters;

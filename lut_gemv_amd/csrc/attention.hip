@@ -26,6 +26,8 @@ using namespace serve;
 constexpr int kThreads = 256;
 constexpr int kFewRows = 16;
 constexpr int kFewWaves = 8;
+constexpr int kShortWaves = 2;    // few_kernel's for parts of up to kShortKeys keys
+constexpr int kShortKeys = 128;
 constexpr int kManyRows = 128;
 constexpr int kSplitKeys = 128;   // a part of the key axis is a multiple of this
 constexpr int kMaxSplits = 128;
@@ -49,6 +51,8 @@ struct AttnParams {
   int32_t few_rows;             // sequences of up to so many rows are few_rows'
   int32_t tiles;                // row tiles of many_rows, an upper bound
   int32_t few_blocks;           // mixed_kernel: the workgroups of its first kind
+  int32_t join_blocks;          // combine_kernel: likewise
+  int32_t join_rows;            // combine_few: workgroups to a sequence and key head
   float scale2;      // scale * log2(e)
 };
 
@@ -75,6 +79,11 @@ __device__ __forceinline__ Seq sequence(const AttnParams& p, int s) {
   return q;
 }
 
+// The first key that a row at this position sees.
+__device__ __forceinline__ int first_key(const AttnParams& p, int pos) {
+  return p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
+}
+
 // The keys [lo, hi) that rows r0 .. r1 - 1 of a sequence see between them, lo brought
 // down to a multiple of 64, and how they are split: parts of `chunk` keys each.
 struct Span {
@@ -86,8 +95,7 @@ __device__ __forceinline__ Span span_of(const AttnParams& p, const Seq& q, int r
   Span a;
   const int first = q.n - q.len + r0 / p.group, last = q.n - q.len + (r1 - 1) / p.group;
   a.hi = last + 1 < 0 ? 0 : last + 1;
-  int lo = p.window > 0 ? first - p.window + 1 : 0;
-  a.lo = lo < 0 ? 0 : lo & ~63;
+  a.lo = first_key(p, first) & ~63;
   const int keys = a.hi > a.lo ? a.hi - a.lo : 0;
   // a sequence longer than the launch was made for takes longer parts
   const int need = (keys + p.splits[Kind] - 1) / p.splits[Kind];
@@ -118,6 +126,19 @@ __device__ __forceinline__ int table_at(const AttnParams& p, int blk) {
 
 __device__ __forceinline__ int slot_of(const AttnParams& p, int blk) {
   return (blk & ((1 << (p.page_log2 - 4)) - 1)) << 4;
+}
+
+// What a workgroup met: a page outside the cache or more keys than the table holds;
+// infinities or NaN that were taken out of the values.
+constexpr int kBad = 1, kFound = 2;
+
+// Key k's value, for the seldom path that takes them one by one.
+template <class Row>
+__device__ __forceinline__ const uint16_t* value_at(const AttnParams& p, Row table, int k, int kvh,
+                                                    bool* bad) {
+  const int id = page_of(p, table[table_at(p, k >> 4)], bad);
+  return p.v + (int64_t)id * p.v_page + (int64_t)(slot_of(p, k >> 4) + (k & 15)) * p.v_slot +
+         kvh * p.v_head;
 }
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -187,7 +208,7 @@ __device__ __forceinline__ void few_load(const AttnParams& p, FewTile<D>& t, con
 template <int W>
 struct FewShared {
   float m[W][kFewRows], l[W][kFewRows];
-  int any_bad;
+  int marks;
 };
 
 template <class T, int D, int W, class Region>
@@ -210,7 +231,7 @@ __device__ __forceinline__ void few_rows(const AttnParams& p, int block, Region 
     if (split >= span.parts) continue;
     const int from = span.lo + split * span.chunk;
     const int to = min_of(span.hi, from + span.chunk);
-    if (threadIdx.x == 0) shared.any_bad = seq.bad;
+    if (threadIdx.x == 0) shared.marks = seq.bad ? kBad : 0;
     __syncthreads();
 
     // this lane's row: its query operand and the keys [row_lo, row_hi) it sees
@@ -219,7 +240,7 @@ __device__ __forceinline__ void few_rows(const AttnParams& p, int block, Region 
     const int tok = rc / p.group, head = kvh * p.group + rc % p.group;
     const int pos = seq.n - seq.len + tok;
     const int row_hi = r < r1 ? pos + 1 : 0;
-    const int row_lo = p.window > 0 ? pos - p.window + 1 : 0;
+    const int row_lo = first_key(p, pos);
     u4v q[D / 32];
     {
       const uint16_t* qp = p.q + (int64_t)(seq.begin + tok) * p.q_token + head * p.q_head + 8 * c;
@@ -230,7 +251,13 @@ __device__ __forceinline__ void few_rows(const AttnParams& p, int block, Region 
 #pragma unroll
     for (int d = 0; d < D / 16; ++d) o[d] = f4v{0.f, 0.f, 0.f, 0.f};
     float m = -INFINITY, l = 0.f;
-    bool bad = false;
+    bool bad = false, found = false;
+    // Values that some row of the tile may not see must be finite in the product, where a
+    // hidden one is multiplied by zero: infinities and NaN among them are taken out here
+    // and added at the end to the rows that see them.
+    const int all_hi = seq.n - seq.len + r0 / p.group + 1;
+    const int all_lo = first_key(p, seq.n - seq.len + (r1 - 1) / p.group);
+    auto partly = [&](int kt) { return 32 * kt + 32 > all_hi || 32 * kt < all_lo; };
     char* keys = region(wave);
     char* vals = keys + 32 * D * 2;
     FewTile<D> t;
@@ -248,6 +275,11 @@ __device__ __forceinline__ void few_rows(const AttnParams& p, int block, Region 
     }
     for (; kt < end; kt += W) {
       constexpr int words = D / 8, vr = 64 / words;
+      if (partly(kt) && __any(any_non_finite<T>(t.v))) {
+        found = true;
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) t.v[j] = finite<T>(t.v[j]);
+      }
 #pragma unroll
       for (int j = 0; j < D / 16; ++j) {
         *(u4v*)(keys + k_word<D>(vr * j + lane / words, lane % words)) = t.k[j];
@@ -317,7 +349,8 @@ __device__ __forceinline__ void few_rows(const AttnParams& p, int block, Region 
     // join the waves
     l += __shfl_xor(l, 16, 64);
     l += __shfl_xor(l, 32, 64);
-    if (bad && lane == 0) shared.any_bad = 1;
+    const int marks = (__any(bad) ? kBad : 0) | (found ? kFound : 0);
+    if (marks && lane == 0) atomicOr(&shared.marks, marks);
     if (c == 0) {
       shared.m[wave][lane] = m;
       shared.l[wave][lane] = l;
@@ -342,8 +375,17 @@ __device__ __forceinline__ void few_rows(const AttnParams& p, int block, Region 
         for (int e = 0; e < E; ++e)
           sum[e] += ((const float*)region(w))[jr * kPitch + jc + e] * f[w];
       }
-      if (shared.any_bad) total = __builtin_nanf("");
+      if (shared.marks & kBad) total = __builtin_nanf("");
       const int token = seq.begin + (r0 + jr) / p.group, hd = kvh * p.group + (r0 + jr) % p.group;
+      if (shared.marks & kFound) {
+        const int at = seq.n - seq.len + (r0 + jr) / p.group;
+        for (int k = from; k < to; ++k) {
+          if (!partly(k >> 5) || k > at || k < first_key(p, at)) continue;
+          const uint16_t* v = value_at(p, table, k, kvh, &bad) + jc;
+#pragma unroll
+          for (int e = 0; e < E; ++e) sum[e] = with_non_finite<T>(sum[e], v[e]);
+        }
+      }
       if (span.parts == 1) {
         const float inv = total == 0.f ? 0.f : 1.f / total;
         uint32_t* to32 = (uint32_t*)(p.out + (int64_t)token * p.o_token + hd * p.o_head + jc);
@@ -360,11 +402,12 @@ __device__ __forceinline__ void few_rows(const AttnParams& p, int block, Region 
   }
 }
 
-template <class T, int D>
-__global__ __launch_bounds__(64 * kFewWaves, 2) void few_kernel(AttnParams p) {
-  __shared__ __attribute__((aligned(16))) char mem[kFewWaves * 64 * D * 2];
-  __shared__ FewShared<kFewWaves> shared;
-  few_rows<T, D, kFewWaves>(p, blockIdx.x, [&](int w) { return mem + w * (64 * D * 2); }, shared);
+template <class T, int D, int W>
+__global__ __launch_bounds__(64 * W, 2) void few_kernel(AttnParams p) {
+  __shared__ __attribute__((aligned(16))) char mem[W * 64 * D * 2];
+  __shared__ FewShared<W> shared;
+  fetch(p);
+  few_rows<T, D, W>(p, blockIdx.x, [&](int w) { return mem + w * (64 * D * 2); }, shared);
 }
 
 // ------------------------------------------------------------------ many rows
@@ -382,7 +425,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void few_kernel(AttnParams p) {
 
 template <class T, int D>
 __device__ __forceinline__ void many_rows(const AttnParams& p, int block, char* keys0, char* vals0,
-                                          char* keys1, char* vals1, int& any_bad) {
+                                          char* keys1, char* vals1, int& marks) {
   const int kvh = block % p.kv_heads;
   const int nth = block / p.kv_heads % p.tiles, split = block / p.kv_heads / p.tiles;
   const int tile = p.tiles - 1 - nth;  // the longest rows first
@@ -412,7 +455,7 @@ __device__ __forceinline__ void many_rows(const AttnParams& p, int block, char* 
   const int from = span.lo + split * span.chunk;
   const int to = min_of(span.hi, from + span.chunk);
   const int32_t* table = p.table + s * p.table_stride;
-  if (threadIdx.x == 0) any_bad = seq.bad;
+  if (threadIdx.x == 0) marks = seq.bad ? kBad : 0;
 
   // this lane's row, and the wave's rows together
   const int w0 = r0 + 32 * wave, r = w0 + (lane & 31);
@@ -420,12 +463,12 @@ __device__ __forceinline__ void many_rows(const AttnParams& p, int block, char* 
   const int tok = rc / p.group, head = kvh * p.group + rc % p.group;
   const int pos = seq.n - seq.len + tok;
   const int row_hi = pos + 1;
-  const int row_lo = p.window > 0 ? pos - p.window + 1 : 0;
+  const int row_lo = first_key(p, pos);
   const int first = uniform(seq.n - seq.len + min_of(w0, r1 - 1) / p.group);
   const int last = uniform(seq.n - seq.len + min_of(w0 + 31, r1 - 1) / p.group);
   // the keys that every row of the wave sees
   const int all_hi = first + 1;
-  const int all_lo = p.window > 0 ? last - p.window + 1 : 0;
+  const int all_lo = first_key(p, last);
   u4v q[D / 16];
   {
     const uint16_t* qp = p.q + (int64_t)(seq.begin + tok) * p.q_token + head * p.q_head + 8 * h;
@@ -543,6 +586,23 @@ __device__ __forceinline__ void many_rows(const AttnParams& p, int block, char* 
 
   const int begin = from >> 6, end = (to + 63) >> 6;
   constexpr int kHalf = 32 * D * 2;
+  // As in few_rows: of a tile that not every row of the workgroup sees whole, infinities
+  // and NaN are taken out of the values before the products, by the lanes that brought
+  // them and before the barrier that hands the tile over.
+  const int group_hi = seq.n - seq.len + r0 / p.group + 1;
+  const int group_lo = first_key(p, seq.n - seq.len + (r1 - 1) / p.group);
+  auto partly = [&](int kt) { return 64 * kt + 64 > group_hi || 64 * kt < group_lo; };
+  auto clean = [&](int kt, char* vals) {
+    if (!partly(kt)) return;
+    u4v* const mine = (u4v*)(vals + 16 * wave * 2 * D) + lane;
+    u4v w[kLoads];
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) w[j] = mine[64 * j];
+    if (!__any(any_non_finite<T>(w))) return;
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) mine[64 * j] = finite<T>(w[j]);
+    if (lane == 0) atomicOr(&marks, kFound);
+  };
   if (begin < end) {
     read_ids(begin);
     load_keys(begin - 1, keys1);
@@ -553,6 +613,7 @@ __device__ __forceinline__ void many_rows(const AttnParams& p, int block, char* 
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) asm volatile("" : "+v"(q[ks]));
     wait_for_loads();
+    clean(begin, vals0);
     __syncthreads();
     if (w0 < r1) {
       f16v s0, s1;
@@ -571,6 +632,7 @@ __device__ __forceinline__ void many_rows(const AttnParams& p, int block, char* 
         weigh(s1, vals + kHalf);
         settle(s0, 64 * kt + 64);
         wait_for_loads();
+        clean(kt + 1, next_vals);
         __syncthreads();
       };
       auto last = [&](int kt, char* keys, char* vals) {
@@ -597,17 +659,29 @@ __device__ __forceinline__ void many_rows(const AttnParams& p, int block, char* 
         load_keys(kt + 1, even ? keys1 : keys0);
         load_values(kt + 1, even ? vals1 : vals0);
         wait_for_loads();
+        clean(kt + 1, even ? vals1 : vals0);
         __syncthreads();
       }
     }
   } else {
     __syncthreads();
   }
-  if (bad && lane == 0) any_bad = 1;
+  if (__any(bad) && lane == 0) atomicOr(&marks, kBad);
   __syncthreads();
   if (r >= r1) return;
   l += __shfl_xor(l, 32, 64);
-  if (any_bad) l = __builtin_nanf("");
+  if (marks & kFound) {
+    for (int k = from; k < to; ++k) {
+      if (!partly(k >> 6) || k >= row_hi || k < row_lo) continue;
+      const uint16_t* v = value_at(p, table, k, kvh, &bad) + 4 * h;
+#pragma unroll
+      for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          o[d][e] = with_non_finite<T>(o[d][e], v[32 * d + 8 * (e >> 2) + (e & 3)]);
+    }
+  }
+  if (marks & kBad) l = __builtin_nanf("");
   const int token = seq.begin + tok;
   if (span.parts == 1) {
     const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -635,8 +709,9 @@ template <class T, int D>
 __global__ __launch_bounds__(kThreads, 2) void many_kernel(AttnParams p) {
   constexpr int kTile = 64 * D * 2;
   __shared__ __attribute__((aligned(16))) char keys0[kTile], vals0[kTile], keys1[kTile], vals1[kTile];
-  __shared__ int any_bad;
-  many_rows<T, D>(p, blockIdx.x, keys0, vals0, keys1, vals1, any_bad);
+  __shared__ int marks;
+  fetch(p);
+  many_rows<T, D>(p, blockIdx.x, keys0, vals0, keys1, vals1, marks);
 }
 
 // A batch with sequences of both kinds in one launch: the reading of the one runs
@@ -646,26 +721,33 @@ __global__ __launch_bounds__(kThreads, 2) void mixed_kernel(AttnParams p) {
   constexpr int kTile = 64 * D * 2;
   __shared__ __attribute__((aligned(16))) char keys0[kTile], vals0[kTile], keys1[kTile], vals1[kTile];
   __shared__ FewShared<kThreads / 64> shared;
+  fetch(p);
   if ((int)blockIdx.x < p.few_blocks)
     few_rows<T, D, kThreads / 64>(
         p, blockIdx.x,
         [&](int w) { return w == 0 ? keys0 : w == 1 ? vals0 : w == 2 ? keys1 : vals1; }, shared);
   else
-    many_rows<T, D>(p, blockIdx.x - p.few_blocks, keys0, vals0, keys1, vals1, shared.any_bad);
+    many_rows<T, D>(p, blockIdx.x - p.few_blocks, keys0, vals0, keys1, vals1, shared.marks);
 }
 
 // -------------------------------------------------------------- joining parts
 //
 // One wave for each row that was split: the parts' sums brought to one maximum. The
-// lanes read the parts' maxima together, and four parts' sums are under way at a time.
+// lanes read the parts' maxima together, and the sums of kAhead parts are under way with them.
 
 template <class T, int D>
 __device__ __forceinline__ void combine_row(const AttnParams& p, int parts, int token, int head) {
-  constexpr int E = D / 64;
+  constexpr int E = D / 64, kAhead = 16;
   typedef float fE __attribute__((ext_vector_type(E)));
   const int lane = threadIdx.x & 63;
   const int64_t row = (int64_t)token * p.heads + head, step = (int64_t)p.tokens * p.heads;
   const float* from = p.part_o + row * D + lane * E;
+  fE o[kAhead];
+  auto read = [&](int j) {  // parts past the last one are the last again
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) o[i] = *(const fE*)(from + min_of(j + i, parts - 1) * step * D);
+  };
+  read(0);
   float top = -INFINITY, total = 0.f;
   fE sum = {};
   for (int j0 = 0; j0 < parts; j0 += 64) {
@@ -685,14 +767,12 @@ __device__ __forceinline__ void combine_row(const AttnParams& p, int parts, int 
     total = total * old + l;
     sum *= old;
     const int n = min_of(parts - j0, 64);
-    for (int j = 0; j < n; j += 4) {
-      fE o[4];
+    for (int j = 0; j < n; j += kAhead) {
+      if (j0 + j) read(j0 + j);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = *(const fE*)(from + (j0 + min_of(j + i, n - 1)) * step * D);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float w = j + i < n ? __shfl(f, j + i, 64) : 0.f;
-        sum += o[i] * w;
+      for (int i = 0; i < kAhead; ++i) {
+        const float w = __shfl(f, j + i, 64);
+        if (j + i < n) sum += o[i] * w;
       }
     }
   }
@@ -706,13 +786,14 @@ __device__ __forceinline__ void combine_row(const AttnParams& p, int parts, int 
 
 // few_rows' rows: four of one sequence and key head at a time.
 template <class T, int D>
-__global__ __launch_bounds__(kThreads) void combine_few_kernel(AttnParams p) {
-  const int s = blockIdx.x / p.kv_heads, kvh = blockIdx.x % p.kv_heads;
+__device__ __forceinline__ void combine_few(const AttnParams& p, int block) {
+  const int first = block % p.join_rows;
+  const int s = block / p.join_rows / p.kv_heads, kvh = block / p.join_rows % p.kv_heads;
   const Seq seq = sequence(p, s);
   const int rows = seq.len * p.group;
   if (rows > p.few_rows) return;
   const int wave = uniform(threadIdx.x >> 6);
-  for (int r = blockIdx.y * 4 + wave; r < rows; r += 4 * gridDim.y) {
+  for (int r = first * 4 + wave; r < rows; r += 4 * p.join_rows) {
     const int r0 = r / kFewRows * kFewRows;
     const Span span = span_of<0>(p, seq, r0, min_of(r0 + kFewRows, rows));
     if (span.parts > 1)
@@ -722,9 +803,9 @@ __global__ __launch_bounds__(kThreads) void combine_few_kernel(AttnParams p) {
 
 // many_rows' rows: one wave each.
 template <class T, int D>
-__global__ __launch_bounds__(kThreads) void combine_many_kernel(AttnParams p) {
+__device__ __forceinline__ void combine_many(const AttnParams& p, int block) {
   const int lane = threadIdx.x & 63;
-  const int64_t row = (int64_t)blockIdx.x * 4 + uniform(threadIdx.x >> 6);
+  const int64_t row = (int64_t)block * 4 + uniform(threadIdx.x >> 6);
   if (row >= (int64_t)p.tokens * p.heads) return;
   const int token = (int)(row / p.heads), head = (int)(row % p.heads);
   int s = token;
@@ -747,6 +828,15 @@ __global__ __launch_bounds__(kThreads) void combine_many_kernel(AttnParams p) {
   if (span.parts > 1) combine_row<T, D>(p, span.parts, token, head);
 }
 
+template <class T, int D>
+__global__ __launch_bounds__(kThreads) void combine_kernel(AttnParams p) {
+  fetch(p);
+  if ((int)blockIdx.x < p.join_blocks)
+    combine_few<T, D>(p, blockIdx.x);
+  else
+    combine_many<T, D>(p, blockIdx.x - p.join_blocks);
+}
+
 // ------------------------------------------------------------------ host side
 
 int check_attention(const lutgemm_attention* a) {
@@ -759,7 +849,7 @@ int check_attention(const lutgemm_attention* a) {
     return LUTGEMM_ERR_SHAPE;
   if (a->seqs < 0 || a->seqs >= (1 << 20) || a->tokens < 0 || a->tokens >= (1 << 24))
     return LUTGEMM_ERR_SHAPE;
-  if (a->table_width < 1 || (int64_t)a->table_width * a->page_size >= ((int64_t)1 << 31) - 128 ||
+  if (a->table_width < 1 || (int64_t)a->table_width * a->page_size > ((int64_t)1 << 30) ||
       a->table_stride < 0 || a->table_stride >= ((int64_t)1 << 40))
     return LUTGEMM_ERR_SHAPE;
   if (a->pages < 1 || a->pages >= ((int64_t)1 << 31)) return LUTGEMM_ERR_SHAPE;
@@ -771,6 +861,8 @@ int check_attention(const lutgemm_attention* a) {
       !stride_ok(a->v_head))
     return LUTGEMM_ERR_SHAPE;
   if (a->k_slot >= (1 << 24) || a->v_slot >= (1 << 24)) return LUTGEMM_ERR_SHAPE;
+  if (!serve::apart({{a->tokens, a->o_token}, {a->heads, a->o_head}}, a->head_dim))
+    return LUTGEMM_ERR_SHAPE;
   return LUTGEMM_OK;
 }
 
@@ -807,7 +899,7 @@ AttnPlan plan(const lutgemm_attention* a) {
   if (a->window > 0 && keys > a->window + max_q + 64) keys = a->window + max_q + 64;
   if (keys < 1) keys = 1;
   r.many = max_q * group > kFewRows;
-  r.few = !r.many || a->seqs > 1;
+  r.few = !r.many || (a->seqs > 1 && group <= kFewRows);  // a token alone has `group` rows
   r.tiles = a->tokens * group / kManyRows + a->seqs;
   // Workgroups to fill the card with: few_kernel's are one to a compute unit, and four
   // rounds of them even out sequences of different lengths (48 of 800 .. 8000 keys: 164 us;
@@ -835,15 +927,14 @@ int run_attention(const AttnPlan& r, const AttnParams& p, hipStream_t stream) {
   else if (r.many)
     st = launch(many_kernel<T, D>, dim3((unsigned)many), kThreads, p, stream);
   else
-    st = launch(few_kernel<T, D>, dim3((unsigned)few), 64 * kFewWaves, p, stream);
-  if (!st && r.many && r.splits[1] > 1)
-    st = launch(combine_many_kernel<T, D>,
-                dim3((unsigned)(((int64_t)p.tokens * p.heads + 3) / 4)), kThreads, p, stream);
-  if (!st && r.few && r.splits[0] > 1)
-    st = launch(combine_few_kernel<T, D>,
-                dim3((unsigned)(p.seqs * p.kv_heads),
-                     (unsigned)(r.many || p.group >= kFewRows ? kFewRows / 4 : (p.group + 3) / 4)),
-                kThreads, p, stream);
+    // short parts leave most of eight waves idle, and their LDS keeps other workgroups from
+    // the compute unit (39 x 32 heads of up to 50 keys: 23.4 us, with two waves 9.8)
+    st = r.chunk[0] <= kShortKeys
+             ? launch(few_kernel<T, D, kShortWaves>, dim3((unsigned)few), 64 * kShortWaves, p, stream)
+             : launch(few_kernel<T, D, kFewWaves>, dim3((unsigned)few), 64 * kFewWaves, p, stream);
+  const int64_t joined = r.many && r.splits[1] > 1 ? ((int64_t)p.tokens * p.heads + 3) / 4 : 0;
+  if (!st && p.join_blocks + joined > 0)
+    st = launch(combine_kernel<T, D>, dim3((unsigned)(p.join_blocks + joined)), kThreads, p, stream);
   return st;
 }
 
@@ -878,8 +969,9 @@ extern "C" int lutgemm_paged_attention(const lutgemm_attention* a, const void* d
     // a launch has fewer than 2^32 threads along each axis of its grid
     constexpr int64_t kMost = (int64_t)1 << 24;
     const int64_t few = (int64_t)a->seqs * r.splits[0] * a->kv_heads;
-    if (r.tiles * a->kv_heads * r.splits[1] + few >= kMost / 2 ||
-        (r.splits[1] > 1 && a->tokens * a->heads / 4 + 1 >= kMost))
+    const int64_t joined = (r.splits[0] > 1 ? (int64_t)a->seqs * a->kv_heads * 4 : 0) +
+                           (r.splits[1] > 1 ? a->tokens * a->heads / 4 + 1 : 0);
+    if (r.tiles * a->kv_heads * r.splits[1] + few >= kMost / 2 || joined >= kMost)
       return LUTGEMM_ERR_SHAPE;
     if (r.ws_bytes) {
       if (!d_workspace) return LUTGEMM_ERR_NULL;
@@ -926,6 +1018,8 @@ extern "C" int lutgemm_paged_attention(const lutgemm_attention* a, const void* d
       p.chunk[i] = r.chunk[i];
     }
     p.few_blocks = (int32_t)few;
+    p.join_rows = r.many || p.group >= kFewRows ? kFewRows / 4 : (p.group + 3) / 4;
+    p.join_blocks = r.few && r.splits[0] > 1 ? a->seqs * a->kv_heads * p.join_rows : 0;
     p.few_rows = !r.many ? 0x7FFFFFFF : r.few ? kFewRows : 0;
     p.tiles = (int32_t)r.tiles;
     p.scale2 = a->scale * 1.4426950408889634f;

@@ -218,6 +218,78 @@ def test_attention_non_finite_keys_stay_behind_the_mask():
     assert torch.isfinite(got[:row]).all() and torch.isnan(got[row:]).all()
 
 
+@pytest.mark.parametrize("dtype,heads,kv_heads,dim", [(F16, 4, 2, 128), (BF16, 3, 1, 64)])
+@pytest.mark.parametrize("lens,news,window", [
+    ([200], [100], 0), ([200, 90], [5, 4], 0), ([200, 190], [1, 1], 40), ([4000], [40], 0),
+    ([300, 280, 150], [130, 1, 3], 50), ([2200, 700], [3, 1], 90),
+])
+def test_attention_non_finite_values_stay_behind_the_mask(dtype, heads, kv_heads, dim, lens, news,
+                                                          window):
+    """NaN and infinities among the values reach the rows that see them, in their own
+    columns, and no others. The first two lie at the first new token and one before it
+    (rows see the last keys, windows only some), the third before the window."""
+    b = Batch(dtype, heads, kv_heads, dim, 16, lens, news, seed=21)
+    marks = []
+    for i, (n, new) in enumerate(zip(lens, news)):
+        first = n - new
+        for key, col, value in ((first + new // 2, 5, NAN), (first, 18, float("inf")),
+                                (max(first - window - 1, 0), dim - 1, float("-inf"))):
+            b.v_pages[int(b.table[i, key // 16]), key % 16, :, col] = value
+            b.v[i][key, :, col] = 0
+            marks.append((i, key, col, value))
+    got = b.call(window=window)
+    at = np.concatenate([[0], np.cumsum(news)])
+    seen = torch.zeros(got.shape, dtype=torch.bool, device=DEV)
+    for i, key, col, value in marks:
+        for t in range(news[i]):
+            pos = lens[i] - news[i] + t
+            if key <= pos and (not window or key > pos - window):
+                seen[at[i] + t, :, col] = True
+                mine = got[at[i] + t, :, col]
+                assert (torch.isnan(mine) if value != value else mine == value).all(), (i, t, col)
+    assert seen.any() and not seen.all()
+    assert torch.isfinite(got[~seen]).all()
+    b.check(_patched(b, got, seen, window), "the rest", window=window)
+
+
+def _patched(b, got, seen, window):
+    """`got` with the exact values in the marked places."""
+    got, at = got.clone(), 0
+    for i, (n, new) in enumerate(zip(b.lens, b.news)):
+        want, _ = plain.attention(_np(b.q[at:at + new]), _np(b.k[i]), _np(b.v[i]), new, n,
+                                  b.dim ** -0.5, window, U[b.dtype])
+        want = torch.from_numpy(want).to(got)
+        got[at:at + new] = torch.where(seen[at:at + new], want, got[at:at + new])
+        at += new
+    return got
+
+
+def test_operators_refuse_tensors_that_need_gradients():
+    """The operators have no backward pass: a graph is not cut without a word."""
+    b = Batch(F16, 4, 2, 64, 16, [20], [1], seed=22)
+    b.q.requires_grad_()
+    with pytest.raises(ValueError, match="no gradient"):
+        b.call()
+    with torch.no_grad():
+        b.check(b.call(), "without gradients")
+    qkv, table, positions, _ = _heads_case(F16, 3, 2, 1, 64, 64, False, False)
+    with pytest.raises(ValueError, match="no gradient"):
+        lg.qk_norm_rotate(qkv.requires_grad_(), 2, 1, positions, table)
+    y, x, a, w, ids, scales = _adapters_case(F16, 2, 64, 40, 8, 2, [0, 1])
+    with pytest.raises(ValueError, match="no gradient"):
+        lg.adapters_add(y, x, a.requires_grad_(), w, ids, scales)
+
+
+def test_outputs_that_overlap_are_refused():
+    b = Batch(F16, 4, 2, 64, 16, [20, 20], [1, 1], seed=23)
+    with pytest.raises(lg.LutGemmError):
+        b.call(out=torch.zeros((1, 4, 64), dtype=F16, device=DEV).expand(2, 4, 64))
+    with pytest.raises(lg.LutGemmError):
+        b.call(out=torch.zeros((2, 1, 64), dtype=F16, device=DEV).expand(2, 4, 64))
+    turned = torch.zeros((4, 2, 64), dtype=F16, device=DEV).transpose(0, 1)
+    b.check(b.call(out=turned), "heads outside tokens")
+
+
 def test_attention_far_pages():
     """Pages more than 2^32 bytes, and 2^31 elements, into the cache."""
     pages = (1 << 31) // (64 * 8 * 128) + 40

@@ -57,6 +57,23 @@ def test_attention_refusals(change, status):
     assert _attention(**change) == status
 
 
+@pytest.mark.parametrize("call,change", [
+    ("attention", dict(o_token=0)), ("attention", dict(o_head=0)), ("attention", dict(o_head=120)),
+    ("attention", dict(o_token=128)), ("attention", dict(o_token=1016)),
+    ("heads", dict(q_token=0)), ("heads", dict(q_token=248)), ("heads", dict(k_head=0)),
+    ("heads", dict(k_slot=64)), ("heads", dict(v_page=0)), ("heads", dict(v_slot=120)),
+    ("adapters", dict(out_row=0)), ("adapters", dict(out_row=39)),
+])
+def test_outputs_that_overlap_are_refused(call, change):
+    assert {"attention": _attention, "heads": _heads, "adapters": _adapters}[call](**change) == SHAPE
+
+
+def test_attention_positions_stay_in_32_bits():
+    """Tables of up to 2^30 keys: a position, a window and a tile past them add up."""
+    assert _attention(q=None, table_width=1 << 26) == NULL
+    assert _attention(q=None, table_width=(1 << 26) + 1) == SHAPE
+
+
 def test_attention_empty_calls_and_workspace():
     assert _attention(tokens=0) == 0 and _attention(tokens=0, seqs=0, starts=None) == 0
     L = lg.lib()
