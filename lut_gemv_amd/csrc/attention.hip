@@ -50,7 +50,7 @@ struct AttnParams {
   int32_t splits[2], chunk[2];  // of few_rows and of many_rows
   int32_t few_rows;             // sequences of up to so many rows are few_rows'
   int32_t tiles;                // row tiles of many_rows, an upper bound
-  int32_t few_blocks;           // mixed_kernel: the workgroups of its first kind
+  int32_t many_blocks;          // mixed_kernel: the workgroups of its first kind
   int32_t join_blocks;          // combine_kernel: likewise
   int32_t join_rows;            // combine_few: workgroups to a sequence and key head
   float scale2;      // scale * log2(e)
@@ -423,17 +423,34 @@ __global__ __launch_bounds__(64 * W, 2) void few_kernel(AttnParams p) {
 // their own, so that the compiler sees that a load into one and a read of the other
 // need not wait for each other.
 
-template <class T, int D>
-__device__ __forceinline__ void many_rows(const AttnParams& p, int block, char* keys0, char* vals0,
-                                          char* keys1, char* vals1, int& marks) {
-  const int kvh = block % p.kv_heads;
-  const int nth = block / p.kv_heads % p.tiles, split = block / p.kv_heads / p.tiles;
-  const int tile = p.tiles - 1 - nth;  // the longest rows first
-  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  const int h = lane >> 5;
+// The nth row tile in the order in which they start: the sequence and the first row.
+// Long sequences first, and each from its last rows, so that no long tile begins when
+// the others end (10 chunks of 253 tokens x 32 heads on 820 .. 4099 keys beside 6
+// single tokens: 114 us in the sequences' order, 108 so). More sequences than
+// lanes are taken from the last to the first.
+struct RowTile {
+  int s, r0;  // s < 0: there is no such tile
+};
 
-  // the sequence of this row tile: tiles of sequence s begin at start * group / 128 + s,
-  // which leaves each at least as many as its rows need
+__device__ __forceinline__ RowTile row_tile(const AttnParams& p, int nth, int lane) {
+  if (p.seqs <= 64) {
+    const Seq q = sequence(p, min_of(lane, p.seqs - 1));
+    const int rows = lane < p.seqs && q.len * p.group > p.few_rows ? q.len * p.group : 0;
+    const int tiles = (rows + kManyRows - 1) / kManyRows;
+    int before = 0;
+    for (int s = 0; s < p.seqs; ++s) {
+      const int n = __builtin_amdgcn_readlane(q.n, s);
+      if (n > q.n || (n == q.n && s < lane)) before += __builtin_amdgcn_readlane(tiles, s);
+    }
+    const uint64_t mine = __ballot(nth >= before && nth < before + tiles);
+    if (!mine) return {-1, 0};
+    const int s = __builtin_ctzll(mine);
+    const int left = __builtin_amdgcn_readlane(before + tiles, s) - 1 - nth;
+    return {s, left * kManyRows};
+  }
+  // tiles of sequence s begin at start * group / 128 + s, which leaves each at least as
+  // many as its rows need
+  const int tile = p.tiles - 1 - nth;
   int found = 0;
   for (int s0 = 0; s0 < p.seqs; s0 += 64) {
     const bool begun = s0 + lane < p.seqs &&
@@ -442,13 +459,25 @@ __device__ __forceinline__ void many_rows(const AttnParams& p, int block, char* 
     found += __popcll(votes);
     if (votes != ~0ull) break;
   }
-  if (found == 0) return;
   const int s = uniform(found - 1);
+  if (s < 0) return {-1, 0};
+  return {s, (tile - (int)((int64_t)start_of(p, s) * p.group / kManyRows) - s) * kManyRows};
+}
+
+template <class T, int D>
+__device__ __forceinline__ void many_rows(const AttnParams& p, int block, char* keys0, char* vals0,
+                                          char* keys1, char* vals1, int& marks) {
+  const int kvh = block % p.kv_heads;
+  const int nth = block / p.kv_heads % p.tiles, split = block / p.kv_heads / p.tiles;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int h = lane >> 5;
+
+  const RowTile at = row_tile(p, nth, lane);
+  if (at.s < 0) return;
+  const int s = at.s, r0 = at.r0;
   const Seq seq = sequence(p, s);
   const int rows = seq.len * p.group;
-  if (rows <= p.few_rows) return;
-  const int r0 = (tile - (int)((int64_t)seq.begin * p.group / kManyRows) - s) * kManyRows;
-  if (r0 < 0 || r0 >= rows) return;
+  if (rows <= p.few_rows || r0 < 0 || r0 >= rows) return;
   const int r1 = min_of(r0 + kManyRows, rows);
   const Span span = span_of<1>(p, seq, r0, r1);
   if (split >= span.parts) return;
@@ -722,17 +751,18 @@ __global__ __launch_bounds__(kThreads, 2) void mixed_kernel(AttnParams p) {
   __shared__ __attribute__((aligned(16))) char keys0[kTile], vals0[kTile], keys1[kTile], vals1[kTile];
   __shared__ FewShared<kThreads / 64> shared;
   fetch(p);
-  if ((int)blockIdx.x < p.few_blocks)
-    few_rows<T, D, kThreads / 64>(
-        p, blockIdx.x,
-        [&](int w) { return w == 0 ? keys0 : w == 1 ? vals0 : w == 2 ? keys1 : vals1; }, shared);
+  const int block = (int)blockIdx.x - p.many_blocks;
+  if (block < 0)
+    many_rows<T, D>(p, blockIdx.x, keys0, vals0, keys1, vals1, shared.marks);
   else
-    many_rows<T, D>(p, blockIdx.x - p.few_blocks, keys0, vals0, keys1, vals1, shared.marks);
+    few_rows<T, D, kThreads / 64>(
+        p, block,
+        [&](int w) { return w == 0 ? keys0 : w == 1 ? vals0 : w == 2 ? keys1 : vals1; }, shared);
 }
 
 // -------------------------------------------------------------- joining parts
 //
-// One wave for each row that was split: the parts' sums brought to one maximum. The
+// The parts' sums of a row brought to one maximum. Here by one wave for each row: the
 // lanes read the parts' maxima together, and the sums of kAhead parts are under way with them.
 
 template <class T, int D>
@@ -801,31 +831,63 @@ __device__ __forceinline__ void combine_few(const AttnParams& p, int block) {
   }
 }
 
-// many_rows' rows: one wave each.
+// many_rows' rows, kJoinRows of one row tile and key head: all have as many parts, and
+// D / 4 lanes join a row. (One wave to a row, which looked for its sequence by itself: 25
+// us for 1002 tokens x 32 heads in two parts; 10 us so.)
+constexpr int kJoinRows = 32;
+
 template <class T, int D>
 __device__ __forceinline__ void combine_many(const AttnParams& p, int block) {
-  const int lane = threadIdx.x & 63;
-  const int64_t row = (int64_t)block * 4 + uniform(threadIdx.x >> 6);
-  if (row >= (int64_t)p.tokens * p.heads) return;
-  const int token = (int)(row / p.heads), head = (int)(row % p.heads);
-  int s = token;
-  if (p.q_starts) {
-    s = 0;
-    for (int s0 = 0; s0 < p.seqs; s0 += 64) {
-      const uint64_t votes =
-          __ballot(s0 + lane < p.seqs && start_of(p, s0 + lane + 1) <= token);
-      s += __popcll(votes);
-      if (votes != ~0ull) break;
-    }
-    s = uniform(s);
-    if (s >= p.seqs) return;
-  }
-  const Seq seq = sequence(p, s);
+  constexpr int G = D / 4, kAhead = 4;
+  const int kvh = block % p.kv_heads, sub = block / p.kv_heads % (kManyRows / kJoinRows);
+  const RowTile at = row_tile(p, block / p.kv_heads / (kManyRows / kJoinRows), threadIdx.x & 63);
+  if (at.s < 0) return;
+  const Seq seq = sequence(p, at.s);
   const int rows = seq.len * p.group;
-  if (token < seq.begin || token >= seq.begin + seq.len || rows <= p.few_rows) return;
-  const int r0 = ((token - seq.begin) * p.group + head % p.group) / kManyRows * kManyRows;
-  const Span span = span_of<1>(p, seq, r0, min_of(r0 + kManyRows, rows));
-  if (span.parts > 1) combine_row<T, D>(p, span.parts, token, head);
+  if (rows <= p.few_rows || at.r0 < 0 || at.r0 >= rows) return;
+  const int end = min_of(at.r0 + kManyRows, rows);
+  const int parts = span_of<1>(p, seq, at.r0, end).parts;
+  if (parts == 1) return;
+  const int64_t step = (int64_t)p.tokens * p.heads;
+  const int c = threadIdx.x % G, first = at.r0 + sub * kJoinRows;
+  for (int r = first + threadIdx.x / G; r < min_of(first + kJoinRows, end); r += kThreads / G) {
+    const int token = seq.begin + r / p.group, head = kvh * p.group + r % p.group;
+    const int64_t row = (int64_t)token * p.heads + head;
+    const f2v* const ml = (const f2v*)p.part_ml + row;
+    const f4v* const from = (const f4v*)(p.part_o + row * D) + c;
+    f4v o[kAhead];
+    float m[kAhead];
+    auto read = [&](int j) {  // parts past the last one are the last again
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int64_t part = min_of(j + i, parts - 1) * step;
+        m[i] = ml[part].x;
+        o[i] = from[part * G];
+      }
+    };
+    read(0);
+    float top = -INFINITY, total = 0.f;
+    for (int i = c; i < parts; i += G) top = fmaxf(top, ml[i * step].x);
+#pragma unroll
+    for (int d = 1; d < G; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
+    auto weight = [&](float m) { return m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - top); };
+    for (int i = c; i < parts; i += G) {
+      const f2v x = ml[i * step];
+      total += x.y != x.y ? x.y : x.y * weight(x.x);  // NaN marks a part that met a bad page
+    }
+#pragma unroll
+    for (int d = 1; d < G; d <<= 1) total += __shfl_xor(total, d, 64);
+    f4v sum = {};
+    for (int j = 0; j < parts; j += kAhead) {
+      if (j) read(j);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (j + i < parts) sum += o[i] * weight(m[i]);
+    }
+    sum *= total == 0.f ? 0.f : 1.f / total;
+    *(u2v*)(p.out + (int64_t)token * p.o_token + head * p.o_head + 4 * c) =
+        u2v{T::pack(sum[0], sum[1]), T::pack(sum[2], sum[3])};
+  }
 }
 
 template <class T, int D>
@@ -903,8 +965,10 @@ AttnPlan plan(const lutgemm_attention* a) {
   r.tiles = a->tokens * group / kManyRows + a->seqs;
   // Workgroups to fill the card with: few_kernel's are one to a compute unit, and four
   // rounds of them even out sequences of different lengths (48 of 800 .. 8000 keys: 164 us;
-  // one round 181, two 181, twelve 181); beside many_kernel's two rounds are enough.
-  split_keys(keys, (int64_t)a->seqs * a->kv_heads, r.many ? 512 : 1024, 512, &r.splits[0],
+  // one round 181, two 181, twelve 181). Beside many_rows' they start last and short parts
+  // fill what the long tiles leave (row_tile's batch: in one part 106 us, in three 98);
+  // that batch's own tiles in two parts take 120 us.
+  split_keys(keys, (int64_t)a->seqs * a->kv_heads, r.many ? 1536 : 1024, 512, &r.splits[0],
              &r.chunk[0]);
   split_keys(keys, (a->tokens * group / kManyRows + (a->seqs + 1) / 2) * a->kv_heads, 512, 512,
              &r.splits[1], &r.chunk[1]);
@@ -932,7 +996,7 @@ int run_attention(const AttnPlan& r, const AttnParams& p, hipStream_t stream) {
     st = r.chunk[0] <= kShortKeys
              ? launch(few_kernel<T, D, kShortWaves>, dim3((unsigned)few), 64 * kShortWaves, p, stream)
              : launch(few_kernel<T, D, kFewWaves>, dim3((unsigned)few), 64 * kFewWaves, p, stream);
-  const int64_t joined = r.many && r.splits[1] > 1 ? ((int64_t)p.tokens * p.heads + 3) / 4 : 0;
+  const int64_t joined = r.splits[1] > 1 ? r.tiles * p.kv_heads * (kManyRows / kJoinRows) : 0;
   if (!st && p.join_blocks + joined > 0)
     st = launch(combine_kernel<T, D>, dim3((unsigned)(p.join_blocks + joined)), kThreads, p, stream);
   return st;
@@ -970,7 +1034,7 @@ extern "C" int lutgemm_paged_attention(const lutgemm_attention* a, const void* d
     constexpr int64_t kMost = (int64_t)1 << 24;
     const int64_t few = (int64_t)a->seqs * r.splits[0] * a->kv_heads;
     const int64_t joined = (r.splits[0] > 1 ? (int64_t)a->seqs * a->kv_heads * 4 : 0) +
-                           (r.splits[1] > 1 ? a->tokens * a->heads / 4 + 1 : 0);
+                           (r.splits[1] > 1 ? r.tiles * a->kv_heads * (kManyRows / kJoinRows) : 0);
     if (r.tiles * a->kv_heads * r.splits[1] + few >= kMost / 2 || joined >= kMost)
       return LUTGEMM_ERR_SHAPE;
     if (r.ws_bytes) {
@@ -1017,7 +1081,7 @@ extern "C" int lutgemm_paged_attention(const lutgemm_attention* a, const void* d
       p.splits[i] = r.splits[i];
       p.chunk[i] = r.chunk[i];
     }
-    p.few_blocks = (int32_t)few;
+    p.many_blocks = (int32_t)(r.tiles * a->kv_heads * r.splits[1]);
     p.join_rows = r.many || p.group >= kFewRows ? kFewRows / 4 : (p.group + 3) / 4;
     p.join_blocks = r.few && r.splits[0] > 1 ? a->seqs * a->kv_heads * p.join_rows : 0;
     p.few_rows = !r.many ? 0x7FFFFFFF : r.few ? kFewRows : 0;

@@ -152,6 +152,18 @@ def test_attention_one_long_chunk_split():
     b.check(b.call(), "17 of 3000 beside one of 2500")
 
 
+@pytest.mark.parametrize("heads,kv_heads,dim", [(4, 2, 64), (8, 1, 128)])
+def test_attention_more_sequences_than_lanes(heads, kv_heads, dim):
+    """Row tiles are found otherwise from 65 sequences on; long ones among them are split."""
+    rng = np.random.default_rng(3)
+    news = [int(rng.choice([0, 1, 1, 3, 20, 70])) for _ in range(131)]
+    lens = [n + int(rng.integers(0, 90)) for n in news]
+    lens[5], news[5], lens[100], news[100] = 1700, 150, 2600, 1
+    lens[64], news[64], lens[130], news[130] = 1300, 33, 1100, 129
+    b = Batch(F16, heads, kv_heads, dim, 16, lens, news, seed=24)
+    b.check(b.call(), "131 sequences")
+
+
 def test_attention_large_and_small_scores():
     """Scores of some hundreds, where one key takes all the weight, and a small scale."""
     b = Batch(F16, 8, 2, 128, 16, [900, 33], [20, 1], seed=7, scale=4.0)
