@@ -375,8 +375,35 @@ __global__ __launch_bounds__(kThreads) void shrink_kernel(AdapterParams p) {
 //
 // 64 output columns to a wave at a time. Row i of column block k's operand is output
 // column 32 (k / 2) + 8 (i / 4) + 4 (k % 2) + i % 4, so a lane's results are twice eight
-// consecutive columns of its row, and four lanes' together 64 bytes of y and out. y and B are
-// read before t is needed.
+// consecutive columns of its row, and four lanes' together 64 bytes of y and out. Lanes of
+// neighbouring rows exchange halves, so that a load or store moves 128 bytes of a row
+// (4096 rows, K = N = 8192, rank 32: 63.0 us, so 60.5). y and B are read before t is needed.
+
+// The neighbouring lane's v.
+__device__ __forceinline__ uint32_t neighbour(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true);
+}
+
+// From a lane's two halves of its own row to the two rows of a pair of lanes, half
+// lane % 2 of each, and back.
+__device__ __forceinline__ void exchange(u4v (&w)[2]) {
+  const bool odd = threadIdx.x & 1;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t got = neighbour(odd ? w[0][e] : w[1][e]);
+    w[0][e] = odd ? got : w[0][e];
+    w[1][e] = odd ? w[1][e] : got;
+  }
+}
+
+// Where column n of row i of this pair of lanes is in y or out.
+template <int R>
+__device__ __forceinline__ uint32_t place(const Tile<R>& t, int j, int i, int n, int row_step,
+                                          int N) {
+  const int odd = threadIdx.x & 1, row = (int)neighbour((uint32_t)t.row[j]);
+  const bool in = 16 * j + (int)(threadIdx.x & 14) + i < t.count && n < N;
+  return in ? 2 * ((uint32_t)(i == odd ? t.row[j] : row) * (uint32_t)row_step + n) : kNowhere;
+}
 
 template <class T, int NB, int R>
 struct Columns {
@@ -385,26 +412,28 @@ struct Columns {
 
   __device__ __forceinline__ void load(const AdapterParams& p, const Tile<R>& t, int n0) {
     const int lane = threadIdx.x & 63, c = lane >> 4, col = lane & 15;
-    const int n = n0 + 8 * c;
+    const int n = n0 + 8 * c, odd = lane & 1;
     const __amdgpu_buffer_rsrc_t from = buffer(p.y, p.y_bytes);
 #pragma unroll
     for (int j = 0; j < R; ++j) {
+      if (p.wide) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          y[j][i] = load16(from, place(t, j, i, n + 32 * odd, p.y_row, p.N));
+        continue;
+      }
       const uint32_t at = 2 * ((uint32_t)t.row[j] * (uint32_t)p.y_row + n);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        if (p.wide) {
-          y[j][i] = load16(from, t.has(j) && n + 32 * i < p.N ? at + 64 * i : kNowhere);
-        } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int m = n + 32 * i + 2 * e;
-            const uint32_t to = at + 64 * i + 4 * e;
-            const uint32_t e0 = __builtin_amdgcn_raw_buffer_load_b16(
-                from, t.has(j) && m < p.N ? to : kNowhere, 0, 0);
-            const uint32_t e1 = __builtin_amdgcn_raw_buffer_load_b16(
-                from, t.has(j) && m + 1 < p.N ? to + 2 : kNowhere, 0, 0);
-            y[j][i][e] = (e0 & 0xFFFF) | (e1 << 16);
-          }
+        for (int e = 0; e < 4; ++e) {
+          const int m = n + 32 * i + 2 * e;
+          const uint32_t to = at + 64 * i + 4 * e;
+          const uint32_t e0 = __builtin_amdgcn_raw_buffer_load_b16(
+              from, t.has(j) && m < p.N ? to : kNowhere, 0, 0);
+          const uint32_t e1 = __builtin_amdgcn_raw_buffer_load_b16(
+              from, t.has(j) && m + 1 < p.N ? to + 2 : kNowhere, 0, 0);
+          y[j][i][e] = (e0 & 0xFFFF) | (e1 << 16);
         }
       }
     }
@@ -485,6 +514,7 @@ __device__ __forceinline__ void expand(const AdapterParams& p, const Tile<R>& t,
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[i] = f4v{0.f, 0.f, 0.f, 0.f};
     u4v r[2] = {w.y[j][0], w.y[j][1]};
+    if (p.wide) exchange(r);
     if (t.adapter >= 0) {
 #pragma unroll
       for (int s = 0; s < Inner<T, NB>::kSteps; ++s)
@@ -500,20 +530,22 @@ __device__ __forceinline__ void expand(const AdapterParams& p, const Tile<R>& t,
                                   f.y + acc[i / 2][2 * (i % 2) + 1] * v[j].factor);
       }
     }
+    if (p.wide) {
+      exchange(r);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        __builtin_amdgcn_raw_buffer_store_b128(
+            r[i], to, place(t, j, i, n + 32 * (lane & 1), p.out_row, p.N), 0, 0);
+      continue;
+    }
     const uint32_t at = 2 * ((uint32_t)t.row[j] * (uint32_t)p.out_row + n);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (p.wide) {
-        __builtin_amdgcn_raw_buffer_store_b128(
-            r[i], to, t.has(j) && n + 32 * i < p.N ? at + 64 * i : kNowhere, 0, 0);
-      } else {
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          __builtin_amdgcn_raw_buffer_store_b16(
-              (short)(r[i][e / 2] >> (16 * (e % 2))), to,
-              t.has(j) && n + 32 * i + e < p.N ? at + 64 * i + 2 * e : kNowhere, 0, 0);
-      }
-    }
+      for (int e = 0; e < 8; ++e)
+        __builtin_amdgcn_raw_buffer_store_b16(
+            (short)(r[i][e / 2] >> (16 * (e % 2))), to,
+            t.has(j) && n + 32 * i + e < p.N ? at + 64 * i + 2 * e : kNowhere, 0, 0);
   }
 }
 
