@@ -373,7 +373,7 @@ typedef enum lutgemm_type { LUTGEMM_F16 = 0, LUTGEMM_BF16 = 1 } lutgemm_type;
  *   d_slots  int64 [tokens]: the token's key and value go to slot
  *            slots[t] % page_size of page slots[t] / page_size; a slot outside
  *            [0, pages * page_size) writes neither. Two tokens with one slot
- *            leave either one's key and either one's value there.
+ *            leave there some entries of the one and some of the other.
  * With d_slots NULL there is no cache: d_k is [tokens][kv_heads][head_dim] with
  * token stride k_page and head stride k_head, d_v is not used and the values stay
  * where they are (pages, page_size, k_slot and the v strides are ignored).

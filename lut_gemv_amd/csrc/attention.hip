@@ -41,8 +41,9 @@ struct AttnParams {
   const int32_t* kv_lens;
   const int32_t* q_starts;
   uint16_t* out;
-  float* part_o;  // [split][token][head][dim], the parts' sums, not yet divided
-  float* part_ml;  // [split][token][head][2], their maximum and sum of weights
+  float* part_o;  // [part row][dim], the parts' sums, not yet divided
+  float* part_ml;  // [part row][2], their maximum and sum of weights
+  int64_t few_step, many_step, many_at;  // part rows of one split; where many_rows' begin
   int64_t table_stride, q_token, q_head, o_token, o_head;
   int64_t k_page, k_head, v_page, v_head;
   int32_t k_slot, v_slot;
@@ -98,11 +99,19 @@ __device__ __forceinline__ Span span_of(const AttnParams& p, const Seq& q, int r
   a.lo = first_key(p, first) & ~63;
   const int keys = a.hi > a.lo ? a.hi - a.lo : 0;
   // a sequence longer than the launch was made for takes longer parts
-  const int need = (keys + p.splits[Kind] - 1) / p.splits[Kind];
+  int need = (keys + p.splits[Kind] - 1) / p.splits[Kind];
+  // few_rows has room for the parts of so many rows; a longer chunk, which a launch made
+  // for short ones meets, is not split
+  if (Kind == 0 && q.len * p.group > kFewRows) need = keys;
   a.chunk = need > p.chunk[Kind] ? (need + kSplitKeys - 1) / kSplitKeys * kSplitKeys
                                  : p.chunk[Kind];
   a.parts = keys > a.chunk ? (keys + a.chunk - 1) / a.chunk : 1;
   return a;
+}
+
+// The part row of split 0 of row r of a sequence's key head in few_rows.
+__device__ __forceinline__ int64_t few_part(const AttnParams& p, int s, int kvh, int r) {
+  return ((int64_t)s * p.kv_heads + kvh) * kFewRows + r;
 }
 
 // A row of the page table, read by scalar loads: they do not wait in turn behind the
@@ -392,7 +401,7 @@ __device__ __forceinline__ void few_rows(const AttnParams& p, int block, Region 
 #pragma unroll
         for (int e = 0; e < E / 2; ++e) to32[e] = T::pack(sum[2 * e] * inv, sum[2 * e + 1] * inv);
       } else {
-        const int64_t at = ((int64_t)split * p.tokens + token) * p.heads + hd;
+        const int64_t at = split * p.few_step + few_part(p, s, kvh, r0 + jr);
 #pragma unroll
         for (int e = 0; e < E; ++e) p.part_o[at * D + jc + e] = sum[e];
         if (jc == 0) *(f2v*)(p.part_ml + 2 * at) = f2v{top, total};
@@ -722,7 +731,7 @@ __device__ __forceinline__ void many_rows(const AttnParams& p, int block, char* 
         *(u2v*)(dst + 32 * d + 8 * e) = u2v{T::pack(o[d][4 * e] * inv, o[d][4 * e + 1] * inv),
                                             T::pack(o[d][4 * e + 2] * inv, o[d][4 * e + 3] * inv)};
   } else {
-    const int64_t at = ((int64_t)split * p.tokens + token) * p.heads + head;
+    const int64_t at = p.many_at + split * p.many_step + (int64_t)token * p.heads + head;
     float* dst = p.part_o + at * D + 4 * h;
 #pragma unroll
     for (int d = 0; d < D / 32; ++d)
@@ -766,11 +775,12 @@ __global__ __launch_bounds__(kThreads, 2) void mixed_kernel(AttnParams p) {
 // lanes read the parts' maxima together, and the sums of kAhead parts are under way with them.
 
 template <class T, int D>
-__device__ __forceinline__ void combine_row(const AttnParams& p, int parts, int token, int head) {
+__device__ __forceinline__ void combine_row(const AttnParams& p, int parts, int64_t row, int token,
+                                            int head) {
   constexpr int E = D / 64, kAhead = 16;
   typedef float fE __attribute__((ext_vector_type(E)));
   const int lane = threadIdx.x & 63;
-  const int64_t row = (int64_t)token * p.heads + head, step = (int64_t)p.tokens * p.heads;
+  const int64_t step = p.few_step;
   const float* from = p.part_o + row * D + lane * E;
   fE o[kAhead];
   auto read = [&](int j) {  // parts past the last one are the last again
@@ -826,8 +836,9 @@ __device__ __forceinline__ void combine_few(const AttnParams& p, int block) {
   for (int r = first * 4 + wave; r < rows; r += 4 * p.join_rows) {
     const int r0 = r / kFewRows * kFewRows;
     const Span span = span_of<0>(p, seq, r0, min_of(r0 + kFewRows, rows));
+    const int token = seq.begin + r / p.group, head = kvh * p.group + r % p.group;
     if (span.parts > 1)
-      combine_row<T, D>(p, span.parts, seq.begin + r / p.group, kvh * p.group + r % p.group);
+      combine_row<T, D>(p, span.parts, few_part(p, s, kvh, r), token, head);
   }
 }
 
@@ -848,11 +859,11 @@ __device__ __forceinline__ void combine_many(const AttnParams& p, int block) {
   const int end = min_of(at.r0 + kManyRows, rows);
   const int parts = span_of<1>(p, seq, at.r0, end).parts;
   if (parts == 1) return;
-  const int64_t step = (int64_t)p.tokens * p.heads;
+  const int64_t step = p.many_step;
   const int c = threadIdx.x % G, first = at.r0 + sub * kJoinRows;
   for (int r = first + threadIdx.x / G; r < min_of(first + kJoinRows, end); r += kThreads / G) {
     const int token = seq.begin + r / p.group, head = kvh * p.group + r % p.group;
-    const int64_t row = (int64_t)token * p.heads + head;
+    const int64_t row = p.many_at + (int64_t)token * p.heads + head;
     const f2v* const ml = (const f2v*)p.part_ml + row;
     const f4v* const from = (const f4v*)(p.part_o + row * D) + c;
     f4v o[kAhead];
@@ -932,6 +943,7 @@ struct AttnPlan {
   bool few, many;
   int splits[2], chunk[2];
   int64_t tiles;
+  int64_t few_step, part_rows;  // part rows of one of few_rows' splits, and all of them
   size_t ws_bytes;
 };
 
@@ -974,10 +986,10 @@ AttnPlan plan(const lutgemm_attention* a) {
              &r.splits[1], &r.chunk[1]);
   if (!r.few) r.splits[0] = 1;
   if (!r.many) r.splits[1] = 1;
-  const int most = r.splits[0] > r.splits[1] ? r.splits[0] : r.splits[1];
-  if (most > 1)
-    r.ws_bytes = (size_t)most * (size_t)a->tokens * (size_t)a->heads *
-                 (size_t)(a->head_dim + 2) * sizeof(float);
+  const int64_t rows = a->tokens * a->heads;
+  r.few_step = r.splits[0] > 1 ? (int64_t)a->seqs * a->kv_heads * kFewRows : 0;
+  r.part_rows = r.splits[0] * r.few_step + (r.splits[1] > 1 ? r.splits[1] * rows : 0);
+  r.ws_bytes = (size_t)r.part_rows * (size_t)(a->head_dim + 2) * sizeof(float);
   return r;
 }
 
@@ -1054,9 +1066,10 @@ extern "C" int lutgemm_paged_attention(const lutgemm_attention* a, const void* d
     p.q_starts = d_q_starts;
     p.out = (uint16_t*)d_out;
     p.part_o = (float*)d_workspace;
-    p.part_ml = r.ws_bytes ? (float*)d_workspace +
-                                 r.ws_bytes / sizeof(float) / (a->head_dim + 2) * a->head_dim
-                           : nullptr;
+    p.part_ml = r.ws_bytes ? (float*)d_workspace + r.part_rows * a->head_dim : nullptr;
+    p.few_step = r.few_step;
+    p.many_step = a->tokens * a->heads;
+    p.many_at = r.splits[0] * r.few_step;
     p.table_stride = a->table_stride;
     p.q_token = a->q_token;
     p.q_head = a->q_head;

@@ -70,10 +70,10 @@ int type_of(const at::Tensor& t, const char* what) {
 }
 
 // The operators have no gradients: a graph that would silently end here is refused.
-void no_gradient(std::initializer_list<const at::Tensor*> inputs) {
+void no_gradient(PyObject* const* args, int n) {
   if (!at::GradMode::is_enabled()) return;
-  for (const at::Tensor* t : inputs)
-    if (t->requires_grad())
+  for (int i = 0; i < n; ++i)
+    if (THPVariable_Check(args[i]) && THPVariable_Unpack(args[i]).requires_grad())
       refuse("the operator has no gradient: call it under torch.no_grad() or on detached tensors");
 }
 
@@ -126,7 +126,6 @@ PyObject* heads(PyObject* const* a) {
   h.type = type_of(qkv, "qkv");
   on_gpu(qkv, "qkv");
   like(qkv, qkv, 2, "qkv");
-  no_gradient({&qkv});
   h.heads = small(whole(a[1]), "heads");
   h.kv_heads = small(whole(a[2]), "kv_heads");
   const int64_t parts = (int64_t)h.heads + 2 * (int64_t)h.kv_heads;
@@ -217,7 +216,6 @@ PyObject* attention(PyObject* const* a) {
   like(q, q, 3, "q");
   like(k, q, 4, "k_pages");
   like(v, q, 4, "v_pages");
-  no_gradient({&q, &k, &v});
   const int64_t tokens = q.size(0), heads = q.size(1), dim = q.size(2);
   if (k.size(3) != dim || k.sizes() != v.sizes())
     refuse("k_pages and v_pages must both be [pages][page_size][kv_heads][" + std::to_string(dim) +
@@ -288,7 +286,6 @@ PyObject* adapters(PyObject* const* a) {
   const int64_t rows = x.size(0), K = x.size(1), N = y.size(1);
   if (y.size(0) != rows) refuse("x and y must have the same rows");
   const at::Tensor& first = tensor(a[2], "a");
-  no_gradient({&x, &y, &first, &tensor(a[3], "b")});
   if (first.dim() != 3) refuse("a must be [adapters][rank][K]");
   const int64_t count = first.size(0), rank = first.size(1);
   const void* pa = flat(first, x.scalar_type(), x, {count, rank, K}, "a");
@@ -337,6 +334,7 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return nullptr;
   }
   try {
+    no_gradient(args, N);
     return F(args);
   } catch (const Refused& e) {
     PyErr_SetString(PyExc_ValueError, e.what());

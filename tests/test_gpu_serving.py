@@ -292,6 +292,33 @@ def test_operators_refuse_tensors_that_need_gradients():
         lg.adapters_add(y, x, a.requires_grad_(), w, ids, scales)
 
 
+@pytest.mark.parametrize("which", ["q_weight", "out", "scales", "k_pages"])
+def test_operators_refuse_any_tensor_that_needs_gradients(which):
+    b = Batch(F16, 4, 2, 64, 16, [20], [1], seed=25)
+    qkv, table, positions, w = _heads_case(F16, 3, 2, 1, 64, 64, False, True)
+    y, x, a, up, ids, scales = _adapters_case(F16, 2, 64, 40, 8, 2, [0, 1])
+    with pytest.raises(ValueError, match="no gradient"):
+        if which == "q_weight":
+            lg.qk_norm_rotate(qkv, 2, 1, positions, table, w[0].requires_grad_(), w[1])
+        elif which == "out":
+            b.call(out=torch.zeros_like(b.q).requires_grad_())
+        elif which == "scales":
+            lg.adapters_add(y, x, a, up, ids, scales.requires_grad_())
+        else:
+            b.k_pages.requires_grad_()
+            b.call()
+
+
+def test_attention_padded_batch():
+    """Rows behind the last sequence, in a batch much larger than its tokens, with the hints of
+    a decode step, split and not."""
+    for lens in ([3000, 40, 900], [50, 60, 20]):
+        b = Batch(F16, 8, 2, 128, 16, lens, [1, 1, 1], seed=26, lead=5, tail=200)
+        out = torch.full_like(b.q, 3.0)
+        b.check(b.call(max_q=1, max_kv=3000, out=out), "padded")
+        assert (out[:5] == 3).all() and (out[8:] == 3).all()
+
+
 def test_outputs_that_overlap_are_refused():
     b = Batch(F16, 4, 2, 64, 16, [20, 20], [1, 1], seed=23)
     with pytest.raises(lg.LutGemmError):

@@ -74,6 +74,20 @@ def test_attention_positions_stay_in_32_bits():
     assert _attention(q=None, table_width=(1 << 26) + 1) == SHAPE
 
 
+@pytest.mark.parametrize("change", [
+    dict(seqs=16, tokens=8192, heads=64, kv_heads=8, max_q=8000),   # chunks beside single tokens
+    dict(seqs=16, tokens=8192, heads=64, kv_heads=8, max_q=1),      # a padded batch, or a wrong bound
+    dict(seqs=1, tokens=1, heads=128, kv_heads=1, max_q=1),
+    dict(seqs=1, tokens=300, heads=8, kv_heads=1, max_q=300),
+])
+def test_attention_workspace_stays_small(change):
+    """Room for the parts of the rows that can be split, not for every row of the batch."""
+    n = ctypes.c_size_t()
+    d = _ATTENTION.pack(*{**ATT, "max_kv": 1 << 20, "table_width": 1 << 16, "o_token": 1 << 14, **change}.values())
+    assert lg.lib().lutgemm_paged_attention_workspace(d, ctypes.byref(n)) == 0
+    assert 0 < n.value < 80 << 20
+
+
 def test_attention_empty_calls_and_workspace():
     assert _attention(tokens=0) == 0 and _attention(tokens=0, seqs=0, starts=None) == 0
     L = lg.lib()
