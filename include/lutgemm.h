@@ -431,9 +431,9 @@ int lutgemm_qk_norm_rotate(const lutgemm_heads* h, const void* d_qkv, const int6
  * of two from 16 to 65536; pages >= 1; 0 <= seqs < 2^20, 0 <= tokens < 2^24, heads
  * <= 1024, table_width >= 1 with table_width * page_size <= 2^30; scale > 0 and
  * finite; window >= 0; strides non-negative multiples of 8, slot strides below 2^24,
- * and the output's keep its rows apart, one axis inside the other. Calls too large for one grid (from about
- * tokens * heads = 2^30 or seqs * kv_heads = 2^22 on) are refused with
- * LUTGEMM_ERR_SHAPE.
+ * and the output's keep its rows apart, one axis inside the other. Calls too large
+ * for one grid (from about tokens * heads = 2^30 or seqs * kv_heads = 2^22 on) are
+ * refused with LUTGEMM_ERR_SHAPE.
  * Alignment: d_q, d_k, d_v, d_out and d_workspace 16 bytes, the int32 arrays 4. */
 typedef struct lutgemm_attention {
   int32_t type, heads, kv_heads, head_dim;

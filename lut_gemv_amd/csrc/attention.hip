@@ -226,7 +226,7 @@ __device__ __forceinline__ void few_rows(const AttnParams& p, int block, Region 
   constexpr int kPitch = D + 4;
   static_assert(kFewRows * kPitch * 4 <= 64 * D * 2, "a wave's sums fit its region");
   const int part = block / p.kv_heads, kvh = block % p.kv_heads;
-  const int s = part / p.splits[0], split = part % p.splits[0];
+  const int s = part % p.seqs, split = part / p.seqs;
   const Seq seq = sequence(p, s);
   const int rows = seq.len * p.group;
   if (rows > p.few_rows) return;
@@ -947,17 +947,36 @@ struct AttnPlan {
   size_t ws_bytes;
 };
 
-// Parts of a key axis of up to `keys` keys for `base` workgroups to fill the card
-// with `fill` of them, none shorter than `least`.
-void split_keys(int64_t keys, int64_t base, int64_t fill, int64_t least, int* splits, int* chunk) {
-  int64_t n = (fill + base - 1) / base;
-  const int64_t most = (keys + least - 1) / least;
+// The length of n parts of `keys` keys, and how many of that length there are.
+int64_t part_keys(int64_t keys, int64_t n) {
+  return ((keys + n - 1) / n + kSplitKeys - 1) / kSplitKeys * kSplitKeys;
+}
+void split_keys(int64_t keys, int64_t n, int* splits, int* chunk) {
+  const int64_t most = (keys + 511) / 512;  // none shorter than 512 keys
   if (n > most) n = most;
   if (n > kMaxSplits) n = kMaxSplits;
   if (n < 1) n = 1;
-  const int64_t each = ((keys + n - 1) / n + kSplitKeys - 1) / kSplitKeys * kSplitKeys;
+  const int64_t each = part_keys(keys, n);
   *splits = (int)((keys + each - 1) / each);
   *chunk = (int)each;
+}
+
+// The number of parts for `base` row tiles of as many keys, of which `slots` run at a time:
+// the one that takes least time, where a part costs as much as `more` keys besides its
+// own (one token x 64 heads of 8 on 32768 keys: 30 us, with four rounds of parts 36; 300
+// tokens x 32 heads of 8 on 16384: 106 us, with as many parts as cover the slots 121).
+int64_t parts_for(int64_t keys, int64_t base, int64_t slots, int64_t more) {
+  int64_t best = 1, least = INT64_MAX;
+  for (int64_t n = 1; n <= kMaxSplits; ++n) {
+    const int64_t each = part_keys(keys, n);
+    const int64_t rounds = (base * keys + each * slots - 1) / (each * slots);
+    const int64_t time = rounds * (each + more * (n > 1));
+    if (time < least) {
+      least = time;
+      best = n;
+    }
+  }
+  return best;
 }
 
 // Which kernels run and how many parts the longest key axis is cut into.
@@ -975,15 +994,25 @@ AttnPlan plan(const lutgemm_attention* a) {
   r.many = max_q * group > kFewRows;
   r.few = !r.many || (a->seqs > 1 && group <= kFewRows);  // a token alone has `group` rows
   r.tiles = a->tokens * group / kManyRows + a->seqs;
-  // Workgroups to fill the card with: few_kernel's are one to a compute unit, and four
-  // rounds of them even out sequences of different lengths (48 of 800 .. 8000 keys: 164 us;
-  // one round 181, two 181, twelve 181). Beside many_rows' they start last and short parts
-  // fill what the long tiles leave (row_tile's batch: in one part 106 us, in three 98);
-  // that batch's own tiles in two parts take 120 us.
-  split_keys(keys, (int64_t)a->seqs * a->kv_heads, r.many ? 1536 : 1024, 512, &r.splits[0],
-             &r.chunk[0]);
-  split_keys(keys, (a->tokens * group / kManyRows + (a->seqs + 1) / 2) * a->kv_heads, 512, 512,
-             &r.splits[1], &r.chunk[1]);
+  const int64_t few = (int64_t)a->seqs * a->kv_heads;
+  int64_t few_parts, many_parts;
+  if (a->seqs == 1) {
+    few_parts = parts_for(keys, few, 256, 200);
+    many_parts = parts_for(keys, (a->tokens * group + kManyRows - 1) / kManyRows * a->kv_heads, 512,
+                           300);
+  } else {
+    // Lengths that differ even out over four rounds of few_kernel's workgroups, one to a
+    // compute unit (48 of 800 .. 8000 keys: 164 us; one round 181, two 178, twelve
+    // 180). Beside many_rows' they start last and short parts fill what the long tiles
+    // leave (row_tile's batch: in one part 106 us, in three 98); that batch's own tiles in
+    // two parts take 120 us.
+    const int64_t fill = r.many ? 1536 : 1024;
+    few_parts = few > 256 ? (fill + few - 1) / few : fill / few;
+    const int64_t many = (a->tokens * group / kManyRows + (a->seqs + 1) / 2) * a->kv_heads;
+    many_parts = (512 + many - 1) / many;
+  }
+  split_keys(keys, few_parts, &r.splits[0], &r.chunk[0]);
+  split_keys(keys, many_parts, &r.splits[1], &r.chunk[1]);
   if (!r.few) r.splits[0] = 1;
   if (!r.many) r.splits[1] = 1;
   const int64_t rows = a->tokens * a->heads;
