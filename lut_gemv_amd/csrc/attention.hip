@@ -163,7 +163,8 @@ __device__ __forceinline__ int k_word(int row, int word) {
 }
 template <int D>
 __device__ __forceinline__ int v_word(int row, int word) {
-  const int turn = D == 128 ? row & 7 : (row >> 1) & 3;
+  // four rows of two blocks (many_rows) and eight of one (few_rows) cover all banks
+  const int turn = D == 128 ? (row & 3) << 1 | ((row >> 2) & 1) : (row & 2) | ((row >> 2) & 1);
   return row * (2 * D) + (((word >> 1) ^ turn) << 5) + ((word & 1) << 4);
 }
 
