@@ -423,7 +423,7 @@ __global__ __launch_bounds__(64 * W, 2) void few_kernel(AttnParams p) {
 // ------------------------------------------------------------------ many rows
 //
 // Bound by the matrix cores, the exponentials beside them and the power both draw:
-// 2048 tokens x 32 heads on 16384 keys take 490 us, 1050 TFLOP/s, at a clock that the
+// 2048 tokens x 32 heads on 16384 keys take 487 us, 1060 TFLOP/s, at a clock that the
 // card lowers from 2.0 to 1.7 GHz meanwhile (a large library product in bf16 reaches 1200).
 // A wave owns 32 rows; the four share 64 keys and values in LDS, in two buffers that
 // loads fill without passing registers, one barrier a tile. (Through registers, with
