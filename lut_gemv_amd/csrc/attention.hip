@@ -25,8 +25,9 @@ using namespace serve;
 
 constexpr int kThreads = 256;
 constexpr int kFewRows = 16;
-constexpr int kFewWaves = 8;
-constexpr int kShortWaves = 2;    // few_kernel's for parts of up to kShortKeys keys
+constexpr int kFewWaves = 4;      // few_kernel's waves
+constexpr int kLoneWaves = 8;     // with one workgroup to a compute unit at most
+constexpr int kShortWaves = 2;    // for parts of up to kShortKeys keys
 constexpr int kShortKeys = 128;
 constexpr int kManyRows = 128;
 constexpr int kSplitKeys = 128;   // a part of the key axis is a multiple of this
@@ -176,8 +177,8 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t sixteen_rows(const uint16_t* b
 
 // ------------------------------------------------------------------- few rows
 //
-// Bound by reading the cache. The eight waves of a workgroup take turns at 32-key
-// tiles of its part and keep their own softmax. A tile's keys and values pass through
+// Bound by reading the cache. The waves of a workgroup take turns at 32-key tiles of its
+// part and keep their own softmax. A tile's keys and values pass through
 // the wave's own 64 rows of LDS, so the loop has no barrier; the next tile's loads
 // follow at once into the registers that this frees and are in flight while the tile is
 // computed, 128 KB per compute unit. Loads cover whole
@@ -1002,13 +1003,12 @@ AttnPlan plan(const lutgemm_attention* a) {
     many_parts = parts_for(keys, (a->tokens * group + kManyRows - 1) / kManyRows * a->kv_heads, 512,
                            300);
   } else {
-    // Lengths that differ even out over four rounds of few_kernel's workgroups, one to a
-    // compute unit (48 of 800 .. 8000 keys: 164 us; one round 181, two 178, twelve
-    // 180). Beside many_rows' they start last and short parts fill what the long tiles
-    // leave (row_tile's batch: in one part 106 us, in three 98); that batch's own tiles in
-    // two parts take 120 us.
-    const int64_t fill = r.many ? 1536 : 1024;
-    few_parts = few > 256 ? (fill + few - 1) / few : fill / few;
+    // Lengths that differ even out over a few rounds of workgroups (48 sequences of 800 ..
+    // 8000 keys: 197 us in one part, 168 in three, 164 in four, 162 in six, 177 in
+    // sixteen; equal ones, 4 of 128k keys: 318 us in 8, 329 in 32, 345 in 64). Beside
+    // many_rows' they start last and short parts fill what the long tiles leave (row_tile's
+    // batch: in one part 106 us, in three 98); that batch's own tiles in two parts take 120.
+    few_parts = few > 256 ? (1536 + few - 1) / few : (r.many ? 1536 : 1024) / few;
     const int64_t many = (a->tokens * group / kManyRows + (a->seqs + 1) / 2) * a->kv_heads;
     many_parts = (512 + many - 1) / many;
   }
@@ -1023,6 +1023,21 @@ AttnPlan plan(const lutgemm_attention* a) {
   return r;
 }
 
+// Two workgroups of four waves share a compute unit, so that one begins or ends while the
+// other reads (4 sequences of 128k keys: 329 us, with eight waves and one workgroup
+// 332; 48 of 800 .. 8000: 164 and 167). Where there is only one to a unit it takes
+// eight waves (one sequence of 512 keys x 32 heads: 8.6 us, with four 9.5). Short parts leave
+// most waves idle, and their LDS keeps other workgroups from the unit (39 x 32 heads of
+// up to 50 keys: 23.4 us with eight, with two 9.8).
+template <class T, int D>
+int launch_few(const AttnPlan& r, int64_t few, const AttnParams& p, hipStream_t stream) {
+  const dim3 grid((unsigned)few);
+  if (r.chunk[0] <= kShortKeys)
+    return launch(few_kernel<T, D, kShortWaves>, grid, 64 * kShortWaves, p, stream);
+  if (few <= 256) return launch(few_kernel<T, D, kLoneWaves>, grid, 64 * kLoneWaves, p, stream);
+  return launch(few_kernel<T, D, kFewWaves>, grid, 64 * kFewWaves, p, stream);
+}
+
 template <class T, int D>
 int run_attention(const AttnPlan& r, const AttnParams& p, hipStream_t stream) {
   const int64_t few = (int64_t)p.seqs * r.splits[0] * p.kv_heads;
@@ -1033,11 +1048,7 @@ int run_attention(const AttnPlan& r, const AttnParams& p, hipStream_t stream) {
   else if (r.many)
     st = launch(many_kernel<T, D>, dim3((unsigned)many), kThreads, p, stream);
   else
-    // short parts leave most of eight waves idle, and their LDS keeps other workgroups from
-    // the compute unit (39 x 32 heads of up to 50 keys: 23.4 us, with two waves 9.8)
-    st = r.chunk[0] <= kShortKeys
-             ? launch(few_kernel<T, D, kShortWaves>, dim3((unsigned)few), 64 * kShortWaves, p, stream)
-             : launch(few_kernel<T, D, kFewWaves>, dim3((unsigned)few), 64 * kFewWaves, p, stream);
+    st = launch_few<T, D>(r, few, p, stream);
   const int64_t joined = r.splits[1] > 1 ? r.tiles * p.kv_heads * (kManyRows / kJoinRows) : 0;
   if (!st && p.join_blocks + joined > 0)
     st = launch(combine_kernel<T, D>, dim3((unsigned)(p.join_blocks + joined)), kThreads, p, stream);
