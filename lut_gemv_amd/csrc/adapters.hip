@@ -4,8 +4,8 @@
 // Two products on the matrix cores, t = A[a] x and out = y + s B[a] t, over tiles of
 // up to 16 or 32 rows that share an adapter. Memory and the latency of a few dependent
 // reads bound both: a decode step reads each adapter it uses once, a prompt reads x and y.
-// Rows come in any order; up to 64 of them every wave sorts for itself (one row per lane, no
-// extra launch), above that one workgroup sorts them first (sort_kernel).
+// Rows come in any order; up to 64 of them every wave groups for itself (one row per lane),
+// up to 1024 every workgroup, above that one workgroup sorts them first (sort_kernel).
 //
 // shrink_kernel splits K over workgroups and waves; its parts are summed when
 // expand_kernel reads them, in a fixed order. t is rounded for the second product to
@@ -13,7 +13,7 @@
 // the rounding of the output, for two small matrix products in place of one.
 //
 // 61 rows of 24 adapters of rank 64, K = 11008, N = 4096 (49 MB): 16.5 us, 2.9 TB/s;
-// 4096 rows of 8, K = N = 8192, rank 32 (210 MB): 63 us, 3.3 TB/s, of them 8 sorting.
+// 4096 rows of 8, K = N = 8192, rank 32 (210 MB): 60.5 us, 3.5 TB/s, of them 8 sorting.
 #include "serve.h"
 
 namespace lutgemm {
@@ -24,6 +24,8 @@ using namespace serve;
 constexpr int kThreads = 256;
 constexpr int kTileRows = 16;    // of a set of rows
 constexpr int kLaneRows = 64;    // up to so many rows are sorted by each wave itself
+constexpr int kFindRows = 1024;  // up to so many, of up to kFindBins - 1 adapters, by each workgroup
+constexpr int kFindBins = 256;
 constexpr int kSortThreads = 1024;
 constexpr int kMaxAdapters = 4096;
 constexpr int kTileCols = 64;    // output columns of a wave at a time
@@ -39,7 +41,7 @@ struct AdapterParams {
   const int32_t* ids;
   uint16_t* out;
   float* part;       // [split][row][rank]
-  int32_t* order;    // rows sorted by adapter (above kLaneRows rows)
+  int32_t* order;    // rows sorted by adapter, NULL if workgroups find theirs
   int32_t* tiles;    // [tile][3]: adapter (-1: none, -2: no such tile), start, count
   int32_t x_row, y_row, out_row;
   uint32_t x_bytes, y_bytes, out_bytes;
@@ -95,21 +97,11 @@ __device__ __forceinline__ uint64_t lanes_with(int v, int bits) {
   return same;
 }
 
-// Tile `g` of the rows grouped by adapter, sixteen rows to a tile; up to 64 rows each
-// wave finds it from the ids, one to a lane.
-template <int R>
-__device__ __forceinline__ Tile<R> find_tile(const AdapterParams& p, int g) {
+// Tile `g` of up to 64 rows grouped by adapter, sixteen rows to a tile: each wave finds it
+// from the ids, one to a lane.
+__device__ __forceinline__ Tile<1> lane_tile(const AdapterParams& p, int g) {
   const int lane = threadIdx.x & 63;
-  Tile<R> t;
-  if (R > 1 || p.rows > kLaneRows) {
-    t.adapter = uniform(p.tiles[3 * g]);
-    const int start = uniform(p.tiles[3 * g + 1]);
-    t.count = uniform(p.tiles[3 * g + 2]);
-#pragma unroll
-    for (int j = 0; j < R; ++j)
-      t.row[j] = t.adapter == -2 ? 0 : p.order[start + (t.has(j) ? 16 * j + (lane & 15) : 0)];
-    return t;
-  }
+  Tile<1> t;
   const bool here = lane < p.rows;
   const int id = here ? id_of(p, lane) : -1;
   const uint64_t same = lanes_with(id < 0 ? p.adapters : id, p.id_bits) & __ballot(here);
@@ -130,6 +122,113 @@ __device__ __forceinline__ Tile<R> find_tile(const AdapterParams& p, int g) {
   // row number to the lane of its column; the others' go to a lane that is not read
   const int placed = __builtin_amdgcn_ds_permute(4 * (member ? place : 63), lane);
   t.row[0] = __shfl(placed, t.has(0) ? lane & 15 : 0, 64);
+  return t;
+}
+
+// Tile `g` of up to kFindRows rows, found by a workgroup of four waves: each counts the
+// adapters of its quarter of the rows, all waves find the tile from the counts, and the
+// rows of the tile's adapter place themselves, in their order. Sorting in a launch of its
+// own costs more up to some 1700 rows (117 rows of 5 adapters: 17.7 us, so 15.0; 1076 of 3:
+// 26.4 and 24.6; 1723 of 9: 28.0 and 28.3; 4096 of 8: 61 and 73).
+struct Found {
+  int count[4][kFindBins];
+  int row[32];
+};
+
+template <int R>
+__device__ __forceinline__ Tile<R> group_tile(const AdapterParams& p, int g, Found& found) {
+  constexpr int kIds = kFindRows / kThreads;  // of a lane
+  constexpr int kRows = 16 * R;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int each = (p.rows + kThreads - 1) / kThreads * 64;  // rows of a wave
+  const int row0 = wave * each + lane;
+  int bin[kIds], before[kIds];  // the last bin: rows without an adapter; -1: no such row
+#pragma unroll
+  for (int i = 0; i < kIds; ++i) {
+    bin[i] = -1;
+    if (64 * i < each) bin[i] = p.ids[at_most(row0 + 64 * i, p.rows - 1)];
+  }
+  for (int i = threadIdx.x; i < 4 * kFindBins; i += kThreads) (&found.count[0][0])[i] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kIds; ++i) {
+    if (64 * i >= each) break;
+    const bool here = row0 + 64 * i < p.rows;
+    bin[i] = !here ? -1 : (uint32_t)bin[i] < (uint32_t)p.adapters ? bin[i] : p.adapters;
+    // the wave's rows of a bin are counted at once; no other wave has its counters
+    const uint64_t same = lanes_with(here ? bin[i] : 0, p.id_bits) & __ballot(here);
+    const int old = here ? found.count[wave][bin[i]] : 0;
+    before[i] = old + __popcll(same & (((uint64_t)1 << lane) - 1));
+    if (here && lane == __builtin_ctzll(same)) found.count[wave][bin[i]] = old + __popcll(same);
+  }
+  __syncthreads();
+  // four bins to a lane: the tiles before them, and the one that holds tile g
+  int count[4], tiles = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    count[e] = 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) count[e] += found.count[w][4 * lane + e];
+    tiles += (count[e] + kRows - 1) / kRows;
+  }
+  int until = tiles;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int x = __shfl_up(until, d, 64);
+    until += lane >= d ? x : 0;
+  }
+  Tile<R> t;
+  t.adapter = -2;
+  t.count = 0;
+#pragma unroll
+  for (int j = 0; j < R; ++j) t.row[j] = 0;
+  const uint64_t holds = __ballot(g < until && g >= until - tiles);
+  if (!holds) return t;
+  int nth = g - (until - tiles), its = 0, rows = 0;
+  bool open = true;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int n = (count[e] + kRows - 1) / kRows;
+    if (open && nth < n) {
+      open = false;
+      its = 4 * lane + e;
+      rows = count[e];
+    } else if (open) {
+      nth -= n;
+    }
+  }
+  const int owner = __builtin_ctzll(holds);
+  its = __builtin_amdgcn_readlane(its, owner);
+  const int first = __builtin_amdgcn_readlane(nth, owner) * kRows;
+  t.adapter = its == p.adapters ? -1 : its;
+  t.count = at_most(__builtin_amdgcn_readlane(rows, owner) - first, kRows);
+  int earlier = -first;
+  for (int w = 0; w < wave; ++w) earlier += found.count[w][its];
+#pragma unroll
+  for (int i = 0; i < kIds; ++i) {
+    if (64 * i >= each) break;
+    const int place = before[i] + earlier;
+    if (bin[i] == its && place >= 0 && place < t.count) found.row[place] = row0 + 64 * i;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < R; ++j) t.row[j] = found.row[t.has(j) ? 16 * j + (lane & 15) : 0];
+  return t;
+}
+
+template <int R>
+__device__ __forceinline__ Tile<R> find_tile(const AdapterParams& p, int g, Found& found) {
+  if (p.rows > kLaneRows && !p.order) return group_tile<R>(p, g, found);
+  if constexpr (R == 1)
+    if (p.rows <= kLaneRows) return lane_tile(p, g);
+  const int lane = threadIdx.x & 63;
+  Tile<R> t;
+  t.adapter = uniform(p.tiles[3 * g]);
+  const int start = uniform(p.tiles[3 * g + 1]);
+  t.count = uniform(p.tiles[3 * g + 2]);
+#pragma unroll
+  for (int j = 0; j < R; ++j)
+    t.row[j] = t.adapter == -2 ? 0 : p.order[start + (t.has(j) ? 16 * j + (lane & 15) : 0)];
   return t;
 }
 
@@ -344,8 +443,10 @@ __global__ __launch_bounds__(kThreads) void shrink_kernel(AdapterParams p) {
   __shared__ __attribute__((aligned(16))) char stage[4 * S::kBytes];
   static_assert(S::kBytes >= R * NB * 1024, "the waves' sums fit their stage");
   fetch(p);
-  const Tile<R> t = find_tile<R>(p, blockIdx.x);
+  static_assert(sizeof(Found) <= sizeof stage, "both use the same memory");
+  const Tile<R> t = find_tile<R>(p, blockIdx.x, *(Found*)stage);
   if (t.adapter < 0) return;
+  __syncthreads();
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int from = blockIdx.y * p.split_k;
   const int to = from + p.split_k < p.K ? from + p.split_k : p.K;
@@ -377,7 +478,10 @@ __global__ __launch_bounds__(kThreads) void shrink_kernel(AdapterParams p) {
 // column 32 (k / 2) + 8 (i / 4) + 4 (k % 2) + i % 4, so a lane's results are twice eight
 // consecutive columns of its row, and four lanes' together 64 bytes of y and out. Lanes of
 // neighbouring rows exchange halves, so that a load or store moves 128 bytes of a row
-// (4096 rows, K = N = 8192, rank 32: 63.0 us, so 60.5). y and B are read before t is needed.
+// (4096 rows, K = N = 8192, rank 32: 63.0 us, so 60.5). y and B are read before t is
+// needed. Where rows do not begin at multiples of 16 bytes, whole tiles of columns are
+// read and written by unaligned words of 16 bytes (156 rows, N = 10925: 12.4 us, by single
+// elements 20.5), the last tile by single elements.
 
 // The neighbouring lane's v.
 __device__ __forceinline__ uint32_t neighbour(uint32_t v) {
@@ -420,6 +524,14 @@ struct Columns {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
           y[j][i] = load16(from, place(t, j, i, n + 32 * odd, p.y_row, p.N));
+        continue;
+      }
+      if (n0 + kTileCols <= p.N) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t at = place(t, j, i, n + 32 * odd, p.y_row, p.N);
+          __builtin_memcpy(&y[j][i], (const char*)p.y + (at == kNowhere ? 0 : at), 16);
+        }
         continue;
       }
       const uint32_t at = 2 * ((uint32_t)t.row[j] * (uint32_t)p.y_row + n);
@@ -514,7 +626,8 @@ __device__ __forceinline__ void expand(const AdapterParams& p, const Tile<R>& t,
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[i] = f4v{0.f, 0.f, 0.f, 0.f};
     u4v r[2] = {w.y[j][0], w.y[j][1]};
-    if (p.wide) exchange(r);
+    const bool whole = p.wide || n0 + kTileCols <= p.N;
+    if (whole) exchange(r);
     if (t.adapter >= 0) {
 #pragma unroll
       for (int s = 0; s < Inner<T, NB>::kSteps; ++s)
@@ -530,12 +643,16 @@ __device__ __forceinline__ void expand(const AdapterParams& p, const Tile<R>& t,
                                   f.y + acc[i / 2][2 * (i % 2) + 1] * v[j].factor);
       }
     }
-    if (p.wide) {
+    if (whole) {
       exchange(r);
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        __builtin_amdgcn_raw_buffer_store_b128(
-            r[i], to, place(t, j, i, n + 32 * (lane & 1), p.out_row, p.N), 0, 0);
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t at = place(t, j, i, n + 32 * (lane & 1), p.out_row, p.N);
+        if (p.wide)
+          __builtin_amdgcn_raw_buffer_store_b128(r[i], to, at, 0, 0);
+        else if (at != kNowhere)
+          __builtin_memcpy((char*)p.out + at, &r[i], 16);
+      }
       continue;
     }
     const uint32_t at = 2 * ((uint32_t)t.row[j] * (uint32_t)p.out_row + n);
@@ -558,7 +675,8 @@ __global__ __launch_bounds__(kThreads) void expand_kernel(AdapterParams p) {
   __shared__ __attribute__((aligned(16))) float inner[16 * R * kPitch];
   __shared__ int row_of[16 * R];
   fetch(p);
-  const Tile<R> t = find_tile<R>(p, blockIdx.y);
+  __shared__ Found found;
+  const Tile<R> t = find_tile<R>(p, blockIdx.y, found);
   if (t.adapter == -2 || (t.adapter == -1 && p.in_place)) return;
   const int wave = uniform(threadIdx.x >> 6), col = threadIdx.x & 15;
   const int n0 = ((int)blockIdx.x * 4 + wave) * kTurns * kTileCols;
@@ -614,7 +732,7 @@ __global__ __launch_bounds__(64 * kFusedWaves) void fused_kernel(AdapterParams p
   __shared__ __attribute__((aligned(16))) char stage[kFusedWaves * S::kBytes];
   __shared__ __attribute__((aligned(16))) float inner[16 * kPitch];
   fetch(p);
-  const Tile<1> t = find_tile<1>(p, blockIdx.y);
+  const Tile<1> t = lane_tile(p, blockIdx.y);
   if (t.adapter == -2 || (t.adapter == -1 && p.in_place)) return;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int n0 = ((int)blockIdx.x * kFusedWaves + wave) * kTileCols;
@@ -671,7 +789,7 @@ int check_adapters(const lutgemm_adapters* l) {
 }
 
 struct AdapterPlan {
-  bool fused;
+  bool fused, sorted;
   int tile_rows, tiles, splits, split_k;
   size_t part_at, ws_bytes;
 };
@@ -704,7 +822,8 @@ AdapterPlan plan(const lutgemm_adapters* l) {
   r.split_k = (l->K / 8 + splits - 1) / splits * 8;
   r.split_k = (r.split_k + 4 * kStepK - 1) / (4 * kStepK) * (4 * kStepK);
   r.splits = l->K > 0 ? (l->K + r.split_k - 1) / r.split_k : 0;
-  if (l->rows > kLaneRows)
+  r.sorted = l->rows > kFindRows || (l->rows > kLaneRows && l->adapters >= kFindBins);
+  if (r.sorted)
     r.part_at = (((size_t)l->rows + 3 * (size_t)r.tiles) * sizeof(int32_t) + 15) / 16 * 16;
   r.ws_bytes = r.part_at + (size_t)r.splits * l->rows * l->rank * sizeof(float);
   return r;
@@ -732,7 +851,7 @@ int run_adapters(const AdapterPlan& r, const AdapterParams& p, hipStream_t strea
                     dim3((unsigned)((p.N + cols - 1) / cols), (unsigned)r.tiles),
                     64 * kFusedWaves, p, stream);
     }
-  if (p.rows > kLaneRows) {
+  if (r.sorted) {
     const int st = launch(sort_kernel, dim3(1), kSortThreads, p, stream);
     if (st) return st;
   }
@@ -791,7 +910,7 @@ extern "C" int lutgemm_adapters_add(const lutgemm_adapters* l, const void* d_x, 
     p.scales = d_scales;
     p.ids = d_ids;
     p.out = (uint16_t*)d_out;
-    if (l->rows > kLaneRows) {
+    if (r.sorted) {
       p.order = (int32_t*)d_workspace;
       p.tiles = p.order + l->rows;
     }

@@ -530,6 +530,20 @@ def test_adapters(dtype, K, N, rank, rows, count):
     assert torch.equal(got, lg.adapters_add(*case))   # the same bits again
 
 
+@pytest.mark.parametrize("rows,count", [(65, 255), (65, 256), (300, 255), (300, 256), (257, 1),
+                                        (1025, 40), (4095, 7), (4096, 255), (4097, 7)])
+@pytest.mark.parametrize("order", ["mixed", "runs", "one", "none"])
+def test_adapters_of_many_rows(rows, count, order):
+    """Rows grouped by each workgroup and by a launch of its own: numbers of rows and adapters
+    on both sides of the limits, ids in any order, all alike and all outside."""
+    ids = _ids(rows, count, rows + count)
+    ids = {"mixed": ids, "runs": sorted(ids), "one": [count - 1] * rows, "none": [-1] * rows}[order]
+    case = _adapters_case(F16, rows, 64, 40, 8, count, ids, seed=rows)
+    got = lg.adapters_add(*case)
+    _adapters_check(got, *case, f"{rows} rows, {count} adapters, {order}")
+    assert torch.equal(got, lg.adapters_add(*case))
+
+
 def test_adapters_rows_do_not_depend_on_others():
     """A row alone, in a full batch and in a sorted batch gives the same bits when the
     work is split alike, and the same value in any case."""
