@@ -307,7 +307,7 @@ PyObject* adapters(PyObject* const* a) {
   d.N = small(N, "N");
   d.rank = small(rank, "rank");
   d.adapters = small(count, "adapters");
-  d.x_row = step(x, 0);
+  d.x_row = K ? step(x, 0) : 0;  // rows of no entries have any stride
   d.y_row = step(y, 0);
   d.out_row = step(out, 0);
   constexpr const char* where = "lutgemm_adapters_add";

@@ -593,6 +593,13 @@ def test_adapters_nothing_to_add():
     assert torch.equal(flat, y)
 
 
+def test_adapters_of_no_inputs():
+    """K = 0, of a tensor of its own: its rows have a stride of one."""
+    y, x, a, b, ids, s = _adapters_case(F16, 33, 0, 40, 8, 2, [0] * 33, seed=36)
+    assert x.stride(0) == 1
+    assert torch.equal(lg.adapters_add(y, x, a, b, ids, s), y)
+
+
 def test_adapters_graph_and_streams():
     case = _adapters_case(BF16, 100, 1024, 512, 32, 9, _ids(100, 9, 3), seed=35)
     want = lg.adapters_add(*case)
