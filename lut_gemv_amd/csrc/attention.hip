@@ -953,10 +953,13 @@ struct AttnPlan {
 int64_t part_keys(int64_t keys, int64_t n) {
   return ((keys + n - 1) / n + kSplitKeys - 1) / kSplitKeys * kSplitKeys;
 }
+int64_t most_parts(int64_t keys) {  // none shorter than 512 keys
+  const int64_t most = (keys + 511) / 512;
+  return most < kMaxSplits ? most : kMaxSplits;
+}
 void split_keys(int64_t keys, int64_t n, int* splits, int* chunk) {
-  const int64_t most = (keys + 511) / 512;  // none shorter than 512 keys
+  const int64_t most = most_parts(keys);
   if (n > most) n = most;
-  if (n > kMaxSplits) n = kMaxSplits;
   if (n < 1) n = 1;
   const int64_t each = part_keys(keys, n);
   *splits = (int)((keys + each - 1) / each);
@@ -969,7 +972,8 @@ void split_keys(int64_t keys, int64_t n, int* splits, int* chunk) {
 // tokens x 32 heads of 8 on 16384: 106 us, with as many parts as cover the slots 121).
 int64_t parts_for(int64_t keys, int64_t base, int64_t slots, int64_t more) {
   int64_t best = 1, least = INT64_MAX;
-  for (int64_t n = 1; n <= kMaxSplits; ++n) {
+  const int64_t most = most_parts(keys);
+  for (int64_t n = 1; n <= most && base * (n - 1) < 4 * slots; ++n) {
     const int64_t each = part_keys(keys, n);
     const int64_t rounds = (base * keys + each * slots - 1) / (each * slots);
     const int64_t time = rounds * (each + more * (n > 1));
@@ -997,11 +1001,13 @@ AttnPlan plan(const lutgemm_attention* a) {
   r.few = !r.many || (a->seqs > 1 && group <= kFewRows);  // a token alone has `group` rows
   r.tiles = a->tokens * group / kManyRows + a->seqs;
   const int64_t few = (int64_t)a->seqs * a->kv_heads;
-  int64_t few_parts, many_parts;
+  int64_t few_parts = 1, many_parts = 1;
   if (a->seqs == 1) {
-    few_parts = parts_for(keys, few, 256, 200);
-    many_parts = parts_for(keys, (a->tokens * group + kManyRows - 1) / kManyRows * a->kv_heads, 512,
-                           300);
+    if (r.few)
+      few_parts = parts_for(keys, few, 256, 200);
+    else
+      many_parts = parts_for(
+          keys, (a->tokens * group + kManyRows - 1) / kManyRows * a->kv_heads, 512, 300);
   } else {
     // Lengths that differ even out over a few rounds of workgroups (48 sequences of 800 ..
     // 8000 keys: 197 us in one part, 168 in three, 164 in four, 162 in six, 177 in

@@ -70,11 +70,14 @@ int type_of(const at::Tensor& t, const char* what) {
 }
 
 // The operators have no gradients: a graph that would silently end here is refused.
-void no_gradient(PyObject* const* args, int n) {
+// Bit i of `which`: argument i is a tensor or None.
+void no_gradient(PyObject* const* args, unsigned which) {
   if (!at::GradMode::is_enabled()) return;
-  for (int i = 0; i < n; ++i)
-    if (THPVariable_Check(args[i]) && THPVariable_Unpack(args[i]).requires_grad())
+  for (; which; which &= which - 1) {
+    PyObject* const o = args[__builtin_ctz(which)];
+    if (o != Py_None && THPVariable_Check(o) && THPVariable_Unpack(o).requires_grad())
       refuse("the operator has no gradient: call it under torch.no_grad() or on detached tensors");
+  }
 }
 
 void on_gpu(const at::Tensor& t, const char* what) {
@@ -322,8 +325,9 @@ PyObject* adapters(PyObject* const* a) {
   return THPVariable_Wrap(out);
 }
 
-// One call: so many arguments, and every C++ exception as a Python error.
-template <PyObject* (*F)(PyObject* const*), Py_ssize_t N>
+// One call: so many arguments, those of `Tensors` tensors or None, and every C++ exception
+// as a Python error.
+template <PyObject* (*F)(PyObject* const*), Py_ssize_t N, unsigned Tensors>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (n != N) {
     PyErr_Format(PyExc_TypeError, "%zd arguments expected, not %zd", N, n);
@@ -334,7 +338,7 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return nullptr;
   }
   try {
-    no_gradient(args, N);
+    no_gradient(args, Tensors);
     return F(args);
   } catch (const Refused& e) {
     PyErr_SetString(PyExc_ValueError, e.what());
@@ -372,9 +376,9 @@ PyObject* init(PyObject*, PyObject* args) {
 
 PyMethodDef kMethods[] = {
     {"init", init, METH_VARARGS, nullptr},
-    {"qk_norm_rotate", (PyCFunction)(void (*)(void))entry<heads, 13>, METH_FASTCALL, nullptr},
-    {"paged_attention", (PyCFunction)(void (*)(void))entry<attention, 11>, METH_FASTCALL, nullptr},
-    {"adapters_add", (PyCFunction)(void (*)(void))entry<adapters, 7>, METH_FASTCALL, nullptr},
+    {"qk_norm_rotate", (PyCFunction)(void*)entry<heads, 13, 0x1671>, METH_FASTCALL, nullptr},
+    {"paged_attention", (PyCFunction)(void*)entry<attention, 11, 0x407>, METH_FASTCALL, nullptr},
+    {"adapters_add", (PyCFunction)(void*)entry<adapters, 7, 0x6F>, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, kMethods,
