@@ -13,7 +13,7 @@
 // the rounding of the output, for two small matrix products in place of one.
 //
 // 61 rows of 24 adapters of rank 64, K = 11008, N = 4096 (49 MB): 16.5 us, 2.9 TB/s;
-// 4096 rows of 8, K = N = 8192, rank 32 (210 MB): 60.5 us, 3.5 TB/s, of them 8 sorting.
+// 4096 rows of 8, K = N = 8192, rank 32 (210 MB): 57 us, 3.7 TB/s, of them 8 sorting.
 #include "serve.h"
 
 namespace lutgemm {
@@ -75,9 +75,16 @@ constexpr uint32_t kNowhere = 0x80000000u;
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* base, uint32_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, (int)bytes, 0x00027000);
 }
+template <int Hint = 0>
 __device__ __forceinline__ u4v load16(__amdgpu_buffer_rsrc_t b, uint32_t at) {
-  return __builtin_bit_cast(u4v, __builtin_amdgcn_raw_buffer_load_b128(b, at, 0, 0));
+  return __builtin_bit_cast(u4v, __builtin_amdgcn_raw_buffer_load_b128(b, at, 0, Hint));
 }
+
+// The hint (non-temporal) for y and out where many rows pass through: it keeps B and t in
+// the L2 (4096 rows, K = N = 8192, rank 32: 60.4 us without it, 57.0 with; for x as well
+// 58.9). Few rows stay in the L2 for the next reader.
+template <int R>
+constexpr int kOnce = R == 2 ? 2 : 0;
 
 __device__ __forceinline__ int at_most(int v, int most) { return v < most ? v : most; }
 
@@ -523,7 +530,7 @@ struct Columns {
       if (p.wide) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          y[j][i] = load16(from, place(t, j, i, n + 32 * odd, p.y_row, p.N));
+          y[j][i] = load16<kOnce<R>>(from, place(t, j, i, n + 32 * odd, p.y_row, p.N));
         continue;
       }
       if (n0 + kTileCols <= p.N) {
@@ -649,7 +656,7 @@ __device__ __forceinline__ void expand(const AdapterParams& p, const Tile<R>& t,
       for (int i = 0; i < 2; ++i) {
         const uint32_t at = place(t, j, i, n + 32 * (lane & 1), p.out_row, p.N);
         if (p.wide)
-          __builtin_amdgcn_raw_buffer_store_b128(r[i], to, at, 0, 0);
+          __builtin_amdgcn_raw_buffer_store_b128(r[i], to, at, 0, kOnce<R>);
         else if (at != kNowhere)
           __builtin_memcpy((char*)p.out + at, &r[i], 16);
       }

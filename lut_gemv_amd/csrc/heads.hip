@@ -3,8 +3,8 @@
 // output (lutgemm_qk_norm_rotate; the formulas are in lutgemm.h).
 //
 // Memory bounds it: every element is read once and written once, with a few fp32
-// operations between. 8192 tokens of 64 + 2 x 8 heads of 128 (336 MB) take 63 us, 5.3
-// TB/s, what a plain copy of the same bytes takes. A thread owns sixteen entries of a head as two
+// operations between. 8192 tokens of 64 + 2 x 8 heads of 128 (336 MB) take 60 us, 5.6
+// TB/s; a plain copy of the same bytes takes 63. A thread owns sixteen entries of a head as two
 // 16-byte words, chosen so that both halves of each rotated pair are its own (entries 8u ..
 // 8u+7 and R/2 + 8u .. for pairs of halves, 16u .. 16u+15 for neighbours); the only
 // exchange between lanes is the norm's sum over a head. A workgroup serves one token, so
@@ -89,7 +89,9 @@ __device__ __forceinline__ float sum_lanes(float v, int log2) {
   return v;
 }
 
-template <class T>
+// Once: the heads do not stay in the L2 until their next reader, and pass it by
+// (8192 tokens: 60.3 us, without the hint 64.2).
+template <class T, bool Once>
 __global__ __launch_bounds__(kThreads) void heads_kernel(HeadsParams p) {
   fetch(p);
   const int64_t t = blockIdx.x;
@@ -108,7 +110,16 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(HeadsParams p) {
 
   // the first head's words are on their way while the slot and the angles are looked up
   auto head_at = [&](int h) { return src + (uint32_t)min(h, p.all - 1) * (uint32_t)p.dim; };
-  u4v w0 = *(const u4v*)(head_at(first) + c0), w1 = *(const u4v*)(head_at(first) + c1);
+  auto read = [](const uint16_t* from) {
+    return Once ? __builtin_nontemporal_load((const u4v*)from) : *(const u4v*)from;
+  };
+  auto write = [](uint16_t* to, u4v w) {
+    if constexpr (Once)
+      __builtin_nontemporal_store(w, (u4v*)to);
+    else
+      *(u4v*)to = w;
+  };
+  u4v w0 = read(head_at(first) + c0), w1 = read(head_at(first) + c1);
   u4v qw0 = {}, qw1 = {}, kw0 = {}, kw1 = {};
   if (p.q_weight) {
     qw0 = *(const u4v*)(p.q_weight + c0);
@@ -144,8 +155,8 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(HeadsParams p) {
     const int h = first + g * per_group;
     if (h >= p.all) break;
     if (g) {
-      w0 = *(const u4v*)(head_at(h) + c0);
-      w1 = *(const u4v*)(head_at(h) + c1);
+      w0 = read(head_at(h) + c0);
+      w1 = read(head_at(h) + c1);
     }
     const bool is_q = h < p.heads, is_v = h >= p.heads + p.kv_heads;
     if (!is_v) {
@@ -180,8 +191,8 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(HeadsParams p) {
     uint16_t* to = is_q ? q_to + (uint32_t)h * (uint32_t)p.dim
                  : is_v ? v_to + (int64_t)(h - p.heads - p.kv_heads) * p.v_head
                         : k_to + (int64_t)(h - p.heads) * p.k_head;
-    *(u4v*)(to + c0) = w0;
-    *(u4v*)(to + c1) = w1;
+    write(to + c0, w0);
+    write(to + c1, w1);
   }
 }
 
@@ -277,8 +288,11 @@ extern "C" int lutgemm_qk_norm_rotate(const lutgemm_heads* h, const void* d_qkv,
     p.walk = (int64_t)h->tokens * groups <= 8 * (int64_t)cus ? 1 : groups;
     p.all = all;
     const dim3 grid((unsigned)h->tokens, (unsigned)((groups + p.walk - 1) / p.walk));
-    return serve::launch(h->type == LUTGEMM_F16 ? heads_kernel<serve::F16>
-                                                : heads_kernel<serve::BF16>,
+    const bool once = (int64_t)h->tokens * all * h->head_dim * 2 > (int64_t)32 << 20;  // the L2s
+    const bool f16 = h->type == LUTGEMM_F16;
+    return serve::launch(once ? f16 ? heads_kernel<serve::F16, true> : heads_kernel<serve::BF16, true>
+                         : f16 ? heads_kernel<serve::F16, false>
+                               : heads_kernel<serve::BF16, false>,
                          grid, kThreads, p, (hipStream_t)stream);
   } catch (...) {
     return LUTGEMM_ERR_INTERNAL;

@@ -485,6 +485,25 @@ def test_heads_many_tokens_and_tiny_values():
     _inside(k, kw, kb, "keys")
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_heads_larger_than_the_caches(dtype):
+    """More than 32 MB of heads, in place and into the cache."""
+    heads, kv, dim, tokens = 64, 8, 128, 1700
+    qkv, table, positions, w = _heads_case(dtype, tokens, heads, kv, dim, dim, False, True, seed=41)
+    k_pages = torch.zeros((107, 16, kv, dim), dtype=dtype, device=DEV)
+    v_pages = torch.zeros_like(k_pages)
+    slots = torch.arange(tokens, device=DEV).flip(0).contiguous()
+    some = torch.tensor([0, 1, 255, 256, 1024, tokens - 1], device=DEV)
+    (qw, qb), (kw, kb), vw = _heads_want(qkv[some], table, positions[some], w, heads, kv, dim, False,
+                                         1e-6, U[dtype])
+    out = qkv[:, :heads * dim].unflatten(1, (heads, dim))
+    q = lg.qk_norm_rotate(qkv, heads, kv, positions, table, *w, k_pages=k_pages, v_pages=v_pages,
+                          slots=slots, out=out)
+    _inside(q[some], qw, qb, "queries")
+    _inside(k_pages.reshape(-1, kv, dim)[slots[some]], kw, kb, "keys")
+    assert np.array_equal(_np(v_pages.reshape(-1, kv, dim)[slots[some]]), vw)
+
+
 def test_rotary_table_is_rounded_from_64_bits():
     t = lg.rotary_table(70000, 64, 10000.0, device="cpu").double().numpy()
     p = np.arange(70000)[:, None] * 10000.0 ** (-np.arange(0, 64, 2) / 64)
