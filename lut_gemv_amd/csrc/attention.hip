@@ -521,7 +521,7 @@ __device__ __forceinline__ void many_rows(const AttnParams& p, int block, char* 
 #pragma unroll
     for (int e = 0; e < 16; ++e) o[d][e] = 0.f;
   float m = -INFINITY, l = 0.f, base = 0.f;
-  bool bad = false;
+  bool bad = false, found = false;
 
   // A wave brings sixteen of a tile's keys and values, straight from memory to LDS:
   // a load places 1 KB of whole rows there in lane order, so each lane reads the word
@@ -641,7 +641,7 @@ __device__ __forceinline__ void many_rows(const AttnParams& p, int block, char* 
     if (!__any(any_non_finite<T>(w))) return;
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) mine[64 * j] = finite<T>(w[j]);
-    if (lane == 0) atomicOr(&marks, kFound);
+    found = true;
   };
   if (begin < end) {
     read_ids(begin);
@@ -706,7 +706,9 @@ __device__ __forceinline__ void many_rows(const AttnParams& p, int block, char* 
   } else {
     __syncthreads();
   }
-  if (__any(bad) && lane == 0) atomicOr(&marks, kBad);
+  // a barrier lies between the word's first value and these
+  const int met = (__any(bad) ? kBad : 0) | (found ? kFound : 0);
+  if (met && lane == 0) atomicOr(&marks, met);
   __syncthreads();
   if (r >= r1) return;
   l += __shfl_xor(l, 32, 64);

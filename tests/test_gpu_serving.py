@@ -264,6 +264,33 @@ def test_attention_non_finite_values_stay_behind_the_mask(dtype, heads, kv_heads
     b.check(_patched(b, got, seen, window), "the rest", window=window)
 
 
+@pytest.mark.parametrize("lens,news,window", [
+    ([130, 64], [130, 64], 0), ([100, 300, 40], [100, 1, 40], 0), ([900, 800], [200, 150], 30),
+])
+@pytest.mark.parametrize("dtype,heads,kv_heads,dim", [(F16, 16, 8, 128), (BF16, 32, 8, 64)])
+def test_attention_non_finite_values_of_a_chunks_first_tile(dtype, heads, kv_heads, dim, lens, news,
+                                                            window):
+    """Infinities among the very first values that a workgroup brings, in each wave's share
+    of them, in chunks and in a batch with single tokens."""
+    b = Batch(dtype, heads, kv_heads, dim, 16, lens, news, seed=31)
+    got_at = np.concatenate([[0], np.cumsum(news)])
+    seen = torch.zeros((sum(news), heads, dim), dtype=torch.bool, device=DEV)
+    for i, (n, new) in enumerate(zip(lens, news)):
+        low = max(n - new - window + 1, 0) if window else 0   # the first row's first key
+        for j, key in enumerate(range(low + 1, min(low + 64, n), 17)):
+            b.v_pages[int(b.table[i, key // 16]), key % 16, :, 7 + j] = float("inf")
+            b.v[i][key, :, 7 + j] = 0
+            for t in range(new):
+                pos = n - new + t
+                if key <= pos and (not window or key > pos - window):
+                    seen[got_at[i] + t, :, 7 + j] = True
+    got = b.call(window=window)
+    assert seen.any() and not seen.all()
+    assert (got[seen] == float("inf")).all()
+    assert torch.isfinite(got[~seen]).all()
+    b.check(_patched(b, got, seen, window), "the rest", window=window)
+
+
 def _patched(b, got, seen, window):
     """`got` with the exact values in the marked places."""
     got, at = got.clone(), 0
