@@ -410,7 +410,8 @@ int lutgemm_qk_norm_rotate(const lutgemm_heads* h, const void* d_qkv, const int6
  *   d_k, d_v    pages [pages][page_size][kv_heads][head_dim], strides as in lutgemm_heads
  *   d_table     int32 [seqs][table_width], rows table_stride apart: key j of sequence
  *               s is in page table[s][j / page_size]; entries past a sequence's
- *               last key are not read
+ *               last key, and those whose keys all lie before the window of its first
+ *               new token, are not read: their pages may have been released
  *   d_kv_lens   int32 [seqs]
  *   d_q_starts  int32 [seqs + 1], non-decreasing, or NULL: one new token for each
  *               sequence (tokens == seqs). Output rows before q_starts[0] and from

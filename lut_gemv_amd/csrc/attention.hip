@@ -86,10 +86,16 @@ __device__ __forceinline__ int first_key(const AttnParams& p, int pos) {
   return p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
 }
 
-// The keys [lo, hi) that rows r0 .. r1 - 1 of a sequence see between them, lo brought
-// down to a multiple of 64, and how they are split: parts of `chunk` keys each.
+// The keys [first, hi) that rows r0 .. r1 - 1 of a sequence see between them, first
+// brought down to a multiple of 64 (lo), and how they are split: parts of `chunk` keys
+// each. Blocks of sixteen keys before first's and from hi on are never asked for: their
+// pages may be gone. first's or the last one stands in for them, and no row sees it there.
 struct Span {
-  int lo, hi, chunk, parts;
+  int first, lo, hi, chunk, parts;
+  __device__ __forceinline__ int block(int blk) const {
+    const int least = first >> 4, most = (hi - 1) >> 4;
+    return blk < least ? least : blk > most ? most : blk;
+  }
 };
 
 template <int Kind>  // 0: few_rows', 1: many_rows'
@@ -97,7 +103,8 @@ __device__ __forceinline__ Span span_of(const AttnParams& p, const Seq& q, int r
   Span a;
   const int first = q.n - q.len + r0 / p.group, last = q.n - q.len + (r1 - 1) / p.group;
   a.hi = last + 1 < 0 ? 0 : last + 1;
-  a.lo = first_key(p, first) & ~63;
+  a.first = first_key(p, first);
+  a.lo = a.first & ~63;
   const int keys = a.hi > a.lo ? a.hi - a.lo : 0;
   // a sequence longer than the launch was made for takes longer parts
   int need = (keys + p.splits[Kind] - 1) / p.splits[Kind];
@@ -194,12 +201,11 @@ struct FewTile {
 
 template <int D>
 __device__ __forceinline__ void few_load(const AttnParams& p, FewTile<D>& t, const int (&ids)[2],
-                                         int kvh, int kt, int n, int lane, bool* bad) {
+                                         int kvh, int kt, const Span& span, int lane, bool* bad) {
   constexpr int words = D / 8, rows = 64 / words, each = 16 / rows;
-  const int last = (n - 1) >> 4;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int blk = min_of(2 * kt + i, last), most = n - 1 - 16 * blk;
+    const int blk = span.block(2 * kt + i), most = span.hi - 1 - 16 * blk;
     const int id = page_of(p, ids[i], bad), slot = slot_of(p, blk);
     const uint16_t* kb = p.k + (int64_t)id * p.k_page + (int64_t)slot * p.k_slot + kvh * p.k_head;
     const uint16_t* vb = p.v + (int64_t)id * p.v_page + (int64_t)slot * p.v_slot + kvh * p.v_head;
@@ -273,15 +279,15 @@ __device__ __forceinline__ void few_rows(const AttnParams& p, int block, Region 
     char* vals = keys + 32 * D * 2;
     FewTile<D> t;
     int ids[2];
-    const int end = (to + 31) >> 5, end_blk = (span.hi - 1) >> 4;
+    const int end = (to + 31) >> 5;
     auto next_ids = [&](int kt) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) ids[i] = table[table_at(p, min_of(2 * kt + i, end_blk))];
+      for (int i = 0; i < 2; ++i) ids[i] = table[table_at(p, span.block(2 * kt + i))];
     };
     int kt = (from >> 5) + wave;
     if (kt < end) {
       next_ids(kt);
-      few_load<D>(p, t, ids, kvh, kt, span.hi, lane, &bad);
+      few_load<D>(p, t, ids, kvh, kt, span, lane, &bad);
       next_ids(kt + W);
     }
     for (; kt < end; kt += W) {
@@ -297,7 +303,7 @@ __device__ __forceinline__ void few_rows(const AttnParams& p, int block, Region 
         *(u4v*)(vals + v_word<D>(vr * j + lane / words, lane % words)) = t.v[j];
       }
       if (kt + W < end) {
-        few_load<D>(p, t, ids, kvh, kt + W, span.hi, lane, &bad);
+        few_load<D>(p, t, ids, kvh, kt + W, span, lane, &bad);
         next_ids(kt + 2 * W);
       }
       // the wave's own stores to LDS are complete and visible to its other lanes
@@ -527,15 +533,13 @@ __device__ __forceinline__ void many_rows(const AttnParams& p, int block, char* 
   // a load places 1 KB of whole rows there in lane order, so each lane reads the word
   // whose place in the LDS layout its own is.
   constexpr int kWords = D / 8, kRowsEach = 64 / kWords, kLoads = 16 / kRowsEach;
-  const int end_blk = (span.hi - 1) >> 4;
   // lane i: the page of this wave's values of tile ids_from + i - 1, lanes' keys being two
   // blocks of sixteen further on
   int k_ids = 0, v_ids = 0, ids_from = 0;
-  auto block_at = [&](int blk) { return min_of(blk < 0 ? 0 : blk, end_blk); };
   auto read_ids = [&](int kt) {
     ids_from = kt - 1;
-    k_ids = table[table_at(p, block_at(4 * (ids_from + lane) + 2 + wave))];
-    v_ids = table[table_at(p, block_at(4 * (ids_from + lane) + wave))];
+    k_ids = table[table_at(p, span.block(4 * (ids_from + lane) + 2 + wave))];
+    v_ids = table[table_at(p, span.block(4 * (ids_from + lane) + wave))];
     asm volatile("" : "+v"(k_ids), "+v"(v_ids));  // they arrive here, not behind later loads
   };
   auto load = [&](int blk, int id, const uint16_t* cache, int64_t page_step, int64_t head_step,
@@ -554,11 +558,11 @@ __device__ __forceinline__ void many_rows(const AttnParams& p, int block, char* 
   };
   auto load_keys = [&](int kt, char* to) {
     if (kt - ids_from >= 64) read_ids(kt);
-    load(block_at(4 * kt + 2 + wave), __builtin_amdgcn_readlane(k_ids, kt - ids_from), p.k, p.k_page,
+    load(span.block(4 * kt + 2 + wave), __builtin_amdgcn_readlane(k_ids, kt - ids_from), p.k, p.k_page,
          p.k_head, p.k_slot, to, [](int r, int w) { return k_word<D>(r, w); });
   };
   auto load_values = [&](int kt, char* to) {
-    load(block_at(4 * kt + wave), __builtin_amdgcn_readlane(v_ids, kt - ids_from), p.v, p.v_page,
+    load(span.block(4 * kt + wave), __builtin_amdgcn_readlane(v_ids, kt - ids_from), p.v, p.v_page,
          p.v_head, p.v_slot, to, [](int r, int w) { return v_word<D>(r, w); });
   };
   constexpr int kSteps = D / 16;

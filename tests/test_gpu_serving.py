@@ -220,6 +220,24 @@ def test_attention_bad_pages_and_lengths(news):
     assert (got[at[3]:] == 0).all()
 
 
+@pytest.mark.parametrize("page", [16, 32, 64])
+@pytest.mark.parametrize("lens,news,window", [
+    ([127, 700, 64, 33], [1, 1, 1, 1], 64), ([127, 700, 90], [40, 1, 90], 40),
+    ([5000, 4800], [1, 1], 700), ([3000, 2500], [20, 30], 600), ([300, 290], [1, 3], 1),
+])
+def test_attention_pages_released_behind_the_window(page, lens, news, window):
+    """Table entries whose keys all lie before the window of a sequence's first new token
+    may hold anything."""
+    b = Batch(F16, 8, 2, 128, page, lens, news, seed=page + window)
+    want = b.call(window=window, max_q=max(news))
+    for i, (n, new) in enumerate(zip(lens, news)):
+        gone = max(n - new - window + 1, 0) // page
+        b.table[i, :gone] = torch.tensor([-1, 2 ** 31 - 1, len(b.k_pages)] * gone)[:gone]
+    got = b.call(window=window, max_q=max(news))
+    b.check(got, "released pages", window=window)
+    assert torch.equal(got, want)
+
+
 def test_attention_non_finite_keys_stay_behind_the_mask():
     """NaN and infinity among the keys reach exactly the rows that see them."""
     b = Batch(F16, 2, 1, 64, 16, [200], [100], seed=12)
