@@ -8,8 +8,12 @@
 // maximum and sum stay in the lane but for one exchange, and the weights are already
 // in the operand layout of the second product, O^T = V^T P^T, whose V columns come
 // from LDS by transposing reads. Softmax runs in base 2 with a running maximum that
-// is raised only when a score passes it by more than 8: until then weights stay below
-// 2^8, inside fp16's range, and the accumulators need no rescaling.
+// is raised only when a score passes it by more than 8: until then the accumulators need
+// no rescaling. fp16's weights are all multiplied by 2^7 (kLift), which their sum divides
+// out again: at most 2^15 then, they are inside its range, and lose digits only below 2^-21
+// of the running maximum's and vanish only below 2^-32. Unlifted, those below 2^-25 would
+// vanish from the products while their sum counts them: of 131072 keys at 2^-25.4 beside a
+// large one, 0.3% of the output.
 //
 // Two bodies, chosen per sequence by its rows (tokens x group):
 //   few_rows   up to 16 rows, memory-bound: each wave streams its own 32-key tiles
@@ -33,6 +37,8 @@ constexpr int kManyRows = 128;
 constexpr int kSplitKeys = 128;   // a part of the key axis is a multiple of this
 constexpr int kMaxSplits = 128;
 constexpr float kRaise = 8.0f;
+template <class T>
+constexpr float kLift = T::kHalf ? 7.0f : 0.0f;  // bf16 has fp32's range
 
 struct AttnParams {
   const uint16_t* q;
@@ -338,7 +344,7 @@ __device__ __forceinline__ void few_rows(const AttnParams& p, int block, Region 
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[d][e] *= f;
       }
-      const float base = m == -INFINITY ? 0.f : m;
+      const float base = m == -INFINITY ? 0.f : m - kLift<T>;
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -594,7 +600,7 @@ __device__ __forceinline__ void many_rows(const AttnParams& p, int block, char* 
       const float raised = fmaxf(m, top);
       const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - raised);
       m = raised;
-      base = m == -INFINITY ? 0.f : m;
+      base = m == -INFINITY ? 0.f : m - kLift<T>;
       l *= f;
 #pragma unroll
       for (int d = 0; d < D / 32; ++d)

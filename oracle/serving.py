@@ -19,8 +19,8 @@ _F32 = 2.0 ** -24
 def attention(q, k, v, len_new, n, scale, window, u):
     """One sequence: q [len][H][D], k and v [n][Hk][D] (fp64 arrays). The bound counts
     the rounding of the output (u |o|), of the softmax weights (u A and, where fp16
-    weights below 2^-14 lose digits, 2^-25 per key, against a sum of weights of at
-    least 1), the fp32 sums over the keys, and the error of a score, which moves a
+    weights lose digits, 2^-32 per key against a sum of weights of at least 1: half of its
+    smallest number, the largest weight being kept as 2^7 or more), the fp32 sums over the keys, and the error of a score, which moves a
     weight by as much: D products in fp32, the scaling and the base-2 exponential."""
     H, D = q.shape[1:]
     group = H // k.shape[1] if k.shape[1] else 1
@@ -40,7 +40,7 @@ def attention(q, k, v, len_new, n, scale, window, u):
             size = w @ np.abs(vv)
             ds = (D + 16) * _F32 * scale * (np.abs(kk) @ np.abs(q[t, h])).max() + 2.0 ** -20
             keys = p + 1 - lo
-            tol[t, h] = (u * np.abs(out[t, h]) + u * size + 2.0 ** -25 * np.abs(vv).sum(0)
+            tol[t, h] = (u * np.abs(out[t, h]) + u * size + 2.0 ** -32 * np.abs(vv).sum(0)
                          + (2 * keys * _F32 + 2 * ds) * (size + np.abs(out[t, h])) + 2.0 ** -25)
     return out, 1.01 * tol
 

@@ -171,6 +171,28 @@ def test_attention_large_and_small_scores():
     b.check(b.call(scale=1e-4), "scale 1e-4", scale=1e-4)
 
 
+@pytest.mark.parametrize("lens,news,hints", [
+    ([40000, 30000], [1, 1], dict(max_q=1, max_kv=1)), ([40000, 30000], [1, 1], dict(max_q=1)),
+    ([40000, 30000], [3, 4], dict(max_kv=1)), ([40000], [3], {}), ([40000, 50, 30000], [3, 1, 1], {}),
+])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_attention_many_small_weights_beside_a_large_one(dtype, lens, news, hints):
+    """One key takes nearly all the weight and its value is zero: the output is what
+    thousands of keys add whose weights are each about 2^-25.4 of it."""
+    b = Batch(dtype, 8, 1, 64, 64, lens, news, seed=41)
+    for i, n in enumerate(lens):
+        b.k[i].zero_()
+        b.k[i][0] = 2.2        # 64 x 2.2 / 8: 17.6, in base 2 25.4
+        b.v[i][:] = 1.0 + (torch.arange(n) % 5)[:, None, None].to(dtype) / 8
+        b.v[i][0] = 0
+        for j in range(-(-n // 64)):
+            part = slice(64 * j, min(n, 64 * j + 64))
+            b.k_pages[int(b.table[i, j]), :part.stop - part.start] = b.k[i][part].to(DEV)
+            b.v_pages[int(b.table[i, j]), :part.stop - part.start] = b.v[i][part].to(DEV)
+    b.q.fill_(1.0)
+    b.check(b.call(**hints), f"small weights {hints}")
+
+
 def test_attention_rising_scores():
     """Every key scores higher than the one before: the running maximum moves all along."""
     b = Batch(F16, 4, 4, 64, 16, [640, 640], [1, 64], seed=8)
