@@ -402,7 +402,7 @@ int lutgemm_qk_norm_rotate(const lutgemm_heads* h, const void* d_qkv, const int6
  * of the sequence stands at p = n - len + t and sees the keys j <= p, and with a
  * window > 0 only j > p - window:
  *   out = sum_j softmax_j(scale * q . k_j) v_j     over the keys that it sees,
- * zero for a row that sees none (p < 0). Query head h reads key head
+ * zero for a row that sees none (p < 0), NaN for one whose scores are all -infinity. Query head h reads key head
  * h / (heads / kv_heads). Scores, softmax and sums are fp32; the softmax weights
  * are rounded to the element type for the matrix product with the values; the
  * output is rounded once.

@@ -151,6 +151,13 @@ __device__ __forceinline__ int slot_of(const AttnParams& p, int blk) {
   return (blk & ((1 << (p.page_log2 - 4)) - 1)) << 4;
 }
 
+// What a row's sums are divided by: its weights' total, which is zero for a row that stands
+// before the first key (its output is zero), and for one whose scores are all minus
+// infinity, which has no softmax (0 / 0: NaN).
+__device__ __forceinline__ float inverse(float total, int pos) {
+  return total == 0.f && pos < 0 ? 0.f : 1.f / total;
+}
+
 // What a workgroup met: a page outside the cache or more keys than the table holds;
 // infinities or NaN that were taken out of the values.
 constexpr int kBad = 1, kFound = 2;
@@ -410,7 +417,7 @@ __device__ __forceinline__ void few_rows(const AttnParams& p, int block, Region 
         }
       }
       if (span.parts == 1) {
-        const float inv = total == 0.f ? 0.f : 1.f / total;
+        const float inv = inverse(total, seq.n - seq.len + (r0 + jr) / p.group);
         uint32_t* to32 = (uint32_t*)(p.out + (int64_t)token * p.o_token + hd * p.o_head + jc);
 #pragma unroll
         for (int e = 0; e < E / 2; ++e) to32[e] = T::pack(sum[2 * e] * inv, sum[2 * e + 1] * inv);
@@ -736,7 +743,7 @@ __device__ __forceinline__ void many_rows(const AttnParams& p, int block, char* 
   if (marks & kBad) l = __builtin_nanf("");
   const int token = seq.begin + tok;
   if (span.parts == 1) {
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const float inv = inverse(l, pos);
     uint16_t* dst = p.out + (int64_t)token * p.o_token + head * p.o_head + 4 * h;
 #pragma unroll
     for (int d = 0; d < D / 32; ++d)
@@ -790,7 +797,7 @@ __global__ __launch_bounds__(kThreads, 2) void mixed_kernel(AttnParams p) {
 
 template <class T, int D>
 __device__ __forceinline__ void combine_row(const AttnParams& p, int parts, int64_t row, int token,
-                                            int head) {
+                                            int head, int pos) {
   constexpr int E = D / 64, kAhead = 16;
   typedef float fE __attribute__((ext_vector_type(E)));
   const int lane = threadIdx.x & 63;
@@ -830,7 +837,7 @@ __device__ __forceinline__ void combine_row(const AttnParams& p, int parts, int6
       }
     }
   }
-  const float inv = total == 0.f ? 0.f : 1.f / total;
+  const float inv = inverse(total, pos);
   uint16_t* dst = p.out + (int64_t)token * p.o_token + head * p.o_head + lane * E;
   if constexpr (D == 128)
     *(uint32_t*)dst = T::pack(sum[0] * inv, sum[1] * inv);
@@ -852,7 +859,8 @@ __device__ __forceinline__ void combine_few(const AttnParams& p, int block) {
     const Span span = span_of<0>(p, seq, r0, min_of(r0 + kFewRows, rows));
     const int token = seq.begin + r / p.group, head = kvh * p.group + r % p.group;
     if (span.parts > 1)
-      combine_row<T, D>(p, span.parts, few_part(p, s, kvh, r), token, head);
+      combine_row<T, D>(p, span.parts, few_part(p, s, kvh, r), token, head,
+                        seq.n - seq.len + r / p.group);
   }
 }
 
@@ -909,7 +917,7 @@ __device__ __forceinline__ void combine_many(const AttnParams& p, int block) {
       for (int i = 0; i < kAhead; ++i)
         if (j + i < parts) sum += o[i] * weight(m[i]);
     }
-    sum *= total == 0.f ? 0.f : 1.f / total;
+    sum *= inverse(total, seq.n - seq.len + r / p.group);
     *(u2v*)(p.out + (int64_t)token * p.o_token + head * p.o_head + 4 * c) =
         u2v{T::pack(sum[0], sum[1]), T::pack(sum[2], sum[3])};
   }

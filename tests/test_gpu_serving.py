@@ -270,6 +270,28 @@ def test_attention_non_finite_keys_stay_behind_the_mask():
     assert torch.isfinite(got[:row]).all() and torch.isnan(got[row:]).all()
 
 
+@pytest.mark.parametrize("lens,news", [
+    ([1, 40], [1, 1]), ([40, 129], [40, 129]), ([3000, 2000], [1, 1]), ([3000], [20]),
+    ([700, 30], [130, 1]),
+])
+def test_attention_rows_whose_scores_are_all_minus_infinity(lens, news):
+    """The softmax of such a row is not defined: it is NaN, and not the zero of a row that
+    sees no key. Among finite scores minus infinity is a weight of zero."""
+    b = Batch(F16, 8, 2, 64, 16, lens, news, seed=43)
+    b.q[:, :, 3] = 1.0
+    keep = b.k_pages.clone()
+    b.k_pages[..., 3] = float("-inf")
+    assert torch.isnan(b.call()).all()
+    b.k_pages.copy_(keep)
+    for i in range(len(lens)):   # one key of many
+        if lens[i] > 5 and lens[i] - news[i] > 5:
+            b.k_pages[int(b.table[i, 0]), 4, :, 3] = float("-inf")
+            b.v[i] = torch.cat([b.v[i][:4], b.v[i][5:]])
+            b.k[i] = torch.cat([b.k[i][:4], b.k[i][5:]])
+            b.lens = b.lens[:i] + [lens[i] - 1] + b.lens[i + 1:]
+    b.check(b.call(), "one score of minus infinity")
+
+
 @pytest.mark.parametrize("dtype,heads,kv_heads,dim", [(F16, 4, 2, 128), (BF16, 3, 1, 64)])
 @pytest.mark.parametrize("lens,news,window", [
     ([200], [100], 0), ([200, 90], [5, 4], 0), ([200, 190], [1, 1], 40), ([4000], [40], 0),
