@@ -10,8 +10,8 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/AutogradState.h>
 #include <c10/hip/HIPGuard.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -69,14 +69,21 @@ int type_of(const at::Tensor& t, const char* what) {
   refuse(std::string(what) + " must be fp16 or bf16");
 }
 
-// The operators have no gradients: a graph that would silently end here is refused.
+// The operators have no gradients: a graph that would silently end here is refused, and
+// so is a forward-mode tangent, which torch.no_grad() does not switch off.
 // Bit i of `which`: argument i is a tensor or None.
 void no_gradient(PyObject* const* args, unsigned which) {
-  if (!at::GradMode::is_enabled()) return;
+  const c10::AutogradState& state = c10::AutogradState::get_tls_state();
+  const bool backward = state.get_grad_mode(), forward = state.get_fw_grad_mode();
+  if (!backward && !forward) return;
   for (; which; which &= which - 1) {
     PyObject* const o = args[__builtin_ctz(which)];
-    if (o != Py_None && THPVariable_Check(o) && THPVariable_Unpack(o).requires_grad())
+    if (o == Py_None || !THPVariable_Check(o)) continue;
+    const at::Tensor& t = THPVariable_Unpack(o);
+    if (backward && t.requires_grad())
       refuse("the operator has no gradient: call it under torch.no_grad() or on detached tensors");
+    if (forward && t._fw_grad(/*level=*/0).defined())
+      refuse("the operator has no gradient: call it on the primals of dual tensors");
   }
 }
 

@@ -7,7 +7,7 @@ torch tensors in device memory, fp16 or bf16, checked and handed over by
 shape, LutGemmError for numbers that an entry point refuses. Every call runs on the
 current stream of the tensors' device and allocates its workspace in that
 stream's order, so calls on different streams and captured graphs share nothing.
-The operators serve; they have no gradients.
+The operators serve; they have no gradients, and refuse tensors that need one.
 """
 from __future__ import annotations
 

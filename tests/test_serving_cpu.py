@@ -187,6 +187,26 @@ def test_binding_refuses_cpu_tensors_and_types():
         lg.rotary_table(8, 7)
 
 
+@pytest.mark.parametrize("which", ["qkv", "k_weight", "k_pages", "scales"])
+def test_binding_refuses_forward_mode_tangents(which):
+    """A dual tensor's tangent is not dropped without a word, under no_grad neither."""
+    from torch.autograd import forward_ad
+    h, flat = torch.zeros((2, 256), dtype=torch.float16), torch.zeros(2)
+    calls = {"qkv": (lambda t: lg.qk_norm_rotate(t, 2, 1), h),
+             "k_weight": (lambda t: lg.qk_norm_rotate(h, 2, 1, None, None, h, t), h),
+             "k_pages": (lambda t: lg.paged_attention(h.view(2, 2, 128), t, h, h, h), h),
+             "scales": (lambda t: lg.adapters_add(h, h, h, h, h, t), flat)}
+    call, t = calls[which]
+    with forward_ad.dual_level():
+        dual = forward_ad.make_dual(t, torch.ones_like(t))
+        with pytest.raises(ValueError, match="no gradient"):
+            call(dual)
+        with torch.no_grad(), pytest.raises(ValueError, match="no gradient"):
+            call(dual)
+        with pytest.raises(ValueError, match="GPU"):
+            call(forward_ad.unpack_dual(dual).primal)
+
+
 def test_packed_call_needs_adapters_and_ids_together():
     import workloads
     w = workloads.random_bcq(32, 512, 2, 128, seed=1)
