@@ -122,6 +122,12 @@ at::Tensor scratch(size_t bytes, const at::Tensor& ref) {
   return at::empty({(int64_t)bytes}, ref.options().dtype(at::kByte));
 }
 
+// A tensor of the caller's has been written: autograd tells by its version that a copy
+// kept for a backward pass is no longer what it was. Tensors of inference mode have none.
+void written(const at::Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 void check(int status, const char* where) {
   if (status != LUTGEMM_OK) throw Status{status, where};
 }
@@ -187,6 +193,7 @@ PyObject* heads(PyObject* const* a) {
     check(g_heads(&h, qkv.data_ptr(), (const int64_t*)positions, (const float*)table, qw, kw,
                   out.data_ptr(), keys.data_ptr(), nullptr, nullptr, stream_of(qkv)),
           where);
+    if (a[12] != Py_None) written(out);
     PyObject* first = THPVariable_Wrap(out);
     PyObject* second = THPVariable_Wrap(keys);
     PyObject* both = first && second ? PyTuple_Pack(2, first, second) : nullptr;
@@ -214,6 +221,9 @@ PyObject* heads(PyObject* const* a) {
                   out.data_ptr(), k.data_ptr(), v.data_ptr(), (const int64_t*)slots,
                   stream_of(qkv)),
           where);
+  written(k);
+  written(v);
+  if (a[12] != Py_None) written(out);
   return THPVariable_Wrap(out);
 }
 
@@ -283,6 +293,7 @@ PyObject* attention(PyObject* const* a) {
                     (const int32_t*)lens, (const int32_t*)starts, out.data_ptr(),
                     need ? ws.data_ptr() : nullptr, need, stream_of(q)),
         where);
+  if (a[10] != Py_None) written(out);
   return THPVariable_Wrap(out);
 }
 
@@ -329,6 +340,7 @@ PyObject* adapters(PyObject* const* a) {
                    (const int32_t*)ids, out.data_ptr(), need ? ws.data_ptr() : nullptr, need,
                    stream_of(x)),
         where);
+  if (a[6] != Py_None) written(out);
   return THPVariable_Wrap(out);
 }
 

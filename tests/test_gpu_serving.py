@@ -398,6 +398,34 @@ def test_operators_refuse_any_tensor_that_needs_gradients(which):
             b.call()
 
 
+def test_tensors_that_are_written_count_it():
+    """Autograd tells by a tensor's version that a saved one was written over."""
+    b = Batch(F16, 4, 2, 64, 16, [20], [1], seed=49)
+    qkv, table, positions, _ = _heads_case(F16, 1, 4, 2, 64, 64, False, False)
+    y, x, a, up, ids, s = _adapters_case(F16, 2, 64, 40, 8, 2, [0, 1])
+    slots = torch.zeros(1, dtype=torch.int64, device=DEV)
+    out = torch.zeros_like(b.q)
+    w = torch.ones_like(out, requires_grad=True)
+    saved = (w * out).sum()
+    calls = [
+        ((out,), lambda: b.call(out=out)),
+        ((out, b.k_pages, b.v_pages),
+         lambda: lg.qk_norm_rotate(qkv, 4, 2, positions, table, k_pages=b.k_pages, v_pages=b.v_pages,
+                                   slots=slots, out=out)),
+        ((y,), lambda: lg.adapters_add(y, x, a, up, ids, s, out=y)),
+    ]
+    for written, call in calls:
+        before = [t._version for t in written]
+        call()
+        assert [t._version for t in written] == [v + 1 for v in before]
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        saved.backward()
+    with torch.inference_mode():
+        hidden = torch.zeros_like(out)
+    lg.paged_attention(b.q, b.k_pages, b.v_pages, b.table, b.kv_lens, out=hidden)
+    assert torch.equal(hidden, b.call())
+
+
 def test_attention_padded_batch():
     """Rows behind the last sequence, in a batch much larger than its tokens, with the hints of
     a decode step, split and not."""
