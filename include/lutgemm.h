@@ -456,7 +456,8 @@ int lutgemm_paged_attention(const lutgemm_attention* a, const void* d_q, const v
  *   out_i = y_i + scales[a] * B[a] (A[a] x_i),  a = ids[i],
  * and out_i = y_i where ids[i] is outside [0, adapters): a row without an adapter.
  *   d_x    [rows][K], rows x_row apart      d_y, d_out  [rows][N], rows y_row and
- *   out_row apart; d_out may be d_y (with the same stride), not otherwise overlap it
+ *   out_row apart; d_out may be d_y (with the same stride) or lie beside x and y in
+ *   one array's rows; it is refused if it overlaps either otherwise
  *   d_a    [adapters][rank][K], contiguous  d_b  [adapters][N][rank], contiguous
  *   d_scales  fp32 [adapters], or NULL: 1   d_ids  int32 [rows], in any order
  * Sums are fp32. A x is kept to about 2^-21 of its largest entry in fp16 (a power of

@@ -900,6 +900,11 @@ extern "C" int lutgemm_adapters_add(const lutgemm_adapters* l, const void* d_x, 
         !aligned(d_scales, 4) || !aligned(d_y, 2) || !aligned(d_out, 2))
       return LUTGEMM_ERR_ALIGN;
     if (d_y == d_out && l->y_row != l->out_row) return LUTGEMM_ERR_SHAPE;
+    // workgroups read x, and y where it is not theirs, while others write their part of out
+    const Rows out{d_out, l->rows, l->out_row, l->N};
+    if ((d_y != d_out && overlap(out, {d_y, l->rows, l->y_row, l->N})) ||
+        (l->adapters > 0 && overlap(out, {d_x, l->rows, l->x_row, l->K})))
+      return LUTGEMM_ERR_SHAPE;
     const AdapterPlan r = plan(l);
     if (r.ws_bytes) {
       if (!d_workspace) return LUTGEMM_ERR_NULL;

@@ -197,6 +197,26 @@ bool apart(Axis (&&axes)[N], int64_t width) {
   return true;
 }
 
+// n rows of `width` 2-byte elements, `step` elements apart.
+struct Rows {
+  const void* at;
+  int64_t n, step, width;
+};
+
+// Whether two arrays of as many rows have memory in common. Rows of one fused buffer (the
+// same step) may lie beside each other; arrays of other steps must lie apart as a whole.
+inline bool overlap(const Rows& a, const Rows& b) {
+  if (a.n < 1 || b.n < 1 || a.width < 1 || b.width < 1) return false;
+  const __int128 a0 = (uintptr_t)a.at, b0 = (uintptr_t)b.at;
+  const __int128 a1 = a0 + 2 * ((__int128)(a.n - 1) * a.step + a.width);
+  const __int128 b1 = b0 + 2 * ((__int128)(b.n - 1) * b.step + b.width);
+  if (a1 <= b0 || b1 <= a0) return false;
+  if (a.n == 1 || b.n == 1 || a.step != b.step || a.step == 0) return true;
+  const __int128 step = 2 * (__int128)a.step;
+  const __int128 after = ((b0 - a0) % step + step) % step;  // of b's rows behind a's
+  return after < 2 * (__int128)a.width || after + 2 * (__int128)b.width > step;
+}
+
 template <class P>
 int launch(void (*kernel)(P), dim3 grid, int threads, const P& p, hipStream_t stream) {
   P copy = p;

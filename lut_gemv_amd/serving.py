@@ -91,6 +91,6 @@ def adapters_add(y, x, a, b, ids, scales=None, out=None):
     ``y`` [rows][N] and ``x`` [rows][K], the projection's output and input; ``a``
     [adapters][rank][K], ``b`` [adapters][N][rank]; ``ids`` int32 [rows], a row whose id is
     outside [0, adapters) keeps its y; ``scales`` fp32 [adapters] or None. Returns ``out``
-    (a new tensor if None; it may be ``y``).
+    (a new tensor if None; it may be ``y``, but not overlap ``x`` or ``y`` otherwise).
     """
     return (_ops or _load()).adapters_add(y, x, a, b, ids, scales, out)

@@ -736,6 +736,33 @@ def test_adapters_of_no_inputs():
     assert torch.equal(lg.adapters_add(y, x, a, b, ids, s), y)
 
 
+@pytest.mark.parametrize("rows", [5, 40, 200])
+def test_adapters_outputs_over_their_inputs_are_refused(rows):
+    """K = N: `out` may be y, not x, and no other rows of either."""
+    y, x, a, b, ids, s = _adapters_case(F16, rows, 512, 512, 16, 3, _ids(rows, 3, 5), seed=48)
+    want = lg.adapters_add(y, x, a, b, ids, s)
+    wide = torch.zeros((rows + 1, 3 * 512), dtype=F16, device=DEV)
+    wide[:rows, :512], wide[:rows, 512:1024] = x, y
+    x, y = wide[:rows, :512], wide[:rows, 512:1024]
+    for out in (x, wide[:rows, 8:520], wide[:rows, 600:1112], wide[1:, 512:1024], wide[1:, :512],
+                wide.view(-1)[64:64 + rows * 512].view(rows, 512)):
+        with pytest.raises(lg.LutGemmError, match="SHAPE"):
+            lg.adapters_add(y, x, a, b, ids, s, out=out)
+    assert torch.equal(lg.adapters_add(y, x, a, b, ids, s, out=wide[:rows, 1024:]), want)
+    assert torch.equal(lg.adapters_add(y, x, a, b, ids, s, out=y), want)
+
+
+@pytest.mark.parametrize("rows,count", [(1100, 5), (1500, 300), (130, 260)])
+@pytest.mark.parametrize("dtype,K,N,rank", [(BF16, 2056, 129, 128), (F16, 1544, 333, 40),
+                                            (BF16, 4104, 256, 64), (F16, 520, 72, 24)])
+def test_adapters_of_sorted_rows(dtype, K, N, rank, rows, count):
+    """Rows sorted by a launch of its own, with wide ranks, K in several parts and odd N."""
+    case = _adapters_case(dtype, rows, K, N, rank, count, _ids(rows, count, rows + count), seed=rows)
+    got = lg.adapters_add(*case)
+    _adapters_check(got, *case, f"{rows} rows, {count} adapters, {K}->{N}, rank {rank}")
+    assert torch.equal(got, lg.adapters_add(*case))
+
+
 def test_adapters_graph_and_streams():
     case = _adapters_case(BF16, 100, 1024, 512, 32, 9, _ids(100, 9, 3), seed=35)
     want = lg.adapters_add(*case)

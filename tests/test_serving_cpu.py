@@ -163,6 +163,30 @@ def test_adapters_refusals(change, status):
     assert _adapters(**change) == status
 
 
+@pytest.mark.parametrize("change", [
+    dict(x=2 * A, K=40, x_row=40),                                   # x itself
+    dict(x=2 * A + 16, x_row=64), dict(x=2 * A - 16, x_row=64),      # x, other rows' steps
+    dict(x=2 * A + 80 * 80 - 16, x_row=64), dict(x=2 * A - 2 * (79 * 64 + 64) + 16),
+    dict(y=2 * A + 2), dict(y=2 * A - 2), dict(y=2 * A + 80), dict(y=2 * A, y_row=48, out_row=40),
+    dict(x=2 * A + 64, x_row=104, out_row=104), dict(y=2 * A + 78, y_row=200, out_row=200),
+    dict(x=2 * A + 80, x_row=96, out_row=96), dict(y=2 * A + 80 * 99, y_row=80, out_row=79),
+    dict(rows=1, x=2 * A + 64), dict(rows=1, y=2 * A - 78, y_row=0, out_row=0),
+])
+def test_adapters_outputs_over_their_inputs_are_refused(change):
+    assert _adapters(**{**dict(x=4 * A, y=6 * A), **change}) == SHAPE
+
+
+@pytest.mark.parametrize("change", [
+    dict(y=2 * A), dict(x=2 * A + 80 * 80), dict(x=2 * A - 2 * (79 * 64 + 64)),
+    dict(x=2 * A + 80, x_row=104, out_row=104), dict(x=2 * A - 128, x_row=104, out_row=104),
+    dict(y=2 * A + 80, y_row=80, out_row=80), dict(y=2 * A - 80, y_row=80, out_row=80),
+    dict(rows=1, x=2 * A + 80), dict(rows=1, y=2 * A - 80), dict(adapters=0, x=2 * A, K=40, x_row=40),
+])
+def test_adapters_outputs_beside_their_inputs_are_not(change):
+    """Another error is the first to be found (no workspace): nothing is launched."""
+    assert _adapters(**{**dict(x=4 * A, y=6 * A, ws=None, rank=128), **change}) == NULL
+
+
 def test_adapters_empty_calls():
     assert _adapters(rows=0) == 0 and _adapters(N=0) == 0
     assert lg.lib().lutgemm_adapters_add(None, A, A, A, A, A, A, A, A, 0, None) == NULL
