@@ -367,7 +367,7 @@ typedef enum lutgemm_type { LUTGEMM_F16 = 0, LUTGEMM_BF16 = 1 } lutgemm_type;
  *   d_table  fp32 [positions][rotary], contiguous (ignored when rotary is 0)
  *   d_q_weight, d_k_weight  [head_dim] of the same type, or both NULL
  *   d_q      [tokens][heads][head_dim], row t at t * q_token; may be the query
- *            part of d_qkv itself
+ *            part of d_qkv itself, and is refused if it overlaps d_qkv otherwise
  *   d_k, d_v  cache pages [pages][page_size][kv_heads][head_dim] with strides
  *            (k_page, k_slot, k_head) and (v_page, v_slot, v_head)
  *   d_slots  int64 [tokens]: the token's key and value go to slot
@@ -406,7 +406,9 @@ int lutgemm_qk_norm_rotate(const lutgemm_heads* h, const void* d_qkv, const int6
  * h / (heads / kv_heads). Scores, softmax and sums are fp32; the softmax weights
  * are rounded to the element type for the matrix product with the values; the
  * output is rounded once.
- *   d_q, d_out  [tokens][heads][head_dim], strides (q_token, q_head), (o_token, o_head)
+ *   d_q, d_out  [tokens][heads][head_dim], strides (q_token, q_head), (o_token, o_head);
+ *               d_out may be d_q (with the same strides) or lie beside it in one array's
+ *               rows, and is refused if it overlaps it otherwise
  *   d_k, d_v    pages [pages][page_size][kv_heads][head_dim], strides as in lutgemm_heads
  *   d_table     int32 [seqs][table_width], rows table_stride apart: key j of sequence
  *               s is in page table[s][j / page_size]; entries past a sequence's

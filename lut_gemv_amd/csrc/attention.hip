@@ -1108,6 +1108,19 @@ extern "C" int lutgemm_paged_attention(const lutgemm_attention* a, const void* d
     if (!aligned(d_q, 16) || !aligned(d_k, 16) || !aligned(d_v, 16) || !aligned(d_out, 16) ||
         !aligned(d_table, 4) || !aligned(d_kv_lens, 4) || !aligned(d_q_starts, 4))
       return LUTGEMM_ERR_ALIGN;
+    // a workgroup has read its own rows of q before it writes them, but no other's
+    const bool in_place = d_out == d_q && (a->tokens == 1 || a->o_token == a->q_token) &&
+                          (a->heads == 1 || a->o_head == a->q_head);
+    auto tokens_of = [&](const void* at, int64_t token, int64_t head) {
+      return Rows{at, a->tokens, token, (a->heads - 1) * head + a->head_dim};
+    };
+    auto heads_of = [&](const void* at, int64_t token, int64_t head) {
+      return Rows{at, a->heads, head, (a->tokens - 1) * token + a->head_dim};
+    };
+    if (!in_place &&
+        overlap(tokens_of(d_out, a->o_token, a->o_head), tokens_of(d_q, a->q_token, a->q_head)) &&
+        overlap(heads_of(d_out, a->o_token, a->o_head), heads_of(d_q, a->q_token, a->q_head)))
+      return LUTGEMM_ERR_SHAPE;
     const AttnPlan r = plan(a);
     // a launch has fewer than 2^32 threads along each axis of its grid
     constexpr int64_t kMost = (int64_t)1 << 24;

@@ -249,6 +249,12 @@ extern "C" int lutgemm_qk_norm_rotate(const lutgemm_heads* h, const void* d_qkv,
         !aligned(d_table, 16) || !aligned(d_q_weight, 16) || !aligned(d_k_weight, 16) ||
         !aligned(d_positions, 8) || !aligned(d_slots, 8))
       return LUTGEMM_ERR_ALIGN;
+    // a thread writes the queries that it has read, where other threads' heads do not lie
+    const int64_t dim = h->head_dim;
+    if (!(d_q == d_qkv && (h->tokens == 1 || h->q_token == h->qkv_token)) &&
+        overlap({d_q, h->tokens, h->q_token, h->heads * dim},
+                {d_qkv, h->tokens, h->qkv_token, (h->heads + 2 * (int64_t)h->kv_heads) * dim}))
+      return LUTGEMM_ERR_SHAPE;
     int cus = 0;
     st = serve::check_device(&cus);
     if (st) return st;

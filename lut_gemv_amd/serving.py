@@ -60,8 +60,9 @@ def qk_norm_rotate(qkv, heads: int, kv_heads: int, positions=None, table=None, q
     for no norm; ``k_pages``, ``v_pages`` [pages][page_size][kv_heads][head_dim], of any
     strides over the head dimension, and ``slots`` int64 [tokens], the cache slots of the
     tokens (one outside the cache is not written).
-    Returns the queries [tokens][heads][head_dim] (in ``out`` if given); without a
-    cache, the queries and the keys [tokens][kv_heads][head_dim].
+    Returns the queries [tokens][heads][head_dim] (in ``out`` if given, which may be
+    ``qkv``'s own query part); without a cache, the queries and the keys
+    [tokens][kv_heads][head_dim].
     """
     return (_ops or _load()).qk_norm_rotate(qkv, heads, kv_heads, positions, table, q_weight, k_weight,
                                             eps, interleaved, k_pages, v_pages, slots, out)
@@ -78,7 +79,7 @@ def paged_attention(q, k_pages, v_pages, page_table, kv_lens, q_starts=None, max
     of the last (None: one new token each). ``max_q`` and ``max_kv``, the most new tokens and keys
     of one sequence, help to choose the launch (None: no bound known). ``scale``: None for
     head_dim ** -0.5; ``window``: the last so many keys only, 0 for all. Returns
-    [tokens][heads][head_dim] (in ``out`` if given).
+    [tokens][heads][head_dim] (in ``out`` if given, which may be ``q``).
     """
     return (_ops or _load()).paged_attention(q, k_pages, v_pages, page_table, kv_lens, q_starts, max_q,
                                              max_kv, scale, window, out)

@@ -446,6 +446,23 @@ def test_outputs_that_overlap_are_refused():
     b.check(b.call(out=turned), "heads outside tokens")
 
 
+def test_attention_output_in_place_of_the_queries():
+    """`out` may be `q` itself, for single tokens, chunks, parts; it may not overlap it
+    otherwise."""
+    for lens, news in (([40, 3000], [1, 1]), ([300, 70], [130, 70]), ([3000], [20])):
+        b = Batch(F16, 8, 2, 64, 16, lens, news, seed=47)
+        want = b.call()
+        fused = torch.zeros((len(b.q), 24, 64), dtype=F16, device=DEV)
+        fused[:, 4:12] = b.q
+        b.q = fused[:, 4:12]
+        for out in (fused[:, 3:11], fused[:, 8:16], fused.view(-1)[256:256 + want.numel()].view_as(want)):
+            with pytest.raises(lg.LutGemmError, match="SHAPE"):
+                b.call(out=out)
+        assert torch.equal(b.call(out=fused[:, 12:20]), want)
+        assert torch.equal(b.call(out=b.q), want)
+        assert (fused[:, :4] == 0).all() and (fused[:, 20:] == 0).all()
+
+
 def test_attention_far_pages():
     """Pages more than 2^32 bytes, and 2^31 elements, into the cache."""
     pages = (1 << 31) // (64 * 8 * 128) + 40
@@ -619,6 +636,22 @@ def test_heads_larger_than_the_caches(dtype):
     _inside(q[some], qw, qb, "queries")
     _inside(k_pages.reshape(-1, kv, dim)[slots[some]], kw, kb, "keys")
     assert np.array_equal(_np(v_pages.reshape(-1, kv, dim)[slots[some]]), vw)
+
+
+def test_heads_outputs_over_other_parts_of_qkv_are_refused():
+    qkv, table, positions, _ = _heads_case(F16, 6, 2, 1, 64, 64, False, False, seed=46)
+    before = qkv.clone()
+    heads = qkv.view(6, 4, 64)
+    for out in (heads[:, 1:3], heads[:, 2:4], qkv.view(-1)[:6 * 128].view(6, 2, 64)):
+        with pytest.raises(lg.LutGemmError, match="SHAPE"):
+            lg.qk_norm_rotate(qkv, 2, 1, positions, table, out=out)
+    assert torch.equal(qkv, before)
+    want, _ = lg.qk_norm_rotate(qkv, 2, 1, positions, table)
+    wide = torch.zeros((6, 6, 64), dtype=F16, device=DEV)   # the queries beside qkv's own rows
+    wide[:, 2:] = heads
+    inner = wide.view(6, -1)[:, 128:]
+    got, _ = lg.qk_norm_rotate(inner, 2, 1, positions, table, out=wide[:, :2])
+    assert torch.equal(got, want) and torch.equal(wide[:, 2:], heads)
 
 
 def test_rotary_table_is_rounded_from_64_bits():

@@ -88,6 +88,29 @@ def test_attention_workspace_stays_small(change):
     assert 0 < n.value < 80 << 20
 
 
+@pytest.mark.parametrize("change", [
+    dict(out=A + 16), dict(out=A - 16), dict(out=A + 256), dict(out=A - 256),
+    dict(q_token=2048, o_token=2048, out=A + 1920), dict(q_token=2048, o_token=2048, out=A - 1920),
+    dict(q_token=2048, out=A), dict(q_head=256, q_token=2048, o_token=2048, out=A),
+    dict(q_token=2048, out=A + 29 * 4096),
+    dict(q_token=128, q_head=3840, o_token=128, o_head=3840, out=A + 256),  # heads outside tokens
+])
+def test_attention_outputs_over_the_queries_are_refused(change):
+    assert _attention(**change) == SHAPE
+
+
+@pytest.mark.parametrize("change", [
+    dict(), dict(q=2 * A), dict(q_token=2048, o_token=2048, out=A + 2048),
+    dict(q_token=2048, o_token=2048, out=A - 2048), dict(out=A + 30 * 2048), dict(out=A - 30 * 2048),
+    dict(q_token=128, q_head=3840, o_token=128, o_head=3840),
+    dict(q_token=128, q_head=7680, o_token=128, o_head=7680, out=A + 2 * 3840),  # heads outside tokens
+])
+def test_attention_outputs_in_place_or_beside_the_queries_are_not(change):
+    """Another error is the first to be found (no workspace): nothing is launched."""
+    long = dict(seqs=1, max_kv=65536, table_width=4096)
+    assert _attention(**{**long, **change}) == NULL
+
+
 def test_attention_empty_calls_and_workspace():
     assert _attention(tokens=0) == 0 and _attention(tokens=0, seqs=0, starts=None) == 0
     L = lg.lib()
@@ -130,6 +153,14 @@ def _heads(qkv=A, at=A, table=A, qw=A, kw=A, q=A, k=A, v=A, slots=A, **change):
 ])
 def test_heads_refusals(change, status):
     assert _heads(**change) == status
+
+
+@pytest.mark.parametrize("change", [
+    dict(q=A), dict(q=A + 16, q_token=512), dict(q=A + 512, q_token=512), dict(q=A + 1008, q_token=512),
+    dict(q=A - 16, q_token=512), dict(q=A + 4 * 1024 + 1008), dict(tokens=1, q=A + 128),
+])
+def test_heads_outputs_over_other_parts_of_qkv_are_refused(change):
+    assert _heads(**{**dict(k=2 * A, v=3 * A), **change}) == SHAPE
 
 
 def test_heads_empty_call():
