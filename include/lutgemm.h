@@ -359,7 +359,8 @@ typedef enum lutgemm_type { LUTGEMM_F16 = 0, LUTGEMM_BF16 = 1 } lutgemm_type;
  *                = (n[2i], n[2i + 1])                            (interleaved = 1)
  *   a' = a cos_i - b sin_i, b' = b cos_i + a sin_i; entries from R on are kept,
  * with cos_i = table[p][i], sin_i = table[p][R/2 + i], p = positions[t]. fp32
- * throughout, rounded once at the end. Values are copied.
+ * throughout, rounded once at the end: heads of which mean(x^2) + eps leaves its range
+ * (bf16 entries from about 2^60 on, or below 2^-70 with eps = 0) have no norm. Values are copied.
  *   d_qkv    [tokens][heads + 2 kv_heads][head_dim], rows qkv_token apart:
  *            queries, keys, values
  *   d_positions int64 [tokens]; a position outside [0, positions) makes the

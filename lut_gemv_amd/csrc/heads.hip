@@ -89,9 +89,18 @@ __device__ __forceinline__ float sum_lanes(float v, int log2) {
   return v;
 }
 
+// 1 / sqrt(v). The instruction takes v below the normal numbers for zero.
+template <bool Tiny>
+__device__ __forceinline__ float inverse_root(float v) {
+  const bool small = Tiny && v < 0x1p-126f;
+  return __builtin_amdgcn_rsqf(small ? v * 0x1p64f : v) * (small ? 0x1p32f : 1.f);
+}
+
 // Once: the heads do not stay in the L2 until their next reader, and pass it by
-// (8192 tokens: 60.3 us, without the hint 64.2).
-template <class T, bool Once>
+// (8192 tokens: 60.3 us, without the hint 64.2). Tiny: eps lies below the normal numbers, and
+// mean squares may (a kernel of its own: with the test for it, or a branch on the launch's
+// eps, it takes 73 registers in place of 72, a wave less to a SIMD, and 59.5 us in place of 58.8).
+template <class T, bool Once, bool Tiny>
 __global__ __launch_bounds__(kThreads) void heads_kernel(HeadsParams p) {
   fetch(p);
   const int64_t t = blockIdx.x;
@@ -171,7 +180,7 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(HeadsParams p) {
           sum = __builtin_fmaf(b[i], b[i], sum);
         }
         sum = sum_lanes(active ? sum : 0.f, p.lanes_log2);
-        const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(sum, p.inv_dim, p.eps));
+        const float r = inverse_root<Tiny>(__builtin_fmaf(sum, p.inv_dim, p.eps));
         unpack16<T>(is_q ? qw0 : kw0, wa);
         unpack16<T>(is_q ? qw1 : kw1, wb);
 #pragma unroll
@@ -194,6 +203,12 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(HeadsParams p) {
     write(to + c0, w0);
     write(to + c1, w1);
   }
+}
+
+template <class T>
+auto pick(bool once, bool tiny) {
+  return once ? tiny ? heads_kernel<T, true, true> : heads_kernel<T, true, false>
+              : tiny ? heads_kernel<T, false, true> : heads_kernel<T, false, false>;
 }
 
 int check_heads(const lutgemm_heads* h, bool paged) {
@@ -295,10 +310,9 @@ extern "C" int lutgemm_qk_norm_rotate(const lutgemm_heads* h, const void* d_qkv,
     p.all = all;
     const dim3 grid((unsigned)h->tokens, (unsigned)((groups + p.walk - 1) / p.walk));
     const bool once = (int64_t)h->tokens * all * h->head_dim * 2 > (int64_t)32 << 20;  // the L2s
-    const bool f16 = h->type == LUTGEMM_F16;
-    return serve::launch(once ? f16 ? heads_kernel<serve::F16, true> : heads_kernel<serve::BF16, true>
-                         : f16 ? heads_kernel<serve::F16, false>
-                               : heads_kernel<serve::BF16, false>,
+    const bool tiny = d_q_weight && h->eps < 0x1p-126f;
+    return serve::launch(h->type == LUTGEMM_F16 ? pick<serve::F16>(once, tiny)
+                                                : pick<serve::BF16>(once, tiny),
                          grid, kThreads, p, (hipStream_t)stream);
   } catch (...) {
     return LUTGEMM_ERR_INTERNAL;

@@ -638,6 +638,34 @@ def test_heads_larger_than_the_caches(dtype):
     assert np.array_equal(_np(v_pages.reshape(-1, kv, dim)[slots[some]]), vw)
 
 
+@pytest.mark.parametrize("eps", [0.0, 1e-40])
+def test_heads_mean_squares_below_the_normal_numbers(eps):
+    """Squares of about 1e-39, and heads of zeros beside an epsilon below 2^-126."""
+    qkv, table, positions, w = _heads_case(BF16, 9, 4, 2, 128, 64, False, True, seed=45)
+    qkv = (qkv.float() * 3e-20).to(BF16)
+    if eps:
+        qkv[4] = 0
+    q, k = lg.qk_norm_rotate(qkv, 4, 2, positions, table, *w, eps=eps)
+    eps = float(np.float32(eps))
+    (qw, qb), (kw, kb), _ = _heads_want(qkv, table, positions, w, 4, 2, 128, False, eps, U[BF16])
+    _inside(q, qw, qb, "queries")
+    _inside(k, kw, kb, "keys")
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("tokens", [3, 1700])
+def test_heads_of_zeros_with_a_tiny_epsilon(dtype, tokens):
+    """0 / sqrt(1e-40) is zero, in launches of both sizes; other heads have their norm."""
+    qkv, table, positions, w = _heads_case(dtype, tokens, 64, 8, 128, 128, True, True, seed=47)
+    qkv[1] = 0
+    q, k = lg.qk_norm_rotate(qkv, 64, 8, positions, table, *w, eps=1e-40, interleaved=True)
+    assert (q[1] == 0).all() and (k[1] == 0).all()
+    (qw, qb), (kw, kb), _ = _heads_want(qkv[:3], table, positions[:3], w, 64, 8, 128, True,
+                                        float(np.float32(1e-40)), U[dtype])
+    _inside(q[:3], qw, qb, "queries")
+    _inside(k[:3], kw, kb, "keys")
+
+
 def test_heads_outputs_over_other_parts_of_qkv_are_refused():
     qkv, table, positions, _ = _heads_case(F16, 6, 2, 1, 64, 64, False, False, seed=46)
     before = qkv.clone()
