@@ -164,6 +164,15 @@ def test_attention_more_sequences_than_lanes(heads, kv_heads, dim):
     b.check(b.call(), "131 sequences")
 
 
+@pytest.mark.parametrize("window", [0, 8500])
+@pytest.mark.parametrize("dtype,heads,kv_heads,dim", [(F16, 8, 2, 64), (BF16, 4, 1, 128)])
+def test_attention_chunks_on_long_unsplit_keys(dtype, heads, kv_heads, dim, window):
+    """A launch made for short sequences takes a long key axis in one part: the pages'
+    numbers are read 64 tiles at a time."""
+    b = Batch(dtype, heads, kv_heads, dim, 16, [9000, 8300, 4200], [20, 17, 9], seed=44)
+    b.check(b.call(max_kv=1, window=window), f"one part, window {window}", window=window)
+
+
 def test_attention_large_and_small_scores():
     """Scores of some hundreds, where one key takes all the weight, and a small scale."""
     b = Batch(F16, 8, 2, 128, 16, [900, 33], [20, 1], seed=7, scale=4.0)
