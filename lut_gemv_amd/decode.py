@@ -208,6 +208,17 @@ class DecodeStack:
             return 0
         return self.layers * self.m * (self.context + 1) * 2 * self.heads * HEAD_DIM * 2
 
+    def adapter_bytes_per_step(self) -> int:
+        """Bytes of the adapters that one decode step's sequences use (all layers)."""
+        used = min(self.adapters, self.m)
+        return sum(2 * used * a.shape[1] * (p.K + p.N)
+                   for lw in self.lora for p in self.projs for a in lw[p.name][:1])
+
+    def read_bytes_per_step(self) -> int:
+        """All that one decode step reads: packed weights, cache and adapters."""
+        return (self.bytes_per_step() + self.cache_bytes_per_step()
+                + self.adapter_bytes_per_step())
+
     # ------------------------------------------------------------ one token
     def _src(self, p: Projection, x_layer):
         if p.src == "qkv" and self.context:
@@ -270,7 +281,8 @@ class DecodeStack:
 
     def time_tokens(self, kernel: str = "lut", tokens: int = 20, warmup: int = 5) -> dict:
         """Time of one decode step (one token for each of the m sequences),
-        replaying the captured step graph `tokens` times."""
+        replaying the captured step graph `tokens` times. The rate is that of all
+        that the step reads."""
         import torch
         if self.graph is None or self.graph_kernel != kernel:
             self.capture(kernel)
@@ -288,8 +300,7 @@ class DecodeStack:
         ms = e0.elapsed_time(e1) / tokens
         return {"kernel": kernel, "ms_per_step": ms, "wall_ms_per_step": wall,
                 "tokens_per_s": self.m / (ms * 1e-3),
-                "GBps": self.bytes_per_step() / (ms * 1e-3) / 1e9}
-
+                "GBps": self.read_bytes_per_step() / (ms * 1e-3) / 1e9}
 
     def time_projection(self, name: str, kernel: str = "lut", reps: int = 10,
                         warmup: int = 3) -> dict:
@@ -367,13 +378,14 @@ def main(argv=None) -> int:
           f"weights, set up in {setup_s:.1f} s", flush=True)
     res = {}
     kernels = ["lut", "dequant"] if a.kernel == "both" else [a.kernel]
+    read = ", ".join(["weights"] + ["cache"] * bool(a.context) + ["adapters"] * bool(a.adapters))
     for k in kernels:
         r = st.time_tokens(k, a.tokens, a.warmup)
         y = st.outs[st.out_name]
         r["finite"] = bool(torch.isfinite(y).all().item())
         res[k] = r
         print(f"[decode] {k}: {r['ms_per_step']:.3f} ms per step of {st.m} token(s) "
-              f"({r['tokens_per_s']:.0f} tokens/s, {r['GBps']:.0f} GB/s of weights)", flush=True)
+              f"({r['tokens_per_s']:.0f} tokens/s, {r['GBps']:.0f} GB/s of {read})", flush=True)
     if a.breakdown:
         for k in kernels:
             rows = []
@@ -389,8 +401,10 @@ def main(argv=None) -> int:
     if a.context:
         line.update(context=a.context, cache_bytes_per_step=st.cache_bytes_per_step())
     if a.adapters:
-        line.update(adapters=a.adapters, rank=a.rank)
-    if "lut" in res and "dequant" in res:
+        line.update(adapters=a.adapters, rank=a.rank,
+                    adapter_bytes_per_step=st.adapter_bytes_per_step())
+    # the products' ratio: with a cache or adapters both steps hold the same time besides
+    if "lut" in res and "dequant" in res and not (a.context or a.adapters):
         line["dequant_over_lut"] = res["dequant"]["ms_per_step"] / res["lut"]["ms_per_step"]
     print(json.dumps(line), flush=True)
     return 0

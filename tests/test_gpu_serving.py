@@ -951,3 +951,61 @@ def test_decode_stack_with_a_cache(model, adapters):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(st.outs[st.out_name], eager), f"replay {r}"
+
+
+def test_decode_stack_adds_the_adapters_of_every_projection():
+    """Each projection's output in a step is its product and then its adapters, those of
+    sequence i being adapter i modulo their number."""
+    from lut_gemv_amd import decode
+    st = decode.DecodeStack("llama7b", layers=1, q=2, g=128, m=3, device=DEV, context=70, page_size=16,
+                            adapters=2, rank=8)
+    st.token()
+    torch.cuda.synchronize()
+    for p in st.projs:
+        src = st._src(p, st.x).contiguous()
+        product = st.weights[0][p.name](src)
+        a, b = st.lora[0][p.name]
+        assert not torch.equal(st.outs[p.name], product)
+        cols = torch.arange(0, p.N, 37, device=DEV)
+        want, bound = plain.adapters(_np(product[:, cols]), _np(src), _np(a), _np(b[:, cols]), [0, 1, 0],
+                                     None, U[F16], 2.0 ** -21)
+        _inside(st.outs[p.name][:, cols], want, bound, p.name)
+
+
+def test_decode_stack_attends_in_every_layer(monkeypatch):
+    """Each layer's queries, keys and attention are those of its own QKV output and cache."""
+    from lut_gemv_amd import decode
+    st = decode.DecodeStack("llama7b", layers=2, q=2, g=128, m=2, device=DEV, context=90, page_size=16)
+    left, attend = [], st._attend
+
+    def noted(layer):
+        attend(layer)
+        left.append([st.outs["qkv"].clone(), st.queries.clone(), st.attended.clone()])
+
+    monkeypatch.setattr(st, "_attend", noted)
+    st.token()
+    assert len(left) == 2 and not torch.equal(left[0][2], left[1][2])
+    angle = _np(st.rotary[90])[None].repeat(2, 0)
+    for layer, (qkv, queries, attended) in enumerate(left):
+        x = _np(qkv).reshape(2, 3 * st.heads, 128)
+        want, bound = plain.heads(x[:, :st.heads], None, 0.0, angle[:, :64], angle[:, 64:], False, U[F16])
+        _inside(queries, want, bound, f"queries of layer {layer}")
+        k_pages, v_pages = st.caches[layer]
+        for i in range(2):
+            ks, vs = (t[st.page_table[i].long()].flatten(0, 1)[:91] for t in (k_pages, v_pages))
+            assert np.array_equal(_np(vs[90]), x[i, 2 * st.heads:])
+            want, bound = plain.attention(_np(queries[i:i + 1]), _np(ks), _np(vs), 1, 91, 128 ** -0.5, 0,
+                                          U[F16])
+            _inside(attended.view(2, st.heads, 128)[i:i + 1], want, bound, f"layer {layer} sequence {i}")
+
+
+@pytest.mark.parametrize("extra", [{}, dict(context=100, adapters=3, rank=8)])
+def test_decode_rate_counts_all_that_a_step_reads(extra):
+    from lut_gemv_amd import decode
+    st = decode.DecodeStack("llama7b", layers=1, q=2, g=128, m=2, device=DEV, page_size=16, **extra)
+    read = st.bytes_per_step()
+    if extra:
+        entries = sum(p.K + p.N for p in st.projs)
+        read += 2 * 101 * 2 * 4096 * 2 + 2 * 2 * 8 * entries   # two sequences, two of three adapters
+    r = st.time_tokens(tokens=2, warmup=1)
+    assert r["GBps"] == pytest.approx(read / (r["ms_per_step"] * 1e-3) / 1e9, rel=1e-9)
