@@ -6,10 +6,12 @@ two are linked into one shared library next to this file. The same sources
 built with ``-DLUTGEMM_PHASE_TRACE`` give ``liblutgemm_trace.so``, the variant
 whose kernels stamp their phase boundaries (``lutgemm_trace_attach``; read by
 ``python -m lut_gemv_amd.phases``). ``_binding.so`` takes the serving operators'
-torch tensors to the library; it is built against the installed torch.
+torch tensors to the library; it is built against the installed torch, and left
+out where there is none, as the C library needs it not.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -123,7 +125,12 @@ def build(verbose: bool = False, extra_hip_flags=(), trace: bool = True) -> str:
                 jobs.append([HIPCC, *HIP_FLAGS, *extra_hip_flags, *defs, *incs, f"-DLUTGEMM_Q={q}",
                              "-c", "-Rpass-analysis=kernel-resource-usage",
                              os.path.join(CSRC, "lutgemv_q.hip"), "-o", o])
-        jobs.append(_binding_job(os.path.join(tmp, "_binding.so")))
+        binding = None
+        if importlib.util.find_spec("torch") is None:
+            print("torch is not installed: _binding.so is not built", file=sys.stderr)
+        else:
+            binding = os.path.join(tmp, "_binding.so")
+            jobs.append(_binding_job(binding))
         workers = max(1, min(len(jobs), int(os.environ.get("MAX_JOBS", os.cpu_count() or 1))))
         with ThreadPoolExecutor(max_workers=workers) as ex:
             outs = [f.result() for f in [ex.submit(_run, j, False) for j in jobs]]
@@ -137,8 +144,9 @@ def build(verbose: bool = False, extra_hip_flags=(), trace: bool = True) -> str:
             _run([HIPCC, "-shared", "-fPIC", f"--offload-arch={ARCH}", *ob,
                   "-pthread", "-o", out_tmp], verbose)
             os.replace(out_tmp, path)
-        shutil.copyfile(os.path.join(tmp, "_binding.so"), BINDING_PATH + ".tmp")
-        os.replace(BINDING_PATH + ".tmp", BINDING_PATH)
+        if binding:
+            shutil.copyfile(binding, BINDING_PATH + ".tmp")
+            os.replace(BINDING_PATH + ".tmp", BINDING_PATH)
     finally:
         shutil.rmtree(tmp, ignore_errors=True)
     return LIB_PATH

@@ -279,6 +279,31 @@ def test_decode_stack_arguments():
             decode.DecodeStack("llama7b", layers=1, device="cpu", **kw)
 
 
+@pytest.mark.parametrize("torch_found", [True, False])
+def test_the_library_builds_without_torch(torch_found, tmp_path, monkeypatch):
+    """Where torch is not installed the C library is built, and only the binding is not."""
+    from lut_gemv_amd import build
+    calls = []
+
+    def run(cmd, verbose):
+        calls.append(cmd)
+        open(cmd[cmd.index("-o") + 1], "w").close()
+        return ""
+
+    monkeypatch.setattr(build, "_run", run)
+    for name in ("LIB_PATH", "TRACE_LIB_PATH", "BINDING_PATH"):
+        monkeypatch.setattr(build, name, str(tmp_path / name))
+    if not torch_found:
+        find = build.importlib.util.find_spec
+        monkeypatch.setattr(build.importlib.util, "find_spec",
+                            lambda name, *a: None if name == "torch" else find(name, *a))
+        monkeypatch.setattr(build, "_binding_job", None)
+    assert build.build() == str(tmp_path / "LIB_PATH")
+    built = sorted(f.name for f in tmp_path.iterdir())
+    assert built == ["BINDING_PATH"] * torch_found + ["LIB_PATH", "TRACE_LIB_PATH"]
+    assert any(cmd[-1] == str(tmp_path / "LIB_PATH.tmp") for cmd in calls)
+
+
 def test_descriptors_match_the_header(tmp_path):
     cc = shutil.which("gcc") or shutil.which("cc")
     if cc is None:
