@@ -403,8 +403,8 @@ int lutgemm_qk_norm_rotate(const lutgemm_heads* h, const void* d_qkv, const int6
  * of the sequence stands at p = n - len + t and sees the keys j <= p, and with a
  * window > 0 only j > p - window:
  *   out = sum_j softmax_j(scale * q . k_j) v_j     over the keys that it sees,
- * zero for a row that sees none (p < 0), NaN for one whose scores are all -infinity. Query head h reads key head
- * h / (heads / kv_heads). Scores, softmax and sums are fp32; the softmax weights
+ * zero for a row that sees none (p < 0), NaN for one whose scores are all -infinity.
+ * Query head h reads key head h / (heads / kv_heads). Scores, softmax and sums are fp32; the softmax weights
  * are rounded to the element type for the matrix product with the values; the
  * output is rounded once.
  *   d_q, d_out  [tokens][heads][head_dim], strides (q_token, q_head), (o_token, o_head);
@@ -423,7 +423,8 @@ int lutgemm_qk_norm_rotate(const lutgemm_heads* h, const void* d_qkv, const int6
  * make other rows of the sequence NaN; a kv_lens[s] larger than table_width *
  * page_size makes all rows of the sequence NaN; a negative one counts as 0. Slots past
  * a sequence's last key are not read, whatever they hold. A NaN or infinity among a
- * sequence's keys or values reaches the rows that see it and no others.
+ * sequence's keys or values reaches the rows that see it and no others (a key whose
+ * score is -infinity has a weight of zero).
  * max_q and max_kv say how many new tokens and keys the host expects one sequence
  * to have at most; the launch is chosen by them, results are right without them
  * being so. Results for the same sizes, max_q and max_kv are bitwise reproducible.
@@ -465,7 +466,8 @@ int lutgemm_paged_attention(const lutgemm_attention* a, const void* d_q, const v
  *   d_scales  fp32 [adapters], or NULL: 1   d_ids  int32 [rows], in any order
  * Sums are fp32. A x is kept to about 2^-21 of its largest entry in fp16 (a power of
  * two per row and a pair of fp16 numbers per entry) and to 2^-16 of each entry in
- * bf16 (a pair of bf16 numbers); out is rounded once. A row's result does not depend
+ * bf16 (a pair of bf16 numbers); out is rounded once. An infinity in b makes the outputs
+ * of its column infinite or NaN. A row's result does not depend
  * on the other rows' ids.
  *   d_workspace  at least lutgemm_adapters_workspace bytes; as for attention.
  * Shape rules: 0 <= rows <= 65535, K a multiple of 8 below 2^23, N below 2^23, rank a

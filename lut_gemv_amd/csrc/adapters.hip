@@ -12,8 +12,8 @@
 // a pair of numbers, high + low, of the element type: the pair's error is far below
 // the rounding of the output, for two small matrix products in place of one.
 //
-// 61 rows of 24 adapters of rank 64, K = 11008, N = 4096 (49 MB): 16.5 us, 2.9 TB/s;
-// 4096 rows of 8, K = N = 8192, rank 32 (210 MB): 57 us, 3.7 TB/s, of them 8 sorting.
+// 61 rows of 24 adapters of rank 64, K = 11008, N = 4096 (49 MB): 16.8 us, 2.9 TB/s;
+// 4096 rows of 8, K = N = 8192, rank 32 (210 MB): 56 us, 3.7 TB/s, of them 8 sorting.
 #include "serve.h"
 
 namespace lutgemm {

@@ -15,6 +15,10 @@
 // vanish from the products while their sum counts them: of 131072 keys at 2^-25.4 beside a
 // large one, 0.3% of the output.
 //
+// The weights are rounded to the element type for the second product, their sum is not:
+// outputs are 1.2 to 1.4 times as far from 64 bits as with weights in fp32. Pairs of numbers
+// would double that product's matrix instructions, which bound many_rows.
+//
 // Two bodies, chosen per sequence by its rows (tokens x group):
 //   few_rows   up to 16 rows, memory-bound: each wave streams its own 32-key tiles
 //   many_rows  more rows: 128 rows x 64 keys per step, keys and values through LDS
@@ -443,8 +447,8 @@ __global__ __launch_bounds__(64 * W, 2) void few_kernel(AttnParams p) {
 // ------------------------------------------------------------------ many rows
 //
 // Bound by the matrix cores, the exponentials beside them and the power both draw:
-// 2048 tokens x 32 heads on 16384 keys take 487 us, 1060 TFLOP/s, at a clock that the
-// card lowers from 2.0 to 1.7 GHz meanwhile (a large library product in bf16 reaches 1200).
+// 2048 tokens x 32 heads on 16384 keys take 483 to 526 us by the machine, up to 1070
+// TFLOP/s, at a clock that the card lowers from 2.0 to 1.7 GHz meanwhile (a large library product in bf16 reaches 1200).
 // A wave owns 32 rows; the four share 64 keys and values in LDS, in two buffers that
 // loads fill without passing registers, one barrier a tile. (Through registers, with
 // the operands' LDS reads waiting on them: 605 us.) The scores of one block of 32 keys are computed
