@@ -346,8 +346,9 @@ int lutgemm_stream_read(const void* d_src, size_t bytes, uint32_t* d_sink, size_
  * are those of lutgemm_type. Indices, lengths and page numbers are device data,
  * which the host cannot check: what each call does with a value outside its
  * range is stated there, and no such value makes a kernel access memory outside
- * the arrays described. All argument checks run before any HIP call; on error
- * nothing is launched. */
+ * the arrays described. What is written (outputs, cache pages, workspaces) overlaps no
+ * other array of the call unless that is stated. All argument checks run before any HIP
+ * call; on error nothing is launched. */
 typedef enum lutgemm_type { LUTGEMM_F16 = 0, LUTGEMM_BF16 = 1 } lutgemm_type;
 
 /* Per-head norms of queries and keys, rotation by position, and the append of
