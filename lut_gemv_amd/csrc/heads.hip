@@ -7,9 +7,10 @@
 // 58.9 us by the machine, 5.8 to 6.0 TB/s; a plain copy of the same bytes takes 63. A
 // thread owns sixteen entries of a head as two 16-byte words, chosen so that both halves of
 // each rotated pair are its own (entries 8u .. 8u+7 and R/2 + 8u .. for pairs of halves,
-// 16u .. 16u+15 for neighbours); the only exchange between lanes is the norm's sum over a head. A workgroup serves one token, so
-// its slot and angles are looked up once for all the heads that it walks; reading several
-// heads ahead (64 to 66 us) or a workgroup for each group of heads (87 us) did not gain.
+// 16u .. 16u+15 for neighbours); the only exchange between lanes is the norm's sum over a
+// head. A workgroup serves one token, so its slot and angles are looked up once for all the
+// heads that it walks; reading several heads ahead (64 to 66 us) or a workgroup for each
+// group of heads (87 us) did not gain.
 #include <type_traits>
 
 #include "serve.h"
