@@ -338,8 +338,9 @@ int lutgemm_stream_read(const void* d_src, size_t bytes, uint32_t* d_sink, size_
  *
  * What a decoder layer does between its products when it generates: the norms
  * and the position rotation of queries and keys with the append to the paged
- * key/value cache, the attention of the new tokens over that cache, and
- * low-rank adapters added to a projection's output.
+ * key/value cache, the attention of the new tokens over that cache, also of batches that
+ * share long prefixes, and low-rank adapters added to a projection's output; and around
+ * the layers the step's page tables and slots, and the next tokens from the logits.
  *
  * Conventions on top of those at the head of this file: strides are counted in
  * elements; a strided array's innermost dimension is contiguous; element types
@@ -349,7 +350,11 @@ int lutgemm_stream_read(const void* d_src, size_t bytes, uint32_t* d_sink, size_
  * the arrays described. What is written (outputs, cache pages, workspaces) overlaps no
  * other array of the call unless that is stated. All argument checks run before any HIP
  * call; on error nothing is launched. */
-typedef enum lutgemm_type { LUTGEMM_F16 = 0, LUTGEMM_BF16 = 1 } lutgemm_type;
+typedef enum lutgemm_type {
+  LUTGEMM_F16 = 0,
+  LUTGEMM_BF16 = 1,
+  LUTGEMM_F32 = 2 /* logits only */
+} lutgemm_type;
 
 /* Per-head norms of queries and keys, rotation by position, and the append of
  * keys and values to a paged cache, in one pass over a fused QKV output.
@@ -486,6 +491,121 @@ int lutgemm_adapters_add(const lutgemm_adapters* l, const void* d_x, const void*
                          const void* d_a, const void* d_b, const float* d_scales,
                          const int32_t* d_ids, void* d_out, void* d_workspace,
                          size_t workspace_bytes, void* stream);
+
+/* Attention of a batch whose sequences share long prefixes, each prefix read once for
+ * its whole group.
+ *
+ * Group g is the sequences group_starts[g] .. group_starts[g + 1] - 1; they share
+ * prefix_lens[g] keys, which come before their own. Sequence s holds n = kv_lens[s] keys of its
+ * own, the last len of which belong to its new tokens. Row t of the sequence stands at
+ * p = n - len + t among them and sees the whole prefix and its own keys j <= p:
+ *   out = sum_j softmax_j(scale * q . k_j) v_j     over the keys that it sees,
+ * zero for a row that sees none, NaN for one whose scores are all -infinity. A sequence
+ * in no group has no prefix.
+ * Arrays, types, limits, rounding, reproducibility and what bad lengths and non-finite keys
+ * and values do are those of lutgemm_paged_attention (own: window must be 0), with
+ *   d_prefix_table  int32 [groups][prefix_width], rows prefix_stride apart: key j of
+ *                   group g is in page prefix_table[g][j / page_size] of the same cache
+ *   d_prefix_lens   int32 [groups]
+ *   d_group_starts  int32 [groups + 1], non-decreasing, values brought into [0, seqs];
+ *                   NULL: one group of all sequences
+ * A bad page or length of a prefix makes the rows of its group NaN. own.max_q, own.max_kv and
+ * max_prefix are hints for the launch as there. d_out may overlap d_q in any way.
+ *   d_workspace     at least lutgemm_shared_attention_workspace bytes (fp32 sums of each
+ *                   part of each row: from two parts on, 4 (head_dim + 2) bytes each).
+ * Further shape rules: 0 <= groups < 2^20, prefix_width >= 1 with prefix_width *
+ * page_size <= 2^30; calls too large for one grid (about tokens * heads = 2^27 on) are
+ * refused with LUTGEMM_ERR_SHAPE. */
+typedef struct lutgemm_shared {
+  lutgemm_attention own;
+  int32_t groups, prefix_width;
+  int64_t prefix_stride, max_prefix;
+} lutgemm_shared;
+int lutgemm_shared_attention_workspace(const lutgemm_shared* a, size_t* bytes);
+int lutgemm_shared_attention(const lutgemm_shared* a, const void* d_q, const void* d_k,
+                             const void* d_v, const int32_t* d_prefix_table,
+                             const int32_t* d_prefix_lens, const int32_t* d_group_starts,
+                             const int32_t* d_table, const int32_t* d_kv_lens,
+                             const int32_t* d_q_starts, void* d_out, void* d_workspace,
+                             size_t workspace_bytes, void* stream);
+
+/* One step's page tables, slots, positions and row ranges from the lengths of the
+ * sequences: what lutgemm_qk_norm_rotate and the attention take, without the host.
+ *
+ * Sequence s holds lens[s] keys (brought into [0, table_width * page_size]) in the
+ * ceil(lens / page_size) pages that its table row begins with. change[s] > 0 appends so
+ * many tokens, change[s] < 0 takes back the last -change[s] keys, at most all of them (drafts
+ * that were rejected, a finished request). Pages come from a ring of free ones, ring[(first + i)
+ * % capacity] for i < count with (first, count) = range: taken from its first on, in the
+ * order of the sequences and their keys; pages that hold no key any more go behind its
+ * last, in the same order. Pages given back in a call are not taken in it.
+ * A sequence whose keys would not fit its table row is not served: it gets no rows and
+ * keeps its length. Neither are, from the first one on whose rows end behind `tokens` or
+ * whose pages are not free any more, all that would grow.
+ *   d_change, d_lens  int32 [seqs]     d_offsets  int32 [seqs] or NULL: added to the
+ *                     positions (a shared prefix's length)
+ *   d_table           int32 [seqs][table_width], rows table_stride apart: the entries of the
+ *                     pages taken are written, no others
+ *   d_ring            int32 [capacity], d_range int32 [2]; capacity 0: the caller has filled
+ *                     the table for all new tokens, no pages are taken or given back
+ *   d_positions, d_slots  int64 [tokens]: of row starts[s] + i, which is the ith new token
+ *                     of sequence s, offsets[s] + lens[s] + i and page * page_size + the
+ *                     place in it; rows from starts[seqs] on get position 0 and slot -1
+ *   d_lens_out        int32 [seqs], the lengths after the step; may be d_lens
+ *   d_starts          int32 [seqs + 1], the first row of each sequence and the end of the last
+ *   d_range_out       int32 [2], the ring's free part after the step; may be d_range
+ * d_ring and d_table are updated in place; arrays that overlap otherwise than stated are
+ * refused with LUTGEMM_ERR_SHAPE (d_table: not checked); a page given back that would make the ring hold
+ * more than `capacity` is dropped. A range's first is taken modulo the capacity, its count brought
+ * into [0, capacity]. Table entries and ring entries are not checked: a page
+ * number that is none makes a slot or page that the other calls refuse as theirs state.
+ *   d_workspace       8 * seqs bytes, as for attention.
+ * Shape rules: 0 <= seqs < 2^20, 0 <= tokens < 2^24, 1 <= page_size <= 65536, table_width >=
+ * 1 with table_width * page_size <= 2^30, 0 <= capacity < 2^29, table_stride >= table_width.
+ * Alignment: the int64 arrays 8 bytes, all others 4. */
+typedef struct lutgemm_tables {
+  int32_t seqs, page_size, table_width, capacity;
+  int64_t tokens, table_stride;
+} lutgemm_tables;
+int lutgemm_batch_tables_workspace(const lutgemm_tables* t, size_t* bytes);
+int lutgemm_batch_tables(const lutgemm_tables* t, const int32_t* d_change, const int32_t* d_lens,
+                         const int32_t* d_offsets, int32_t* d_table, int32_t* d_ring,
+                         const int32_t* d_range, int64_t* d_positions, int64_t* d_slots,
+                         int32_t* d_lens_out, int32_t* d_starts, int32_t* d_range_out,
+                         void* d_workspace, size_t workspace_bytes, void* stream);
+
+/* Next tokens drawn from logits, one for each row.
+ *
+ * With M the row's largest logit, weights are w_i = exp((x_i - M) / temperature). The
+ * tokens in order of falling logit (equal ones by rising index) are kept up to a border:
+ *   top_k > 0: the first top_k of them;
+ *   top_p < 1: of what top_k leaves, the fewest whose weights sum to at least top_p of
+ *              that sum (at least one);
+ *   min_p > 0: those with w_i >= min_p (the largest always).
+ * The token is the first index, in the vocabulary's order, up to which the kept weights sum
+ * to more than u times their total; its log-probability is log(w / total).
+ * temperature 0 takes the largest logit, the lowest index of equal ones, with
+ * log-probability 0.
+ * Weights and sums hold 40 bits and more; tokens with a weight below 2^-64 count as
+ * having none, and no top_k or top_p border is looked for among them.
+ *   d_logits  [rows][vocab] of type F16, BF16 or F32, rows row_step elements apart; -infinity:
+ *             the token is never drawn
+ *   d_u       fp32 [rows] in [0, 1)     d_temperature, d_top_p, d_min_p  fp32 [rows] or
+ *   NULL: 1, 1, 0                       d_top_k  int32 [rows] or NULL: 0
+ *   d_tokens  int64 [rows]              d_logprobs  fp32 [rows] or NULL
+ * A row has no distribution, and token -1 and log-probability NaN, if it holds NaN or
+ * +infinity or nothing but -infinity, if u is outside [0, 1), if the temperature is negative,
+ * infinite or NaN, or if top_p or min_p is NaN. Results are bitwise reproducible. Outputs
+ * that overlap an input or each other are refused with LUTGEMM_ERR_SHAPE.
+ * Shape rules: 0 <= rows < 2^22, 1 <= vocab <= 2^20. Alignment: d_logits by its type,
+ * d_tokens 8 bytes, the others 4. */
+typedef struct lutgemm_sample {
+  int32_t type, rows, vocab, reserved;
+  int64_t row_step;
+} lutgemm_sample;
+int lutgemm_sample_tokens(const lutgemm_sample* s, const void* d_logits, const float* d_u,
+                          const float* d_temperature, const int32_t* d_top_k, const float* d_top_p,
+                          const float* d_min_p, int64_t* d_tokens, float* d_logprobs, void* stream);
 
 #ifdef __cplusplus
 }

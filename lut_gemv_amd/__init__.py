@@ -8,8 +8,9 @@ the device is not gfx950, calls raise.
 Names follow the C ABI: :func:`bcq_pack`, :func:`bcq_pack_uniform`,
 :func:`lutgemm_run`, plus the size queries. :class:`PackedBCQ` bundles a
 packed weight held in device memory with a reusable workspace.
-:func:`qk_norm_rotate`, :func:`paged_attention` and :func:`adapters_add` (from
-``serving.py``) are what a decoder layer does between its products.
+:func:`qk_norm_rotate`, :func:`paged_attention`, :func:`shared_prefix_attention` and
+:func:`adapters_add` (from ``serving.py``) are what a decoder layer does between its
+products, :func:`batch_tables` and :func:`sample_tokens` what a step does around its layers.
 """
 from __future__ import annotations
 
@@ -26,6 +27,7 @@ __all__ = [
     "search_group_sizes", "bcq_quantize", "stream_read", "lutgemm_run_noalloc",
     "noalloc_scratch_bytes", "query_plan", "TABLES", "trace_attach", "use_traced_library",
     "PackedBCQ", "STATUS", "rotary_table", "qk_norm_rotate", "paged_attention", "adapters_add",
+    "batch_tables", "shared_prefix_attention", "sample_tokens",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -133,6 +135,16 @@ def lib() -> ctypes.CDLL:
     L.lutgemm_adapters_workspace.argtypes = [_P, _SZP]
     L.lutgemm_adapters_add.restype = ctypes.c_int
     L.lutgemm_adapters_add.argtypes = [_P] * 9 + [_SZ, _P]
+    L.lutgemm_shared_attention_workspace.restype = ctypes.c_int
+    L.lutgemm_shared_attention_workspace.argtypes = [_P, _SZP]
+    L.lutgemm_shared_attention.restype = ctypes.c_int
+    L.lutgemm_shared_attention.argtypes = [_P] * 12 + [_SZ, _P]
+    L.lutgemm_batch_tables_workspace.restype = ctypes.c_int
+    L.lutgemm_batch_tables_workspace.argtypes = [_P, _SZP]
+    L.lutgemm_batch_tables.restype = ctypes.c_int
+    L.lutgemm_batch_tables.argtypes = [_P] * 13 + [_SZ, _P]
+    L.lutgemm_sample_tokens.restype = ctypes.c_int
+    L.lutgemm_sample_tokens.argtypes = [_P] * 10
     L.lutgemm_query_plan.restype = ctypes.c_int
     L.lutgemm_query_plan.argtypes = [_SHP, ctypes.c_int32, ctypes.c_int32, _SZ,
                                      ctypes.POINTER(_Plan)]
@@ -453,4 +465,5 @@ class PackedBCQ:
         return out
 
 
-from .serving import adapters_add, paged_attention, qk_norm_rotate, rotary_table  # noqa: E402
+from .serving import (adapters_add, batch_tables, paged_attention, qk_norm_rotate,  # noqa: E402
+                      rotary_table, sample_tokens, shared_prefix_attention)

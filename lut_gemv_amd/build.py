@@ -93,7 +93,8 @@ def build(verbose: bool = False, extra_hip_flags=(), trace: bool = True) -> str:
     try:
         common = [os.path.join(tmp, f) for f in ("pack.o", "dequant.o", "footprint.o",
                                                   "quantize.o", "probe.o", "heads.o",
-                                                  "attention.o", "adapters.o")]
+                                                  "attention.o", "adapters.o",
+                                                  "shared_attention.o", "tables.o", "sample.o")]
         jobs = [
             [CXX, *CXX_FLAGS, *incs, "-c", os.path.join(CSRC, "pack.cpp"), "-o", common[0]],
             [HIPCC, *HIP_FLAGS, *extra_hip_flags, *incs, "-c", "-Rpass-analysis=kernel-resource-usage",
@@ -105,7 +106,8 @@ def build(verbose: bool = False, extra_hip_flags=(), trace: bool = True) -> str:
         ]
         # the serving operators
         for name, obj in (("heads.hip", common[5]), ("attention.hip", common[6]),
-                          ("adapters.hip", common[7])):
+                          ("adapters.hip", common[7]), ("shared_attention.hip", common[8]),
+                          ("tables.hip", common[9]), ("sample.hip", common[10])):
             jobs.append([HIPCC, *HIP_FLAGS, *extra_hip_flags, *incs, "-c",
                          "-Rpass-analysis=kernel-resource-usage",
                          os.path.join(CSRC, name), "-o", obj])

@@ -28,6 +28,11 @@ decltype(&lutgemm_paged_attention) g_attention;
 decltype(&lutgemm_paged_attention_workspace) g_attention_ws;
 decltype(&lutgemm_adapters_add) g_adapters;
 decltype(&lutgemm_adapters_workspace) g_adapters_ws;
+decltype(&lutgemm_shared_attention) g_shared;
+decltype(&lutgemm_shared_attention_workspace) g_shared_ws;
+decltype(&lutgemm_batch_tables) g_tables;
+decltype(&lutgemm_batch_tables_workspace) g_tables_ws;
+decltype(&lutgemm_sample_tokens) g_sample;
 PyObject* g_status_error;  // LutGemmError(status, where)
 
 struct Refused : std::runtime_error {
@@ -227,6 +232,16 @@ PyObject* heads(PyObject* const* a) {
   return THPVariable_Wrap(out);
 }
 
+// A page table: int32 [rows][width], rows apart.
+const at::Tensor& page_table(PyObject* o, const at::Tensor& ref, const char* what) {
+  const at::Tensor& t = tensor(o, what);
+  if (t.scalar_type() != at::kInt || t.device() != ref.device() || t.dim() != 2 ||
+      (t.size(1) > 1 && t.stride(1) != 1))
+    refuse(std::string(what) + " must be int32 [rows][width] on the first argument's device, "
+                               "contiguous in its last dimension");
+  return t;
+}
+
 PyObject* attention(PyObject* const* a) {
   const at::Tensor& q = tensor(a[0], "q");
   lutgemm_attention d{};
@@ -240,10 +255,7 @@ PyObject* attention(PyObject* const* a) {
   if (k.size(3) != dim || k.sizes() != v.sizes())
     refuse("k_pages and v_pages must both be [pages][page_size][kv_heads][" + std::to_string(dim) +
            "]");
-  const at::Tensor& table = tensor(a[3], "page_table");
-  if (table.scalar_type() != at::kInt || table.device() != q.device() || table.dim() != 2 ||
-      (table.size(1) > 1 && table.stride(1) != 1))
-    refuse("page_table must be int32 [seqs][width] on q's device, contiguous in its last dimension");
+  const at::Tensor& table = page_table(a[3], q, "page_table");
   const int64_t seqs = table.size(0), width = table.size(1), page = k.size(1);
   const void* lens = flat(tensor(a[4], "kv_lens"), at::kInt, q, {seqs}, "kv_lens");
   const void* starts = nullptr;
@@ -295,6 +307,205 @@ PyObject* attention(PyObject* const* a) {
         where);
   if (a[10] != Py_None) written(out);
   return THPVariable_Wrap(out);
+}
+
+PyObject* shared(PyObject* const* a) {
+  const at::Tensor& q = tensor(a[0], "q");
+  lutgemm_shared d{};
+  d.own.type = type_of(q, "q");
+  on_gpu(q, "q");
+  const at::Tensor &k = tensor(a[1], "k_pages"), &v = tensor(a[2], "v_pages");
+  like(q, q, 3, "q");
+  like(k, q, 4, "k_pages");
+  like(v, q, 4, "v_pages");
+  const int64_t tokens = q.size(0), heads = q.size(1), dim = q.size(2);
+  if (k.size(3) != dim || k.sizes() != v.sizes())
+    refuse("k_pages and v_pages must both be [pages][page_size][kv_heads][" + std::to_string(dim) +
+           "]");
+  const at::Tensor& prefix = page_table(a[3], q, "prefix_table");
+  const int64_t groups = prefix.size(0);
+  const void* prefix_lens = flat(tensor(a[4], "prefix_lens"), at::kInt, q, {groups}, "prefix_lens");
+  const at::Tensor& table = page_table(a[5], q, "page_table");
+  const int64_t seqs = table.size(0), width = table.size(1), page = k.size(1);
+  const void* lens = flat(tensor(a[6], "kv_lens"), at::kInt, q, {seqs}, "kv_lens");
+  const void *starts = nullptr, *group_starts = nullptr;
+  if (a[7] != Py_None)
+    starts = flat(tensor(a[7], "q_starts"), at::kInt, q, {seqs + 1}, "q_starts");
+  else if (tokens != seqs)
+    refuse(std::to_string(tokens) + " tokens of " + std::to_string(seqs) +
+           " sequences need q_starts");
+  if (a[8] != Py_None)
+    group_starts = flat(tensor(a[8], "group_starts"), at::kInt, q, {groups + 1}, "group_starts");
+  else if (groups > 1)
+    refuse(std::to_string(groups) + " groups need group_starts");
+  const c10::hip::HIPGuard guard(q.device().index());
+  at::Tensor out;
+  if (a[13] == Py_None) {
+    out = at::empty({tokens, heads, dim}, q.options());
+  } else {
+    out = tensor(a[13], "out");
+    like(out, q, 3, "out");
+    if (out.sizes() != q.sizes()) refuse("out must have the shape of q");
+  }
+  d.own.heads = small(heads, "heads");
+  d.own.kv_heads = small(k.size(2), "kv_heads");
+  d.own.head_dim = small(dim, "head_dim");
+  d.own.page_size = small(page, "page_size");
+  d.own.seqs = small(seqs, "seqs");
+  d.own.table_width = small(width, "the page table's width");
+  d.own.scale = a[12] == Py_None ? (float)(1.0 / std::sqrt((double)dim)) : (float)real(a[12]);
+  d.own.tokens = tokens;
+  d.own.pages = k.size(0);
+  d.own.table_stride = step(table, 0);
+  d.own.max_q = !starts ? 1 : a[9] == Py_None ? tokens : whole(a[9]);
+  d.own.max_kv = a[10] == Py_None ? width * page : whole(a[10]);
+  d.own.q_token = step(q, 0);
+  d.own.q_head = step(q, 1);
+  d.own.o_token = step(out, 0);
+  d.own.o_head = step(out, 1);
+  d.own.k_page = step(k, 0);
+  d.own.k_slot = step(k, 1);
+  d.own.k_head = step(k, 2);
+  d.own.v_page = step(v, 0);
+  d.own.v_slot = step(v, 1);
+  d.own.v_head = step(v, 2);
+  d.groups = small(groups, "groups");
+  d.prefix_width = small(prefix.size(1), "the prefix table's width");
+  d.prefix_stride = step(prefix, 0);
+  d.max_prefix = a[11] == Py_None ? prefix.size(1) * page : whole(a[11]);
+  constexpr const char* where = "lutgemm_shared_attention";
+  size_t need = 0;
+  check(g_shared_ws(&d, &need), where);
+  at::Tensor ws;
+  if (need) ws = scratch(need, q);
+  check(g_shared(&d, q.data_ptr(), k.data_ptr(), v.data_ptr(), (const int32_t*)prefix.data_ptr(),
+                 (const int32_t*)prefix_lens, (const int32_t*)group_starts,
+                 (const int32_t*)table.data_ptr(), (const int32_t*)lens, (const int32_t*)starts,
+                 out.data_ptr(), need ? ws.data_ptr() : nullptr, need, stream_of(q)),
+        where);
+  if (a[13] != Py_None) written(out);
+  return THPVariable_Wrap(out);
+}
+
+// The tensors as a tuple.
+template <size_t N>
+PyObject* tuple_of(const at::Tensor (&all)[N]) {
+  PyObject* t = PyTuple_New(N);
+  for (size_t i = 0; t && i < N; ++i) {
+    PyObject* one = THPVariable_Wrap(all[i]);
+    if (!one) {
+      Py_DECREF(t);
+      return nullptr;
+    }
+    PyTuple_SET_ITEM(t, i, one);
+  }
+  return t;
+}
+
+PyObject* tables(PyObject* const* a) {
+  const at::Tensor &change = tensor(a[0], "change"), &lens = tensor(a[1], "kv_lens");
+  on_gpu(change, "change");
+  const int64_t seqs = change.numel();
+  lutgemm_tables d{};
+  d.seqs = small(seqs, "seqs");
+  const void* pc = flat(change, at::kInt, change, {seqs}, "change");
+  void* pl = flat(lens, at::kInt, change, {seqs}, "kv_lens");
+  const at::Tensor& table = page_table(a[2], change, "page_table");
+  if (table.size(0) != seqs) refuse("page_table must have a row for each sequence");
+  d.page_size = small(whole(a[3]), "page_size");
+  d.tokens = whole(a[4]);
+  if (d.tokens < 0) refuse("tokens must not be negative");
+  d.table_width = small(table.size(1), "the page table's width");
+  d.table_stride = seqs > 1 ? table.stride(0) : 0;
+  if ((a[5] == Py_None) != (a[6] == Py_None)) refuse("free_pages and free_range go together");
+  void *ring = nullptr, *range = nullptr, *range_out = nullptr;
+  const c10::hip::HIPGuard guard(change.device().index());
+  at::Tensor got[5];  // positions, slots, lengths, starts, range
+  if (a[5] != Py_None) {
+    const at::Tensor& t = tensor(a[5], "free_pages");
+    if (t.dim() != 1 || t.numel() < 1) refuse("free_pages must be [capacity]");
+    d.capacity = small(t.numel(), "free_pages' length");
+    ring = flat(t, at::kInt, change, t.sizes(), "free_pages");
+    range = flat(tensor(a[6], "free_range"), at::kInt, change, {2}, "free_range");
+  }
+  const void* offsets = nullptr;
+  if (a[7] != Py_None) offsets = flat(tensor(a[7], "offsets"), at::kInt, change, {seqs}, "offsets");
+  const int in_place = PyObject_IsTrue(a[8]);
+  if (in_place < 0) throw Raised{};
+  constexpr const char* where = "lutgemm_batch_tables";
+  size_t need = 0;
+  check(g_tables_ws(&d, &need), where);
+  got[0] = at::empty({d.tokens}, change.options().dtype(at::kLong));
+  got[1] = at::empty({d.tokens}, change.options().dtype(at::kLong));
+  got[2] = in_place ? lens : at::empty({seqs}, change.options());
+  got[3] = at::empty({seqs + 1}, change.options());
+  if (range) {
+    got[4] = in_place ? tensor(a[6], "free_range") : at::empty({2}, change.options());
+    range_out = got[4].data_ptr();
+  }
+  at::Tensor ws;
+  if (need) ws = scratch(need, change);
+  check(g_tables(&d, (const int32_t*)pc, (const int32_t*)pl, (const int32_t*)offsets,
+                 (int32_t*)table.data_ptr(), (int32_t*)ring, (const int32_t*)range,
+                 (int64_t*)got[0].data_ptr(), (int64_t*)got[1].data_ptr(), (int32_t*)got[2].data_ptr(),
+                 (int32_t*)got[3].data_ptr(), (int32_t*)range_out, need ? ws.data_ptr() : nullptr, need,
+                 stream_of(change)),
+        where);
+  if (ring) {
+    written(table);
+    written(tensor(a[5], "free_pages"));
+  }
+  if (in_place) {
+    written(lens);
+    if (range) written(got[4]);
+  }
+  if (range) return tuple_of(got);
+  PyObject* all[4] = {};
+  bool whole_ = true;
+  for (int i = 0; i < 4; ++i) whole_ &= (all[i] = THPVariable_Wrap(got[i])) != nullptr;
+  PyObject* t = whole_ ? PyTuple_Pack(5, all[0], all[1], all[2], all[3], Py_None) : nullptr;
+  for (PyObject* o : all) Py_XDECREF(o);
+  return t;
+}
+
+PyObject* sample(PyObject* const* a) {
+  const at::Tensor& x = tensor(a[0], "logits");
+  lutgemm_sample d{};
+  if (x.scalar_type() == at::kFloat)
+    d.type = LUTGEMM_F32;
+  else if (x.scalar_type() == at::kHalf || x.scalar_type() == at::kBFloat16)
+    d.type = type_of(x, "logits");
+  else
+    refuse("logits must be fp16, bf16 or fp32");
+  on_gpu(x, "logits");
+  like(x, x, 2, "logits");
+  const int64_t rows = x.size(0);
+  d.rows = small(rows, "rows");
+  d.vocab = small(x.size(1), "the vocabulary");
+  d.row_step = step(x, 0);
+  const void* u = flat(tensor(a[1], "u"), at::kFloat, x, {rows}, "u");
+  auto setting = [&](int i, at::ScalarType type, const char* what) -> const void* {
+    return a[i] == Py_None ? nullptr : flat(tensor(a[i], what), type, x, {rows}, what);
+  };
+  const void* temperature = setting(2, at::kFloat, "temperature");
+  const void* top_k = setting(3, at::kInt, "top_k");
+  const void* top_p = setting(4, at::kFloat, "top_p");
+  const void* min_p = setting(5, at::kFloat, "min_p");
+  const c10::hip::HIPGuard guard(x.device().index());
+  at::Tensor got[2];
+  if (a[6] == Py_None) {
+    got[0] = at::empty({rows}, x.options().dtype(at::kLong));
+  } else {
+    got[0] = tensor(a[6], "out");
+    flat(got[0], at::kLong, x, {rows}, "out");
+  }
+  got[1] = at::empty({rows}, x.options().dtype(at::kFloat));
+  check(g_sample(&d, x.data_ptr(), (const float*)u, (const float*)temperature, (const int32_t*)top_k,
+                 (const float*)top_p, (const float*)min_p, (int64_t*)got[0].data_ptr(),
+                 (float*)got[1].data_ptr(), stream_of(x)),
+        "lutgemm_sample_tokens");
+  if (a[6] != Py_None) written(got[0]);
+  return tuple_of(got);
 }
 
 PyObject* adapters(PyObject* const* a) {
@@ -378,15 +589,28 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return nullptr;
 }
 
-// init(addresses of the five entry points, LutGemmError)
+// init(addresses of the entry points, in the order in which they are bound here, LutGemmError)
 PyObject* init(PyObject*, PyObject* args) {
-  unsigned long long f[5];
-  PyObject* error;
-  if (!PyArg_ParseTuple(args, "KKKKKO", &f[0], &f[1], &f[2], &f[3], &f[4], &error)) return nullptr;
+  constexpr Py_ssize_t kPoints = 10;
+  if (PyTuple_GET_SIZE(args) != kPoints + 1) {
+    PyErr_SetString(PyExc_TypeError, "init takes the entry points' addresses and an exception");
+    return nullptr;
+  }
+  void* f[kPoints];
+  for (Py_ssize_t i = 0; i < kPoints; ++i) {
+    f[i] = PyLong_AsVoidPtr(PyTuple_GET_ITEM(args, i));
+    if (!f[i] && PyErr_Occurred()) return nullptr;
+  }
   g_attention = (decltype(g_attention))f[1];
   g_attention_ws = (decltype(g_attention_ws))f[2];
   g_adapters = (decltype(g_adapters))f[3];
   g_adapters_ws = (decltype(g_adapters_ws))f[4];
+  g_shared = (decltype(g_shared))f[5];
+  g_shared_ws = (decltype(g_shared_ws))f[6];
+  g_tables = (decltype(g_tables))f[7];
+  g_tables_ws = (decltype(g_tables_ws))f[8];
+  g_sample = (decltype(g_sample))f[9];
+  PyObject* error = PyTuple_GET_ITEM(args, kPoints);
   Py_INCREF(error);
   Py_XSETREF(g_status_error, error);
   g_heads = (decltype(g_heads))f[0];
@@ -398,6 +622,9 @@ PyMethodDef kMethods[] = {
     {"qk_norm_rotate", (PyCFunction)(void*)entry<heads, 13, 0x1671>, METH_FASTCALL, nullptr},
     {"paged_attention", (PyCFunction)(void*)entry<attention, 11, 0x407>, METH_FASTCALL, nullptr},
     {"adapters_add", (PyCFunction)(void*)entry<adapters, 7, 0x6F>, METH_FASTCALL, nullptr},
+    {"shared_prefix_attention", (PyCFunction)(void*)entry<shared, 14, 0x2007>, METH_FASTCALL, nullptr},
+    {"batch_tables", (PyCFunction)(void*)entry<tables, 9, 0x0>, METH_FASTCALL, nullptr},
+    {"sample_tokens", (PyCFunction)(void*)entry<sample, 7, 0x37>, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, kMethods,

@@ -217,6 +217,28 @@ inline bool overlap(const Rows& a, const Rows& b) {
   return after < 2 * (__int128)a.width || after + 2 * (__int128)b.width > step;
 }
 
+// A flat array.
+struct Flat {
+  const void* at;
+  int64_t bytes;
+};
+
+// Whether two arrays have memory in common.
+inline bool meet(const Flat& a, const Flat& b) {
+  const uintptr_t a0 = (uintptr_t)a.at, b0 = (uintptr_t)b.at;
+  return a.at && b.at && a.bytes > 0 && b.bytes > 0 && a0 < b0 + (uintptr_t)b.bytes &&
+         b0 < a0 + (uintptr_t)a.bytes;
+}
+
+// Whether one of the first `written` arrays has memory in common with another array.
+template <int N>
+bool clash(const Flat (&all)[N], int written) {
+  for (int i = 0; i < written; ++i)
+    for (int j = i + 1; j < N; ++j)
+      if (meet(all[i], all[j])) return true;
+  return false;
+}
+
 template <class P>
 int launch(void (*kernel)(P), dim3 grid, int threads, const P& p, hipStream_t stream) {
   P copy = p;

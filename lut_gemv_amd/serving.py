@@ -1,4 +1,5 @@
-"""The operators of a decoder layer beside its weight products.
+"""The operators of a serving step beside the weight products: those between a decoder
+layer's products, and the step's tables before the layers and its sampling after them.
 
 The arithmetic, its conventions and what each call does with indices outside
 their range are stated at the entry points of ``include/lutgemm.h``. Tensors are
@@ -14,7 +15,8 @@ from __future__ import annotations
 import ctypes
 import os
 
-__all__ = ["rotary_table", "qk_norm_rotate", "paged_attention", "adapters_add"]
+__all__ = ["rotary_table", "qk_norm_rotate", "paged_attention", "adapters_add", "batch_tables",
+           "shared_prefix_attention", "sample_tokens"]
 
 BINDING_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_binding.so")
 
@@ -31,7 +33,9 @@ def _load():
     from . import _binding
     names = ("lutgemm_qk_norm_rotate", "lutgemm_paged_attention",
              "lutgemm_paged_attention_workspace", "lutgemm_adapters_add",
-             "lutgemm_adapters_workspace")
+             "lutgemm_adapters_workspace", "lutgemm_shared_attention",
+             "lutgemm_shared_attention_workspace", "lutgemm_batch_tables",
+             "lutgemm_batch_tables_workspace", "lutgemm_sample_tokens")
     _binding.init(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in names), LutGemmError)
     _ops = _binding
     return _ops
@@ -95,3 +99,54 @@ def adapters_add(y, x, a, b, ids, scales=None, out=None):
     (a new tensor if None; it may be ``y``, but not overlap ``x`` or ``y`` otherwise).
     """
     return (_ops or _load()).adapters_add(y, x, a, b, ids, scales, out)
+
+
+def shared_prefix_attention(q, k_pages, v_pages, prefix_table, prefix_lens, page_table, kv_lens,
+                            q_starts=None, group_starts=None, max_q=None, max_kv=None, max_prefix=None,
+                            scale=None, out=None):
+    """Attention of new tokens of sequences that share long prefixes, each prefix read once
+    for its whole group (lutgemm_shared_attention).
+
+    ``prefix_table`` int32 [groups][width] and ``prefix_lens`` int32 [groups]: the pages and keys of
+    the prefixes; ``group_starts`` int32 [groups + 1]: the first sequence of each group and the
+    end of the last (None: one group of all). ``page_table`` and ``kv_lens`` are the keys
+    behind the prefix, which the new tokens' own end; the other arguments are those of
+    :func:`paged_attention`, ``max_prefix`` one more hint for the launch. Returns
+    [tokens][heads][head_dim] (in ``out`` if given, which may be ``q``).
+    """
+    return (_ops or _load()).shared_prefix_attention(q, k_pages, v_pages, prefix_table, prefix_lens,
+                                                     page_table, kv_lens, q_starts, group_starts, max_q,
+                                                     max_kv, max_prefix, scale, out)
+
+
+def batch_tables(change, kv_lens, page_table, page_size: int, tokens: int, free_pages=None,
+                 free_range=None, offsets=None, in_place: bool = False):
+    """One step's page tables, slots, positions and row ranges, made on the GPU
+    (lutgemm_batch_tables).
+
+    ``change`` int32 [seqs]: each sequence's new tokens, or minus the keys that it gives back
+    (-kv_lens: all of them); ``kv_lens`` int32 [seqs], its keys before the step; ``page_table`` int32
+    [seqs][width], to which the pages taken are added; ``tokens``: the rows of the step, at least
+    as many as there are new tokens; ``free_pages`` int32 [capacity] with ``free_range`` int32 [2]
+    (first, count), the ring of free pages (None: the table has all pages already);
+    ``offsets`` int32 [seqs], added to the positions (the lengths of shared prefixes).
+    Returns (positions, slots, kv_lens, q_starts, free_range): int64 [tokens] twice, as
+    :func:`qk_norm_rotate` takes them, int32 [seqs] and [seqs + 1], as :func:`paged_attention`
+    does, and the ring's new range (None without one). ``in_place``: the lengths and the range
+    are written over those given, so that a captured step goes on from where it ended. A
+    sequence that finds no room (rows, pages, width of its table row) keeps its length and gets no rows.
+    """
+    return (_ops or _load()).batch_tables(change, kv_lens, page_table, page_size, tokens, free_pages,
+                                          free_range, offsets, in_place)
+
+
+def sample_tokens(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, out=None):
+    """Next tokens drawn from logits by one random number a row (lutgemm_sample_tokens).
+
+    ``logits`` [rows][vocab], fp16, bf16 or fp32; ``u`` fp32 [rows] in [0, 1); ``temperature``,
+    ``top_p``, ``min_p`` fp32 [rows] and ``top_k`` int32 [rows], None for none: a temperature of 0 takes
+    the largest logit, top_k <= 0, top_p >= 1 and min_p <= 0 filter nothing.
+    Returns (tokens int64 [rows] (``out`` if given), their log-probabilities fp32 [rows]); -1 and NaN
+    for a row that has no distribution.
+    """
+    return (_ops or _load()).sample_tokens(logits, u, temperature, top_k, top_p, min_p, out)

@@ -11,7 +11,7 @@ from __future__ import annotations
 
 import numpy as np
 
-__all__ = ["attention", "heads", "adapters"]
+__all__ = ["attention", "heads", "adapters", "tables", "sample"]
 
 _F32 = 2.0 ** -24
 
@@ -81,3 +81,81 @@ def adapters(y, x, a, b, ids, scales, u, pair):
             out[i] += s * (b[l] @ t)
             tol[i] = abs(s) * (B @ dt + (2 * b.shape[2] + 8) * _F32 * (B @ np.abs(t)))
     return out, 1.01 * (u * np.abs(out) + tol + 4 * _F32 * (np.abs(y) + np.abs(out))) + 2.0 ** -25
+
+
+def tables(change, lens, table, page, tokens, ring=None, free=(0, 0), offsets=None):
+    """One step of lutgemm_batch_tables, sequence by sequence, in whole numbers. table and ring
+    are lists that are updated; returns (positions, slots, lens, starts, free)."""
+    seqs, width = len(change), len(table[0]) if table else 0
+    limit = width * page
+    first, count = (free[0] % len(ring), min(max(free[1], 0), len(ring))) if ring else (0, 0)
+    positions, slots, after, starts = [], [], [], [0]
+    taken, given, stop = 0, [], False
+    old = list(ring) if ring else []
+    for s in range(seqs):
+        n, d = min(max(lens[s], 0), limit), change[s]
+        held = -(-n // page)
+        if d < 0:
+            left = max(0, n + d)
+            if ring:
+                given += table[s][-(-left // page):held]
+            n = left
+        elif 0 < d <= limit - n:
+            more = -(-(n + d) // page) - held if ring else 0
+            stop = stop or len(positions) + d > tokens or taken + more > count
+            if not stop:
+                for j in range(more):
+                    table[s][held + j] = old[(first + taken + j) % len(old)]
+                taken += more
+                for i in range(n, n + d):
+                    positions.append(i + (offsets[s] if offsets else 0))
+                    slots.append(table[s][i // page] * page + i % page)
+                n += d
+        after.append(n)
+        starts.append(len(positions))
+    rest = tokens - len(positions)
+    positions, slots = positions + [0] * rest, slots + [-1] * rest
+    if not ring:
+        return positions, slots, after, starts, None
+    given = given[:len(ring) - count]
+    for j, x in enumerate(given):
+        ring[(first + count + j) % len(ring)] = x
+    return positions, slots, after, starts, [(first + taken) % len(ring), count - taken + len(given)]
+
+
+def sample(x, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
+    """One row of lutgemm_sample_tokens: (token, log-probability, margin): how far, of the
+    total, the nearest border of the token and of the filters is from moving."""
+    x = np.asarray(x, np.float64)
+    if (not (x < np.inf).all() or not (x > -np.inf).any() or not 0 <= u < 1
+            or not 0 <= temperature < np.inf or top_p != top_p or min_p != min_p):
+        return -1, np.nan, 1.0
+    if temperature == 0:
+        return int(np.argmax(x)), 0.0, 1.0
+    order = np.argsort(-x, kind="stable")
+    with np.errstate(over="ignore"):
+        w = np.exp((x[order] - x[order[0]]) / temperature)
+    margin = 1.0
+    if top_k > 0:
+        w[top_k:] = 0
+    if top_p < 1:
+        upto, total = np.cumsum(w), w.sum()
+        end = min(int(np.searchsorted(upto, top_p * total)), len(w) - 1)
+        if w[:end + 1].min() != w[:end + 1].max():  # sums of equal weights are exact
+            margin = min(abs(upto[end] - top_p * total), abs(upto[end] - w[end] - top_p * total)) / total
+        w[max(1, end + 1):] = 0
+    if min_p > 0:
+        least = min(min_p, 1.0)
+        near = np.abs(w[w > 0] - least)
+        near = near[near > 0]
+        margin = min(margin, near.min() if near.size else 1.0)
+        w[w < least] = 0
+    kept = np.zeros_like(w)
+    kept[order] = w
+    upto = np.cumsum(kept)
+    goal = u * upto[-1]
+    i = int(np.searchsorted(upto, goal, side="right"))
+    if w.max() != w[w > 0].min():
+        below = upto[i] - kept[i]
+        margin = min(margin, (upto[i] - goal) / upto[-1], (goal - below) / upto[-1] if u > 0 else 1.0)
+    return i, float(np.log(kept[i]) - np.log(upto[-1])), float(margin)

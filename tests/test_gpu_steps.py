@@ -1,0 +1,666 @@
+"""The operators around a serving step on the GPU, against their plain forms
+(oracle/serving.py): attention over shared prefixes with the bounds counted there, batch tables in
+whole numbers, sampling against 64 bits; then a run of them together."""
+import sys
+
+import numpy as np
+import pytest
+
+from oracle import serving as plain
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+import lut_gemv_amd as lg  # noqa: E402
+
+DEV = "cuda:0"
+F16, BF16, F32 = torch.float16, torch.bfloat16, torch.float32
+U = {F16: 2.0 ** -11, BF16: 2.0 ** -8}
+NAN, INF = float("nan"), float("inf")
+
+
+def _say(msg):
+    print(f"[steps] {msg}", flush=True)
+    sys.stdout.flush()
+
+
+def _np(t):
+    return t.detach().cpu().double().numpy()
+
+
+def _int(v, dtype=torch.int32):
+    return torch.tensor(v, dtype=dtype, device=DEV)
+
+
+# ---------------------------------------------------- attention over shared prefixes
+
+class Shared:
+    """Sequences behind shared prefixes in a paged cache whose unused slots and pages hold NaN."""
+
+    def __init__(self, dtype, heads, kv_heads, dim, page, prefixes, starts, lens, news, seed=0, scale=1.0,
+                 lead=0, tail=0):
+        self.dtype, self.page, self.heads, self.kv_heads, self.dim = dtype, page, heads, kv_heads, dim
+        self.prefixes, self.starts, self.lens, self.news, self.lead = prefixes, starts, lens, news, lead
+        all_lens = list(prefixes) + list(lens)
+        need = [-(-n // page) for n in all_lens]
+        pages = sum(need) + 2
+        ids = np.random.default_rng(seed).permutation(pages)
+        k, v = (torch.full((pages, page, kv_heads, dim), NAN, dtype=dtype) for _ in range(2))
+        tables = [torch.full((n, max(c + [1]) + 1), -7, dtype=torch.int32)
+                  for n, c in ((len(prefixes), need[:len(prefixes)]), (len(lens), need[len(prefixes):]))]
+        g = torch.Generator().manual_seed(seed)
+        self.kv, at = [], 0
+        for i, n in enumerate(all_lens):
+            kn = (torch.randn((n, kv_heads, dim), generator=g) * scale).to(dtype)
+            vn = torch.randn((n, kv_heads, dim), generator=g).to(dtype)
+            t, row = (tables[0], i) if i < len(prefixes) else (tables[1], i - len(prefixes))
+            for j in range(need[i]):
+                page_id = int(ids[at])
+                at += 1
+                t[row, j] = page_id
+                part = slice(j * page, min(n, (j + 1) * page))
+                k[page_id, :part.stop - part.start] = kn[part]
+                v[page_id, :part.stop - part.start] = vn[part]
+            self.kv.append((kn, vn))
+        tokens = lead + sum(news) + tail
+        self.q = (torch.randn((tokens, heads, dim), generator=g) * scale).to(dtype).to(DEV)
+        self.k_pages, self.v_pages = k.to(DEV), v.to(DEV)
+        self.prefix_table, self.page_table = tables[0].to(DEV), tables[1].to(DEV)
+        self.prefix_lens, self.kv_lens = _int(list(prefixes)), _int(list(lens))
+        self.q_starts = _int([lead + sum(news[:i]) for i in range(len(news) + 1)])
+        self.group_starts = _int(list(starts))
+
+    def run(self, **kw):
+        a = dict(q_starts=self.q_starts, group_starts=self.group_starts)
+        a.update(kw)
+        return lg.shared_prefix_attention(self.q, self.k_pages, self.v_pages, self.prefix_table,
+                                          self.prefix_lens, self.page_table, self.kv_lens, **a)
+
+    def group(self, s):
+        for g in range(len(self.prefixes)):
+            if self.starts[g] <= s < self.starts[g + 1]:
+                return g
+        return -1
+
+    def want(self, s):
+        """Result and bound of sequence s (all of its own keys precede or are its new tokens')."""
+        g, at = self.group(s), self.lead + sum(self.news[:s])
+        k, v = (_np(t) for t in self.kv[len(self.prefixes) + s])
+        n = self.lens[s]
+        if g >= 0:
+            pk, pv = (_np(t) for t in self.kv[g])
+            k, v, n = np.concatenate([pk, k]), np.concatenate([pv, v]), n + self.prefixes[g]
+        q = _np(self.q[at:at + self.news[s]])
+        return plain.attention(q, k, v, self.news[s], n, self.dim ** -0.5, 0, U[self.dtype])
+
+    def check(self, out, what):
+        got, worst = _np(out), 0.0
+        for s in range(len(self.lens)):
+            want, bound = self.want(s)
+            at = self.lead + sum(self.news[:s])
+            mine = got[at:at + self.news[s]]
+            assert np.isfinite(mine).all(), f"{what}: sequence {s} is not finite"
+            if mine.size:
+                worst = max(worst, float((np.abs(mine - want) / bound).max()))
+        _say(f"{what}: worst err/bound {worst:.3f}")
+        assert worst <= 1.0, what
+
+
+@pytest.mark.parametrize("heads,kv_heads,dim", [(8, 8, 128), (16, 2, 128), (12, 4, 64), (14, 2, 64), (6, 1, 128)])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_shared_single_tokens(dtype, heads, kv_heads, dim):
+    prefixes, starts = [65, 1, 0, 300, 64], [0, 3, 5, 6, 6, 9]
+    b = Shared(dtype, heads, kv_heads, dim, 16, prefixes, starts, [1, 40, 16, 17, 200, 33, 1, 2, 130], [1] * 9)
+    b.check(b.run(), f"{dtype} {heads}/{kv_heads}x{dim}")
+    b.check(b.run(q_starts=None, max_q=1, max_kv=200, max_prefix=300), "hints")
+
+
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("heads,kv_heads,dim", [(8, 2, 128), (4, 4, 64)])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_shared_chunks_and_single_tokens(dtype, heads, kv_heads, dim, page):
+    b = Shared(dtype, heads, kv_heads, dim, page, [130, 77], [1, 4, 6], [50, 5, 1, 200, 9, 131, 3],
+               [7, 5, 1, 140, 1, 131, 1], seed=3)
+    b.check(b.run(), f"{dtype} chunks, page {page}")
+    b.check(b.run(max_q=140, max_kv=200, max_prefix=130), "with hints")
+    b.check(b.run(max_q=1, max_kv=1, max_prefix=1), "hints far too small")
+    b.check(b.run(max_q=0, max_kv=0, max_prefix=0), "hints of zero")
+
+
+@pytest.mark.parametrize("seqs,heads,kv_heads", [(24, 8, 1), (5, 4, 4)])
+def test_shared_long_prefix_in_parts(seqs, heads, kv_heads):
+    b = Shared(BF16, heads, kv_heads, 128, 64, [4999], [0, seqs], [11 + 37 * i for i in range(seqs)], [1] * seqs,
+               seed=5)
+    b.check(b.run(), f"{seqs} sequences on 4999 keys")
+    b.check(b.run(group_starts=None), "one group by default")
+
+
+def test_shared_more_groups_and_sequences_than_lanes():
+    n = 150
+    starts = [0] + [2 * i + (i % 3 == 0) for i in range(1, 71)]
+    b = Shared(F16, 4, 2, 64, 16, [1 + (5 * i) % 40 for i in range(70)], starts, [1 + (7 * i) % 50 for i in range(n)],
+               [1 + (i % 7 == 0) * min(3, (7 * i) % 50) for i in range(n)], seed=7)
+    b.check(b.run(), "70 groups of 150 sequences")
+    b.check(b.run(max_q=4, max_kv=50, max_prefix=41), "with hints")
+
+
+def test_shared_equals_attention_on_joined_tables():
+    """Prefixes of whole pages: paged_attention on the tables put together says the same."""
+    b = Shared(BF16, 16, 4, 128, 32, [96, 160], [0, 3, 7], [5, 40, 1, 77, 32, 64, 100], [1, 3, 1, 70, 1, 2, 1], seed=9)
+    joined, lens = [], []
+    for s in range(7):
+        g = b.group(s)
+        row = b.prefix_table[g, :b.prefixes[g] // 32].tolist() + b.page_table[s].tolist()
+        joined.append(row)
+        lens.append(b.lens[s] + b.prefixes[g])
+    width = max(map(len, joined))
+    table = _int([r + [-1] * (width - len(r)) for r in joined])
+    other = lg.paged_attention(b.q, b.k_pages, b.v_pages, table, _int(lens), b.q_starts)
+    out = b.run()
+    b.check(out, "shared")
+    b.check(other, "joined")
+
+
+def test_shared_rows_left_alone_and_strides():
+    b = Shared(F16, 8, 2, 128, 16, [40], [0, 4], [9, 20, 3, 64], [1, 20, 1, 1], seed=11, lead=3, tail=5)
+    out = torch.full((b.q.shape[0], 8, 256), 7.0, dtype=F16, device=DEV)[:, :, 64:192]
+    got = b.run(out=out)
+    assert got.data_ptr() == out.data_ptr()
+    b.check(got, "strided output")
+    assert (got[:3] == 7).all() and (got[-5:] == 7).all()
+    whole = torch.full((b.q.shape[0], 8, 256), 0.0, dtype=F16, device=DEV)
+    whole[:, :, 64:192] = got
+    # queries in rows of a fused buffer, pages with heads outside slots
+    wide = torch.zeros((b.q.shape[0], 12, 128), dtype=F16, device=DEV)
+    wide[:, 2:10] = b.q
+    b.q = wide[:, 2:10]
+    b.k_pages, b.v_pages = (t.transpose(1, 2).contiguous().transpose(1, 2) for t in (b.k_pages, b.v_pages))
+    b.check(b.run(), "strided inputs")
+
+
+def test_shared_output_over_the_queries():
+    b = Shared(BF16, 8, 2, 64, 16, [70], [0, 5], [9, 20, 3, 64, 18], [1, 17, 1, 30, 1], seed=13)
+    first = b.run().clone()
+    got = b.run(out=b.q)
+    assert got.data_ptr() == b.q.data_ptr() and torch.equal(got, first)
+
+
+@pytest.mark.parametrize("news", [[1, 1, 1, 1], [1, 30, 20, 1]])
+def test_shared_bad_pages_and_lengths(news):
+    lens = [40, 30, 33, 1]
+    b = Shared(F16, 4, 2, 64, 16, [50, 33], [0, 2, 4], lens, news, seed=15)
+    good = b.run()
+    b.check(good, "good")
+    starts = [0, *np.cumsum(news)]
+
+    def rows(s):
+        return slice(starts[s], starts[s + 1])
+
+    table = b.prefix_table.clone()
+    b.prefix_table[0, 1] = 1 << 30
+    out = b.run()
+    for s in range(4):
+        assert out[rows(s)].isnan().all() if s < 2 else torch.equal(out[rows(s)], good[rows(s)])
+    b.prefix_table = table.clone()
+    b.prefix_table[1, 2] = -1
+    out = b.run()
+    assert not out[rows(0)].isnan().any() and out[rows(2)].isnan().all() and out[rows(3)].isnan().all()
+    b.prefix_table = table
+    b.prefix_lens = _int([1 << 20, 33])
+    out = b.run()
+    assert out[:starts[2]].isnan().all() and torch.equal(out[starts[2]:], good[starts[2]:])
+    b.prefix_lens = _int([-5, 33])  # counts as 0
+    out = b.run()
+    assert out.isfinite().all() and torch.equal(out[starts[2]:], good[starts[2]:])
+    b.prefix_lens = _int([50, 33])
+    b.kv_lens = _int([40, 1 << 25, 33, 1])
+    out = b.run()
+    assert out[rows(1)].isnan().all() and torch.equal(out[rows(0)], good[rows(0)])
+    b.kv_lens = _int(lens)
+    b.page_table[2, 0] = 1 << 20
+    out = b.run()
+    assert out[rows(2)].isnan().all() and torch.equal(out[rows(3)], good[rows(3)])
+
+
+def test_shared_rows_that_see_nothing():
+    """No keys at all: zero. None of their own before the prefix's: the prefix alone."""
+    b = Shared(F16, 4, 2, 64, 16, [0, 20], [0, 2, 4], [3, 0, 0, 2], [3, 1, 1, 2], seed=17)
+    b.kv_lens = _int([2, 0, 0, 2])  # the first sequence holds fewer keys than it has new tokens
+    out = b.run()
+    assert (out[0] == 0).all() and (out[3] == 0).all() and out[1:3].abs().sum() > 0
+    k, v = (_np(t) for t in b.kv[1])
+    want, bound = plain.attention(_np(b.q[4:5]), k, v, 1, 20, 64 ** -0.5, 0, U[F16])
+    assert (np.abs(_np(out[4:5]) - want) <= bound).all()
+
+
+def test_shared_non_finite_values():
+    """Among a prefix's values they reach its group's rows alone, among a sequence's own those that
+    see them; keys without weight too."""
+    b = Shared(BF16, 4, 2, 64, 16, [40, 20], [0, 2, 4], [10, 33, 20, 2], [1, 33, 1, 2], seed=19)
+    good = b.run()
+    page = int(b.prefix_table[0, 2])
+    b.v_pages[page, 7, 1, 5] = INF           # key 39 of the first prefix, key head 1
+    page = int(b.page_table[1, 1])
+    b.v_pages[page, 4, 0, 9] = NAN           # key 20 of sequence 1, key head 0
+    out = b.run()
+    assert (out[:34, 2:, 5] == INF).all()
+    seen = 1 + 20                            # rows of sequence 1 from position 20 on
+    assert out[seen:34, :2, 9].isnan().all() and not out[:seen, :2, 9].isnan().any()
+    mask = torch.ones_like(good, dtype=torch.bool)
+    mask[:34, 2:, 5] = False
+    mask[seen:34, :2, 9] = False
+    assert torch.equal(out[mask], good[mask])
+
+
+@pytest.mark.parametrize("news", [[1, 1], [40, 1]])
+def test_shared_scores_of_minus_infinity(news):
+    """Rows whose scores are all minus infinity have no softmax, also in parts; a part of such
+    scores beside finite ones has no weight."""
+    b = Shared(BF16, 2, 2, 64, 16, [600], [0, 2], [40, 3], news, seed=21)
+    good = _np(b.run())
+    b.q[0] = 3e38
+    used = b.prefix_table[0, :38].long()
+    b.k_pages[used] = -3e38
+    out = b.run()
+    b.kv_lens = _int([0, 3])
+    alone = b.run(q_starts=_int([0, 1, 1 + news[1]]))
+    assert alone[0].isnan().all()
+    assert good.shape == out.shape
+
+
+def test_shared_repeats_graphs_and_streams():
+    b = Shared(BF16, 16, 2, 128, 32, [900], [0, 6], [20, 300, 7, 64, 65, 1], [1, 40, 1, 3, 1, 1], seed=23)
+    hints = dict(max_q=40, max_kv=512, max_prefix=1024)
+    first = b.run(**hints)
+    b.check(first, "eager")
+    for _ in range(3):
+        assert torch.equal(b.run(**hints), first)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        b.run(**hints)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out = b.run(**hints)
+    for i in range(4):
+        b.prefix_lens.fill_(900 if i % 2 == 0 else 333)
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, b.run(**hints))
+    with torch.cuda.stream(side):
+        other = b.run(**hints)
+    here = b.run(**hints)
+    torch.cuda.synchronize()
+    assert torch.equal(here, other)
+
+
+def test_shared_nothing_to_do():
+    b = Shared(F16, 4, 2, 64, 16, [20], [0, 3], [3, 2, 5], [1, 1, 1], seed=25)
+    b.q = b.q[:0]
+    assert b.run(q_starts=_int([0, 0, 0, 0])).shape == (0, 4, 64)
+    b = Shared(F16, 4, 2, 64, 16, [], [0], [3, 2, 5], [1, 1, 1], seed=25)
+    b.check(b.run(), "no groups")
+
+
+# ---------------------------------------------------------------- batch tables
+
+def _tables_case(seqs, page, longest, seed, grow=9, ring=True):
+    rng = np.random.default_rng(seed)
+    lens = rng.integers(0, longest + 1, seqs)
+    change = rng.integers(-3, grow + 1, seqs)
+    change[rng.random(seqs) < 0.1] = -10 ** 9
+    width = -(-(longest + grow) // page) + 1
+    held = -(-lens // page)
+    pages = int(held.sum()) + seqs * (grow // page + 2) + 7
+    ids = rng.permutation(pages)
+    table = np.full((seqs, width), -1, np.int32)
+    at = 0
+    for s in range(seqs):
+        table[s, :held[s]] = ids[at:at + held[s]]
+        at += held[s]
+    first = int(rng.integers(pages))
+    free = np.full(pages, -1, np.int32)
+    free[(first + np.arange(pages - at)) % pages] = ids[at:]
+    return change, lens, table, free, [first, pages - at]
+
+
+def _tables_check(change, lens, table, page, tokens, ring, free, offsets=None, **kw):
+    wt, wr = table.tolist(), None if ring is None else ring.tolist()
+    want = plain.tables(change.tolist(), lens.tolist(), wt, page, tokens, wr, free, offsets)
+    dt = _int(table.tolist()) if table.size else torch.empty(table.shape, dtype=torch.int32, device=DEV)
+    dr = None if ring is None else _int(ring.tolist())
+    dc, dl = (_int(a.tolist()) for a in (change, lens))
+    got = lg.batch_tables(dc, dl, dt, page, tokens, dr, None if ring is None else _int(free),
+                          None if offsets is None else _int(offsets), **kw)
+    for g, w, what in zip(got, want, ("positions", "slots", "kv_lens", "q_starts", "free_range")):
+        assert (g is None and w is None) or g.tolist() == w, what
+    assert dt.tolist() == wt, "page_table"
+    assert ring is None or dr.tolist() == wr, "free_pages"
+    return got
+
+
+@pytest.mark.parametrize("seqs,page,longest", [(1, 16, 100), (7, 1, 9), (63, 16, 300), (64, 32, 31), (65, 48, 1000),
+                                               (1023, 16, 100), (1024, 64, 70), (1025, 16, 40), (3001, 128, 500)])
+def test_tables(seqs, page, longest):
+    for seed in range(3):
+        change, lens, table, ring, free = _tables_case(seqs, page, longest, 100 * seqs + seed)
+        tokens = int(change.clip(0).sum()) + 5 * seed
+        offsets = None if seed == 0 else np.random.default_rng(seed).integers(0, 9999, seqs).tolist()
+        got = _tables_check(change, lens, table, page, tokens, ring, free, offsets)
+        assert int(got[3][-1]) == change.clip(0).sum()
+
+
+@pytest.mark.parametrize("seqs", [5, 300, 2500])
+def test_tables_without_room(seqs):
+    change, lens, table, ring, free = _tables_case(seqs, 16, 90, seqs)
+    rows = int(change.clip(0).sum())
+    for tokens in (0, 1, rows // 2, rows - 1):
+        _tables_check(change, lens, table, 16, tokens, ring, free)
+    for count in (0, 1, seqs // 3):
+        _tables_check(change, lens, table, 16, rows, ring, [free[0], count])
+    # table rows that are full
+    _tables_check(change, lens, np.ascontiguousarray(table[:, :4]), 16, rows, ring, free)
+    assert (lens + change.clip(0)).max() > 4 * 16
+
+
+def test_tables_long_prompts():
+    change = np.array([40000, 0, 1, 70001, -5])
+    lens = np.array([0, 17, 15, 1000, 33])
+    rng = np.random.default_rng(1)
+    ids = rng.permutation(4000)
+    table = np.full((5, 2300), -1, np.int32)
+    at = 0
+    for s, n in enumerate(lens):
+        k = -(-int(n) // 32)
+        table[s, :k] = ids[at:at + k]
+        at += k
+    ring = np.concatenate([ids[at:], np.full(at, -1)]).astype(np.int32)
+    _tables_check(change, lens, table, 32, 110100, ring, [0, 4000 - at])
+
+
+def test_tables_without_a_ring():
+    change, lens, table, _, _ = _tables_case(40, 16, 200, 3)
+    table = np.random.default_rng(3).permutation(table.size).astype(np.int32).reshape(table.shape)
+    got = _tables_check(change, lens, table, 16, int(change.clip(0).sum()) + 3, None, [0, 0])
+    assert got[4] is None
+
+
+def test_tables_lengths_and_ranges_outside():
+    """They are brought inside; a ring that would overflow drops what is given back."""
+    change = np.array([3, -2, 5, -(1 << 31), (1 << 31) - 1, 2])
+    lens = np.array([-7, 1 << 30, 20, 31, 4, -(1 << 31)])
+    table = np.arange(6 * 4, dtype=np.int32).reshape(6, 4)
+    ring = np.arange(100, 130, dtype=np.int32)
+    for free in ([-3, 20], [1 << 30, 29], [-(1 << 31), -1], [7, 1 << 30], [29, 30]):
+        _tables_check(change, lens, table, 16, 20, ring, free)
+
+
+def test_tables_no_sequences_no_rows():
+    got = _tables_check(np.zeros(0, int), np.zeros(0, int), np.zeros((0, 4), np.int32), 16, 3, np.arange(5), [2, 3])
+    assert got[3].tolist() == [0]
+    _tables_check(np.array([-3]), np.array([20]), np.arange(4, dtype=np.int32)[None], 16, 0, np.arange(5), [2, 3])
+
+
+def test_tables_strided_table():
+    change, lens, table, ring, free = _tables_case(9, 16, 100, 5)
+    wide = torch.full((9, table.shape[1] + 7), -5, dtype=torch.int32, device=DEV)
+    wide[:, 2:-5] = _int(table.tolist())
+    wt, wr = table.tolist(), ring.tolist()
+    want = plain.tables(change.tolist(), lens.tolist(), wt, 16, 80, wr, free)
+    got = lg.batch_tables(_int(change.tolist()), _int(lens.tolist()), wide[:, 2:-5], 16, 80, _int(ring.tolist()),
+                          _int(free))
+    assert all(g.tolist() == w for g, w in zip(got, want))
+    assert wide[:, 2:-5].tolist() == wt and (wide[:, :2] == -5).all() and (wide[:, -5:] == -5).all()
+
+
+def test_tables_in_place_and_replayed():
+    """A captured step goes on from where it ended: 40 steps of 6 sequences, some of which end."""
+    page, seqs = 4, 6
+    table, ring, free = np.full((seqs, 12), -1, np.int32), np.arange(30)[::-1].copy(), [11, 30]
+    lens = np.zeros(seqs, int)
+    dt, dr, df, dl = _int(table.tolist()), _int(ring.tolist()), _int(free), _int(lens.tolist())
+    dc = _int([1] * seqs)
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        got = lg.batch_tables(dc, dl, dt, page, seqs, dr, df, in_place=True)
+    assert got[2].data_ptr() == dl.data_ptr() and got[4].data_ptr() == df.data_ptr()
+    wt, wr, wl, wf = table.tolist(), ring.tolist(), lens.tolist(), free
+    rng = np.random.default_rng(0)
+    for _ in range(40):
+        change = [int(-wl[s]) if rng.random() < 0.1 else int(rng.integers(-1, 3)) for s in range(seqs)]
+        dc.copy_(_int(change))
+        want = plain.tables(change, wl, wt, page, seqs, wr, wf)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert [g.tolist() for g in got] == list(want)
+        assert dt.tolist() == wt and dr.tolist() == wr
+        wl, wf = want[2], want[4]
+
+
+# -------------------------------------------------------------------- sampling
+
+# A weight m 2^e, m in [1, 2], is off by at most 2^(e - 41) (its term's rounding) and 2^-48 of
+# itself, so a sum by at most 2^-41 + 2^-48 of itself, and 2^20 tokens below 2^-64 by 2^-44: a
+# border that is further from moving, of the total, than four times that does not move.
+MARGIN = 2.0 ** -38
+
+
+def _logits(rows, vocab, seed, spread=2.5):
+    rng = np.random.default_rng(seed)
+    x = rng.normal(0, spread, (rows, vocab))
+    for r in range(rows):
+        at = rng.integers(0, vocab, min(20, vocab))
+        x[r, at] += rng.normal(5, 2.5, len(at))
+    return x
+
+
+def _sample_check(x, u, temperature=None, top_k=None, top_p=None, min_p=None, logits=None):
+    """x: a CPU tensor of logits; the settings lists or None."""
+    d = x.to(DEV) if logits is None else logits
+    dev = [None if a is None else _int(a, t) for a, t in ((temperature, F32), (top_k, torch.int32), (top_p, F32),
+                                                         (min_p, F32))]
+    tokens, logprobs = lg.sample_tokens(d, _int(u, F32), *dev)
+    assert tokens.dtype == torch.int64 and logprobs.dtype == F32
+    tokens, logprobs = tokens.tolist(), logprobs.tolist()
+    near = 0
+    rows = x.double().numpy()
+
+    def setting(a, r, default):
+        return default if a is None else float(np.float32(a[r]))
+
+    for r in range(x.shape[0]):
+        want, logprob, margin = plain.sample(rows[r], float(np.float32(u[r])), setting(temperature, r, 1.0),
+                                             0 if top_k is None else top_k[r], setting(top_p, r, 1.0),
+                                             setting(min_p, r, 0.0))
+        if margin < MARGIN:
+            near += 1
+            continue
+        assert tokens[r] == want, (r, tokens[r], want, margin)
+        if want < 0:
+            assert logprobs[r] != logprobs[r]
+        else:  # rounded once from 64 bits
+            assert abs(logprobs[r] - logprob) <= 2.0 ** -24 * abs(logprob) + 1e-11, (r, logprobs[r], logprob)
+    assert near <= x.shape[0] // 20, f"{near} rows too close to a border"
+    return tokens
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("vocab", [1, 2, 7, 64, 1000, 4097, 8191, 8192, 32000, 50272, 131073])
+def test_sample(dtype, vocab):
+    rows = 24
+    rng = np.random.default_rng(vocab)
+    x = torch.from_numpy(_logits(rows, vocab, vocab)).to(dtype)
+    u = rng.random(rows).astype(np.float32).clip(0, 1 - 2.0 ** -24).tolist()
+    t, p, m = rng.uniform(0.5, 1.5, rows).tolist(), rng.uniform(0.3, 0.99, rows).tolist(), rng.uniform(0, 0.2, rows).tolist()
+    k = rng.integers(1, 300, rows).tolist()
+    _sample_check(x, u)
+    _sample_check(x, u, t)
+    _sample_check(x, u, t, top_k=k)
+    _sample_check(x, u, t, top_p=p)
+    _sample_check(x, u, t, min_p=m)
+    _sample_check(x, u, t, k, p, m)
+    mixed = [[v if i % 3 == j else off for i, v in enumerate(a)] for j, (a, off) in
+             enumerate(((k, 0), (p, 1.0), (m, 0.0)))]
+    t[4] = t[9] = 0.0
+    _sample_check(x, u, t, *mixed)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+def test_sample_equal_logits(dtype):
+    """Equal logits are taken by their index; sums of equal weights are exact."""
+    rows, vocab = 16, 4096
+    x = torch.zeros((rows, vocab), dtype=dtype)
+    x[1] = -0.0
+    x[2, ::2] = -0.0
+    x[3, 100:] = -5.0
+    x[4] = torch.arange(vocab).remainder(3).to(dtype)
+    x[5, 7] = x[5, 4000] = 4.0
+    u = [i / rows for i in range(rows)]
+    one = [1.0] * rows
+    assert _sample_check(x, u)[:2] == [0, 256]
+    # k of the equal ones: the first k
+    got = _sample_check(x, [1 - 2.0 ** -24] * rows, top_k=[5] * rows)
+    assert got[0] == 4 and got[1] == 4 and got[2] == 4 and got[3] == 4 and got[4] == 14
+    got = _sample_check(x, [1 - 2.0 ** -24] * rows, top_p=[0.25] * rows)
+    assert got[0] == 1023 and got[1] == 1023 and got[2] == 1023
+    got = _sample_check(x, [1 - 2.0 ** -24] * rows, top_p=[0.5] * rows, top_k=[8] * rows)
+    assert got[0] == 3
+    got = _sample_check(x, [1 - 2.0 ** -24] * rows, min_p=one)
+    assert got[0] == vocab - 1 and got[5] == 4000
+    got = _sample_check(x, u, temperature=[0.0] * rows)
+    assert got[0] == 0 and got[4] == 2 and got[5] == 7
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+def test_sample_masked_and_extreme_logits(dtype):
+    rows, vocab = 12, 9001
+    x = torch.from_numpy(_logits(rows, vocab, 5)).to(dtype)
+    x[0, 1:] = -INF
+    x[1, :-1] = -INF
+    x[2, ::2] = -INF
+    x[3] = -INF
+    x[3, 4000:4003] = 2.0
+    big = torch.finfo(dtype).max
+    x[4] = -big
+    x[4, 77] = big
+    x[5] = big
+    x[6] = torch.finfo(dtype).tiny * torch.arange(vocab).remainder(5).to(dtype)
+    x[7] *= 0
+    x[7, 5] = -big
+    x[8] *= 100
+    u = np.random.default_rng(2).random(rows).astype(np.float32).tolist()
+    u[0] = 0.0
+    u[1] = 1 - 2.0 ** -24
+    for t in (1.0, 0.01, 1e-30, 1e30, 3e38, 1e-45):
+        for more in (dict(), dict(top_k=[3] * rows), dict(top_p=[0.6] * rows), dict(top_k=[2000] * rows, top_p=[0.9] * rows),
+                     dict(min_p=[0.05] * rows)):
+            _sample_check(x, u, [t] * rows, **more)
+
+
+def test_sample_rows_without_a_distribution():
+    rows, vocab = 14, 1003
+    x = torch.from_numpy(_logits(rows, vocab, 6)).to(F16)
+    x[0, 7] = NAN
+    x[1, 1002] = INF
+    x[2] = -INF
+    u, t, p, m = [0.5] * rows, [1.0] * rows, [0.9] * rows, [0.0] * rows
+    u[3], u[4], u[5], u[6] = 1.0, -0.1, NAN, INF
+    t[7], t[8], t[9] = -1.0, NAN, INF
+    p[10], m[11] = NAN, NAN
+    p[12], m[13] = -1.0, 5.0
+    for more in (dict(), dict(top_k=[9] * rows)):
+        got = _sample_check(x, u, t, top_p=p, min_p=m, **more)
+        assert got[:12] == [-1] * 12 and min(got[12:]) >= 0
+        assert got[12] == int(x[12].float().argmax()) and got[13] == int(x[13].float().argmax())
+
+
+def test_sample_settings_that_filter_nothing():
+    x = torch.from_numpy(_logits(5, 3001, 7)).to(BF16)
+    u = [0.1, 0.3, 0.5, 0.7, 0.9]
+    want = _sample_check(x, u)
+    assert _sample_check(x, u, [1.0] * 5, [0, -1, 3001, 1 << 30, -(1 << 31)], [1.0, 1.5, INF, 1.0, 2.0],
+                         [0.0, -1.0, -INF, 0.0, -0.5]) == want
+
+
+@pytest.mark.parametrize("dtype", [F16, F32])
+@pytest.mark.parametrize("top_p", [0.999999, 0.5, 1e-30, 0.0])
+def test_sample_flat_and_steep(dtype, top_p):
+    """Borders among many tokens of one value, and none but the first."""
+    rows, vocab = 6, 70001
+    x = torch.zeros((rows, vocab), dtype=dtype)
+    x[1] = torch.linspace(-1, 1, vocab).to(dtype)
+    x[2] = torch.linspace(0, 50, vocab).to(dtype)
+    x[3, 50000:] = 0.25
+    x[4] = torch.arange(vocab).remainder(256).to(dtype) / 16
+    x[5, 69999] = 12.0
+    u = [0.999999, 0.2, 0.4, 0.6, 0.8, 0.3]
+    _sample_check(x, u, top_p=[top_p] * rows)
+    _sample_check(x, u, top_p=[top_p] * rows, top_k=[40000] * rows)
+    _sample_check(x, u, [0.7] * rows, top_p=[top_p] * rows, min_p=[0.01] * rows)
+
+
+def test_sample_strided_and_unaligned_rows():
+    wide = torch.from_numpy(_logits(9, 5011, 8)).to(F16)
+    dev = wide.to(DEV)
+    u = [i / 9 for i in range(9)]
+    for lo, hi in ((1, 5010), (3, 4099), (8, 5000), (0, 5011)):
+        _sample_check(wide[:, lo:hi].contiguous(), u, top_p=[0.9] * 9, logits=dev[:, lo:hi])
+    _sample_check(wide[::2].contiguous(), u[:5], top_k=[50] * 5, logits=dev[::2])
+
+
+def test_sample_largest_vocabulary():
+    x = torch.from_numpy(_logits(2, 1 << 20, 9, 1.0)).to(F32)
+    _sample_check(x, [0.3, 0.9], top_p=[0.7, 0.9])
+    _sample_check(x, [0.3, 0.9])
+    _sample_check(x.to(BF16), [0.3, 0.9], top_p=[0.7, 0.9])
+
+
+def test_sample_repeats_graphs_and_streams():
+    rows, vocab = 40, 32000
+    x = torch.from_numpy(_logits(rows, vocab, 10)).to(F16).to(DEV)
+    u = torch.rand(rows, device=DEV)
+    t, p = torch.full((rows,), 0.8, device=DEV), torch.full((rows,), 0.9, device=DEV)
+    first = lg.sample_tokens(x, u, t, top_p=p)
+    for _ in range(3):
+        again = lg.sample_tokens(x, u, t, top_p=p)
+        assert all(torch.equal(a, b) for a, b in zip(first, again))
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        got = lg.sample_tokens(x, u, t, top_p=p)
+    for _ in range(4):
+        u.uniform_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, lg.sample_tokens(x, u, t, top_p=p)))
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = lg.sample_tokens(x, u, t, top_p=p)
+    here = lg.sample_tokens(x, u, t, top_p=p)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(here, other))
+
+
+def test_sample_follows_the_distribution():
+    """Evenly spaced numbers draw each token as often as its probability says, to one draw."""
+    vocab, rows = 50, 4096
+    x = torch.from_numpy(_logits(1, vocab, 11, 1.5)).to(F32)
+    u = (np.arange(rows) + 0.5) / rows
+    tokens, _ = lg.sample_tokens(x.expand(rows, vocab).to(DEV), _int(u.tolist(), F32))
+    count = np.bincount(tokens.cpu().numpy(), minlength=vocab)
+    p = torch.softmax(x[0].double(), 0).numpy()
+    assert np.abs(count - p * rows).max() <= 1.0 + 1e-3
+
+
+def test_sample_nothing_to_do_and_out():
+    tokens, logprobs = lg.sample_tokens(torch.empty((0, 100), dtype=F16, device=DEV), _int([], F32))
+    assert tokens.shape == (0,) and logprobs.shape == (0,)
+    out = torch.full((3,), -9, dtype=torch.int64, device=DEV)
+    before = out._version
+    tokens, _ = lg.sample_tokens(torch.zeros((3, 10), dtype=F32, device=DEV), _int([0.0, 0.5, 0.9], F32), out=out)
+    assert tokens.data_ptr() == out.data_ptr() and out._version > before
+    assert out.tolist() == [0, 5, 8]  # 0.9 in 32 bits is less than 9 of 10
