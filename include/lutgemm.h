@@ -586,26 +586,29 @@ int lutgemm_batch_tables(const lutgemm_tables* t, const int32_t* d_change, const
  * to more than u times their total; its log-probability is log(w / total).
  * temperature 0 takes the largest logit, the lowest index of equal ones, with
  * log-probability 0.
- * Weights and sums hold 40 bits and more; tokens with a weight below 2^-64 count as
+ * Weights and sums hold 40 bits and more; tokens with a weight below 2^-63 count as
  * having none, and no top_k or top_p border is looked for among them.
  *   d_logits  [rows][vocab] of type F16, BF16 or F32, rows row_step elements apart; -infinity:
  *             the token is never drawn
  *   d_u       fp32 [rows] in [0, 1)     d_temperature, d_top_p, d_min_p  fp32 [rows] or
  *   NULL: 1, 1, 0                       d_top_k  int32 [rows] or NULL: 0
  *   d_tokens  int64 [rows]              d_logprobs  fp32 [rows] or NULL
+ *   d_workspace  at least lutgemm_sample_tokens_workspace bytes (50 MB at most); as for attention
  * A row has no distribution, and token -1 and log-probability NaN, if it holds NaN or
  * +infinity or nothing but -infinity, if u is outside [0, 1), if the temperature is negative,
  * infinite or NaN, or if top_p or min_p is NaN. Results are bitwise reproducible. Outputs
  * that overlap an input or each other are refused with LUTGEMM_ERR_SHAPE.
  * Shape rules: 0 <= rows < 2^22, 1 <= vocab <= 2^20. Alignment: d_logits by its type,
- * d_tokens 8 bytes, the others 4. */
+ * d_workspace 16 bytes, d_tokens 8, the others 4. */
 typedef struct lutgemm_sample {
   int32_t type, rows, vocab, reserved;
   int64_t row_step;
 } lutgemm_sample;
+int lutgemm_sample_tokens_workspace(const lutgemm_sample* s, size_t* bytes);
 int lutgemm_sample_tokens(const lutgemm_sample* s, const void* d_logits, const float* d_u,
                           const float* d_temperature, const int32_t* d_top_k, const float* d_top_p,
-                          const float* d_min_p, int64_t* d_tokens, float* d_logprobs, void* stream);
+                          const float* d_min_p, int64_t* d_tokens, float* d_logprobs,
+                          void* d_workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

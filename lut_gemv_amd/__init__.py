@@ -144,7 +144,9 @@ def lib() -> ctypes.CDLL:
     L.lutgemm_batch_tables.restype = ctypes.c_int
     L.lutgemm_batch_tables.argtypes = [_P] * 13 + [_SZ, _P]
     L.lutgemm_sample_tokens.restype = ctypes.c_int
-    L.lutgemm_sample_tokens.argtypes = [_P] * 10
+    L.lutgemm_sample_tokens.argtypes = [_P] * 10 + [_SZ, _P]
+    L.lutgemm_sample_tokens_workspace.restype = ctypes.c_int
+    L.lutgemm_sample_tokens_workspace.argtypes = [_P, _SZP]
     L.lutgemm_query_plan.restype = ctypes.c_int
     L.lutgemm_query_plan.argtypes = [_SHP, ctypes.c_int32, ctypes.c_int32, _SZ,
                                      ctypes.POINTER(_Plan)]

@@ -33,6 +33,7 @@ decltype(&lutgemm_shared_attention_workspace) g_shared_ws;
 decltype(&lutgemm_batch_tables) g_tables;
 decltype(&lutgemm_batch_tables_workspace) g_tables_ws;
 decltype(&lutgemm_sample_tokens) g_sample;
+decltype(&lutgemm_sample_tokens_workspace) g_sample_ws;
 PyObject* g_status_error;  // LutGemmError(status, where)
 
 struct Refused : std::runtime_error {
@@ -500,10 +501,15 @@ PyObject* sample(PyObject* const* a) {
     flat(got[0], at::kLong, x, {rows}, "out");
   }
   got[1] = at::empty({rows}, x.options().dtype(at::kFloat));
+  constexpr const char* where = "lutgemm_sample_tokens";
+  size_t need = 0;
+  check(g_sample_ws(&d, &need), where);
+  at::Tensor ws;
+  if (need) ws = scratch(need, x);
   check(g_sample(&d, x.data_ptr(), (const float*)u, (const float*)temperature, (const int32_t*)top_k,
                  (const float*)top_p, (const float*)min_p, (int64_t*)got[0].data_ptr(),
-                 (float*)got[1].data_ptr(), stream_of(x)),
-        "lutgemm_sample_tokens");
+                 (float*)got[1].data_ptr(), need ? ws.data_ptr() : nullptr, need, stream_of(x)),
+        where);
   if (a[6] != Py_None) written(got[0]);
   return tuple_of(got);
 }
@@ -591,7 +597,7 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
 
 // init(addresses of the entry points, in the order in which they are bound here, LutGemmError)
 PyObject* init(PyObject*, PyObject* args) {
-  constexpr Py_ssize_t kPoints = 10;
+  constexpr Py_ssize_t kPoints = 11;
   if (PyTuple_GET_SIZE(args) != kPoints + 1) {
     PyErr_SetString(PyExc_TypeError, "init takes the entry points' addresses and an exception");
     return nullptr;
@@ -610,6 +616,7 @@ PyObject* init(PyObject*, PyObject* args) {
   g_tables = (decltype(g_tables))f[7];
   g_tables_ws = (decltype(g_tables_ws))f[8];
   g_sample = (decltype(g_sample))f[9];
+  g_sample_ws = (decltype(g_sample_ws))f[10];
   PyObject* error = PyTuple_GET_ITEM(args, kPoints);
   Py_INCREF(error);
   Py_XSETREF(g_status_error, error);

@@ -35,7 +35,8 @@ def _load():
              "lutgemm_paged_attention_workspace", "lutgemm_adapters_add",
              "lutgemm_adapters_workspace", "lutgemm_shared_attention",
              "lutgemm_shared_attention_workspace", "lutgemm_batch_tables",
-             "lutgemm_batch_tables_workspace", "lutgemm_sample_tokens")
+             "lutgemm_batch_tables_workspace", "lutgemm_sample_tokens",
+             "lutgemm_sample_tokens_workspace")
     _binding.init(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in names), LutGemmError)
     _ops = _binding
     return _ops

@@ -120,12 +120,12 @@ def test_tables_workspace():
 SAMPLE = dict(type=0, rows=4, vocab=1000, reserved=0, row_step=1000)
 
 
-def _sample(**change):
+def _sample(wsb=1 << 30, **change):
     at = dict(logits=A, u=A + FAR, temperature=A + 2 * FAR, top_k=A + 3 * FAR, top_p=A + 4 * FAR,
-              min_p=A + 5 * FAR, tokens=A + 6 * FAR, logprobs=A + 7 * FAR)
+              min_p=A + 5 * FAR, tokens=A + 6 * FAR, logprobs=A + 7 * FAR, ws=A + 8 * FAR)
     d = _SAMPLE.pack(*[change.get(k, v) for k, v in SAMPLE.items()])
     at.update({k: v for k, v in change.items() if k in at})
-    return lg.lib().lutgemm_sample_tokens(d, *at.values(), None)
+    return lg.lib().lutgemm_sample_tokens(d, *at.values(), wsb, None)
 
 
 @pytest.mark.parametrize("change,status", [
@@ -136,7 +136,8 @@ def _sample(**change):
     (dict(temperature=A + 2), ALIGN), (dict(top_k=A + 1), ALIGN), (dict(top_p=A + 2), ALIGN),
     (dict(min_p=A + 2), ALIGN), (dict(tokens=A + 6 * FAR + 4), ALIGN), (dict(logprobs=A + 2), ALIGN),
     (dict(tokens=A + 7992), SHAPE), (dict(tokens=A + FAR + 8), SHAPE), (dict(logprobs=A + 6 * FAR + 28), SHAPE),
-    (dict(logprobs=A + 3 * FAR), SHAPE),
+    (dict(logprobs=A + 3 * FAR), SHAPE), (dict(ws=None), NULL), (dict(ws=A + 8 * FAR + 8), ALIGN),
+    (dict(wsb=100), BUFFER), (dict(ws=A), SHAPE), (dict(ws=A + 5 * FAR), SHAPE),
 ])
 def test_sample_refusals(change, status):
     assert _sample(**change) == status
@@ -144,7 +145,16 @@ def test_sample_refusals(change, status):
 
 def test_sample_empty_call():
     assert _sample(rows=0, logits=None, u=None, tokens=None) == 0
-    assert lg.lib().lutgemm_sample_tokens(None, *[A] * 8, None) == NULL
+    assert lg.lib().lutgemm_sample_tokens(None, *[A] * 9, 1 << 30, None) == NULL
+
+
+def test_sample_workspace():
+    n = ctypes.c_size_t(7)
+    for rows, vocab in ((0, 5), (1, 1), (1, 1 << 20), (256, 131073), ((1 << 22) - 1, 1 << 20), (5000, 32000)):
+        d = _SAMPLE.pack(0, rows, vocab, 0, vocab)
+        assert lg.lib().lutgemm_sample_tokens_workspace(d, ctypes.byref(n)) == 0
+        assert (n.value > 0) == (rows > 0) and n.value <= 52 << 20
+    assert lg.lib().lutgemm_sample_tokens_workspace(d, None) == NULL
 
 
 def test_descriptors_match_the_header(tmp_path):
