@@ -586,8 +586,8 @@ int lutgemm_batch_tables(const lutgemm_tables* t, const int32_t* d_change, const
  * to more than u times their total; its log-probability is log(w / total).
  * temperature 0 takes the largest logit, the lowest index of equal ones, with
  * log-probability 0.
- * Weights and sums hold 40 bits and more; tokens with a weight below 2^-63 count as
- * having none, and no top_k or top_p border is looked for among them.
+ * Weights hold 41 bits, sums are exact to 2^-28 of the total (2^-33 for up to 2^17 tokens); tokens with a weight below
+ * 2^-63 count as having none, and no top_k or top_p border is looked for among them.
  *   d_logits  [rows][vocab] of type F16, BF16 or F32, rows row_step elements apart; -infinity:
  *             the token is never drawn
  *   d_u       fp32 [rows] in [0, 1)     d_temperature, d_top_p, d_min_p  fp32 [rows] or

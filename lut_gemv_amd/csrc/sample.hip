@@ -5,8 +5,8 @@
 // a row's kept tokens are those before one border: a value, and among the tokens that
 // have it an index. Borders and the drawn token follow from sums of weights, and of
 // 100000 tokens whose sums are off by 2^-24 the wrong one is taken in 1 of 100 rows.
-// So weights are computed in 64 bits, 2^y = m 2^e from a table of 2^(i/1024) and a cubic
-// polynomial, and all sums are integers, exact and the same in any order: by value, m 2^40 in
+// So weights are computed in 64 bits, 2^y = m 2^e from a table of 2^(i/32), which lies across the
+// LDS banks once, and a polynomial, and all sums are integers, exact and the same in any order: by value, m 2^40 in
 // bins of a sixteenth of an octave, where the bin tells e; in the order of the tokens,
 // 2^S m 2^e with S = 62 - log2(vocab). Tokens below 2^-63 of the largest weight count as none.
 //
@@ -19,6 +19,7 @@
 // they are few (a radix select by weight, on 64-bit codes of value and index, then on
 // the index); where they are many, the bins' sums say in which piece the drawn token lies,
 // and only that is weighed again.
+#include <algorithm>
 #include <type_traits>
 
 #include "serve.h"
@@ -33,11 +34,14 @@ namespace {
 using namespace serve;
 
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
-constexpr int kSteps = 1024;       // table entries of an octave
-constexpr int kBins = 1024;        // sixteenths of octaves below the largest weight
+constexpr int kSteps = 32;         // table entries of an octave
+constexpr int kBins = 1024;        // sixteenths of octaves below a piece's top
+constexpr int kOctaves = kBins / 16;
+constexpr int kListUnit = 50;      // weights of a list: 2^50 m 2^e
 constexpr int kList = 4096;        // tokens of a list
 constexpr int kMine = kList / kThreads;
-constexpr int kStripes = 4;        // words of 16 bytes of a piece that a thread holds at most
+constexpr int kStripes = 5;        // words of 16 bytes of a piece that a thread holds at most
+constexpr int kAhead = 4;          // words whose loads are under way
 constexpr int kLeastPiece = 4096;
 constexpr int kMostPieces = 64;
 constexpr int64_t kMostTokens = 1 << 20;
@@ -86,30 +90,57 @@ __device__ __forceinline__ uint64_t code_of(typename T::Raw raw, int index) {
   return (uint64_t)(~key_of<T>(raw) & all) << kIndexBits | (uint32_t)index;
 }
 
-// 16 bytes at any element's address: rows of odd lengths lie anywhere.
-typedef uint32_t WordOf4 __attribute__((ext_vector_type(4), aligned(4)));
-typedef uint32_t WordOf2 __attribute__((ext_vector_type(4), aligned(2)));
-
 // `n` tokens of a row: stripes of kThreads words of kPer tokens.
 template <class T>
 struct Piece {
   typedef typename T::Raw Raw;
   static constexpr int kPer = 16 / sizeof(Raw);
-  const Raw* at;
-  int n;
+  __amdgpu_buffer_rsrc_t at;
+  int n, lead;
+  // Loads are of whole aligned words of 4 bytes, so a piece at an odd 2-byte address begins with
+  // the element before it, `lead` of them, and one of an odd end ends with the element behind:
+  // these lie in the aligned words of its own and count as -infinity, as does all
+  // that is behind (buffer loads give zeros there).
+  __device__ __forceinline__ Piece(const Raw* from, int count) {
+    lead = sizeof(Raw) == 2 && ((uintptr_t)from & 2) ? 1 : 0;
+    n = count + lead;
+    at = __builtin_amdgcn_make_buffer_rsrc((void*)(from - lead), 0, (n * (int)sizeof(Raw) + 3) & ~3, 0x00027000);
+  }
   __device__ __forceinline__ int stripes() const { return (n + kThreads * kPer - 1) / (kThreads * kPer); }
+  // those in which the wave has tokens
+  __device__ __forceinline__ int wave_stripes() const {
+    const int at = __builtin_amdgcn_readfirstlane((int)threadIdx.x & ~63) * kPer;
+    return n > at ? (n - at + kThreads * kPer - 1) / (kThreads * kPer) : 0;
+  }
   __device__ __forceinline__ int first(int stripe) const {
     return (stripe * kThreads + (int)threadIdx.x) * kPer;
   }
-  // The thread's word of a stripe, with -infinity past the end.
-  __device__ __forceinline__ u4v word(int stripe) const {
-    typedef typename std::conditional<sizeof(Raw) == 4, WordOf4, WordOf2>::type Any;
+  // the token of an element that is one: from 0 on
+  __device__ __forceinline__ int token(int element) const { return element - lead; }
+  __device__ __forceinline__ bool is_token(int element) const { return element >= lead && element < n; }
+  // The thread's word of a stripe as it is loaded, and with -infinity for what is no token.
+  __device__ __forceinline__ u4v load(int stripe) const {
+    return __builtin_bit_cast(
+        u4v, __builtin_amdgcn_raw_buffer_load_b128(at, first(stripe) * (int)sizeof(Raw), 0, 0));
+  }
+  __device__ __forceinline__ void place(u4v& w, int stripe) const {
     const int i = first(stripe);
-    if (i + kPer <= n) return *(const Any*)(at + i);
-    u4v w;
-    Raw* const e = (Raw*)&w;
+    if (i + kPer <= n && i >= lead) return;
+    constexpr int each = 4 / sizeof(Raw);
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) e[j] = i + j < n ? at[i + j] : T::kNone;
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (each == 1) {
+        w[j] = is_token(i + j) ? w[j] : T::kNone;
+      } else {
+        const uint32_t lo = is_token(i + 2 * j) ? w[j] & 0xFFFF : T::kNone;
+        const uint32_t hi = is_token(i + 2 * j + 1) ? w[j] >> 16 : T::kNone;
+        w[j] = hi << 16 | lo;
+      }
+    }
+  }
+  __device__ __forceinline__ u4v word(int stripe) const {
+    u4v w = load(stripe);
+    place(w, stripe);
     return w;
   }
   // An element of which the place is only known when it runs.
@@ -125,14 +156,15 @@ struct Piece {
 };
 
 // What values are measured against: 2^top (a whole octave) is at least the weight of
-// `ref`, whose own distance from it is `shift` in 1024ths of an octave.
+// `ref`, whose own distance from it is `shift` in 32nds of an octave.
 struct Scale {
   double ref, step, shift, top;
+  float least;  // values below it have no weight: they are kOctaves + 1 octaves below the top
   __device__ __forceinline__ void set(float largest, float temperature) {
     const double octaves = 1.4426950408889634074 / (double)temperature;
     ref = (double)largest;
     step = octaves * kSteps;
-    const double p = ref * octaves;
+    const double p = ref * octaves;  // below: p and what its rounding took
     if (__builtin_fabs(p) < 0x1p40) {
       top = __builtin_ceil(p);
       shift = ((p - top) + __builtin_fma(ref, octaves, -p)) * kSteps;
@@ -140,39 +172,66 @@ struct Scale {
       top = p;
       shift = 0.0;
     }
+    const double x = ref + (-kSteps * (kOctaves + 1.0) - shift) / step;
+    least = (float)x;
+    if ((double)least < x) least = up(least);
   }
-  // The weight m 2^(k >> 10) of a value of at most ref, m in [1, 2] but for rounding.
-  __device__ __forceinline__ double weigh(double x, const double* steps, int* k) const {
+  static __device__ __forceinline__ float up(float x) {  // the next float
+    const int32_t b = __builtin_bit_cast(int32_t, x);
+    return x == 0.f ? 1e-45f : __builtin_bit_cast(float, b + (b >= 0 ? 1 : -1));
+  }
+  // The weight of a value from `least` to ref is m 2^(k >> 5), m in [1, 2] but for rounding, and
+  // m = a b. 2^x by its Taylor polynomial with the fifth term, x^5 c^5 / 120, taken as the
+  // nearest lower powers on |x| <= 1/2: off by 2^-43 at most.
+  __device__ __forceinline__ void factors(double x, const double* steps, int* k, double* a,
+                                          double* b) const {
     constexpr double kRound = 0x1.8p52, c = 0.69314718055994530942 / kSteps;
-    double y = __builtin_fma(x - ref, step, shift);
-    y = y < -1e6 ? -1e6 : y;
+    constexpr double c5 = c * c * c * c * c / 120;
+    const double y = __builtin_fma(x - ref, step, shift);
     const double s = y + kRound;
     *k = (int)(uint32_t)__builtin_bit_cast(uint64_t, s);
     const double f = y - (s - kRound);
-    const double p = __builtin_fma(
-        f, __builtin_fma(f, __builtin_fma(f, c * c * c / 6, c * c / 2), c), 1.0);
-    return steps[*k & (kSteps - 1)] * p;
+    double p = __builtin_fma(f, c * c * c * c / 24, c * c * c / 6 + 0.3125 * c5);
+    p = __builtin_fma(f, p, c * c / 2);
+    p = __builtin_fma(f, p, c - 0.01953125 * c5);
+    *a = __builtin_fma(f, p, 1.0);
+    *b = steps[*k & (kSteps - 1)];
+  }
+  // As integers: in its bin's sum, m 2^40, and by place, m 2^(S + e).
+  static __device__ __forceinline__ uint64_t by_term(double a, double b) {
+    constexpr double kUnit = 0x1p12;  // the last place of 2^12 + m is 2^-40
+    return __builtin_bit_cast(uint64_t, __builtin_fma(a, b, kUnit)) - __builtin_bit_cast(uint64_t, kUnit);
+  }
+  __device__ __forceinline__ uint64_t term(double x, const double* steps, int* k) const {
+    double a, b;
+    factors(x, steps, k, &a, &b);
+    return by_term(a, b);
+  }
+  // As a number of 41 bits, of which part sums of equal weights are exact.
+  static __device__ __forceinline__ double by_value(double a, double b, int k) {
+    constexpr double kUnit = 0x1p12;
+    return __builtin_ldexp(__builtin_fma(a, b, kUnit) - kUnit, k >> 5);
+  }
+  // In the unit of a list.
+  __device__ __forceinline__ uint64_t listed(double x, const double* steps) const {
+    constexpr double kOne = 0x1p52;
+    double a, b;
+    int k;
+    factors(x, steps, &k, &a, &b);
+    return __builtin_bit_cast(uint64_t, __builtin_ldexp(by_value(a, b, k), kListUnit) + kOne) -
+           __builtin_bit_cast(uint64_t, kOne);
+  }
+  __device__ __forceinline__ double weight(double x, const double* steps, int* k) const {
+    double a, b;
+    factors(x, steps, k, &a, &b);
+    return a * __builtin_ldexp(b, *k >> 5);
   }
 };
 
 // Sixteenths of octaves below the top, and the octave of such a bin.
-__device__ __forceinline__ int bin_of(int k) { return -(k >> 6); }
+__device__ __forceinline__ int bin_of(int k) { return -(k >> 1); }
 __device__ __forceinline__ int octave_of(int bin) { return (-bin) >> 4; }
 
-// x to the nearest integer, x below 2^51.
-__device__ __forceinline__ uint64_t whole(double x) {
-  constexpr double kOne = 0x1p52;
-  return __builtin_bit_cast(uint64_t, x + kOne) - __builtin_bit_cast(uint64_t, kOne);
-}
-// A weight in a bin's sum: m 2^40.
-__device__ __forceinline__ uint64_t term_of(double m) {
-  constexpr double kUnit = 0x1p12;  // the last place of 2^12 + m is 2^-40
-  return __builtin_bit_cast(uint64_t, m + kUnit) - __builtin_bit_cast(uint64_t, kUnit);
-}
-// A weight in a sum by place: m 2^(S + e).
-__device__ __forceinline__ uint64_t place_of(double m, int k, int scale) {
-  return whole(__builtin_ldexp(m, scale + (k >> 10)));
-}
 // v 2^by, without what falls below 1.
 __device__ __forceinline__ uint64_t shifted(uint64_t v, int by) {
   return by >= 64 || by <= -64 ? 0 : by >= 0 ? v << by : v >> -by;
@@ -190,33 +249,61 @@ __device__ __forceinline__ uint64_t share(float a, uint64_t v, bool up) {
   return (uint64_t)((product + rest) >> down);
 }
 
+// v of the lane that a DPP control names, 0 where there is none.
+template <int Control, int Rows, class V>
+__device__ __forceinline__ V from_lane(V v) {
+  if constexpr (sizeof(V) == 8) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, Control, Rows, 0xF, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), Control, Rows, 0xF, false);
+    return __builtin_bit_cast(V, (uint64_t)hi << 32 | lo);
+  } else {
+    return __builtin_bit_cast(
+        V, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), Control, Rows, 0xF, false));
+  }
+}
+
+// Sums of the lanes up to this one: within rows of sixteen, then of the rows before.
+template <class V>
+__device__ __forceinline__ V wave_scan(V v) {
+  v += from_lane<0x111, 0xF>(v);
+  v += from_lane<0x112, 0xF>(v);
+  v += from_lane<0x114, 0xF>(v);
+  v += from_lane<0x118, 0xF>(v);
+  v += from_lane<0x142, 0xA>(v);  // row 0's into 1, 2's into 3
+  v += from_lane<0x143, 0xC>(v);  // row 1's into 2 and 3
+  return v;
+}
+
+template <class V>
+__device__ __forceinline__ V lane_of(V v, int lane) {  // the lane is the same for the wave
+  if constexpr (sizeof(V) == 8) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)b, lane);
+    const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), lane);
+    return __builtin_bit_cast(V, (uint64_t)hi << 32 | lo);
+  } else {
+    return __builtin_bit_cast(V, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+  }
+}
+
 template <class V>
 __device__ __forceinline__ V wave_sum(V v) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d, 64);
-  return v;
+  return lane_of(wave_scan(v), 63);
 }
 
 // Sums of the threads before this one and itself, in order; *total: of all.
 template <class V>
 __device__ __forceinline__ V block_scan(V v, V* waves, V* total) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const V u = __shfl_up(v, d, 64);
-    if (lane >= d) v += u;
-  }
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  v = wave_scan(v);
   __syncthreads();
   if (lane == 63) waves[wave] = v;
   __syncthreads();
-  V before = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    if (w < wave) before += waves[w];
-    all += waves[w];
-  }
-  *total = all;
-  return v + before;
+  V sums = lane < kWaves ? waves[lane] : V(0);
+  sums = wave_scan(sums);
+  *total = lane_of(sums, 63);
+  return wave ? v + lane_of(sums, wave - 1) : v;
 }
 
 // A row's settings, and what they make of it.
@@ -246,7 +333,7 @@ struct Settings {
 
 // A piece's record in the workspace: this, then the bins' sums and counts or the parts' sums.
 struct Head {
-  double top;
+  double top;     // of Scale::set(largest, temperature)
   float largest;
   int32_t bad, at, pad;  // at: greedy: the first token of the largest value
 };
@@ -256,9 +343,9 @@ constexpr int kRecord = kCountsAt + kBins * 4;
 template <class T>
 __global__ __launch_bounds__(kThreads, 8) void chunk_kernel(SampleParams p) {
   typedef Piece<T> P;
-  __shared__ double steps[kSteps];
-  __shared__ uint64_t sums[kBins];
-  __shared__ uint32_t counts[kBins];
+  __shared__ __attribute__((aligned(256))) double steps[kSteps];
+  __shared__ uint64_t sums[kBins + 1];  // the last: what is not counted
+  __shared__ uint32_t counts[kBins + 1];
   __shared__ float waves[kWaves];
   __shared__ int32_t first;
   fetch(p);
@@ -266,17 +353,15 @@ __global__ __launch_bounds__(kThreads, 8) void chunk_kernel(SampleParams p) {
   const int64_t r = blockIdx.x / (unsigned)p.pieces;
   const int c = (int)(blockIdx.x % (unsigned)p.pieces);
   const int begin = c * p.piece;
-  P piece;
-  piece.at = (const typename T::Raw*)p.logits + r * p.row_step + begin;
-  piece.n = min(p.piece, p.vocab - begin);
-  const int stripes = piece.stripes();
+  const P piece((const typename T::Raw*)p.logits + r * p.row_step + begin, min(p.piece, p.vocab - begin));
+  const int stripes = piece.wave_stripes();
   u4v w[kStripes];
 #pragma unroll
   for (int s = 0; s < kStripes; ++s)
-    if (s < stripes) w[s] = piece.word(s);
+    if (s < stripes) w[s] = piece.load(s);
   const Settings set(p, r);
   // while the loads are under way
-  if (set.sums() || set.places()) steps[t] = exp2((double)t / kSteps);
+  if (t < kSteps) steps[t] = exp2((double)t / kSteps);
   if (set.sums()) sums[t] = 0;
   if (set.counts()) counts[t] = 0;
   if (t == 0) first = INT32_MAX;
@@ -284,13 +369,15 @@ __global__ __launch_bounds__(kThreads, 8) void chunk_kernel(SampleParams p) {
   bool bad = false;
 #pragma unroll
   for (int s = 0; s < kStripes; ++s)
-    if (s < stripes)
+    if (s < stripes) {
+      piece.place(w[s], s);
 #pragma unroll
       for (int e = 0; e < P::kPer; ++e) {
         const float x = T::wide(P::element(w[s], e));
         bad |= !(x < INFINITY);
         most = fmaxf(most, x);
       }
+    }
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) most = fmaxf(most, __shfl_xor(most, d, 64));
   if (lane == 0) waves[wave] = most;
@@ -306,9 +393,10 @@ __global__ __launch_bounds__(kThreads, 8) void chunk_kernel(SampleParams p) {
 #pragma unroll
         for (int e = 0; e < P::kPer; ++e) {
           const int i = piece.first(s) + e;
-          if (T::wide(P::element(w[s], e)) == most && i < least) least = i;
+          if (T::wide(P::element(w[s], e)) == most && piece.is_token(i))
+            least = min(least, piece.token(i));
         }
-    if (least < piece.n) atomicMin(&first, least);
+    if (least < INT32_MAX) atomicMin(&first, least);
     __syncthreads();
   }
   Scale scale;
@@ -316,24 +404,26 @@ __global__ __launch_bounds__(kThreads, 8) void chunk_kernel(SampleParams p) {
   if (t == 0) *(Head*)record = Head{scale.top, most, bad, begin + first, 0};
   if (set.bad || bad || set.greedy() || most == -INFINITY) return;
   if (set.places()) {
-    uint64_t* const parts = (uint64_t*)(record + kPartsAt);
+    double* const parts = (double*)(record + kPartsAt);
 #pragma unroll
     for (int s = 0; s < kStripes; ++s) {
       if (s >= stripes) continue;
-      uint64_t sum = 0;
+      double sum = 0.0;
 #pragma unroll
       for (int e = 0; e < P::kPer; ++e) {
+        const float x = T::wide(P::element(w[s], e));
+        double a, b;
         int k;
-        const double m = scale.weigh((double)T::wide(P::element(w[s], e)), steps, &k);
-        sum += place_of(m, k, p.scale);
+        scale.factors((double)x, steps, &k, &a, &b);
+        sum += x >= scale.least ? Scale::by_value(a, b, k) : 0.0;
       }
       sum = wave_sum(sum);
       if (lane == 0) parts[s * kWaves + wave] = sum;
     }
-    for (int i = stripes * kWaves + t; i < p.parts; i += kThreads) parts[i] = 0;
+    for (int s = stripes; s * kWaves < p.parts; ++s)
+      if (lane == 0) parts[s * kWaves + wave] = 0.0;
     return;
   }
-  if (!set.sums() && !set.counts()) return;
   auto fill = [&](auto with_sums, auto with_counts) {
 #pragma unroll
     for (int s = 0; s < kStripes; ++s) {
@@ -341,22 +431,22 @@ __global__ __launch_bounds__(kThreads, 8) void chunk_kernel(SampleParams p) {
 #pragma unroll
       for (int e = 0; e < P::kPer; ++e) {
         int k;
-        const double m = scale.weigh((double)T::wide(P::element(w[s], e)), steps, &k);
-        const int bin = bin_of(k);
-        if (bin >= kBins) continue;
-        if (with_sums) atomicAdd((unsigned long long*)&sums[bin], (unsigned long long)term_of(m));
+        const float x = T::wide(P::element(w[s], e));
+        const uint64_t term = scale.term((double)x, steps, &k);
+        const int bin = x >= scale.least ? min(bin_of(k), kBins) : kBins;
+        if (with_sums) atomicAdd((unsigned long long*)&sums[bin], (unsigned long long)term);
         if (with_counts) atomicAdd(&counts[bin], 1u);
       }
     }
   };
   constexpr std::true_type yes;
   constexpr std::false_type no;
-  if (!set.sums())
-    fill(no, yes);
-  else if (!set.counts())
-    fill(yes, no);
-  else
+  if (set.sums() && set.counts())
     fill(yes, yes);
+  else if (set.sums())
+    fill(yes, no);
+  else if (set.counts())
+    fill(no, yes);
   __syncthreads();
   if (set.sums()) ((uint64_t*)(record + kSumsAt))[t] = sums[t];
   if (set.counts()) ((uint32_t*)(record + kCountsAt))[t] = counts[t];
@@ -365,69 +455,98 @@ __global__ __launch_bounds__(kThreads, 8) void chunk_kernel(SampleParams p) {
 // ------------------------------------------------------------------ rows
 
 struct RowShared {
-  double steps[kSteps];
+  double steps[kSteps];   // first: across the banks once
   uint64_t list[kList];   // codes; or the parts' sums
   uint64_t inside[kList]; // codes of the border's bin
-  uint64_t sums[256];
-  uint32_t counts[256];
+  uint64_t sums[2][256];
+  uint64_t counts[2][256];
   uint64_t qwaves[kWaves];
   uint32_t waves[kWaves];
-  uint64_t found_sum, found_code;
+  uint64_t found_sum, found_code, found_rest, ones, zeros;
   int32_t found, found_count;
   uint32_t above, within;  // tokens of the lists
 };
 
-// The first code, of those that `members` hands to its argument with a value each, up to which
-// the values sum to `target` (at least 1), in the order of the codes; *before: the sum
-// ahead of it. If the sum is less, the last code. By eight bits at a time from the
-// highest of `bits`, until one code is left.
+// The first code, of those that `members` hands to its argument with a value (at least 1)
+// each, up to which the values sum to `target` (at least 1), in the order of the codes;
+// *before: the sum ahead of it. If the sum is less, the last code. By eight bits at a time,
+// from the highest in which codes differ, until one code is left: wave 0 finds the byte
+// while the others clear the sums of the next eight bits.
 template <class Members>
-__device__ uint64_t select(RowShared& sh, int bits, uint64_t target, uint64_t* before, Members members) {
-  const int t = threadIdx.x;
-  uint64_t prefix = 0, passed = 0;
-  int shift = (bits + 7) / 8 * 8;
-  while (shift > 0) {
-    shift -= 8;
+__device__ __forceinline__ uint64_t select(RowShared& sh, uint64_t target, uint64_t* before, Members members) {
+  const int t = threadIdx.x, lane = t & 63;
+  uint64_t ones = 0, zeros = 0;
+  members([&](uint64_t code, uint64_t) {
+    ones |= code;
+    zeros |= ~code;
+  });
+  __syncthreads();
+  if (t == 0) sh.ones = sh.zeros = 0;
+  if (t < 256) sh.sums[0][t] = sh.counts[0][t] = 0;
+  __syncthreads();
+  if (ones | zeros) {
+    atomicOr((unsigned long long*)&sh.ones, (unsigned long long)ones);
+    atomicOr((unsigned long long*)&sh.zeros, (unsigned long long)zeros);
+  }
+  __syncthreads();
+  const uint64_t differ = sh.ones & sh.zeros;
+  uint64_t prefix = sh.ones & sh.zeros ? 0 : sh.ones, passed = 0;
+  if (!differ) {  // one code, or none
     __syncthreads();
-    if (t < 256) {
-      sh.sums[t] = 0;
-      sh.counts[t] = 0;
-    }
-    __syncthreads();
+    *before = 0;
+    return prefix;
+  }
+  int shift = 64 - __builtin_clzll(differ);  // bits from here up are the same in all
+  prefix = shift < 64 ? sh.ones >> shift : 0;
+  int turn = 0;
+  for (;;) {
+    const int bits = min(shift, 8);
+    shift -= bits;
     members([&](uint64_t code, uint64_t value) {
-      if (code >> (shift + 8) != prefix) return;
-      const int byte = (int)(code >> shift) & 255;
-      atomicAdd((unsigned long long*)&sh.sums[byte], (unsigned long long)value);
-      atomicAdd(&sh.counts[byte], 1u);
+      const uint64_t high = code >> shift;
+      if (high >> bits != prefix) return;
+      const int byte = (int)high & ((1 << bits) - 1);
+      atomicAdd((unsigned long long*)&sh.sums[turn][byte], (unsigned long long)value);
+      atomicAdd((unsigned long long*)&sh.counts[turn][byte], 1ull);
     });
     __syncthreads();
-    const uint64_t v = t < 256 ? sh.sums[t] : 0;
-    const uint32_t n = t < 256 ? sh.counts[t] : 0;
-    uint64_t all;
-    const uint64_t up = block_scan(v, sh.qwaves, &all);
-    const uint64_t want = target < all ? target : all;
-    if (n && v && up >= want && up - v < want) {
-      sh.found = t;
-      sh.found_sum = up - v;
-      sh.found_count = (int)n;
-    }
-    if (all == 0 && t == 0) {  // nothing has a value: there is no such code
-      sh.found = 255;
-      sh.found_sum = 0;
-      sh.found_count = 2;
+    if (t >= 256 && t < 512) sh.sums[turn ^ 1][t - 256] = sh.counts[turn ^ 1][t - 256] = 0;
+    if (t < 64) {
+      uint64_t v[4], four = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = sh.sums[turn][4 * lane + i];
+        four += v[i];
+      }
+      uint64_t up = wave_scan(four);
+      const uint64_t all = lane_of(up, 63), want = target < all ? target : all;
+      up -= four;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (v[i] && up < want && up + v[i] >= want) {
+          sh.found = 4 * lane + i;
+          sh.found_sum = up;
+          sh.found_rest = want - up;
+          sh.found_count = (int)sh.counts[turn][4 * lane + i];
+        }
+        up += v[i];
+      }
     }
     __syncthreads();
-    prefix = prefix << 8 | (uint32_t)sh.found;
+    prefix = prefix << bits | (uint32_t)sh.found;
     passed += sh.found_sum;
-    target = want - sh.found_sum;
-    if (sh.found_count == 1 && shift > 0) {
+    target = sh.found_rest;
+    const bool one = sh.found_count == 1;
+    if (shift == 0) break;
+    if (one) {
       members([&](uint64_t code, uint64_t) {
         if (code >> shift == prefix) sh.found_code = code;
       });
       __syncthreads();
-      *before = passed;
-      return sh.found_code;
+      prefix = sh.found_code;
+      break;
     }
+    turn ^= 1;
   }
   __syncthreads();
   *before = passed;
@@ -438,9 +557,8 @@ template <class T>
 __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
   typedef Piece<T> P;
   typedef typename T::Raw Raw;
-  constexpr int kCodeBits = T::kKeyBits + kIndexBits;
   constexpr uint32_t kKeyAll = T::kKeyBits == 32 ? ~0u : (1u << (T::kKeyBits & 31)) - 1;
-  __shared__ RowShared sh;
+  __shared__ __attribute__((aligned(256))) RowShared sh;
   fetch(p);
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
   const int64_t r = blockIdx.x;
@@ -467,51 +585,46 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
     }
     return;
   }
-  sh.steps[t] = exp2((double)t / kSteps);
+  if (t < kSteps) sh.steps[t] = exp2((double)t / kSteps);
   Scale scale;
   scale.set(most, set.temperature);
-  // octaves of the pieces below the row's, 64 for those without weight
+  // octaves of the pieces' tops below the row's, 64 for those without weight
   const double lower = scale.top - head.top;
   const int down = head.largest > -INFINITY && lower < 64.0 ? (int)lower : 64;
   const int S = p.scale;
-  P row;
-  row.at = (const Raw*)p.logits + r * p.row_step;
-  row.n = p.vocab;
+  const Raw* const logits = (const Raw*)p.logits + r * p.row_step;
+  const P row(logits, p.vocab);
 
   int owner_token = -1;   // of the thread that has found the token
   float owner_value = 0.f;
-  uint64_t total = 0;     // kept weights, 2^S each
+  uint64_t total = 0;     // of the kept weights, in units of 2^-unit
+  int unit = S;
 
-  // the first token up to which `weight` of the tokens of [at, at + 64 kPer) sums to `goal`, by one wave
-  auto pick = [&](const P& piece, int stripe, int part_wave, uint64_t goal, int offset, auto weight) {
-    if (wave != part_wave) return;
-    const u4v w = piece.word(stripe);
-    const int i0 = piece.first(stripe);
-    uint64_t mine[P::kPer], sum = 0;
+  // Of a part's tokens, by one wave: the first one up to which their weights sum to more than
+  // `goal`; the last that has weight if rounding leaves none.
+  auto pick = [&](const P& piece, int part, double goal, int offset, auto weight) {
+    if (wave != part % kWaves) return;
+    const u4v w = piece.word(part / kWaves);
+    const int i0 = piece.first(part / kWaves);
+    double mine[P::kPer], sum = 0.0;
 #pragma unroll 1
     for (int e = 0; e < P::kPer; ++e) {
-      const uint64_t v = i0 + e < piece.n ? weight(P::any(w, e), i0 + e) : 0;
+      const double v = piece.is_token(i0 + e) ? weight(P::any(w, e), piece.token(i0 + e)) : 0.0;
 #pragma unroll
       for (int j = 0; j < P::kPer; ++j)
         if (j == e) mine[j] = v;
       sum += v;
     }
-    uint64_t up = sum;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const uint64_t o = __shfl_up(up, d, 64);
-      if (lane >= d) up += o;
-    }
-    uint64_t cursor = up - sum;
+    double cursor = wave_scan(sum) - sum;
     int token = -1, last = -1;
     float value = 0.f, last_value = 0.f;
 #pragma unroll
     for (int e = 0; e < P::kPer; ++e) {
       cursor += mine[e];
-      if (!mine[e]) continue;
-      last = i0 + e;
+      if (!(mine[e] > 0.0)) continue;
+      last = piece.token(i0 + e);
       last_value = T::wide(P::element(w, e));
-      if (token < 0 && cursor >= goal) {
+      if (token < 0 && cursor > goal) {
         token = last;
         value = last_value;
       }
@@ -523,6 +636,8 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
       owner_value = have ? value : last_value;
     }
   };
+  // A part's sum in the unit 2^-S of the row's top, `by` octaves above the piece's.
+  auto in_units = [&](double v, int by) { return (uint64_t)__builtin_rint(__builtin_ldexp(v, S - by)); };
 
   if (set.places()) {
     // parts in order, a few to a thread
@@ -531,7 +646,7 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
       const int at = min(i, all - 1), c = at / p.parts;
       const int by = __shfl(down, c, 64);  // by all lanes
       if (i >= all || by >= 64) return 0;
-      return shifted(((const uint64_t*)(records + c * p.record + kPartsAt))[at % p.parts], -by);
+      return in_units(((const double*)(records + c * p.record + kPartsAt))[at % p.parts], by);
     };
     uint64_t sum = 0;
     for (int j = 0; j < each; ++j) sum += part_at(t * each + j);
@@ -554,32 +669,55 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
     const int c = part / p.parts, by = __shfl(down, c, 64);
     Scale own;
     own.set(__shfl(head.largest, c, 64), set.temperature);
-    P piece;
-    piece.at = row.at + c * p.piece;
-    piece.n = min(p.piece, p.vocab - c * p.piece);
-    pick(piece, part % p.parts / kWaves, part % p.parts % kWaves, (goal - before) << by, c * p.piece,
+    const P piece(logits + c * p.piece, min(p.piece, p.vocab - c * p.piece));
+    pick(piece, part % p.parts, __builtin_ldexp((double)(goal - 1 - before), by - S), c * p.piece,
          [&](Raw raw, int) {
+           const float x = T::wide(raw);
+           if (!(x >= own.least)) return 0.0;
+           double a, b;
            int k;
-           const double m = own.weigh((double)T::wide(raw), sh.steps, &k);
-           return place_of(m, k, S);
+           own.factors((double)x, sh.steps, &k, &a, &b);
+           return Scale::by_value(a, b, k);
          });
   } else {
     // the bins of all pieces: sums in their own octave's unit and in 2^S
     uint64_t sum = 0;
     uint32_t count = 0;
-    for (int c = 0; c < p.pieces; ++c) {
-      const int by = __builtin_amdgcn_readlane(down, c);
-      const int bin = t - 16 * by;
-      if (by >= 64 || bin < 0) continue;
-      if (set.sums()) sum += ((const uint64_t*)(records + c * p.record + kSumsAt))[bin];
-      if (set.counts()) count += ((const uint32_t*)(records + c * p.record + kCountsAt))[bin];
+    constexpr int kPieces = 4;  // whose loads are under way together
+    for (int c0 = 0; c0 < p.pieces; c0 += kPieces) {
+      uint64_t v[kPieces];
+      uint32_t n[kPieces];
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j) {
+        const int c = min(c0 + j, p.pieces - 1);
+        const int bin = max(t - 16 * __builtin_amdgcn_readlane(down, c), 0);
+        v[j] = 0;
+        n[j] = 0;
+        if (set.sums()) v[j] = ((const uint64_t*)(records + c * p.record + kSumsAt))[bin];
+        if (set.counts()) n[j] = ((const uint32_t*)(records + c * p.record + kCountsAt))[bin];
+      }
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j) {
+        const int by = __builtin_amdgcn_readlane(down, min(c0 + j, p.pieces - 1));
+        if (c0 + j < p.pieces && by < 64 && t >= 16 * by) {
+          sum += v[j];
+          count += n[j];
+        }
+      }
     }
     const int octave = octave_of(t);
     const uint64_t mine = shifted(sum, S - 40 + octave);
-    uint64_t all_sum = 0;
-    uint32_t all_count = 0;
-    const uint64_t upto = block_scan(mine, sh.qwaves, &all_sum);
-    const uint32_t upto_count = block_scan(count, sh.waves, &all_count);
+    uint64_t all_sum = 0, upto = 0;
+    uint32_t all_count = 0, upto_count = 0;
+    float bound = 0.f, upto_bound = 0.f, ignored;
+    if (set.counts()) upto_count = block_scan(count, sh.waves, &all_count);
+    if (set.sums()) {
+      upto = block_scan(mine, sh.qwaves, &all_sum);
+      // a bin's terms are its lower edge's 2^40 m or up to a sixteenth of an octave more, so
+      // their sum bounds their number
+      bound = (float)sum * __builtin_amdgcn_exp2f(-40.f - (float)(-t & 15) * 0.0625f) * 1.01f + 1.f;
+      upto_bound = block_scan(bound, (float*)sh.waves, &ignored);
+    }
 
     // the first bin whose sum or count from the top passes what is asked for, kBins if none
     auto bin_where = [&](bool passes) {
@@ -593,47 +731,73 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
     };
     // a value that no token of the bins up to this one is below
     auto least_of = [&](double bin) {
-      const double x = scale.ref + (-64.0 * bin - 0.5 - scale.shift) / scale.step;
-      return (float)(x - 1e-6 * (__builtin_fabs(x) + __builtin_fabs(scale.ref)) - 1e-30);
+      const double x = scale.ref + (-2.0 * bin - 0.5 - scale.shift) / scale.step;
+      return fmaxf((float)(x - 1e-6 * (__builtin_fabs(x) + __builtin_fabs(scale.ref)) - 1e-30),
+                   -__FLT_MAX__);  // never -infinity
     };
-    // f(raw, index) of every token of at least `least`
-    auto each_from = [&](float least, auto f) {
-      const int stripes = row.stripes();
-      constexpr int kAhead = 4;
-      for (int s0 = 0; s0 < stripes; s0 += kAhead) {
-        u4v w[kAhead];
+    // a value that no token of this bin or a later one is above
+    auto most_of = [&](int bin) {
+      const double x = scale.ref + (-2.0 * bin + 1.5 - scale.shift) / scale.step;
+      return bin == 0 ? INFINITY
+                      : (float)(x + 1e-6 * (__builtin_fabs(x) + __builtin_fabs(scale.ref)) + 1e-30);
+    };
+    // a value's bin, kBins and more for those without weight; and its term
+    auto bin_at = [&](Raw raw, uint64_t* term) {
+      const float x = T::wide(raw);
+      if (!(x >= scale.least)) return kBins;
+      int k;
+      *term = scale.term((double)x, sh.steps, &k);
+      return bin_of(k);
+    };
+    // f(word, mask, first element) of every word that has tokens from `least` to `limit`, by
+    // whole waves
+    auto each_word = [&](float least, float limit, auto f) {
+      const int stripes = row.wave_stripes();
+      u4v w[kAhead];
 #pragma unroll
-        for (int a = 0; a < kAhead; ++a)
-          if (s0 + a < stripes) w[a] = row.word(s0 + a);
+      for (int a = 0; a < kAhead; ++a)
+        if (a < stripes) w[a] = row.load(a);
+      for (int s0 = 0; s0 < stripes; s0 += kAhead) {
 #pragma unroll
         for (int a = 0; a < kAhead; ++a) {
           if (s0 + a >= stripes) continue;
-          const int i0 = row.first(s0 + a);
+          u4v now = w[a];
+          if (s0 + a + kAhead < stripes) w[a] = row.load(s0 + a + kAhead);
+          row.place(now, s0 + a);
           uint32_t some = 0;
 #pragma unroll
-          for (int e = 0; e < P::kPer; ++e) some |= (T::wide(P::element(w[a], e)) >= least) << e;
-          for (; some; some &= some - 1) {
-            const int e = __builtin_ctz(some);
-            if (i0 + e < row.n) f(P::any(w[a], e), i0 + e);
+          for (int e = 0; e < P::kPer; ++e) {
+            const float x = T::wide(P::element(now, e));
+            some |= (x >= least && x <= limit) << e;
           }
+          const int i0 = row.first(s0 + a);
+          if (i0 < row.lead) some &= ~1u;
+          if (__any(some)) f(now, some, i0);
         }
       }
     };
-    // the tokens of the bins before `bin` into the list, those of it into `inside`
-    auto gather = [&](int bin, bool before_too) {
+    // f(raw, index) of every token from `least` to `limit`
+    auto each_from = [&](float least, float limit, auto f) {
+      each_word(least, limit, [&](const u4v& w, uint32_t some, int i0) {
+        for (; some; some &= some - 1) {
+          const int e = __builtin_ctz(some);
+          f(P::any(w, e), row.token(i0 + e));
+        }
+      });
+    };
+    // their codes into a list; *n: how many there are, also where the list ends before
+    auto collect = [&](float least, float limit, uint64_t* list, uint32_t* n) {
       __syncthreads();
-      if (t == 0) sh.above = sh.within = 0;
+      if (t == 0) *n = 0;
       __syncthreads();
-      each_from(least_of(bin), [&](Raw raw, int i) {
-        int k;
-        scale.weigh((double)T::wide(raw), sh.steps, &k);
-        const int b = bin_of(k);
-        if (b == bin) {
-          const uint32_t at = atomicAdd(&sh.within, 1u);
-          if (at < kList) sh.inside[at] = code_of<T>(raw, i);
-        } else if (b < bin && before_too && sh.above < kList) {
-          const uint32_t at = atomicAdd(&sh.above, 1u);
-          if (at < kList) sh.list[at] = code_of<T>(raw, i);
+      each_word(least, limit, [&](const u4v& w, uint32_t some, int i0) {
+        const uint32_t mine = __popc(some), upto = wave_scan(mine);
+        uint32_t at = 0;
+        if (lane == 63) at = atomicAdd(n, upto);
+        at = lane_of(at, 63) + upto - mine;
+        for (; some; some &= some - 1, ++at) {
+          const int e = __builtin_ctz(some);
+          if (at < kList) list[at] = code_of<T>(P::any(w, e), row.token(i0 + e));
         }
       });
       __syncthreads();
@@ -643,41 +807,101 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
       constexpr uint32_t sign = 1u << (T::kKeyBits - 1);
       return (Raw)(key & sign ? key & (sign - 1) : ~key & kKeyAll);
     };
+    // The tokens of a bin into `inside`, those of the bins before it into `list`: by value
+    // first, which may take some of the next bins.
+    auto gather = [&](int bin, bool before_too) {
+      collect(least_of(bin), before_too ? INFINITY : most_of(bin), sh.list, &sh.above);
+      const uint32_t n = sh.above;
+      uint64_t mine[kMine];
+#pragma unroll
+      for (int j = 0; j < kMine; ++j) {
+        const uint32_t i = t + j * kThreads;
+        mine[j] = i < n && n <= kList ? sh.list[i] : ~0ull;
+      }
+      __syncthreads();
+      if (t == 0) {
+        sh.within = n <= kList ? 0 : n;
+        sh.above = n <= kList ? 0 : n;
+      }
+      __syncthreads();
+      if (n > kList) return;
+#pragma unroll
+      for (int j = 0; j < kMine; ++j) {
+        uint64_t ignored;
+        const int b = mine[j] == ~0ull ? kBins : bin_at(raw_of(mine[j]), &ignored);
+        const uint64_t in = __ballot(b == bin), above = __ballot(b < bin);
+        uint32_t at = 0, to = 0;
+        if (lane == 0 && in) at = atomicAdd(&sh.within, (uint32_t)__popcll(in));
+        if (lane == 0 && above) to = atomicAdd(&sh.above, (uint32_t)__popcll(above));
+        const uint64_t below = (1ull << lane) - 1;
+        if (b == bin) sh.inside[lane_of(at, 0) + __popcll(in & below)] = mine[j];
+        if (b < bin) sh.list[lane_of(to, 0) + __popcll(above & below)] = mine[j];
+      }
+      __syncthreads();
+    };
     // the border inside a bin: the code up to which its tokens' number or sum (in the
     // bin's unit) reaches `need`; after gather(bin, .)
     auto border_in = [&](int bin, bool weights, uint64_t need, uint64_t* before) {
       if (need < 1) need = 1;
-      if (sh.within == 0) {  // a value between two bins was rounded into another: the largest alone
-        *before = 0;
+      // a value between two bins may be rounded into the other here: without any, the largest alone
+      auto or_largest = [&](uint64_t code) {
         uint32_t raw = __builtin_bit_cast(uint32_t, most);
         if constexpr (T::kKeyBits == 16) raw = T::one(most);
-        return code_of<T>((Raw)raw, (1 << kIndexBits) - 1);
-      }
+        return code ? code : code_of<T>((Raw)raw, (1 << kIndexBits) - 1);
+      };
       if (sh.within <= kList) {
-        const int n = (int)sh.within;
-        return select(sh, kCodeBits, need, before, [&](auto f) {
-          for (int i = t; i < n; i += kThreads) {
-            const uint64_t code = sh.inside[i];
-            int k;
-            const double m = scale.weigh((double)T::wide(raw_of(code)), sh.steps, &k);
-            f(code, weights ? term_of(m) : 1);
-          }
-        });
+        uint64_t code[kMine], value[kMine];
+#pragma unroll
+        for (int j = 0; j < kMine; ++j) {
+          const int i = t + j * kThreads;
+          value[j] = 0;
+          if (i >= (int)sh.within) continue;
+          code[j] = sh.inside[i];
+          value[j] = 1;
+          if (weights) bin_at(raw_of(code[j]), &value[j]);
+        }
+        return or_largest(select(sh, need, before, [&](auto f) {
+#pragma unroll
+          for (int j = 0; j < kMine; ++j)
+            if (value[j]) f(code[j], value[j]);
+        }));
       }
-      const float least = least_of(bin);
-      return select(sh, kCodeBits, need, before, [&](auto f) {
-        each_from(least, [&](Raw raw, int i) {
-          int k;
-          const double m = scale.weigh((double)T::wide(raw), sh.steps, &k);
-          if (bin_of(k) == bin) f(code_of<T>(raw, i), weights ? term_of(m) : 1);
+      const float least = least_of(bin), limit = most_of(bin);
+      return or_largest(select(sh, need, before, [&](auto f) {
+        each_from(least, limit, [&](Raw raw, int i) {
+          uint64_t term;
+          if (bin_at(raw, &term) == bin) f(code_of<T>(raw, i), weights ? term : 1);
         });
-      });
+      }));
     };
 
+    const double floor_weight =  // of what min_p keeps
+        set.by_least ? (double)(set.min_p < 1.f ? set.min_p : 1.f) : 0.0;
+    int k;
+    const double least_weight = floor_weight * scale.weight(scale.ref, sh.steps, &k);
+    // whether the value has weight, and at least so much
+    auto counted = [&](float x, double at_least) {
+      if (!(x >= scale.least)) return false;
+      int k;
+      const double w = scale.weight((double)x, sh.steps, &k);
+      return bin_of(k) < kBins && w >= at_least;
+    };
+    // the tokens from `least` on that have this weight into the list, `above` of them if they fit
+    auto collect_counted = [&](float least, double at_least) {
+      __syncthreads();
+      if (t == 0) sh.above = sh.within = 0;
+      __syncthreads();
+      each_from(least, INFINITY, [&](Raw raw, int i) {
+        if (sh.above > kList || !counted(T::wide(raw), at_least)) return;
+        const uint32_t at = atomicAdd(&sh.above, 1u);
+        if (at < kList) sh.list[at] = code_of<T>(raw, i);
+      });
+      __syncthreads();
+    };
     uint64_t border = ~0ull;  // kept: codes up to it
     bool listed = false;      // the kept tokens are among the list's first `members`
     int members = 0;
-    int last_bin = kBins - 1; // no kept token is behind this bin
+    int last_bin = kBins - 1;  // no kept token is behind this bin
     int chosen_bin = -1;      // the border is in this bin, of which `inside` has the tokens
     // puts `inside` behind the list, if both have room
     auto join_lists = [&] {
@@ -692,9 +916,13 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
     };
     uint64_t available = all_sum;  // what top_p takes its part of
     if (set.by_count) {
-      int bin = bin_where(upto_count >= (uint32_t)set.top_k);
-      if (bin == kBins && set.few()) bin = kBins - 1;  // fewer than top_k have weight: all of these
-      if (bin < kBins) {
+      const int bin = bin_where(upto_count >= (uint32_t)set.top_k);
+      if (bin == kBins) {  // fewer have weight: all of these
+        if (set.few()) {
+          collect_counted(least_of(kBins - 1), 0.0);
+          listed = join_lists();
+        }
+      } else {
         last_bin = bin;
         if (t == bin) {
           sh.found_count = (int)(upto_count - count);
@@ -713,7 +941,7 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
             __syncthreads();
             if (t == 0) sh.above = 0;
             __syncthreads();
-            each_from(least_of(bin), [&](Raw raw, int i) {
+            each_from(least_of(bin), INFINITY, [&](Raw raw, int i) {
               const uint64_t code = code_of<T>(raw, i);
               if (code > border) return;
               const uint32_t at = atomicAdd(&sh.above, 1u);
@@ -725,10 +953,9 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
           } else {
             // the sum of what is kept: by weight up to the border's code
             uint64_t kept = 0;
-            each_from(least_of(bin), [&](Raw raw, int i) {
-              int k;
-              const double m = scale.weigh((double)T::wide(raw), sh.steps, &k);
-              if (bin_of(k) == bin && code_of<T>(raw, i) <= border) kept += term_of(m);
+            each_from(least_of(bin), most_of(bin), [&](Raw raw, int i) {
+              uint64_t term;
+              if (bin_at(raw, &term) == bin && code_of<T>(raw, i) <= border) kept += term;
             });
             uint64_t all;
             block_scan(kept, sh.qwaves, &all);
@@ -737,7 +964,7 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
         } else {
           uint64_t before;
           const int n = members;
-          border = select(sh, kCodeBits, (uint64_t)set.top_k, &before, [&](auto f) {
+          border = select(sh, (uint64_t)set.top_k, &before, [&](auto f) {
             for (int i = t; i < n; i += kThreads) f(sh.list[i], 1);
           });
         }
@@ -749,10 +976,14 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
       int bin = bin_where(mine && upto >= target);
       if (bin > last_bin) bin = last_bin;
       last_bin = bin;
-      if (t == bin) sh.found_sum = upto - mine;
+      if (t == bin) {
+        sh.found_sum = upto - mine;
+        sh.found_count = upto_bound < (float)kList;
+      }
       __syncthreads();
       const uint64_t ahead = sh.found_sum;
-      gather(bin, true);
+      const bool small = sh.found_count;
+      gather(bin, small);
       const int by = 40 - octave_of(bin) - S;  // from 2^S to the bin's unit
       const uint64_t missing = target > ahead ? target - ahead : 1;
       const uint64_t need = by >= 0 ? shifted(missing, by) : (missing + (1ull << -by) - 1) >> -by;
@@ -762,49 +993,39 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
         border = second;
         chosen_bin = bin;
       }
-      listed = join_lists();
+      listed = small && join_lists();
     }
-    const double floor_weight =  // of what min_p keeps
-        set.by_least ? (double)(set.min_p < 1.f ? set.min_p : 1.f) : 0.0;
-    int km;
-    const double largest = scale.weigh(scale.ref, sh.steps, &km);
-    const double least_weight = floor_weight * __builtin_ldexp(largest, km >> 10);
     float least = least_of(last_bin);
     if (set.by_least) {
       const double bins = 17.0 - 16.0 * log2(floor_weight);  // the top is less than an octave higher
       if (bins < (double)last_bin) least = least_of(bins);
       if (!listed && !set.by_count && !set.by_weight) {
-        __syncthreads();
-        if (t == 0) sh.above = sh.within = 0;
-        __syncthreads();
-        each_from(least, [&](Raw raw, int i) {
-          int k;
-          const double m = scale.weigh((double)T::wide(raw), sh.steps, &k);
-          if (bin_of(k) >= kBins || __builtin_ldexp(m, k >> 10) < least_weight || sh.above > kList) return;
-          const uint32_t at = atomicAdd(&sh.above, 1u);
-          if (at < kList) sh.list[at] = code_of<T>(raw, i);
-        });
-        __syncthreads();
+        collect_counted(least, least_weight);
         listed = join_lists();
       }
     }
-    auto kept_weight = [&](Raw raw, int i) -> uint64_t {
-      if (code_of<T>(raw, i) > border) return 0;
+    // the weight of a token of at least `least` if it is kept, as a part sums it
+    const float edge = border == ~0ull ? least : T::wide(raw_of(border));
+    const int edge_last = border == ~0ull ? INT32_MAX : (int)(border & ((1u << kIndexBits) - 1));
+    auto kept_value = [&](float x, int i) __attribute__((always_inline)) {
       int k;
-      const double m = scale.weigh((double)T::wide(raw), sh.steps, &k);
-      if (bin_of(k) >= kBins || __builtin_ldexp(m, k >> 10) < least_weight) return 0;
-      return place_of(m, k, S);
+      double a, b;
+      scale.factors((double)x, sh.steps, &k, &a, &b);
+      bool kept = x >= scale.least && bin_of(k) < kBins && (x > edge || (x == edge && i <= edge_last));
+      if (set.by_least) kept = kept && a * __builtin_ldexp(b, k >> 5) >= least_weight;
+      return kept ? Scale::by_value(a, b, k) : 0.0;
     };
     if (listed) {
+      unit = kListUnit;
       uint64_t code[kMine], weight[kMine], sum = 0;
       __syncthreads();
 #pragma unroll
       for (int j = 0; j < kMine; ++j) {
         const int i = t + j * kThreads;
         code[j] = i < members ? sh.list[i] : ~0ull;
-        weight[j] = i < members
-                        ? kept_weight(raw_of(code[j]), (int)(code[j] & ((1u << kIndexBits) - 1)))
-                        : 0;
+        weight[j] = 0;
+        if (i < members && code[j] <= border && counted(T::wide(raw_of(code[j])), least_weight))
+          weight[j] = scale.listed((double)T::wide(raw_of(code[j])), sh.steps);
         sum += weight[j];
       }
       block_scan(sum, sh.qwaves, &total);
@@ -816,9 +1037,9 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
         for (int j = 0; j < kMine; ++j) {
           plain[j] = 0;
           if (code[j] <= border && code[j] != ~0ull) {
-            int k;
-            const double m = scale.weigh((double)T::wide(raw_of(code[j])), sh.steps, &k);
-            if (bin_of(k) < kBins) plain[j] = place_of(m, k, S);
+            uint64_t term;
+            if (bin_at(raw_of(code[j]), &term) < kBins)
+              plain[j] = scale.listed((double)T::wide(raw_of(code[j])), sh.steps);
           }
           whole_sum += plain[j];
         }
@@ -826,7 +1047,7 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
         block_scan(whole_sum, sh.qwaves, &all);
         uint64_t target = set.top_p > 0.f ? share(set.top_p, all, true) : 1;
         if (target < 1) target = 1;
-        border = select(sh, kCodeBits, target, &before, [&](auto f) {
+        border = select(sh, target, &before, [&](auto f) {
 #pragma unroll
           for (int j = 0; j < kMine; ++j)
             if (plain[j]) f(code[j], plain[j]);
@@ -840,14 +1061,14 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
         block_scan(sum, sh.qwaves, &total);
       }
       const uint64_t goal = share(set.u, total, false) + 1;
-      const uint64_t token = select(sh, kIndexBits, goal, &before, [&](auto f) {
+      const uint64_t token = select(sh, goal, &before, [&](auto f) {
 #pragma unroll
         for (int j = 0; j < kMine; ++j)
           if (weight[j]) f(code[j] & ((1u << kIndexBits) - 1), weight[j]);
       });
       if (t == 0) {
         owner_token = (int)token;
-        owner_value = T::wide(row.at[token]);
+        owner_value = T::wide(logits[token]);
       }
     } else {
       // the piece in which the token lies, by the bins' sums; then its parts
@@ -856,67 +1077,68 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
       uint64_t ahead = 0, goal = 0;
       const bool by_bins = chosen_bin >= 0 && set.sums() && !set.by_least;
       if (by_bins) {
-        // of the border's bin, the kept tokens' sums by piece
-        uint64_t* const edge = sh.sums;
+        // of each piece the sum of what is kept: a wave adds a piece's bins before the
+        // border's, and the border's own tokens are added by themselves
+        uint64_t* const kept = sh.sums[0];
         __syncthreads();
-        if (t < kMostPieces) edge[t] = 0;
+        for (int c = wave; c < p.pieces; c += kWaves) {
+          const int by = __builtin_amdgcn_readlane(down, c);
+          uint64_t v = 0;
+          if (by < 64)
+            for (int bin = lane + 16 * by; bin < chosen_bin; bin += 64)
+              v += shifted(((const uint64_t*)(records + c * p.record + kSumsAt))[bin - 16 * by],
+                           S - 40 + octave_of(bin));
+          v = wave_sum(v);
+          if (lane == 0) kept[c] = v;
+        }
+        if (t < kMostPieces) kept[128 + t] = 0;
         __syncthreads();
         auto add = [&](Raw raw, int i) {
-          int k;
-          const double m = scale.weigh((double)T::wide(raw), sh.steps, &k);
-          if (bin_of(k) == chosen_bin && code_of<T>(raw, i) <= border)
-            atomicAdd((unsigned long long*)&edge[i / p.piece], (unsigned long long)term_of(m));
+          uint64_t term;
+          if (bin_at(raw, &term) == chosen_bin && code_of<T>(raw, i) <= border)
+            atomicAdd((unsigned long long*)&kept[128 + i / p.piece], (unsigned long long)term);
         };
         if (sh.within <= kList) {
           for (int i = t; i < (int)sh.within; i += kThreads)
             add(raw_of(sh.inside[i]), (int)(sh.inside[i] & ((1u << kIndexBits) - 1)));
         } else {
-          each_from(least_of(chosen_bin), add);
+          each_from(least_of(chosen_bin), most_of(chosen_bin), add);
         }
         __syncthreads();
-        // all pieces' totals first, then the one that passes the goal
-        for (int pass = 0; pass < 2; ++pass) {
-          uint64_t cursor = 0;
-          for (int c = 0; c < p.pieces; ++c) {
-            const int by = __builtin_amdgcn_readlane(down, c);
-            const int bin = t - 16 * by;
-            uint64_t v = 0;
-            if (by < 64 && bin >= 0 && t < chosen_bin)
-              v = shifted(((const uint64_t*)(records + c * p.record + kSumsAt))[bin], S - 40 + octave);
-            uint64_t sum_c;
-            block_scan(v, sh.qwaves, &sum_c);
-            sum_c += shifted(edge[c], S - 40 + octave_of(chosen_bin));
-            if (pass == 1 && (cursor + sum_c >= goal || c + 1 == p.pieces)) {
-              offset = c * p.piece;
-              ahead = cursor;
-              break;
-            }
-            cursor += sum_c;
-          }
-          if (pass == 0) {
-            total = cursor;
-            goal = share(set.u, total, false) + 1;
-          }
-        }
-        piece.at = row.at + offset;
-        piece.n = min(p.piece, p.vocab - offset);
+        // the first piece that passes the goal
+        uint64_t mine_c = 0;
+        if (lane < p.pieces) mine_c = kept[lane] + shifted(kept[128 + lane], S - 40 + octave_of(chosen_bin));
+        const uint64_t up = wave_scan(mine_c);
+        total = lane_of(up, 63);
+        goal = share(set.u, total, false) + 1;
+        const uint64_t passes = __ballot(up >= goal && mine_c);
+        const int c = passes ? __builtin_ctzll(passes) : p.pieces - 1;
+        ahead = lane_of(up - mine_c, c);
+        offset = c * p.piece;
+        piece = P(logits + offset, min(p.piece, p.vocab - offset));
       }
       __syncthreads();
       uint64_t* const parts = sh.list;  // list and inside: 2 kList
       const int stripes = piece.stripes(), all = stripes * kWaves;
-      for (int s = 0; s < stripes; ++s) {
-        const u4v w = piece.word(s);
-        uint64_t sum_s = 0;
-        const int i0 = piece.first(s);
-        uint32_t some = 0;
+      for (int s0 = 0; s0 < stripes; s0 += kAhead) {
+        u4v w[kAhead];
 #pragma unroll
-        for (int e = 0; e < P::kPer; ++e) some |= (T::wide(P::element(w, e)) >= least) << e;
-        for (; some; some &= some - 1) {
-          const int e = __builtin_ctz(some);
-          if (i0 + e < piece.n) sum_s += kept_weight(P::any(w, e), offset + i0 + e);
+        for (int a = 0; a < kAhead; ++a)
+          if (s0 + a < stripes) w[a] = piece.load(s0 + a);
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) {
+          if (s0 + a >= stripes) continue;
+          piece.place(w[a], s0 + a);
+          const int i0 = piece.first(s0 + a);
+          double sum_s = 0.0;
+#pragma unroll
+          for (int e = 0; e < P::kPer; ++e) {
+            const float x = T::wide(P::element(w[a], e));
+            if (__any(x >= least)) sum_s += kept_value(x, offset + piece.token(i0 + e));
+          }
+          sum_s = wave_sum(sum_s);
+          if (lane == 0) parts[(s0 + a) * kWaves + wave] = in_units(sum_s, 0);
         }
-        sum_s = wave_sum(sum_s);
-        if (lane == 0) parts[s * kWaves + wave] = sum_s;
       }
       __syncthreads();
       const int each = (all + kThreads - 1) / kThreads;
@@ -944,17 +1166,17 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
         if (before + v >= rest) break;
         before += v;
       }
-      pick(piece, part / kWaves, part % kWaves, rest - before, offset,
-           [&](Raw raw, int i) { return kept_weight(raw, offset + i); });
+      pick(piece, part, __builtin_ldexp((double)(rest - 1 - before), -S), offset,
+           [&](Raw raw, int i) { return kept_value(T::wide(raw), offset + i); });
     }
   }
   if (owner_token >= 0) {
     p.tokens[r] = owner_token;
     // log(w / total): the kept weights' total is measured from the top, as is the largest
     if (p.logprobs)
-      p.logprobs[r] = (float)(((double)owner_value - scale.ref) / (double)set.temperature +
+      p.logprobs[r] = fminf(0.f, (float)(((double)owner_value - scale.ref) / (double)set.temperature +
                               scale.shift * (0.69314718055994530942 / kSteps) -
-                              (log((double)total) - S * 0.69314718055994530942));
+                              (log((double)total) - unit * 0.69314718055994530942)));
   }
 }
 
@@ -972,24 +1194,31 @@ int check_sample(const lutgemm_sample* s) {
 
 struct SamplePlan {
   int pieces, piece, parts, slab;  // slab: rows of one launch
-  size_t ws_bytes;
+  size_t record, ws_bytes;
 };
 
+// Two workgroups of chunk_kernel run on a compute unit at a time. Rows are cut so that
+// their rounds take least time, where a piece costs as much as kFixed tokens besides its own (256
+// rows of 131073: four pieces 38 us, five, in three rounds, 58).
 SamplePlan plan(const lutgemm_sample* s) {
+  constexpr int64_t kFixed = 12000, kSlots = 512;
   SamplePlan r{};
-  const int vocab = s->vocab, per = s->type == LUTGEMM_F32 ? 4 : 8;
-  const int full = kStripes * kThreads * per, least = (vocab + full - 1) / full;
-  const int most = (vocab + kLeastPiece - 1) / kLeastPiece;
-  int pieces = s->rows ? (512 + s->rows - 1) / s->rows : 1;
-  pieces = pieces > most ? most : pieces;
-  pieces = pieces < least ? least : pieces;
-  pieces = pieces > kMostPieces ? kMostPieces : pieces;
-  r.piece = ((vocab + pieces - 1) / pieces + 7) / 8 * 8;
-  r.pieces = (vocab + r.piece - 1) / r.piece;
-  r.parts = (r.piece + kThreads * per - 1) / (kThreads * per) * kWaves;
-  r.slab = 4096 / r.pieces;
-  if (r.slab > s->rows) r.slab = s->rows;
-  r.ws_bytes = (size_t)r.slab * r.pieces * kRecord;
+  const int vocab = s->vocab, per = kThreads * (s->type == LUTGEMM_F32 ? 4 : 8);
+  const int full = kStripes * per - 8;  // a piece may begin with half a word
+  int64_t best = INT64_MAX;
+  for (int n = (vocab + full - 1) / full; n <= kMostPieces; ++n) {
+    const int piece = ((vocab + n - 1) / n + 7) / 8 * 8, pieces = (vocab + piece - 1) / piece;
+    if (n > 1 && piece < kLeastPiece && best < INT64_MAX) break;
+    const int64_t time = ((int64_t)s->rows * pieces + kSlots - 1) / kSlots * (kFixed + piece);
+    if (piece > full || time >= best) continue;
+    best = time;
+    r.piece = piece;
+    r.pieces = pieces;
+  }
+  r.parts = (r.piece + 1 + per - 1) / per * kWaves;
+  r.record = kRecord;
+  r.slab = std::max(1, std::min(s->rows, 4096 / r.pieces));
+  r.ws_bytes = s->rows ? (size_t)r.slab * r.pieces * r.record : 0;
   return r;
 }
 
@@ -1068,7 +1297,7 @@ extern "C" int lutgemm_sample_tokens(const lutgemm_sample* s, const void* d_logi
     p.logprobs = d_logprobs;
     p.ws = (char*)d_workspace;
     p.row_step = s->row_step;
-    p.record = kRecord;
+    p.record = (int64_t)r.record;
     p.rows = s->rows;
     p.vocab = s->vocab;
     p.pieces = r.pieces;

@@ -442,10 +442,14 @@ def test_tables_in_place_and_replayed():
 
 # -------------------------------------------------------------------- sampling
 
-# A weight m 2^e, m in [1, 2], is off by at most 2^(e - 41) (its term's rounding) and 2^-48 of
-# itself, so a sum by at most 2^-41 + 2^-48 of itself, and 2^20 tokens below 2^-64 by 2^-44: a
-# border that is further from moving, of the total, than four times that does not move.
-MARGIN = 2.0 ** -38
+def _margin(vocab):
+    """How far, of the total, a border has to be from moving so that it does not; a total's
+    logarithm is off by no more. A weight m 2^e, m in [1, 2], is off by at most 2^(e - 41) (rounded
+    to 41 bits) and 2^-43 of itself (its polynomial). Sums in units of 2^-S of the largest weight,
+    S = min(50, 62 - log2(vocab)), lose up to a unit for each of 1024 bins and each 256 tokens;
+    tokens below 2^-63 are left out. Twice all that, for a sum and what it is compared with."""
+    unit = 2.0 ** -min(50, 62 - (vocab - 1).bit_length())
+    return 2 * ((1024 + vocab / 256) * unit + 2.0 ** -41 + 2.0 ** -43 + vocab * 2.0 ** -63)
 
 
 def _logits(rows, vocab, seed, spread=2.5):
@@ -475,14 +479,14 @@ def _sample_check(x, u, temperature=None, top_k=None, top_p=None, min_p=None, lo
         want, logprob, margin = plain.sample(rows[r], float(np.float32(u[r])), setting(temperature, r, 1.0),
                                              0 if top_k is None else top_k[r], setting(top_p, r, 1.0),
                                              setting(min_p, r, 0.0))
-        if margin < MARGIN:
+        if margin < _margin(x.shape[1]):
             near += 1
             continue
         assert tokens[r] == want, (r, tokens[r], want, margin)
         if want < 0:
             assert logprobs[r] != logprobs[r]
         else:  # rounded once from 64 bits
-            assert abs(logprobs[r] - logprob) <= 2.0 ** -24 * abs(logprob) + 1e-11, (r, logprobs[r], logprob)
+            assert abs(logprobs[r] - logprob) <= 2.0 ** -24 * abs(logprob) + _margin(x.shape[1]), (r, logprobs[r], logprob)
     assert near <= x.shape[0] // 20, f"{near} rows too close to a border"
     return tokens
 
@@ -664,3 +668,32 @@ def test_sample_nothing_to_do_and_out():
     tokens, _ = lg.sample_tokens(torch.zeros((3, 10), dtype=F32, device=DEV), _int([0.0, 0.5, 0.9], F32), out=out)
     assert tokens.data_ptr() == out.data_ptr() and out._version > before
     assert out.tolist() == [0, 5, 8]  # 0.9 in 32 bits is less than 9 of 10
+
+
+def test_sample_filters_together_on_few_tokens():
+    """top_k above the number of tokens with weight, with top_p before min_p."""
+    x = torch.full((4, 5000), -INF)
+    x[:, 100:140] = torch.from_numpy(_logits(4, 40, 12, 1.5)).float()
+    u = [0.2, 0.5, 0.8, 0.99]
+    for dtype in (F16, BF16, F32):
+        for k in (39, 40, 41, 1000, 4000):
+            for p, m in ((0.7, 0.0), (0.9, 0.3), (0.5, 0.6), (1.0, 0.2)):
+                _sample_check(x.to(dtype), u, [1.3] * 4, [k] * 4, [p] * 4, [m] * 4)
+
+
+def test_sample_largest_value_late_and_at_ends():
+    """A piece whose first tokens say little of its largest, rows of every alignment and end."""
+    for vocab in (8193, 40000, 70001, 131073):
+        base = _logits(6, vocab + 16, vocab, 1.0)
+        base[0, -vocab // 2] = 60.0
+        base[1, vocab - 1] = 30.0
+        base[2, 0] = 25.0
+        base[3, : vocab // 2] = -INF
+        base[4] = np.sort(base[4]) * 4
+        x = torch.from_numpy(base)
+        for dtype in (F16, F32):
+            dev = x.to(dtype).to(DEV)
+            for lo in (0, 1, 3):
+                part = x.to(dtype)[:, lo:lo + vocab].contiguous()
+                for more in (dict(), dict(top_p=[0.8] * 6), dict(top_k=[40] * 6), dict(min_p=[0.02] * 6)):
+                    _sample_check(part, [0.1, 0.3, 0.5, 0.7, 0.9, 0.97], [0.9] * 6, logits=dev[:, lo:lo + vocab], **more)
