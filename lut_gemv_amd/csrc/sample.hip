@@ -606,24 +606,22 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
     if (wave != part % kWaves) return;
     const u4v w = piece.word(part / kWaves);
     const int i0 = piece.first(part / kWaves);
-    double mine[P::kPer], sum = 0.0;
+    auto weight_of = [&](int e) {
+      return piece.is_token(i0 + e) ? weight(P::any(w, e), piece.token(i0 + e)) : 0.0;
+    };
+    double sum = 0.0;
 #pragma unroll 1
-    for (int e = 0; e < P::kPer; ++e) {
-      const double v = piece.is_token(i0 + e) ? weight(P::any(w, e), piece.token(i0 + e)) : 0.0;
-#pragma unroll
-      for (int j = 0; j < P::kPer; ++j)
-        if (j == e) mine[j] = v;
-      sum += v;
-    }
+    for (int e = 0; e < P::kPer; ++e) sum += weight_of(e);
     double cursor = wave_scan(sum) - sum;
     int token = -1, last = -1;
     float value = 0.f, last_value = 0.f;
-#pragma unroll
+#pragma unroll 1
     for (int e = 0; e < P::kPer; ++e) {
-      cursor += mine[e];
-      if (!(mine[e] > 0.0)) continue;
+      const double v = weight_of(e);
+      cursor += v;
+      if (!(v > 0.0)) continue;
       last = piece.token(i0 + e);
-      last_value = T::wide(P::element(w, e));
+      last_value = T::wide(P::any(w, e));
       if (token < 0 && cursor > goal) {
         token = last;
         value = last_value;
@@ -751,7 +749,7 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
     };
     // f(word, mask, first element) of every word that has tokens from `least` to `limit`, by
     // whole waves
-    auto each_word = [&](float least, float limit, auto f) {
+    auto each_word = [&](float least, float limit, auto f) __attribute__((always_inline)) {
       const int stripes = row.wave_stripes();
       u4v w[kAhead];
 #pragma unroll
@@ -777,7 +775,7 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
       }
     };
     // f(raw, index) of every token from `least` to `limit`
-    auto each_from = [&](float least, float limit, auto f) {
+    auto each_from = [&](float least, float limit, auto f) __attribute__((always_inline)) {
       each_word(least, limit, [&](const u4v& w, uint32_t some, int i0) {
         for (; some; some &= some - 1) {
           const int e = __builtin_ctz(some);
