@@ -287,6 +287,17 @@ __device__ __forceinline__ V lane_of(V v, int lane) {  // the lane is the same f
   }
 }
 
+// The bits that any lane has. (One atomic of each lane on one word instead: 5 us for 1024.)
+__device__ __forceinline__ uint64_t wave_or(uint64_t v) {
+  v |= from_lane<0x111, 0xF>(v);
+  v |= from_lane<0x112, 0xF>(v);
+  v |= from_lane<0x114, 0xF>(v);
+  v |= from_lane<0x118, 0xF>(v);
+  v |= from_lane<0x142, 0xA>(v);
+  v |= from_lane<0x143, 0xC>(v);
+  return lane_of(v, 63);
+}
+
 template <class V>
 __device__ __forceinline__ V wave_sum(V v) {
   return lane_of(wave_scan(v), 63);
@@ -484,7 +495,9 @@ __device__ __forceinline__ uint64_t select(RowShared& sh, uint64_t target, uint6
   if (t == 0) sh.ones = sh.zeros = 0;
   if (t < 256) sh.sums[0][t] = sh.counts[0][t] = 0;
   __syncthreads();
-  if (ones | zeros) {
+  ones = wave_or(ones);
+  zeros = wave_or(zeros);
+  if (lane == 0 && (ones | zeros)) {
     atomicOr((unsigned long long*)&sh.ones, (unsigned long long)ones);
     atomicOr((unsigned long long*)&sh.zeros, (unsigned long long)zeros);
   }
@@ -678,10 +691,19 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
            return Scale::by_value(a, b, k);
          });
   } else {
+    // the row's first words are under way while the bins are joined
+    u4v first[kAhead];
+    auto first_words = [&](u4v (&w)[kAhead]) __attribute__((always_inline)) {
+      const int stripes = row.wave_stripes();
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a)
+        if (a < stripes) w[a] = row.load(a);
+    };
+    first_words(first);
     // the bins of all pieces: sums in their own octave's unit and in 2^S
     uint64_t sum = 0;
     uint32_t count = 0;
-    constexpr int kPieces = 4;  // whose loads are under way together
+    constexpr int kPieces = 8;  // whose loads are under way together
     for (int c0 = 0; c0 < p.pieces; c0 += kPieces) {
       uint64_t v[kPieces];
       uint32_t n[kPieces];
@@ -749,12 +771,8 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
     };
     // f(word, mask, first element) of every word that has tokens from `least` to `limit`, by
     // whole waves
-    auto each_word = [&](float least, float limit, auto f) __attribute__((always_inline)) {
+    auto words_from = [&](u4v (&w)[kAhead], float least, float limit, auto f) __attribute__((always_inline)) {
       const int stripes = row.wave_stripes();
-      u4v w[kAhead];
-#pragma unroll
-      for (int a = 0; a < kAhead; ++a)
-        if (a < stripes) w[a] = row.load(a);
       for (int s0 = 0; s0 < stripes; s0 += kAhead) {
 #pragma unroll
         for (int a = 0; a < kAhead; ++a) {
@@ -774,6 +792,11 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
         }
       }
     };
+    auto each_word = [&](float least, float limit, auto f) __attribute__((always_inline)) {
+      u4v w[kAhead];
+      first_words(w);
+      words_from(w, least, limit, f);
+    };
     // f(raw, index) of every token from `least` to `limit`
     auto each_from = [&](float least, float limit, auto f) __attribute__((always_inline)) {
       each_word(least, limit, [&](const u4v& w, uint32_t some, int i0) {
@@ -784,11 +807,11 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
       });
     };
     // their codes into a list; *n: how many there are, also where the list ends before
-    auto collect = [&](float least, float limit, uint64_t* list, uint32_t* n) {
+    auto collect = [&](u4v (&first)[kAhead], float least, float limit, uint64_t* list, uint32_t* n) {
       __syncthreads();
       if (t == 0) *n = 0;
       __syncthreads();
-      each_word(least, limit, [&](const u4v& w, uint32_t some, int i0) {
+      words_from(first, least, limit, [&](const u4v& w, uint32_t some, int i0) {
         const uint32_t mine = __popc(some), upto = wave_scan(mine);
         uint32_t at = 0;
         if (lane == 63) at = atomicAdd(n, upto);
@@ -807,8 +830,8 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
     };
     // The tokens of a bin into `inside`, those of the bins before it into `list`: by value
     // first, which may take some of the next bins.
-    auto gather = [&](int bin, bool before_too) {
-      collect(least_of(bin), before_too ? INFINITY : most_of(bin), sh.list, &sh.above);
+    auto gather = [&](u4v (&first)[kAhead], int bin, bool before_too) {
+      collect(first, least_of(bin), before_too ? INFINITY : most_of(bin), sh.list, &sh.above);
       const uint32_t n = sh.above;
       uint64_t mine[kMine];
 #pragma unroll
@@ -929,7 +952,7 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
         __syncthreads();
         const uint64_t rest = (uint64_t)(set.top_k - sh.found_count);
         const uint64_t ahead = sh.found_sum;
-        gather(bin, set.few());
+        gather(first, bin, set.few());
         listed = set.few() && join_lists();
         if (!listed) {
           uint64_t before;
@@ -981,7 +1004,8 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
       __syncthreads();
       const uint64_t ahead = sh.found_sum;
       const bool small = sh.found_count;
-      gather(bin, small);
+      if (set.by_count) first_words(first);
+      gather(first, bin, small);
       const int by = 40 - octave_of(bin) - S;  // from 2^S to the bin's unit
       const uint64_t missing = target > ahead ? target - ahead : 1;
       const uint64_t need = by >= 0 ? shifted(missing, by) : (missing + (1ull << -by) - 1) >> -by;
@@ -1091,16 +1115,35 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
         }
         if (t < kMostPieces) kept[128 + t] = 0;
         __syncthreads();
-        auto add = [&](Raw raw, int i) {
-          uint64_t term;
-          if (bin_at(raw, &term) == chosen_bin && code_of<T>(raw, i) <= border)
-            atomicAdd((unsigned long long*)&kept[128 + i / p.piece], (unsigned long long)term);
+        // a wave adds those of one piece at a time (by single tokens: 6 us for 1500 of them)
+        auto add = [&](uint64_t term, int piece) {
+          for (uint64_t left = __ballot(term != 0); left;) {
+            const int c = __builtin_amdgcn_readlane(piece, __builtin_ctzll(left));
+            const bool mine = term && piece == c;
+            const uint64_t sum_c = wave_sum(mine ? term : 0ull);
+            if (lane == 0) atomicAdd((unsigned long long*)&kept[128 + c], (unsigned long long)sum_c);
+            left &= ~__ballot(mine);
+          }
+        };
+        auto kept_term = [&](uint64_t code) {
+          uint64_t term = 0;
+          return code <= border && bin_at(raw_of(code), &term) == chosen_bin ? term : 0ull;
         };
         if (sh.within <= kList) {
-          for (int i = t; i < (int)sh.within; i += kThreads)
-            add(raw_of(sh.inside[i]), (int)(sh.inside[i] & ((1u << kIndexBits) - 1)));
+          for (int i0 = 0; i0 < (int)sh.within; i0 += kThreads) {
+            const uint64_t code = i0 + t < (int)sh.within ? sh.inside[i0 + t] : ~0ull;
+            const bool is = code != ~0ull;
+            add(is ? kept_term(code) : 0ull,
+                is ? (int)(code & ((1u << kIndexBits) - 1)) / p.piece : 0);
+          }
         } else {
-          each_from(least_of(chosen_bin), most_of(chosen_bin), add);
+          each_word(least_of(chosen_bin), most_of(chosen_bin), [&](const u4v& w, uint32_t some, int i0) {
+            for (int e = 0; e < P::kPer; ++e) {
+              const bool is = some >> e & 1;
+              const int i = row.token(i0 + e);
+              add(is ? kept_term(code_of<T>(P::any(w, e), i)) : 0ull, is ? i / p.piece : 0);
+            }
+          });
         }
         __syncthreads();
         // the first piece that passes the goal
@@ -1117,7 +1160,9 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
       }
       __syncthreads();
       uint64_t* const parts = sh.list;  // list and inside: 2 kList
-      const int stripes = piece.stripes(), all = stripes * kWaves;
+      const int stripes = piece.wave_stripes(), all = piece.stripes() * kWaves;
+      if (lane == 0)  // of the last stripe, in which the wave may have no tokens
+        parts[(piece.stripes() - 1) * kWaves + wave] = 0;
       for (int s0 = 0; s0 < stripes; s0 += kAhead) {
         u4v w[kAhead];
 #pragma unroll
@@ -1129,10 +1174,13 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
           piece.place(w[a], s0 + a);
           const int i0 = piece.first(s0 + a);
           double sum_s = 0.0;
+          float top = -INFINITY;
 #pragma unroll
-          for (int e = 0; e < P::kPer; ++e) {
-            const float x = T::wide(P::element(w[a], e));
-            if (__any(x >= least)) sum_s += kept_value(x, offset + piece.token(i0 + e));
+          for (int e = 0; e < P::kPer; ++e) top = fmaxf(top, T::wide(P::element(w[a], e)));
+          if (__any(top >= least)) {
+#pragma unroll
+            for (int e = 0; e < P::kPer; ++e)
+              sum_s += kept_value(T::wide(P::element(w[a], e)), offset + piece.token(i0 + e));
           }
           sum_s = wave_sum(sum_s);
           if (lane == 0) parts[(s0 + a) * kWaves + wave] = in_units(sum_s, 0);
