@@ -559,7 +559,7 @@ int lutgemm_shared_attention(const lutgemm_shared* a, const void* d_q, const voi
  * more than `capacity` is dropped. A range's first is taken modulo the capacity, its count brought
  * into [0, capacity]. Table entries and ring entries are not checked: a page
  * number that is none makes a slot or page that the other calls refuse as theirs state.
- *   d_workspace       8 * seqs bytes, as for attention.
+ *   d_workspace       at least lutgemm_batch_tables_workspace bytes, as for attention
  * Shape rules: 0 <= seqs < 2^20, 0 <= tokens < 2^24, 1 <= page_size <= 65536, table_width >=
  * 1 with table_width * page_size <= 2^30, 0 <= capacity < 2^29, table_stride >= table_width.
  * Alignment: the int64 arrays 8 bytes, all others 4. */

@@ -128,6 +128,18 @@ at::Tensor scratch(size_t bytes, const at::Tensor& ref) {
   return at::empty({(int64_t)bytes}, ref.options().dtype(at::kByte));
 }
 
+// A vector of `n` entries at `offset` bytes (a multiple of their size) in an allocation's
+// storage: small results of one call share one, an allocation each costs the host 0.8 us.
+at::Tensor part_of(const at::Tensor& base, at::ScalarType type, int64_t offset, int64_t n) {
+  const caffe2::TypeMeta meta = c10::scalarTypeToTypeMeta(type);
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(base.storage()),
+                                                          base.key_set(), meta);
+  c10::TensorImpl* const impl = t.unsafeGetTensorImpl();
+  impl->set_storage_offset(offset / (int64_t)meta.itemsize());
+  impl->set_sizes_contiguous({n});
+  return t;
+}
+
 // A tensor of the caller's has been written: autograd tells by its version that a copy
 // kept for a backward pass is no longer what it was. Tensors of inference mode have none.
 void written(const at::Tensor& t) {
@@ -436,12 +448,15 @@ PyObject* tables(PyObject* const* a) {
   constexpr const char* where = "lutgemm_batch_tables";
   size_t need = 0;
   check(g_tables_ws(&d, &need), where);
-  got[0] = at::empty({d.tokens}, change.options().dtype(at::kLong));
-  got[1] = at::empty({d.tokens}, change.options().dtype(at::kLong));
-  got[2] = in_place ? lens : at::empty({seqs}, change.options());
-  got[3] = at::empty({seqs + 1}, change.options());
+  const int64_t rows8 = 8 * d.tokens;
+  const at::Tensor all = scratch(2 * rows8 + 4 * (seqs + (seqs + 1) + 2), change);
+  got[0] = part_of(all, at::kLong, 0, d.tokens);
+  got[1] = part_of(all, at::kLong, rows8, d.tokens);
+  got[2] = in_place ? lens : part_of(all, at::kInt, 2 * rows8, seqs);
+  got[3] = part_of(all, at::kInt, 2 * rows8 + 4 * seqs, seqs + 1);
   if (range) {
-    got[4] = in_place ? tensor(a[6], "free_range") : at::empty({2}, change.options());
+    got[4] = in_place ? tensor(a[6], "free_range")
+                      : part_of(all, at::kInt, 2 * rows8 + 4 * (2 * seqs + 1), 2);
     range_out = got[4].data_ptr();
   }
   at::Tensor ws;
@@ -461,11 +476,11 @@ PyObject* tables(PyObject* const* a) {
     if (range) written(got[4]);
   }
   if (range) return tuple_of(got);
-  PyObject* all[4] = {};
-  bool whole_ = true;
-  for (int i = 0; i < 4; ++i) whole_ &= (all[i] = THPVariable_Wrap(got[i])) != nullptr;
-  PyObject* t = whole_ ? PyTuple_Pack(5, all[0], all[1], all[2], all[3], Py_None) : nullptr;
-  for (PyObject* o : all) Py_XDECREF(o);
+  PyObject* four[4] = {};
+  bool made = true;
+  for (int i = 0; i < 4; ++i) made &= (four[i] = THPVariable_Wrap(got[i])) != nullptr;
+  PyObject* t = made ? PyTuple_Pack(5, four[0], four[1], four[2], four[3], Py_None) : nullptr;
+  for (PyObject* o : four) Py_XDECREF(o);
   return t;
 }
 
@@ -494,13 +509,14 @@ PyObject* sample(PyObject* const* a) {
   const void* min_p = setting(5, at::kFloat, "min_p");
   const c10::hip::HIPGuard guard(x.device().index());
   at::Tensor got[2];
+  const at::Tensor all = scratch(12 * rows, x);
   if (a[6] == Py_None) {
-    got[0] = at::empty({rows}, x.options().dtype(at::kLong));
+    got[0] = part_of(all, at::kLong, 0, rows);
   } else {
     got[0] = tensor(a[6], "out");
     flat(got[0], at::kLong, x, {rows}, "out");
   }
-  got[1] = at::empty({rows}, x.options().dtype(at::kFloat));
+  got[1] = part_of(all, at::kFloat, 8 * rows, rows);
   constexpr const char* where = "lutgemm_sample_tokens";
   size_t need = 0;
   check(g_sample_ws(&d, &need), where);

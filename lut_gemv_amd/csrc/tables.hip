@@ -2,9 +2,11 @@
 // requests' lengths (lutgemm_batch_tables; the rules are in lutgemm.h).
 //
 // Integers only, a few megabytes at most: bound by latency. scan_kernel, one workgroup,
-// walks the sequences 1024 at a time with running sums of new rows, of pages taken and of
-// pages given back; a sequence's rows and pages then follow from its sums alone. Sums
-// saturate at 2^30, above every limit that they are compared with.
+// walks the sequences a workgroup's width at a time with running sums of new rows, of pages
+// taken and of pages given back; a sequence's rows and pages then follow from its sums alone.
+// Sums saturate at 2^30, above every limit that they are compared with. Up to kFewRows rows
+// it also writes the rows, those of single tokens by the sequence's own thread; more
+// are fill_kernel's, whose workgroups look for the sequences of their rows.
 #include "serve.h"
 
 namespace lutgemm {
@@ -12,9 +14,10 @@ namespace {
 
 using namespace serve;
 
-constexpr int kScan = 1024;      // threads of scan_kernel: sequences of one turn
 constexpr int kFill = 256;       // threads of fill_kernel
-constexpr int kFillRows = 1024;  // rows of one of its workgroups
+constexpr int kFillRows = 512;   // rows of one of its workgroups
+constexpr int kFewRows = 4096;   // that scan_kernel writes itself
+constexpr int kOwnRows = 4;      // of a sequence, by its own thread
 constexpr uint32_t kFull = 1u << 30;
 
 struct TablesParams {
@@ -39,25 +42,45 @@ __device__ __forceinline__ uint32_t add_full(uint32_t a, uint32_t b) {
   return s < kFull ? s : kFull;
 }
 
-// Inclusive sums over the workgroup's threads; *total: of all of them.
-__device__ __forceinline__ uint32_t scan(uint32_t v, uint32_t* waves, uint32_t* total) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const uint32_t u = __shfl_up(v, d, 64);
-    if (lane >= d) v = add_full(v, u);
+struct Sums {
+  uint32_t rows, pages, given;
+  __device__ __forceinline__ void add(const Sums& o) {
+    rows = add_full(rows, o.rows);
+    pages = add_full(pages, o.pages);
+    given = add_full(given, o.given);
   }
+};
+
+template <int Control, int Rows>
+__device__ __forceinline__ void add_from(Sums& v) {
+  auto from = [](uint32_t x) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, Control, Rows, 0xF, false);
+  };
+  const Sums o = {from(v.rows), from(v.pages), from(v.given)};
+  v.add(o);
+}
+
+// Inclusive sums over the workgroup's threads; *total: of all of them.
+template <int Waves>
+__device__ __forceinline__ Sums scan(Sums v, Sums* waves, Sums* total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  add_from<0x111, 0xF>(v);
+  add_from<0x112, 0xF>(v);
+  add_from<0x114, 0xF>(v);
+  add_from<0x118, 0xF>(v);
+  add_from<0x142, 0xA>(v);
+  add_from<0x143, 0xC>(v);
   if (lane == 63) waves[wave] = v;
   __syncthreads();
-  uint32_t before = 0, all = 0;
+  Sums before = {0, 0, 0}, all = {0, 0, 0};
 #pragma unroll
-  for (int w = 0; w < kScan / 64; ++w) {
-    if (w < wave) before = add_full(before, waves[w]);
-    all = add_full(all, waves[w]);
+  for (int w = 0; w < Waves; ++w) {
+    if (w < wave) before.add(waves[w]);
+    all.add(waves[w]);
   }
-  __syncthreads();
   *total = all;
-  return add_full(v, before);
+  v.add(before);
+  return v;
 }
 
 // Where the ring's entry `nth` behind `first` lies (nth up to the capacity).
@@ -80,107 +103,168 @@ __device__ __forceinline__ Range free_range(const TablesParams& p) {
   return r;
 }
 
-__global__ __launch_bounds__(kScan) void scan_kernel(TablesParams p) {
-  __shared__ uint32_t waves[kScan / 64];
+// The row of a sequence's ith new token: its position and slot, and the table's new entry, by
+// the row whose key is its page's first.
+__device__ __forceinline__ void write_row(const TablesParams& p, int s, int row, int n, int held,
+                                          int taken, int64_t offset, int i) {
+  const int at = n + i, page = at / p.page, place = at - page * p.page;
+  int32_t* const entry = p.table + (int64_t)s * p.table_stride + page;
+  int id;
+  if (p.ring && page >= held) {
+    id = p.ring[around(taken, (uint32_t)(page - held), p.capacity)];
+    if (place == 0) *entry = id;
+  } else {
+    id = *entry;
+  }
+  p.positions[row] = offset + at;
+  p.slots[row] = (int64_t)id * p.page + place;
+}
+
+template <int Threads>
+__global__ __launch_bounds__(Threads) void scan_kernel(TablesParams p) {
+  __shared__ Sums waves[2][Threads / 64];
   __shared__ uint32_t served_rows, served_pages;
   fetch(p);
-  const Range free = free_range(p);
   const int limit = p.width * p.page, lane = threadIdx.x & 63;
+  const bool all_rows = p.tokens <= kFewRows;  // fill_kernel is not launched
+  int n = 0, change = 0;
+  auto read = [&](int s) {
+    if (s >= p.seqs) return;
+    n = p.lens[s];
+    change = p.change[s];
+  };
+  read(threadIdx.x);
+  const Range free = free_range(p);
   const uint32_t room = (uint32_t)(p.capacity - free.count);
   const int behind = around(free.first, (uint32_t)free.count, p.capacity);
-  uint32_t rows = 0, pages = 0, given = 0;  // sums of the turns before
+  Sums sums = {0, 0, 0};  // of the turns before
   if (threadIdx.x == 0) {
     served_rows = served_pages = 0;
     p.starts[0] = 0;
   }
-  for (int s0 = 0; s0 < p.seqs; s0 += kScan) {
+  for (int s0 = 0, turn = 0; s0 < p.seqs; s0 += Threads, turn ^= 1) {
     const int s = s0 + threadIdx.x;
-    int n = 0, change = 0;
-    if (s < p.seqs) {
-      n = p.lens[s];
-      n = n < 0 ? 0 : n > limit ? limit : n;
-      change = p.change[s];
-    }
+    if (s0) read(s);
+    const bool here = s < p.seqs;
+    n = !here || n < 0 ? 0 : n > limit ? limit : n;
+    if (!here) change = 0;
     uint32_t grow = change > 0 && change <= limit - n ? (uint32_t)change : 0;
     const int held = (n + p.page - 1) / p.page;
     uint32_t need = 0, back = 0;
     int after = n;
     if (change < 0) after = n + change < 0 ? 0 : n + change;
     if (p.ring) {
-      need = (uint32_t)((n + (int)grow + p.page - 1) / p.page - held);
-      back = (uint32_t)(held - (after + p.page - 1) / p.page);
+      if (grow) need = (uint32_t)((n + (int)grow + p.page - 1) / p.page - held);
+      if (change < 0) back = (uint32_t)(held - (after + p.page - 1) / p.page);
     }
-    uint32_t all_rows, all_pages, all_given;
-    const uint32_t end = add_full(rows, scan(grow, waves, &all_rows));
-    const uint32_t page_end = add_full(pages, scan(need, waves, &all_pages));
-    const uint32_t given_end = add_full(given, scan(back, waves, &all_given));
-    const bool served = end <= (uint32_t)p.tokens && page_end <= (uint32_t)free.count;
-    if (s < p.seqs && served) {
-      atomicMax(&served_rows, end);
-      atomicMax(&served_pages, page_end);
+    Sums all;
+    Sums end = scan<Threads / 64>({grow, need, back}, waves[turn], &all);
+    end.add(sums);
+    const bool served = end.rows <= (uint32_t)p.tokens && end.pages <= (uint32_t)free.count;
+    // sums rise: the last sequence served of a wave has its largest
+    const uint64_t votes = __ballot(here && served);
+    if (votes && lane == 63 - __builtin_clzll(votes)) {
+      atomicMax(&served_rows, end.rows);
+      atomicMax(&served_pages, end.pages);
     }
     __syncthreads();
-    if (s < p.seqs) {
-      if (!served) grow = 0;
-      p.starts[s + 1] = (int)(served ? end : served_rows);
+    const int first_row = (int)(end.rows - grow);
+    if (!served) grow = 0;
+    int taken = 0;
+    if (here) {
+      p.starts[s + 1] = (int)(served ? end.rows : served_rows);
       p.lens_out[s] = after + (int)grow;
-      p.ws[2 * s] = n;
-      p.ws[2 * s + 1] = served && p.ring ? around(free.first, page_end - need, p.capacity) : 0;
+      if (served && p.ring) taken = around(free.first, end.pages - need, p.capacity);
+      if (!all_rows) {
+        p.ws[2 * s] = n;
+        p.ws[2 * s + 1] = taken;
+      }
     }
     // pages given back, a wave to a sequence at a time
-    uint64_t givers = __ballot(back > 0);
-    while (givers) {
+    for (uint64_t givers = __ballot(back > 0); givers; givers &= givers - 1) {
       const int from = __builtin_ctzll(givers);
-      givers &= givers - 1;
       const int count = __builtin_amdgcn_readlane((int)back, from);
-      const uint32_t at = (uint32_t)__builtin_amdgcn_readlane((int)(given_end - back), from);
+      const uint32_t at = (uint32_t)__builtin_amdgcn_readlane((int)(end.given - back), from);
       const int first = __builtin_amdgcn_readlane(held, from) - count;
       const int32_t* row = p.table + (int64_t)(s0 + (int)(threadIdx.x & ~63u) + from) * p.table_stride;
       for (int j = lane; j < count; j += 64)
-        if (at + (uint32_t)j < room)
-          p.ring[around(behind, at + (uint32_t)j, p.capacity)] = row[first + j];
+        if (at + (uint32_t)j < room) p.ring[around(behind, at + (uint32_t)j, p.capacity)] = row[first + j];
     }
-    rows = add_full(rows, all_rows);
-    pages = add_full(pages, all_pages);
-    given = add_full(given, all_given);
-    __syncthreads();
+    if (all_rows) {
+      const int64_t offset = here && p.offsets && grow ? (int64_t)p.offsets[s] : 0;
+      if (grow && grow <= kOwnRows)
+        for (int i = 0; i < (int)grow; ++i) write_row(p, s, first_row + i, n, held, taken, offset, i);
+      for (uint64_t more = __ballot(grow > kOwnRows); more; more &= more - 1) {
+        const int from = __builtin_ctzll(more);
+        auto of = [&](int v) { return __builtin_amdgcn_readlane(v, from); };
+        const int count = of((int)grow), row = of(first_row), len = of(n), pages = of(held), ring = of(taken);
+        const int64_t off = p.offsets ? (int64_t)of((int)offset) : 0;
+        const int seq = s0 + (int)(threadIdx.x & ~63u) + from;
+        for (int i = lane; i < count; i += 64) write_row(p, seq, row + i, len, pages, ring, off, i);
+      }
+    }
+    sums.add(all);
   }
+  __syncthreads();
   if (threadIdx.x == 0 && p.ring) {
-    const uint32_t put = given < room ? given : room;
+    const uint32_t put = sums.given < room ? sums.given : room;
     p.range_out[0] = around(free.first, served_pages, p.capacity);
     p.range_out[1] = free.count - (int)served_pages + (int)put;
   }
+  if (all_rows)
+    for (int row = (int)served_rows + threadIdx.x; row < p.tokens; row += Threads) {
+      p.positions[row] = 0;
+      p.slots[row] = -1;
+    }
 }
 
-// The rows' positions and slots, and the table's new entries: by the row whose key is
-// its page's first.
+// The last sequence of which the first row is not behind `row`, which the last one's end
+// is: by whole waves, 64 starts at a time.
+__device__ __forceinline__ int owner(const TablesParams& p, int row, int lane) {
+  int lo = 0, n = p.seqs;  // among [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 63) / 64, at = lo + lane * step;
+    const uint64_t votes = __ballot(at < lo + n && p.starts[min(at, p.seqs)] <= row);
+    const int found = __popcll(votes) - 1;
+    lo += found * step;
+    n = min(step, n - found * step);
+  }
+  return lo;
+}
+
 __global__ __launch_bounds__(kFill) void fill_kernel(TablesParams p) {
+  __shared__ int32_t starts[kFillRows + 1];
   fetch(p);
-  const int row0 = blockIdx.x * kFillRows;
-  for (int row = row0 + threadIdx.x; row < min(row0 + kFillRows, p.tokens); row += kFill) {
-    // the sequence: the last one whose first row is not behind this one
-    int lo = 0, hi = p.seqs;  // starts[lo] <= row
-    if (row >= p.starts[p.seqs]) {
+  const int lane = threadIdx.x & 63, rows = p.starts[p.seqs];
+  const int row0 = blockIdx.x * kFillRows, end = min(row0 + kFillRows, p.tokens);
+  const int last = min(end, rows) - 1;
+  int lo = 0, hi = 0;
+  bool near = true;
+  if (last >= row0) {
+    lo = owner(p, row0, lane);
+    hi = owner(p, last, lane);
+    near = hi - lo < kFillRows;  // sequences without rows may lie between
+    if (near)
+      for (int i = threadIdx.x; i <= hi - lo; i += kFill) starts[i] = p.starts[lo + i];
+  }
+  __syncthreads();
+  for (int row = row0 + threadIdx.x; row < end; row += kFill) {
+    if (row > last) {
       p.positions[row] = 0;
       p.slots[row] = -1;
       continue;
     }
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (p.starts[mid] <= row) lo = mid; else hi = mid;
+    int a = lo, b = hi + 1;
+    while (b - a > 1) {
+      const int mid = (a + b) >> 1;
+      if ((near ? starts[mid - lo] : p.starts[mid]) <= row)
+        a = mid;
+      else
+        b = mid;
     }
-    const int n = p.ws[2 * lo], at = n + row - p.starts[lo];
-    const int page = at / p.page, held = (n + p.page - 1) / p.page;
-    int32_t* entry = p.table + (int64_t)lo * p.table_stride + page;
-    int id;
-    if (p.ring && page >= held) {
-      id = p.ring[around(p.ws[2 * lo + 1], (uint32_t)(page - held), p.capacity)];
-      if (at % p.page == 0) *entry = id;
-    } else {
-      id = *entry;
-    }
-    p.positions[row] = (p.offsets ? (int64_t)p.offsets[lo] : 0) + at;
-    p.slots[row] = (int64_t)id * p.page + at % p.page;
+    const int n = p.ws[2 * a], held = (n + p.page - 1) / p.page;
+    write_row(p, a, row, n, held, p.ws[2 * a + 1], p.offsets ? (int64_t)p.offsets[a] : 0,
+              row - (near ? starts[a - lo] : p.starts[a]));
   }
 }
 
@@ -199,6 +283,10 @@ int check_tables(const lutgemm_tables* t) {
   return LUTGEMM_OK;
 }
 
+size_t workspace(const lutgemm_tables* t) {
+  return t->tokens <= kFewRows ? 0 : (size_t)t->seqs * 2 * sizeof(int32_t);
+}
+
 }  // namespace
 }  // namespace lutgemm
 
@@ -208,7 +296,7 @@ extern "C" int lutgemm_batch_tables_workspace(const lutgemm_tables* t, size_t* b
   const int st = check_tables(t);
   if (st) return st;
   if (!bytes) return LUTGEMM_ERR_NULL;
-  *bytes = (size_t)t->seqs * 2 * sizeof(int32_t);
+  *bytes = workspace(t);
   return LUTGEMM_OK;
 }
 
@@ -222,8 +310,9 @@ extern "C" int lutgemm_batch_tables(const lutgemm_tables* t, const int32_t* d_ch
     int st = check_tables(t);
     if (st) return st;
     if (!d_starts || (t->tokens && (!d_positions || !d_slots))) return LUTGEMM_ERR_NULL;
-    if (t->seqs && (!d_change || !d_lens || !d_table || !d_lens_out || !d_workspace))
-      return LUTGEMM_ERR_NULL;
+    const size_t need = workspace(t);
+    if (t->seqs && (!d_change || !d_lens || !d_table || !d_lens_out)) return LUTGEMM_ERR_NULL;
+    if (need && !d_workspace) return LUTGEMM_ERR_NULL;
     if (t->capacity && (!d_ring || !d_range || !d_range_out)) return LUTGEMM_ERR_NULL;
     for (const void* at : {(const void*)d_change, (const void*)d_lens, (const void*)d_offsets,
                            (const void*)d_table, (const void*)d_ring, (const void*)d_range,
@@ -231,7 +320,7 @@ extern "C" int lutgemm_batch_tables(const lutgemm_tables* t, const int32_t* d_ch
                            (const void*)d_workspace})
       if (!aligned(at, 4)) return LUTGEMM_ERR_ALIGN;
     if (!aligned(d_positions, 8) || !aligned(d_slots, 8)) return LUTGEMM_ERR_ALIGN;
-    if (workspace_bytes < (size_t)t->seqs * 2 * sizeof(int32_t)) return LUTGEMM_ERR_BUFFER;
+    if (workspace_bytes < need) return LUTGEMM_ERR_BUFFER;
     const int64_t seqs4 = 4 * (int64_t)t->seqs, rows8 = 8 * t->tokens;
     const bool same_lens = d_lens_out == d_lens, same_range = d_range_out == d_range;
     const Flat all[] = {{d_positions, rows8},
@@ -240,7 +329,7 @@ extern "C" int lutgemm_batch_tables(const lutgemm_tables* t, const int32_t* d_ch
                         {d_lens_out, seqs4},
                         {t->capacity ? d_range_out : nullptr, 8},
                         {t->capacity ? d_ring : nullptr, 4 * (int64_t)t->capacity},
-                        {d_workspace, 2 * seqs4},
+                        {d_workspace, (int64_t)need},
                         {d_change, seqs4},
                         {d_offsets, seqs4},
                         {same_lens ? nullptr : d_lens, seqs4},
@@ -269,8 +358,10 @@ extern "C" int lutgemm_batch_tables(const lutgemm_tables* t, const int32_t* d_ch
     p.capacity = t->capacity;
     p.tokens = t->tokens;
     hipStream_t strm = (hipStream_t)stream;
-    st = launch(scan_kernel, dim3(1), kScan, p, strm);
-    if (st || !t->tokens) return st;
+    // one wave of 256 begins and meets sooner than four
+    st = t->seqs <= 256 ? launch(scan_kernel<256>, dim3(1), 256, p, strm)
+                        : launch(scan_kernel<1024>, dim3(1), 1024, p, strm);
+    if (st || t->tokens <= kFewRows) return st;
     return launch(fill_kernel, dim3((unsigned)((t->tokens + kFillRows - 1) / kFillRows)), kFill, p, strm);
   } catch (...) {
     return LUTGEMM_ERR_INTERNAL;

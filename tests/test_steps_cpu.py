@@ -99,11 +99,12 @@ def _tables(wsb=1 << 30, **change):
     (dict(table_stride=9), SHAPE), (dict(table_stride=1 << 40), SHAPE),
     (dict(change=None), NULL), (dict(lens=None), NULL), (dict(table=None), NULL), (dict(ring=None), NULL),
     (dict(range=None), NULL), (dict(range_out=None), NULL), (dict(positions=None), NULL), (dict(slots=None), NULL),
-    (dict(lens_out=None), NULL), (dict(starts=None), NULL), (dict(ws=None), NULL), (dict(wsb=23), BUFFER),
+    (dict(lens_out=None), NULL), (dict(starts=None), NULL), (dict(tokens=9999, ws=None), NULL),
+    (dict(tokens=9999, wsb=23), BUFFER),
     (dict(change=A + 2), ALIGN), (dict(positions=A + 6 * FAR + 4), ALIGN), (dict(slots=A + 7 * FAR + 4), ALIGN),
     (dict(ring=A + 4 * FAR + 1), ALIGN), (dict(offsets=A + 2), ALIGN), (dict(ws=A + 2), ALIGN),
     (dict(slots=A + 6 * FAR + 152), SHAPE), (dict(lens_out=A + FAR + 4), SHAPE), (dict(starts=A + 4), SHAPE),
-    (dict(range_out=A + 5 * FAR + 4), SHAPE), (dict(ring=A + 2 * FAR - 196), SHAPE), (dict(ws=A + 8), SHAPE),
+    (dict(range_out=A + 5 * FAR + 4), SHAPE), (dict(ring=A + 2 * FAR - 196), SHAPE), (dict(tokens=9999, ws=A + 8), SHAPE),
 ])
 def test_tables_refusals(change, status):
     assert _tables(**change) == status
@@ -111,8 +112,9 @@ def test_tables_refusals(change, status):
 
 def test_tables_workspace():
     n = ctypes.c_size_t(7)
-    assert lg.lib().lutgemm_batch_tables_workspace(_TABLES.pack(*TABLES.values()), ctypes.byref(n)) == 0
-    assert n.value == 24
+    for tokens, need in ((20, 0), (100000, 24)):  # few rows are written by the launch that counts them
+        d = _TABLES.pack(*{**TABLES, "tokens": tokens}.values())
+        assert lg.lib().lutgemm_batch_tables_workspace(d, ctypes.byref(n)) == 0 and n.value == need
     assert lg.lib().lutgemm_batch_tables_workspace(_TABLES.pack(*TABLES.values()), None) == NULL
     assert lg.lib().lutgemm_batch_tables_workspace(None, ctypes.byref(n)) == NULL
 
