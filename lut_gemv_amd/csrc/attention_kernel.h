@@ -165,9 +165,9 @@ __device__ __forceinline__ Span span_of(const typename V::Params& p, const Seq& 
   const int keys = a.hi > a.lo ? a.hi - a.lo : 0;
   // a sequence longer than the launch was made for takes longer parts
   int need = (keys + cut.splits - 1) / cut.splits;
-  // few_rows has room for the parts of so many rows; a longer chunk, which a launch made
-  // for short ones meets, is not split
-  if (Kind == 0 && q.len * p.group > kFewRows) need = keys;
+  // few_rows has room for the parts of so many rows (PagedView's); a longer chunk, which a
+  // launch made for short ones meets, is not split
+  if (V::kDirect && Kind == 0 && q.len * p.group > kFewRows) need = keys;
   a.chunk = need > cut.chunk ? (need + kSplitKeys - 1) / kSplitKeys * kSplitKeys : cut.chunk;
   a.parts = keys > a.chunk ? (keys + a.chunk - 1) / a.chunk : 1;
   return a;
@@ -284,7 +284,7 @@ __device__ __forceinline__ void few_rows(const typename V::Params& p, int block,
   constexpr int kPitch = D + 4;
   static_assert(kFewRows * kPitch * 4 <= 64 * D * 2, "a wave's sums fit its region");
   const int part = block / p.kv_heads, kvh = block % p.kv_heads;
-  const int s = part % p.seqs, split = part / p.seqs;
+  const int s = part % V::count(p), split = part / V::count(p);
   const Seq seq = V::seq(p, s);
   const int rows = seq.len * p.group;
   if (rows > V::few(p)) return;

@@ -18,7 +18,9 @@ struct SharedParams : AttnParams {
   const int32_t* prefix_lens;
   const int32_t* group_starts;
   int64_t prefix_stride, prefix_at;  // prefix_at: where the prefixes' part rows begin
-  int32_t groups, prefix_keys, prefix_tiles, prefix_splits, prefix_chunk, prefix_blocks;
+  int32_t groups, prefix_keys, prefix_tiles, prefix_splits, prefix_chunk;
+  int32_t prefix_few;     // groups of up to so many rows are few_rows': all or none
+  int32_t blocks[3];      // workgroups of the prefixes, of many_rows and of few_rows
 };
 
 // A sequence's own keys. Part row of split s: (s * tokens + token) * heads + head.
@@ -56,7 +58,7 @@ struct PrefixView {
     q.n = n < 0 ? 0 : n > p.prefix_keys ? p.prefix_keys : n;
     return q;
   }
-  static __device__ __forceinline__ int few(const SharedParams&) { return 0; }
+  static __device__ __forceinline__ int few(const SharedParams& p) { return p.prefix_few; }
   static __device__ __forceinline__ int tiles(const SharedParams& p) { return p.prefix_tiles; }
   static __device__ __forceinline__ Cut cut(const SharedParams& p, int) {
     return {p.prefix_splits, p.prefix_chunk};
@@ -65,24 +67,44 @@ struct PrefixView {
     return p.prefix_table + g * p.prefix_stride;
   }
   static __device__ __forceinline__ int pos(const Seq& q, int) { return q.n - 1; }
+  static __device__ __forceinline__ int64_t few_at(const SharedParams& p, int split, int, int, int,
+                                                   int token, int head) {
+    return p.prefix_at + split * p.many_step + (int64_t)token * p.heads + head;
+  }
   static __device__ __forceinline__ int64_t many_at(const SharedParams& p) { return p.prefix_at; }
 };
 
-template <class T, int D>
+// Which bodies a launch has: the prefixes' one (or none), and whether single tokens and
+// chunks are among the own keys. A kernel of all of them at once is slower at each (64
+// sequences on 32768 keys 146 us, so 106).
+enum { kNoPrefix, kManyPrefix, kFewPrefix };
+
+template <class T, int D, int Prefix, bool Few, bool Many>
 __global__ __launch_bounds__(kThreads, 2) void shared_kernel(SharedParams p) {
   constexpr int kTile = 64 * D * 2;
   __shared__ __attribute__((aligned(16))) char keys0[kTile], vals0[kTile], keys1[kTile], vals1[kTile];
   __shared__ FewShared<kThreads / 64> shared;
   fetch(p);
-  const int own = (int)blockIdx.x - p.prefix_blocks, few = own - p.many_blocks;
-  if (own < 0)
-    many_rows<PrefixView, T, D>(p, blockIdx.x, keys0, vals0, keys1, vals1, shared.marks);
-  else if (few < 0)
-    many_rows<OwnView, T, D>(p, own, keys0, vals0, keys1, vals1, shared.marks);
-  else
-    few_rows<OwnView, T, D, kThreads / 64>(
-        p, few, [&](int w) { return w == 0 ? keys0 : w == 1 ? vals0 : w == 2 ? keys1 : vals1; },
-        shared);
+  auto region = [&](int w) { return w == 0 ? keys0 : w == 1 ? vals0 : w == 2 ? keys1 : vals1; };
+  int block = blockIdx.x;
+  if constexpr (Prefix != kNoPrefix) {
+    if (block < p.blocks[0]) {
+      if constexpr (Prefix == kFewPrefix)
+        few_rows<PrefixView, T, D, kThreads / 64>(p, block, region, shared);
+      else
+        many_rows<PrefixView, T, D>(p, block, keys0, vals0, keys1, vals1, shared.marks);
+      return;
+    }
+    block -= p.blocks[0];
+  }
+  if constexpr (Many) {
+    if (block < p.blocks[1]) {
+      many_rows<OwnView, T, D>(p, block, keys0, vals0, keys1, vals1, shared.marks);
+      return;
+    }
+    block -= p.blocks[1];
+  }
+  if constexpr (Few) few_rows<OwnView, T, D, kThreads / 64>(p, block, region, shared);
 }
 
 // The last i in [0, count) whose start is at most `token`, -1 for none; all lanes ask together.
@@ -97,7 +119,9 @@ __device__ __forceinline__ int owner(const SharedParams& p, int count, int token
   return uniform(found - 1);
 }
 
-// Joins the parts of rows of one token: D / 4 lanes to a row.
+// Joins the parts of rows of one token: D / 4 lanes to a row. Bound by reading them: 36 MB for
+// 64 tokens x 64 heads of 128 in 17 parts, 9.7 us. (Parts asked for before it is known how
+// many there are: 10 to 11 us.)
 template <class T, int D>
 __global__ __launch_bounds__(kThreads) void join_kernel(SharedParams p) {
   constexpr int G = D / 4, kRows = kThreads / G, kAhead = 4;
@@ -105,7 +129,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(SharedParams p) {
   const int per = (p.heads + kRows - 1) / kRows;
   const int token = (int)(blockIdx.x / per), head = (int)(blockIdx.x % per) * kRows + threadIdx.x / G;
   const int lane = threadIdx.x & 63, c = threadIdx.x % G;
-  const int s = owner<OwnView>(p, p.seqs, token, lane);
+  const int s = p.q_starts ? owner<OwnView>(p, p.seqs, token, lane) : token;
   if (s < 0) return;
   const Seq seq = sequence(p, s);
   if (token >= seq.begin + seq.len) return;  // behind the last sequence
@@ -184,8 +208,10 @@ int check_shared(const lutgemm_shared* a) {
   return LUTGEMM_OK;
 }
 
+constexpr int64_t kSlots = 512;  // workgroups that run at a time: two to a compute unit
+
 struct SharedPlan {
-  bool few, many;
+  bool few, many, prefix_few;
   int splits[3], chunk[3];  // of few_rows, many_rows and the prefixes
   int64_t tiles, prefix_tiles;
   int64_t rows, part_rows;
@@ -222,31 +248,49 @@ SharedPlan plan(const lutgemm_shared* s) {
   r.many = max_q * group > kFewRows;
   r.few = !r.many || (a->seqs > 1 && group <= kFewRows);
   r.tiles = r.many ? a->tokens * group / kManyRows + a->seqs : 0;
-  r.prefix_tiles = s->groups ? a->tokens * group / kManyRows + s->groups : 0;
+  // a group of up to sixteen rows to a key head reads its prefix as a single token does
+  r.prefix_few = s->groups && (a->tokens + s->groups - 1) / s->groups * group <= kFewRows;
+  r.prefix_tiles = s->groups ? s->groups == 1 ? (a->tokens * group + kManyRows - 1) / kManyRows
+                                              : a->tokens * group / kManyRows + s->groups
+                             : 0;
   const int64_t few = (int64_t)a->seqs * a->kv_heads;
   const int64_t many = (a->tokens * group / kManyRows + (a->seqs + 1) / 2) * a->kv_heads;
-  const int64_t shared = (a->tokens * group / kManyRows + (s->groups + 1) / 2) * a->kv_heads;
-  cut_keys(keys, few, 512, 256, &r.splits[0], &r.chunk[0]);
-  cut_keys(keys, many, 512, 256, &r.splits[1], &r.chunk[1]);
-  cut_keys(prefix, shared, 512, 256, &r.splits[2], &r.chunk[2]);
+  const int64_t shared = (r.prefix_few ? s->groups : s->groups == 1 ? r.prefix_tiles : a->tokens * group / kManyRows + (s->groups + 1) / 2) * a->kv_heads;
+  cut_keys(keys, few, kSlots, 256, &r.splits[0], &r.chunk[0]);
+  cut_keys(keys, many, kSlots, 256, &r.splits[1], &r.chunk[1]);
+  // The prefixes' tiles begin first; an eighth of the slots is left for the single tokens'
+  // own keys to run beside them (64 sequences on 32768 keys, 64 heads of 8: 14 parts 112 to
+  // 116 us, 16, which fill the slots, 119 to 122, 8, which fill half of them, 118). Both
+  // in turn from the start was slower: the tiles then end late (125 to 146 us).
+  cut_keys(prefix, shared, r.many || r.prefix_few ? kSlots : kSlots / 8 * 7, 256, &r.splits[2],
+           &r.chunk[2]);
   if (!r.few) r.splits[0] = 0;
   if (!r.many) r.splits[1] = 0;
   if (!s->groups) r.splits[2] = 0;
   r.rows = a->tokens * a->heads;
   r.part_rows = (std::max(r.splits[0], r.splits[1]) + r.splits[2]) * r.rows;
   r.ws_bytes = (size_t)r.part_rows * (size_t)(a->head_dim + 2) * sizeof(float);
-  r.blocks[0] = r.prefix_tiles * a->kv_heads * r.splits[2];
+  r.blocks[0] = (r.prefix_few ? s->groups : r.prefix_tiles) * a->kv_heads * r.splits[2];
   r.blocks[1] = r.tiles * a->kv_heads * r.splits[1];
   r.blocks[2] = few * r.splits[0];
   return r;
 }
 
+template <class T, int D, int Prefix>
+int launch_shared(const SharedPlan& r, const SharedParams& p, hipStream_t stream) {
+  const dim3 grid((unsigned)(r.blocks[0] + r.blocks[1] + r.blocks[2]));
+  if (r.few && r.many) return launch(shared_kernel<T, D, Prefix, true, true>, grid, kThreads, p, stream);
+  if (r.many) return launch(shared_kernel<T, D, Prefix, false, true>, grid, kThreads, p, stream);
+  return launch(shared_kernel<T, D, Prefix, true, false>, grid, kThreads, p, stream);
+}
+
 template <class T, int D>
 int run_shared(const SharedPlan& r, const SharedParams& p, hipStream_t stream) {
-  const int64_t blocks = r.blocks[0] + r.blocks[1] + r.blocks[2];
   constexpr int kRows = kThreads / (D / 4);
   const int64_t joins = (int64_t)p.tokens * ((p.heads + kRows - 1) / kRows);
-  const int st = launch(shared_kernel<T, D>, dim3((unsigned)blocks), kThreads, p, stream);
+  const int st = !r.blocks[0] ? launch_shared<T, D, kNoPrefix>(r, p, stream)
+                 : r.prefix_few ? launch_shared<T, D, kFewPrefix>(r, p, stream)
+                                : launch_shared<T, D, kManyPrefix>(r, p, stream);
   return st ? st : launch(join_kernel<T, D>, dim3((unsigned)joins), kThreads, p, stream);
 }
 
@@ -338,8 +382,8 @@ extern "C" int lutgemm_shared_attention(const lutgemm_shared* s, const void* d_q
     p.prefix_chunk = r.chunk[2];
     p.groups = s->groups;
     p.prefix_tiles = (int32_t)r.prefix_tiles;
-    p.prefix_blocks = (int32_t)r.blocks[0];
-    p.many_blocks = (int32_t)r.blocks[1];
+    p.prefix_few = r.prefix_few ? 0x7FFFFFFF : 0;
+    for (int i = 0; i < 3; ++i) p.blocks[i] = (int32_t)r.blocks[i];
     p.few_rows = !r.many ? 0x7FFFFFFF : r.few ? kFewRows : 0;
     p.tiles = (int32_t)r.tiles;
     p.scale2 = a->scale * 1.4426950408889634f;
