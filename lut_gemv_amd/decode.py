@@ -21,6 +21,15 @@ What is modelled and what is not:
     over the cache, and the output projection reads its result. By default
     there is no cache, and the output projection reads the first d entries of the
     QKV output in place of the attention output;
+  * with ``prefix`` > 0 the first so many keys of every sequence are one prefix of all, in
+    the cache once, and the attention reads it once for all;
+  * with ``room`` > 0 the cache has room for at least so many steps, in whole pages: each
+    step's page tables, slots and positions are made on the GPU from the lengths, and a
+    replayed step goes on where the one before ended, until the room is full (then its
+    rows are left as they were).
+    By default every step appends the same token;
+  * with ``sample`` the step ends with a product of the vocabulary's size and the draw of
+    the next tokens; the token drawn is not the next step's input, which stays synthetic;
   * with ``adapters`` > 0 every projection has that many low-rank adapters, and
     sequence i uses adapter i modulo their number;
   * activation functions, layer norms and residual additions are left out: the
@@ -45,10 +54,10 @@ from typing import Dict, List, Optional, Tuple
 
 import numpy as np
 
-from . import (PackedBCQ, adapters_add, packed_sizes, paged_attention, qk_norm_rotate,
-               rotary_table)
+from . import (PackedBCQ, adapters_add, batch_tables, packed_sizes, paged_attention, qk_norm_rotate,
+               rotary_table, sample_tokens, shared_prefix_attention)
 
-__all__ = ["MODELS", "Projection", "DecodeStack", "weight_bytes_per_step", "main"]
+__all__ = ["MODELS", "VOCABULARY", "Projection", "DecodeStack", "weight_bytes_per_step", "main"]
 
 
 @dataclass(frozen=True)
@@ -83,6 +92,8 @@ MODELS: Dict[str, Tuple[int, List[Projection], str]] = {
     "llama65b": (80, _llama(8192, 22016), "down"),
 }
 
+VOCABULARY = {"opt175b": 50272, "llama7b": 32000, "llama65b": 32000}
+
 HEAD_DIM = 128                     # of every model's attention heads
 ROTATED = {"llama7b", "llama65b"}  # models that rotate queries and keys by position
 
@@ -105,7 +116,7 @@ class DecodeStack:
     def __init__(self, model: str, layers: Optional[int] = None, q: int = 3, g: int = 128,
                  m: int = 1, seed: int = 0, device: str = "cuda:0", keep_logical: bool = False,
                  log=None, context: int = 0, page_size: int = 64, adapters: int = 0,
-                 rank: int = 16):
+                 rank: int = 16, prefix: int = 0, room: int = 0, sample: bool = False):
         import torch
         import workloads
 
@@ -119,6 +130,9 @@ class DecodeStack:
         self.context, self.adapters = int(context), int(adapters)
         if self.context < 0 or self.adapters < 0:
             raise ValueError("context and adapters must be >= 0")
+        self.prefix, self.room = int(prefix), int(room)
+        if not 0 <= self.prefix <= self.context or self.room < 0 or (self.room and not self.context):
+            raise ValueError("prefix must be in [0, context], room >= 0 and 0 without a context")
         self.projs, self.out_name, self.device = projs, out_name, device
         self.logical = {}
         protos = {}
@@ -156,29 +170,65 @@ class DecodeStack:
         self.lora = []        # per layer: projection name -> (a, b)
         if self.adapters:
             self._make_adapters(rank, seed)
+        self.head = None
+        if sample:
+            N, sigma = VOCABULARY[model], 1.0 / np.sqrt(self.q * d_model)
+            w = workloads.random_bcq(N, d_model, self.q, self.g, self.m, seed=seed + 104729, sigma=sigma,
+                                     name=f"{model}_head")
+            self.head = PackedBCQ.from_bcq(w.bits, w.alpha, None, self.g, device=device)
+            self.logits = torch.empty((self.m, N), dtype=torch.float16, device=device)
+            gen = torch.Generator(device=device).manual_seed(seed + 2)
+            self.u = torch.rand((self.m,), generator=gen, device=device)
+            self.temperature = torch.full((self.m,), 0.8, device=device)
+            self.top_p = torch.full((self.m,), 0.95, device=device)
+            self.tokens = torch.empty((self.m,), dtype=torch.int64, device=device)
+            self.logprobs = None
+            if log:
+                log(f"packed the head {N}x{d_model}")
         self.graph = None
         self.graph_kernel = None
 
     def _make_caches(self, d_model: int, page_size: int, seed: int):
-        """A paged cache a layer that holds `context` keys of every sequence, their pages
-        in any order, with room for the token that a step appends."""
+        """A paged cache a layer that holds `context` keys of every sequence, the prefix's once,
+        their pages in any order, with room for the tokens that the steps append."""
         import torch
         gen = torch.Generator(device=self.device).manual_seed(seed)
         self.heads = d_model // HEAD_DIM
-        each = -(-(self.context + 1) // page_size)
-        shape = (self.m * each, page_size, self.heads, HEAD_DIM)
+        at = self.context - self.prefix            # a sequence's own keys before the step
+        steps = max(1, self.room)
+        each = -(-(at + steps) // page_size)
+        shared = -(-self.prefix // page_size)
+        shape = (self.m * each + shared, page_size, self.heads, HEAD_DIM)
         for _ in range(self.layers):
             self.caches.append(tuple(
                 torch.randn(shape, generator=gen, device=self.device).to(torch.float16)
                 for _ in range(2)))
-        order = torch.randperm(self.m * each, generator=gen, device=self.device)
-        table = order.view(self.m, each)
+        order = torch.randperm(shape[0], generator=gen, device=self.device)
+        table = order[:self.m * each].view(self.m, each)
         self.page_table = table.to(torch.int32)
-        at = self.context
-        self.positions = torch.full((self.m,), at, dtype=torch.int64, device=self.device)
-        self.slots = (table[:, at // page_size] * page_size + at % page_size).contiguous()
-        self.kv_lens = torch.full((self.m,), at + 1, dtype=torch.int32, device=self.device)
-        self.rotary = (rotary_table(at + 1, HEAD_DIM, device=self.device)
+        if self.prefix:
+            self.prefix_table = order[self.m * each:].view(1, shared).to(torch.int32)
+            self.prefix_lens = torch.full((1,), self.prefix, dtype=torch.int32, device=self.device)
+        self.max_kv = each * page_size if self.room else at + 1
+        if self.room:
+            # the pages behind each sequence's keys are free
+            held = -(-at // page_size)
+            self.free_pages = self.page_table[:, held:].reshape(-1).contiguous()
+            count = self.free_pages.numel()
+            self.free_pages = torch.cat([self.free_pages, self.page_table.new_zeros(1)])  # at least one
+            self.free_range = torch.tensor([0, count], dtype=torch.int32, device=self.device)
+            self.page_table[:, held:] = -1
+            self.change = torch.ones((self.m,), dtype=torch.int32, device=self.device)
+            self.offsets = torch.full((self.m,), self.prefix, dtype=torch.int32, device=self.device)
+            self.kv_lens = torch.full((self.m,), at, dtype=torch.int32, device=self.device)
+            self.page_size = page_size
+            self.q_starts = None
+        else:
+            self.positions = torch.full((self.m,), self.context, dtype=torch.int64, device=self.device)
+            self.slots = (table[:, at // page_size] * page_size + at % page_size).contiguous()
+            self.kv_lens = torch.full((self.m,), at + 1, dtype=torch.int32, device=self.device)
+            self.q_starts = None
+        self.rotary = (rotary_table(self.prefix + self.max_kv, HEAD_DIM, device=self.device)
                        if self.model in ROTATED else None)
         self.queries = torch.empty((self.m, self.heads, HEAD_DIM), dtype=torch.float16,
                                    device=self.device)
@@ -206,7 +256,15 @@ class DecodeStack:
         """Bytes of keys and values that one decode step's attention reads (all layers)."""
         if not self.context:
             return 0
-        return self.layers * self.m * (self.context + 1) * 2 * self.heads * HEAD_DIM * 2
+        keys = self.prefix + self.m * (self.context - self.prefix + 1)
+        return self.layers * keys * 2 * self.heads * HEAD_DIM * 2
+
+    def head_bytes_per_step(self) -> int:
+        """Packed bytes of the head's weights that a step reads, and its logits."""
+        if self.head is None:
+            return 0
+        nb, na, _ = packed_sizes(self.head.N, self.head.K, self.q, self.g, False)
+        return nb + 2 * na + 2 * self.logits.numel()
 
     def adapter_bytes_per_step(self) -> int:
         """Bytes of the adapters that one decode step's sequences use (all layers)."""
@@ -215,9 +273,10 @@ class DecodeStack:
                    for lw in self.lora for p in self.projs for a in lw[p.name][:1])
 
     def read_bytes_per_step(self) -> int:
-        """All that one decode step reads: packed weights, cache and adapters."""
+        """All that one decode step reads: packed weights, cache, adapters and head (with
+        ``room``, the cache as it is before the first step)."""
         return (self.bytes_per_step() + self.cache_bytes_per_step()
-                + self.adapter_bytes_per_step())
+                + self.adapter_bytes_per_step() + self.head_bytes_per_step())
 
     # ------------------------------------------------------------ one token
     def _src(self, p: Projection, x_layer):
@@ -231,14 +290,37 @@ class DecodeStack:
         k_pages, v_pages = self.caches[layer]
         qk_norm_rotate(self.outs["qkv"], self.heads, self.heads, self.positions, self.rotary,
                        k_pages=k_pages, v_pages=v_pages, slots=self.slots, out=self.queries)
-        paged_attention(self.queries, k_pages, v_pages, self.page_table, self.kv_lens,
-                        max_kv=self.context + 1,
-                        out=self.attended.view(self.m, self.heads, HEAD_DIM))
+        out = self.attended.view(self.m, self.heads, HEAD_DIM)
+        if self.prefix:
+            shared_prefix_attention(self.queries, k_pages, v_pages, self.prefix_table, self.prefix_lens,
+                                    self.page_table, self.kv_lens, self.q_starts, max_q=1,
+                                    max_kv=self.max_kv, max_prefix=self.prefix, out=out)
+        else:
+            paged_attention(self.queries, k_pages, v_pages, self.page_table, self.kv_lens, self.q_starts,
+                            max_q=1, max_kv=self.max_kv, out=out)
+
+    def _advance(self):
+        """This step's positions and slots, from the lengths that the last one left."""
+        self.positions, self.slots, _, self.q_starts, _ = batch_tables(
+            self.change, self.kv_lens, self.page_table, self.page_size, self.m, self.free_pages,
+            self.free_range, self.offsets, in_place=True)
+
+    def _sample(self, kernel: str):
+        """The next tokens, from the last layer's output."""
+        x = self.outs[self.out_name]
+        if kernel == "lut":
+            self.head(x, out=self.logits)
+        else:
+            self.head.dequant(x, out=self.logits)
+        _, self.logprobs = sample_tokens(self.logits, self.u, self.temperature, top_p=self.top_p,
+                                         out=self.tokens)
 
     def token(self, kernel: str = "lut"):
         """Run every product of every layer once, in order, on the current stream.
         The layer output is the next layer's input; returns the last output (a
         buffer the next token overwrites)."""
+        if self.room:
+            self._advance()
         x_layer = self.x
         for l, lw in enumerate(self.weights):
             for p in self.projs:
@@ -260,12 +342,15 @@ class DecodeStack:
             # the next layer reads this output in place: its first product runs
             # before this buffer is written again
             x_layer = self.outs[self.out_name]
+        if self.head is not None:
+            self._sample(kernel)
         return self.outs[self.out_name]
 
     def capture(self, kernel: str = "lut"):
         """Capture one token into a HIP graph. An eager token runs first on the
         capture stream, so the split-K workspaces (one per stream) are set up
-        outside the capture and the graph reuses them."""
+        outside the capture and the graph reuses them (with ``room``, that is one of its
+        steps)."""
         import torch
         cs = torch.cuda.Stream()
         cs.wait_stream(torch.cuda.current_stream())
@@ -360,6 +445,12 @@ def main(argv=None) -> int:
     ap.add_argument("--page-size", type=int, default=64)
     ap.add_argument("--adapters", type=int, default=0, help="low-rank adapters of every projection")
     ap.add_argument("--rank", type=int, default=16)
+    ap.add_argument("--prefix", type=int, default=0,
+                    help="of the context, the keys that all sequences share")
+    ap.add_argument("--room", type=int, default=0,
+                    help="steps for which the cache has room, tables made on the GPU; 0: every step "
+                         "appends the same token")
+    ap.add_argument("--sample", action="store_true", help="end the step with the head and the draw of tokens")
     ap.add_argument("--breakdown", action="store_true",
                     help="also time each projection on its own (us per GEMV)")
     a = ap.parse_args(argv)
@@ -371,14 +462,16 @@ def main(argv=None) -> int:
     t0 = time.perf_counter()
     st = DecodeStack(a.model, a.layers, a.q, a.g, a.m,
                      log=lambda msg: print(f"[decode] {msg}", flush=True), context=a.context,
-                     page_size=a.page_size, adapters=a.adapters, rank=a.rank)
+                     page_size=a.page_size, adapters=a.adapters, rank=a.rank, prefix=a.prefix,
+                     room=a.room, sample=a.sample)
     torch.cuda.synchronize()
     setup_s = time.perf_counter() - t0
     print(f"[decode] {a.model}: {st.layers} layers, {st.bytes_per_step() / 1e9:.2f} GB packed "
           f"weights, set up in {setup_s:.1f} s", flush=True)
     res = {}
     kernels = ["lut", "dequant"] if a.kernel == "both" else [a.kernel]
-    read = ", ".join(["weights"] + ["cache"] * bool(a.context) + ["adapters"] * bool(a.adapters))
+    read = ", ".join(["weights"] + ["cache"] * bool(a.context) + ["adapters"] * bool(a.adapters)
+                     + ["head"] * a.sample)
     for k in kernels:
         r = st.time_tokens(k, a.tokens, a.warmup)
         y = st.outs[st.out_name]
@@ -400,11 +493,17 @@ def main(argv=None) -> int:
             st.layers * len(st.projs), "tokens": a.tokens, "results": res}
     if a.context:
         line.update(context=a.context, cache_bytes_per_step=st.cache_bytes_per_step())
+    if a.prefix:
+        line.update(prefix=a.prefix)
+    if a.room:
+        line.update(room=a.room)
+    if a.sample:
+        line.update(vocabulary=st.head.N, head_bytes_per_step=st.head_bytes_per_step())
     if a.adapters:
         line.update(adapters=a.adapters, rank=a.rank,
                     adapter_bytes_per_step=st.adapter_bytes_per_step())
     # the products' ratio: with a cache or adapters both steps hold the same time besides
-    if "lut" in res and "dequant" in res and not (a.context or a.adapters):
+    if "lut" in res and "dequant" in res and not (a.context or a.adapters or a.sample):
         line["dequant_over_lut"] = res["dequant"]["ms_per_step"] / res["lut"]["ms_per_step"]
     print(json.dumps(line), flush=True)
     return 0

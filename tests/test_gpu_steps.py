@@ -697,3 +697,122 @@ def test_sample_largest_value_late_and_at_ends():
                 part = x.to(dtype)[:, lo:lo + vocab].contiguous()
                 for more in (dict(), dict(top_p=[0.8] * 6), dict(top_k=[40] * 6), dict(min_p=[0.02] * 6)):
                     _sample_check(part, [0.1, 0.3, 0.5, 0.7, 0.9, 0.97], [0.9] * 6, logits=dev[:, lo:lo + vocab], **more)
+
+
+# ------------------------------------------------------------------- together
+
+def test_requests_on_a_shared_prefix_from_tables_to_tokens():
+    """Requests that share a system prompt: its keys once, then chunks of their own prompts and
+    single tokens, finished ones giving their pages back: tables, rotation and append, attention,
+    head product and draw against the plain forms on the keys appended so far."""
+    heads, kv, dim, page, vocab = 8, 2, 64, 16, 500
+    g = torch.Generator().manual_seed(0)
+    rope = lg.rotary_table(400, dim, device=DEV)
+    pages, width = 60, 9
+    k_pages, v_pages = (torch.full((pages, page, kv, dim), NAN, dtype=F16, device=DEV) for _ in range(2))
+    head = (torch.randn((heads * dim, vocab), generator=g) * 0.2).to(F16).to(DEV)
+    prefix = 37
+    # the prefix by one step of its own
+    ring, free = _int(np.random.default_rng(0).permutation(pages).tolist()), _int([50, pages])
+    ptable, plen = _int([[-1] * 5]), _int([0])
+    pos, slots, plen, starts, free = lg.batch_tables(_int([prefix]), plen, ptable, page, prefix, ring, free)
+    assert plen.tolist() == [prefix] and pos.tolist() == list(range(prefix))
+    qkv = torch.randn((prefix, (heads + 2 * kv) * dim), generator=g).to(F16).to(DEV)
+    q = lg.qk_norm_rotate(qkv, heads, kv, pos, rope, k_pages=k_pages, v_pages=v_pages, slots=slots)
+    lg.paged_attention(q, k_pages, v_pages, ptable, plen, starts)
+
+    def keys(table, n):
+        rows = table[:-(-n // page)].long()
+        return [_np(t[rows].flatten(0, 1)[:n]) for t in (k_pages, v_pages)]
+
+    want_prefix = keys(ptable[0], prefix)
+    assert all(np.isfinite(t).all() for t in want_prefix)
+    table = torch.full((3, width), -1, dtype=torch.int32, device=DEV)
+    lens, offsets = _int([0, 0, 0]), _int([prefix] * 3)
+    host = [0, 0, 0]
+    for step, change in enumerate([[30, 1, 7], [1, 1, 1], [1, -2, 20], [2, 3, 1], [-33, 1, 1], [5, 1, -10]]):
+        tokens = 40
+        pos, slots, lens, starts, free = lg.batch_tables(_int(change), lens, table, page, tokens, ring, free, offsets)
+        at = starts.tolist()
+        for r, c in enumerate(change):
+            assert pos[at[r]:at[r + 1]].tolist() == list(range(prefix + host[r], prefix + host[r] + max(c, 0)))
+            host[r] = max(0, host[r] + c)
+        assert lens.tolist() == host
+        qkv = torch.randn((tokens, (heads + 2 * kv) * dim), generator=g).to(F16).to(DEV)
+        q = lg.qk_norm_rotate(qkv, heads, kv, pos, rope, k_pages=k_pages, v_pages=v_pages, slots=slots)
+        o = lg.shared_prefix_attention(q, k_pages, v_pages, ptable, plen, table, lens, starts)
+        x = _np(qkv).reshape(tokens, heads + 2 * kv, dim)
+        for r, c in enumerate(change):
+            if c <= 0:
+                continue
+            rows = slice(at[r], at[r + 1])
+            ks, vs = keys(table[r], host[r])
+            assert np.array_equal(vs[-c:], x[rows, heads + kv:])
+            ks, vs = np.concatenate([want_prefix[0], ks]), np.concatenate([want_prefix[1], vs])
+            want, bound = plain.attention(_np(q[rows]), ks, vs, c, prefix + host[r], dim ** -0.5, 0, U[F16])
+            assert (np.abs(_np(o[rows]) - want) <= bound).all(), (step, r)
+        live = [r for r, c in enumerate(change) if c > 0]
+        last = torch.tensor([at[r + 1] - 1 for r in live], device=DEV)
+        logits = o[last].reshape(len(live), -1) @ head
+        u = [(0.37 * (step + 1) + 0.21 * r) % 1 for r in live]
+        _sample_check(logits.cpu(), u, [0.7] * len(live), top_p=[0.9] * len(live))
+    # what the requests hold and what is free are all pages, once each
+    used = ptable[0, :3].tolist() + [p for r in range(3) for p in table[r, :-(-host[r] // page)].tolist()]
+    first, count = free.tolist()
+    assert sorted(used + [ring[(first + i) % pages].item() for i in range(count)]) == list(range(pages))
+
+
+@pytest.mark.parametrize("model,prefix", [("llama7b", 70), ("llama7b", 0), ("opt175b", 64)])
+def test_decode_stack_steps_forward(model, prefix):
+    """Captured steps on a cache with room: each appends the next token of every sequence, attends
+    over prefix and own keys, and draws a token; when the room is full nothing moves any more."""
+    from lut_gemv_amd import decode
+    layers = 2 if model == "llama7b" else 1
+    st = decode.DecodeStack(model, layers=layers, q=2, g=128, m=3, device=DEV, context=100, page_size=16,
+                            prefix=prefix, room=6, sample=True)
+    heads, own = st.heads, 100 - prefix
+    room = -(-(own + 6) // 16) * 16      # whole pages
+    graph = st.capture()                 # an eager step: the first
+    held = st.page_table.clone()
+    for step in range(1, room - own + 2):
+        st.u.copy_(_int([0.1 * step % 1, 0.5, 0.9], F32))
+        before = st.attended.clone()
+        graph.replay()
+        torch.cuda.synchronize()
+        n = min(own + step + 1, room)
+        assert st.kv_lens.tolist() == [n] * 3
+        if own + step >= room:
+            assert torch.equal(st.attended, before) and st.slots.tolist() == [-1] * 3
+            continue
+        assert st.positions.tolist() == [100 + step] * 3
+        k_pages, v_pages = st.caches[-1]
+        pk, pv = ([], []) if not prefix else ([t[st.prefix_table[0].long()].flatten(0, 1)[:prefix]] for t in
+                                             (k_pages, v_pages))
+        for i in range(3):
+            rows = st.page_table[i, :-(-n // 16)].long()
+            ks, vs = (torch.cat(a + [t[rows].flatten(0, 1)[:n]]) for a, t in ((pk, k_pages), (pv, v_pages)))
+            want, bound = plain.attention(_np(st.queries[i:i + 1]), _np(ks), _np(vs), 1, prefix + n, 128 ** -0.5, 0,
+                                          U[F16])
+            got = _np(st.attended.view(3, heads, 128)[i:i + 1])
+            assert (np.abs(got - want) <= bound).all(), (step, i)
+            qkv = _np(st.outs["qkv"][i]).reshape(3 * heads, 128)
+            assert np.array_equal(_np(vs[-1]), qkv[2 * heads:])
+        logits = st.head(st.outs[st.out_name])
+        assert torch.equal(logits, st.logits)
+        for i in range(3):
+            token, logprob, margin = plain.sample(_np(logits[i]), float(st.u[i]), float(st.temperature[i]), 0,
+                                                  float(st.top_p[i]))
+            if margin >= _margin(logits.shape[1]):
+                assert int(st.tokens[i]) == token
+                assert abs(float(st.logprobs[i]) - logprob) <= 2.0 ** -24 * abs(logprob) + _margin(logits.shape[1])
+    assert (st.page_table >= 0).sum() >= (held >= 0).sum()
+
+
+def test_decode_rate_counts_prefix_and_head():
+    from lut_gemv_amd import decode
+    st = decode.DecodeStack("llama7b", layers=1, q=2, g=128, m=3, device=DEV, page_size=16, context=100, prefix=60,
+                            sample=True)
+    nb, na, _ = lg.packed_sizes(32000, 4096, 2, 128, False)
+    read = st.bytes_per_step() + (60 + 3 * 41) * 2 * 4096 * 2 + nb + 2 * na + 2 * 3 * 32000
+    r = st.time_tokens(tokens=2, warmup=1)
+    assert r["GBps"] == pytest.approx(read / (r["ms_per_step"] * 1e-3) / 1e9, rel=1e-9)

@@ -260,3 +260,11 @@ def test_plain_tables_keep_every_page_once():
         used = [p for s in range(seqs) for p in table[s][:-(-lens[s] // page)]]
         rest = [ring[(free[0] + i) % pages] for i in range(free[1])]
         assert sorted(used + rest) == list(range(pages))
+
+
+def test_decode_stack_arguments():
+    from lut_gemv_amd import decode
+    for kw in (dict(prefix=1), dict(context=10, prefix=11), dict(context=10, prefix=-1), dict(room=3),
+               dict(context=10, room=-1)):
+        with pytest.raises(ValueError, match="prefix must be"):
+            decode.DecodeStack("llama7b", layers=1, device="cpu", **kw)
