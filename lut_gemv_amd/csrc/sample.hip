@@ -355,8 +355,10 @@ template <class T>
 __global__ __launch_bounds__(kThreads, 8) void chunk_kernel(SampleParams p) {
   typedef Piece<T> P;
   __shared__ __attribute__((aligned(256))) double steps[kSteps];
-  __shared__ uint64_t sums[kBins + 1];  // the last: what is not counted
-  __shared__ uint32_t counts[kBins + 1];
+  // bin b is entry kLast - b; behind the bins there is room for values that have no weight
+  constexpr int kLast = kBins + 31;
+  __shared__ uint64_t sums[kLast + 1];
+  __shared__ uint32_t counts[kLast + 1];
   __shared__ float waves[kWaves];
   __shared__ int32_t first;
   fetch(p);
@@ -373,8 +375,8 @@ __global__ __launch_bounds__(kThreads, 8) void chunk_kernel(SampleParams p) {
   const Settings set(p, r);
   // while the loads are under way
   if (t < kSteps) steps[t] = exp2((double)t / kSteps);
-  if (set.sums()) sums[t] = 0;
-  if (set.counts()) counts[t] = 0;
+  if (set.sums()) sums[kLast - t] = 0;
+  if (set.counts()) counts[kLast - t] = 0;
   if (t == 0) first = INT32_MAX;
   float most = -INFINITY;
   bool bad = false;
@@ -444,9 +446,9 @@ __global__ __launch_bounds__(kThreads, 8) void chunk_kernel(SampleParams p) {
         int k;
         const float x = T::wide(P::element(w[s], e));
         const uint64_t term = scale.term((double)x, steps, &k);
-        const int bin = x >= scale.least ? min(bin_of(k), kBins) : kBins;
-        if (with_sums) atomicAdd((unsigned long long*)&sums[bin], (unsigned long long)term);
-        if (with_counts) atomicAdd(&counts[bin], 1u);
+        const int at = x >= scale.least ? kLast - bin_of(k) : 0;
+        if (with_sums) atomicAdd((unsigned long long*)&sums[at], (unsigned long long)term);
+        if (with_counts) atomicAdd(&counts[at], 1u);
       }
     }
   };
@@ -459,8 +461,8 @@ __global__ __launch_bounds__(kThreads, 8) void chunk_kernel(SampleParams p) {
   else if (set.counts())
     fill(no, yes);
   __syncthreads();
-  if (set.sums()) ((uint64_t*)(record + kSumsAt))[t] = sums[t];
-  if (set.counts()) ((uint32_t*)(record + kCountsAt))[t] = counts[t];
+  if (set.sums()) ((uint64_t*)(record + kSumsAt))[t] = sums[kLast - t];
+  if (set.counts()) ((uint32_t*)(record + kCountsAt))[t] = counts[kLast - t];
 }
 
 // ------------------------------------------------------------------ rows
@@ -743,7 +745,8 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
     auto bin_where = [&](bool passes) {
       if (t == 0) sh.found = kBins;
       __syncthreads();
-      if (passes) atomicMin(&sh.found, t);
+      const uint64_t votes = __ballot(passes);  // each lane by itself: 3 us
+      if (votes && lane == 0) atomicMin(&sh.found, wave * 64 + __builtin_ctzll(votes));
       __syncthreads();
       const int bin = sh.found;
       __syncthreads();
@@ -769,8 +772,8 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
       *term = scale.term((double)x, sh.steps, &k);
       return bin_of(k);
     };
-    // f(word, mask, first element) of every word that has tokens from `least` to `limit`, by
-    // whole waves
+    // f(word, masks, first element) of every word of a wave that has tokens from `least` to
+    // `limit`; mask e: the lanes whose element e is one
     auto words_from = [&](u4v (&w)[kAhead], float least, float limit, auto f) __attribute__((always_inline)) {
       const int stripes = row.wave_stripes();
       for (int s0 = 0; s0 < stripes; s0 += kAhead) {
@@ -780,15 +783,14 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
           u4v now = w[a];
           if (s0 + a + kAhead < stripes) w[a] = row.load(s0 + a + kAhead);
           row.place(now, s0 + a);
-          uint32_t some = 0;
+          uint64_t masks[P::kPer], some = 0;
 #pragma unroll
           for (int e = 0; e < P::kPer; ++e) {
             const float x = T::wide(P::element(now, e));
-            some |= (x >= least && x <= limit) << e;
+            masks[e] = __ballot(x >= least && x <= limit);
+            some |= masks[e];
           }
-          const int i0 = row.first(s0 + a);
-          if (i0 < row.lead) some &= ~1u;
-          if (__any(some)) f(now, some, i0);
+          if (some) f(now, masks, row.first(s0 + a));
         }
       }
     };
@@ -799,7 +801,10 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
     };
     // f(raw, index) of every token from `least` to `limit`
     auto each_from = [&](float least, float limit, auto f) __attribute__((always_inline)) {
-      each_word(least, limit, [&](const u4v& w, uint32_t some, int i0) {
+      each_word(least, limit, [&](const u4v& w, const uint64_t (&masks)[P::kPer], int i0) {
+        uint32_t some = 0;
+#pragma unroll
+        for (int e = 0; e < P::kPer; ++e) some |= (uint32_t)(masks[e] >> lane & 1) << e;
         for (; some; some &= some - 1) {
           const int e = __builtin_ctz(some);
           f(P::any(w, e), row.token(i0 + e));
@@ -811,14 +816,20 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
       __syncthreads();
       if (t == 0) *n = 0;
       __syncthreads();
-      words_from(first, least, limit, [&](const u4v& w, uint32_t some, int i0) {
-        const uint32_t mine = __popc(some), upto = wave_scan(mine);
-        uint32_t at = 0;
-        if (lane == 63) at = atomicAdd(n, upto);
-        at = lane_of(at, 63) + upto - mine;
-        for (; some; some &= some - 1, ++at) {
-          const int e = __builtin_ctz(some);
-          if (at < kList) list[at] = code_of<T>(P::any(w, e), row.token(i0 + e));
+      words_from(first, least, limit, [&](const u4v& w, const uint64_t (&masks)[P::kPer], int i0) {
+        uint32_t count = 0, at = 0;
+#pragma unroll
+        for (int e = 0; e < P::kPer; ++e) count += __popcll(masks[e]);
+        if (lane == 0) at = atomicAdd(n, count);
+        at = __builtin_amdgcn_readfirstlane(at);
+        if (at + count > kList) return;
+#pragma unroll
+        for (int e = 0; e < P::kPer; ++e) {
+          if (!masks[e]) continue;
+          const uint32_t before = __builtin_amdgcn_mbcnt_hi(
+              (uint32_t)(masks[e] >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)masks[e], 0));
+          if (masks[e] >> lane & 1) list[at + before] = code_of<T>(P::element(w, e), row.token(i0 + e));
+          at += __popcll(masks[e]);
         }
       });
       __syncthreads();
@@ -1137,13 +1148,16 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
                 is ? (int)(code & ((1u << kIndexBits) - 1)) / p.piece : 0);
           }
         } else {
-          each_word(least_of(chosen_bin), most_of(chosen_bin), [&](const u4v& w, uint32_t some, int i0) {
-            for (int e = 0; e < P::kPer; ++e) {
-              const bool is = some >> e & 1;
-              const int i = row.token(i0 + e);
-              add(is ? kept_term(code_of<T>(P::any(w, e), i)) : 0ull, is ? i / p.piece : 0);
-            }
-          });
+          each_word(least_of(chosen_bin), most_of(chosen_bin),
+                    [&](const u4v& w, const uint64_t (&masks)[P::kPer], int i0) {
+#pragma unroll
+                      for (int e = 0; e < P::kPer; ++e) {
+                        if (!masks[e]) continue;
+                        const bool is = masks[e] >> lane & 1;
+                        const int i = row.token(i0 + e);
+                        add(is ? kept_term(code_of<T>(P::element(w, e), i)) : 0ull, is ? i / p.piece : 0);
+                      }
+                    });
         }
         __syncthreads();
         // the first piece that passes the goal
