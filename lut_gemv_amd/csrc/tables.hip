@@ -5,7 +5,7 @@
 // walks the sequences a workgroup's width at a time with running sums of new rows, of pages
 // taken and of pages given back; a sequence's rows and pages then follow from its sums alone.
 // Sums saturate at 2^30, above every limit that they are compared with. Up to kFewRows rows
-// it also writes the rows, those of single tokens by the sequence's own thread; more
+// it also writes the rows, those of a few tokens by the sequence's own thread; more
 // are fill_kernel's, whose workgroups look for the sequences of their rows.
 #include "serve.h"
 
@@ -123,6 +123,7 @@ __device__ __forceinline__ void write_row(const TablesParams& p, int s, int row,
 template <int Threads>
 __global__ __launch_bounds__(Threads) void scan_kernel(TablesParams p) {
   __shared__ Sums waves[2][Threads / 64];
+  __shared__ int32_t of_row[Threads], of_len[Threads], of_ring[Threads];
   __shared__ uint32_t served_rows, served_pages;
   fetch(p);
   const int limit = p.width * p.page, lane = threadIdx.x & 63;
@@ -187,21 +188,41 @@ __global__ __launch_bounds__(Threads) void scan_kernel(TablesParams p) {
       const uint32_t at = (uint32_t)__builtin_amdgcn_readlane((int)(end.given - back), from);
       const int first = __builtin_amdgcn_readlane(held, from) - count;
       const int32_t* row = p.table + (int64_t)(s0 + (int)(threadIdx.x & ~63u) + from) * p.table_stride;
-      for (int j = lane; j < count; j += 64)
-        if (at + (uint32_t)j < room) p.ring[around(behind, at + (uint32_t)j, p.capacity)] = row[first + j];
+      constexpr int kTogether = 8;  // reads under way
+      for (int j0 = lane; j0 < count; j0 += 64 * kTogether) {
+        int32_t id[kTogether];
+#pragma unroll
+        for (int k = 0; k < kTogether; ++k) id[k] = row[first + min(j0 + 64 * k, count - 1)];
+#pragma unroll
+        for (int k = 0; k < kTogether; ++k) {
+          const uint32_t nth = at + (uint32_t)(j0 + 64 * k);
+          if (j0 + 64 * k < count && nth < room) p.ring[around(behind, nth, p.capacity)] = id[k];
+        }
+      }
     }
     if (all_rows) {
-      const int64_t offset = here && p.offsets && grow ? (int64_t)p.offsets[s] : 0;
-      if (grow && grow <= kOwnRows)
+      if (grow && grow <= kOwnRows) {
+        const int64_t offset = p.offsets ? (int64_t)p.offsets[s] : 0;
         for (int i = 0; i < (int)grow; ++i) write_row(p, s, first_row + i, n, held, taken, offset, i);
-      for (uint64_t more = __ballot(grow > kOwnRows); more; more &= more - 1) {
-        const int from = __builtin_ctzll(more);
-        auto of = [&](int v) { return __builtin_amdgcn_readlane(v, from); };
-        const int count = of((int)grow), row = of(first_row), len = of(n), pages = of(held), ring = of(taken);
-        const int64_t off = p.offsets ? (int64_t)of((int)offset) : 0;
-        const int seq = s0 + (int)(threadIdx.x & ~63u) + from;
-        for (int i = lane; i < count; i += 64) write_row(p, seq, row + i, len, pages, ring, off, i);
       }
+      of_row[threadIdx.x] = here && served ? first_row : INT32_MAX;
+      of_len[threadIdx.x] = n;
+      of_ring[threadIdx.x] = taken;
+      if (__syncthreads_or(grow > kOwnRows))
+        for (int row = (int)sums.rows + threadIdx.x; row < (int)served_rows; row += Threads) {
+          int a = 0, b = Threads;  // the sequence: the last one that begins here or before
+          while (b - a > 1) {
+            const int mid = (a + b) >> 1;
+            if (of_row[mid] <= row)
+              a = mid;
+            else
+              b = mid;
+          }
+          const int next = a + 1 < Threads ? min(of_row[a + 1], (int)served_rows) : (int)served_rows;
+          if (next - of_row[a] <= kOwnRows) continue;  // written already
+          write_row(p, s0 + a, row, of_len[a], (of_len[a] + p.page - 1) / p.page, of_ring[a],
+                    p.offsets ? (int64_t)p.offsets[s0 + a] : 0, row - of_row[a]);
+        }
     }
     sums.add(all);
   }

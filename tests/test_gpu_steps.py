@@ -380,6 +380,27 @@ def test_tables_long_prompts():
     _tables_check(change, lens, table, 32, 110100, ring, [0, 4000 - at])
 
 
+@pytest.mark.parametrize("tokens", [4096, 4097])
+def test_tables_prompts_beside_single_tokens(tokens):
+    """Rows of every kind of sequence in one launch and in two."""
+    rng = np.random.default_rng(tokens)
+    for seqs, big in ((1, 4000), (7, 500), (256, 40), (257, 30), (1500, 9)):
+        change = np.where(rng.random(seqs) < 0.3, big, rng.integers(-2, 6, seqs))
+        change[np.cumsum(change.clip(0)) > 4000] = -1
+        change[0] = min(big, 90)
+        lens = rng.integers(0, 200, seqs)
+        held = -(-lens // 16)
+        pages = int(held.sum()) + 4000
+        ids = rng.permutation(pages)
+        table = np.full((seqs, 280), -1, np.int32)
+        at = 0
+        for s in range(seqs):
+            table[s, :held[s]] = ids[at:at + held[s]]
+            at += held[s]
+        ring = np.concatenate([ids[at:], np.full(at, -1)]).astype(np.int32)
+        _tables_check(change, lens, table, 16, tokens, ring, [0, pages - at], rng.integers(0, 99, seqs).tolist())
+
+
 def test_tables_without_a_ring():
     change, lens, table, _, _ = _tables_case(40, 16, 200, 3)
     table = np.random.default_rng(3).permutation(table.size).astype(np.int32).reshape(table.shape)
