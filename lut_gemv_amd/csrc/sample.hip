@@ -303,18 +303,40 @@ __device__ __forceinline__ V wave_sum(V v) {
   return lane_of(wave_scan(v), 63);
 }
 
-// Sums of the threads before this one and itself, in order; *total: of all.
+// A wave's part of block_scan, before and after its sums are in LDS.
 template <class V>
-__device__ __forceinline__ V block_scan(V v, V* waves, V* total) {
+__device__ __forceinline__ V scan_join(V v, const V* waves, V* total) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  v = wave_scan(v);
-  __syncthreads();
-  if (lane == 63) waves[wave] = v;
-  __syncthreads();
   V sums = lane < kWaves ? waves[lane] : V(0);
   sums = wave_scan(sums);
   *total = lane_of(sums, 63);
   return wave ? v + lane_of(sums, wave - 1) : v;
+}
+
+// Sums of the threads before this one and itself, in order; *total: of all.
+template <class V>
+__device__ __forceinline__ V block_scan(V v, V* waves, V* total) {
+  v = wave_scan(v);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 63) waves[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return scan_join(v, waves, total);
+}
+
+// Of two values at once.
+template <class V, class W>
+__device__ __forceinline__ void block_scan(V* v, V* v_waves, V* v_total, W* w, W* w_waves) {
+  W ignored;
+  *v = wave_scan(*v);
+  *w = wave_scan(*w);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 63) {
+    v_waves[threadIdx.x >> 6] = *v;
+    w_waves[threadIdx.x >> 6] = *w;
+  }
+  __syncthreads();
+  *v = scan_join(*v, v_waves, v_total);
+  *w = scan_join(*w, w_waves, &ignored);
 }
 
 // A row's settings, and what they make of it.
@@ -582,6 +604,7 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
   // the pieces' heads, one to a lane
   Head head = {0.0, -INFINITY, 0, 0, 0};
   if (lane < p.pieces) head = *(const Head*)(records + lane * p.record);
+  if (t < kSteps) sh.steps[t] = exp2((double)t / kSteps);  // while they are under way
   float most = head.largest;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) most = fmaxf(most, __shfl_xor(most, d, 64));
@@ -600,7 +623,6 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
     }
     return;
   }
-  if (t < kSteps) sh.steps[t] = exp2((double)t / kSteps);
   Scale scale;
   scale.set(most, set.temperature);
   // octaves of the pieces' tops below the row's, 64 for those without weight
@@ -621,22 +643,21 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
     if (wave != part % kWaves) return;
     const u4v w = piece.word(part / kWaves);
     const int i0 = piece.first(part / kWaves);
-    auto weight_of = [&](int e) {
-      return piece.is_token(i0 + e) ? weight(P::any(w, e), piece.token(i0 + e)) : 0.0;
-    };
-    double sum = 0.0;
-#pragma unroll 1
-    for (int e = 0; e < P::kPer; ++e) sum += weight_of(e);
+    double v[P::kPer], sum = 0.0;
+#pragma unroll
+    for (int e = 0; e < P::kPer; ++e) {
+      v[e] = piece.is_token(i0 + e) ? weight(P::element(w, e), piece.token(i0 + e)) : 0.0;
+      sum += v[e];
+    }
     double cursor = wave_scan(sum) - sum;
     int token = -1, last = -1;
     float value = 0.f, last_value = 0.f;
-#pragma unroll 1
+#pragma unroll
     for (int e = 0; e < P::kPer; ++e) {
-      const double v = weight_of(e);
-      cursor += v;
-      if (!(v > 0.0)) continue;
+      cursor += v[e];
+      if (!(v[e] > 0.0)) continue;
       last = piece.token(i0 + e);
-      last_value = T::wide(P::any(w, e));
+      last_value = T::wide(P::element(w, e));
       if (token < 0 && cursor > goal) {
         token = last;
         value = last_value;
@@ -731,26 +752,27 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
     const uint64_t mine = shifted(sum, S - 40 + octave);
     uint64_t all_sum = 0, upto = 0;
     uint32_t all_count = 0, upto_count = 0;
-    float bound = 0.f, upto_bound = 0.f, ignored;
+    float upto_bound = 0.f;
     if (set.counts()) upto_count = block_scan(count, sh.waves, &all_count);
     if (set.sums()) {
-      upto = block_scan(mine, sh.qwaves, &all_sum);
       // a bin's terms are its lower edge's 2^40 m or up to a sixteenth of an octave more, so
       // their sum bounds their number
-      bound = (float)sum * __builtin_amdgcn_exp2f(-40.f - (float)(-t & 15) * 0.0625f) * 1.01f + 1.f;
-      upto_bound = block_scan(bound, (float*)sh.waves, &ignored);
+      upto = mine;
+      upto_bound = (float)sum * __builtin_amdgcn_exp2f(-40.f - (float)(-t & 15) * 0.0625f) * 1.01f + 1.f;
+      block_scan(&upto, sh.qwaves, &all_sum, &upto_bound, (float*)sh.waves);
     }
 
-    // the first bin whose sum or count from the top passes what is asked for, kBins if none
-    auto bin_where = [&](bool passes) {
+    // the bin of the thread that says so, which leaves what `then` writes; kBins if none does
+    auto bin_where = [&](bool here, auto then) {
+      __syncthreads();
       if (t == 0) sh.found = kBins;
       __syncthreads();
-      const uint64_t votes = __ballot(passes);  // each lane by itself: 3 us
-      if (votes && lane == 0) atomicMin(&sh.found, wave * 64 + __builtin_ctzll(votes));
+      if (here) {
+        sh.found = t;
+        then();
+      }
       __syncthreads();
-      const int bin = sh.found;
-      __syncthreads();
-      return bin;
+      return sh.found;
     };
     // a value that no token of the bins up to this one is below
     auto least_of = [&](double bin) {
@@ -772,8 +794,8 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
       *term = scale.term((double)x, sh.steps, &k);
       return bin_of(k);
     };
-    // f(word, masks, first element) of every word of a wave that has tokens from `least` to
-    // `limit`; mask e: the lanes whose element e is one
+    // f(word, in, first element) of every word of a wave that has tokens from `least` to
+    // `limit`; in[e]: whether the lane's element e is one
     auto words_from = [&](u4v (&w)[kAhead], float least, float limit, auto f) __attribute__((always_inline)) {
       const int stripes = row.wave_stripes();
       for (int s0 = 0; s0 < stripes; s0 += kAhead) {
@@ -783,14 +805,14 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
           u4v now = w[a];
           if (s0 + a + kAhead < stripes) w[a] = row.load(s0 + a + kAhead);
           row.place(now, s0 + a);
-          uint64_t masks[P::kPer], some = 0;
+          bool in[P::kPer], some = false;
 #pragma unroll
           for (int e = 0; e < P::kPer; ++e) {
             const float x = T::wide(P::element(now, e));
-            masks[e] = __ballot(x >= least && x <= limit);
-            some |= masks[e];
+            in[e] = x >= least && x <= limit;
+            some |= in[e];
           }
-          if (some) f(now, masks, row.first(s0 + a));
+          if (__any(some)) f(now, in, row.first(s0 + a));
         }
       }
     };
@@ -799,37 +821,40 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
       first_words(w);
       words_from(w, least, limit, f);
     };
+    // that as one word
+    auto bits_of = [&](const bool (&in)[P::kPer]) {
+      uint32_t bits = 0;
+#pragma unroll
+      for (int e = 0; e < P::kPer; ++e) bits |= in[e] ? 1u << e : 0;
+      return bits;
+    };
     // f(raw, index) of every token from `least` to `limit`
     auto each_from = [&](float least, float limit, auto f) __attribute__((always_inline)) {
-      each_word(least, limit, [&](const u4v& w, const uint64_t (&masks)[P::kPer], int i0) {
-        uint32_t some = 0;
-#pragma unroll
-        for (int e = 0; e < P::kPer; ++e) some |= (uint32_t)(masks[e] >> lane & 1) << e;
-        for (; some; some &= some - 1) {
-          const int e = __builtin_ctz(some);
+      each_word(least, limit, [&](const u4v& w, const bool (&in)[P::kPer], int i0) {
+        for (uint32_t bits = bits_of(in); bits; bits &= bits - 1) {
+          const int e = __builtin_ctz(bits);
           f(P::any(w, e), row.token(i0 + e));
         }
       });
     };
-    // their codes into a list; *n: how many there are, also where the list ends before
-    auto collect = [&](u4v (&first)[kAhead], float least, float limit, uint64_t* list, uint32_t* n) {
+    // their indices into a list; *n: how many there are, also where the list ends before
+    auto collect = [&](u4v (&first)[kAhead], float least, float limit, uint32_t* list, uint32_t* n) {
       __syncthreads();
       if (t == 0) *n = 0;
       __syncthreads();
-      words_from(first, least, limit, [&](const u4v& w, const uint64_t (&masks)[P::kPer], int i0) {
+      words_from(first, least, limit, [&](const u4v&, const bool (&in)[P::kPer], int i0) {
         uint32_t count = 0, at = 0;
 #pragma unroll
-        for (int e = 0; e < P::kPer; ++e) count += __popcll(masks[e]);
+        for (int e = 0; e < P::kPer; ++e) count += __popcll(__ballot(in[e]));
         if (lane == 0) at = atomicAdd(n, count);
+        uint32_t bits = bits_of(in);
         at = __builtin_amdgcn_readfirstlane(at);
         if (at + count > kList) return;
-#pragma unroll
-        for (int e = 0; e < P::kPer; ++e) {
-          if (!masks[e]) continue;
+        for (uint64_t some; (some = __ballot(bits != 0)) != 0; bits &= bits - 1) {
           const uint32_t before = __builtin_amdgcn_mbcnt_hi(
-              (uint32_t)(masks[e] >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)masks[e], 0));
-          if (masks[e] >> lane & 1) list[at + before] = code_of<T>(P::element(w, e), row.token(i0 + e));
-          at += __popcll(masks[e]);
+              (uint32_t)(some >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)some, 0));
+          if (bits) list[at + before] = (uint32_t)row.token(i0 + __builtin_ctz(bits));
+          at += __popcll(some);
         }
       });
       __syncthreads();
@@ -842,13 +867,17 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
     // The tokens of a bin into `inside`, those of the bins before it into `list`: by value
     // first, which may take some of the next bins.
     auto gather = [&](u4v (&first)[kAhead], int bin, bool before_too) {
-      collect(first, least_of(bin), before_too ? INFINITY : most_of(bin), sh.list, &sh.above);
+      collect(first, least_of(bin), before_too ? INFINITY : most_of(bin), (uint32_t*)sh.list, &sh.above);
       const uint32_t n = sh.above;
       uint64_t mine[kMine];
 #pragma unroll
       for (int j = 0; j < kMine; ++j) {
         const uint32_t i = t + j * kThreads;
-        mine[j] = i < n && n <= kList ? sh.list[i] : ~0ull;
+        mine[j] = ~0ull;
+        if (i < n && n <= kList) {  // read again: by the collecting lanes 3 us more
+          const uint32_t at = ((const uint32_t*)sh.list)[i];
+          mine[j] = code_of<T>(logits[at], (int)at);
+        }
       }
       __syncthreads();
       if (t == 0) {
@@ -948,7 +977,11 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
     };
     uint64_t available = all_sum;  // what top_p takes its part of
     if (set.by_count) {
-      const int bin = bin_where(upto_count >= (uint32_t)set.top_k);
+      const uint32_t k = (uint32_t)set.top_k;
+      const int bin = bin_where(upto_count >= k && upto_count - count < k, [&] {
+        sh.found_count = (int)(upto_count - count);
+        sh.found_sum = upto - mine;
+      });
       if (bin == kBins) {  // fewer have weight: all of these
         if (set.few()) {
           collect_counted(least_of(kBins - 1), 0.0);
@@ -956,11 +989,6 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
         }
       } else {
         last_bin = bin;
-        if (t == bin) {
-          sh.found_count = (int)(upto_count - count);
-          sh.found_sum = upto - mine;
-        }
-        __syncthreads();
         const uint64_t rest = (uint64_t)(set.top_k - sh.found_count);
         const uint64_t ahead = sh.found_sum;
         gather(first, bin, set.few());
@@ -1005,14 +1033,13 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
     if (set.by_weight && !listed && set.sums()) {
       uint64_t target = set.top_p > 0.f ? share(set.top_p, available, true) : 1;
       if (target < 1) target = 1;
-      int bin = bin_where(mine && upto >= target);
-      if (bin > last_bin) bin = last_bin;
-      last_bin = bin;
-      if (t == bin) {
+      // in the last bin that top_k leaves, if not before
+      const bool passes = mine && upto >= target && upto - mine < target;
+      const int bin = bin_where(t < last_bin ? passes : t == last_bin && upto - mine < target, [&] {
         sh.found_sum = upto - mine;
         sh.found_count = upto_bound < (float)kList;
-      }
-      __syncthreads();
+      });
+      last_bin = bin;
       const uint64_t ahead = sh.found_sum;
       const bool small = sh.found_count;
       if (set.by_count) first_words(first);
@@ -1044,7 +1071,8 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
       int k;
       double a, b;
       scale.factors((double)x, sh.steps, &k, &a, &b);
-      bool kept = x >= scale.least && bin_of(k) < kBins && (x > edge || (x == edge && i <= edge_last));
+      bool kept = x > edge || (x == edge && i <= edge_last);
+      if (border == ~0ull) kept = kept && x >= scale.least && bin_of(k) < kBins;
       if (set.by_least) kept = kept && a * __builtin_ldexp(b, k >> 5) >= least_weight;
       return kept ? Scale::by_value(a, b, k) : 0.0;
     };
@@ -1110,31 +1138,17 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
       uint64_t ahead = 0, goal = 0;
       const bool by_bins = chosen_bin >= 0 && set.sums() && !set.by_least;
       if (by_bins) {
-        // of each piece the sum of what is kept: a wave adds a piece's bins before the
-        // border's, and the border's own tokens are added by themselves
+        // of each piece the sum of what is kept: the border's own tokens are added by themselves, each
+        // lane to a word of its own (a wave's by piece 4 us more, all to one word 6), then
+        // a wave adds a piece's bins before the border's
         uint64_t* const kept = sh.sums[0];
+        uint64_t* const own = sh.list;  // [piece][lane]: of the border's bin
+        static_assert(kMostPieces * 64 <= kList, "a word to each lane of each piece");
         __syncthreads();
-        for (int c = wave; c < p.pieces; c += kWaves) {
-          const int by = __builtin_amdgcn_readlane(down, c);
-          uint64_t v = 0;
-          if (by < 64)
-            for (int bin = lane + 16 * by; bin < chosen_bin; bin += 64)
-              v += shifted(((const uint64_t*)(records + c * p.record + kSumsAt))[bin - 16 * by],
-                           S - 40 + octave_of(bin));
-          v = wave_sum(v);
-          if (lane == 0) kept[c] = v;
-        }
-        if (t < kMostPieces) kept[128 + t] = 0;
+        for (int i = t; i < 64 * p.pieces; i += kThreads) own[i] = 0;
         __syncthreads();
-        // a wave adds those of one piece at a time (by single tokens: 6 us for 1500 of them)
         auto add = [&](uint64_t term, int piece) {
-          for (uint64_t left = __ballot(term != 0); left;) {
-            const int c = __builtin_amdgcn_readlane(piece, __builtin_ctzll(left));
-            const bool mine = term && piece == c;
-            const uint64_t sum_c = wave_sum(mine ? term : 0ull);
-            if (lane == 0) atomicAdd((unsigned long long*)&kept[128 + c], (unsigned long long)sum_c);
-            left &= ~__ballot(mine);
-          }
+          if (term) atomicAdd((unsigned long long*)&own[piece * 64 + lane], (unsigned long long)term);
         };
         auto kept_term = [&](uint64_t code) {
           uint64_t term = 0;
@@ -1149,20 +1163,30 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
           }
         } else {
           each_word(least_of(chosen_bin), most_of(chosen_bin),
-                    [&](const u4v& w, const uint64_t (&masks)[P::kPer], int i0) {
+                    [&](const u4v& w, const bool (&in)[P::kPer], int i0) {
 #pragma unroll
                       for (int e = 0; e < P::kPer; ++e) {
-                        if (!masks[e]) continue;
-                        const bool is = masks[e] >> lane & 1;
+                        if (!in[e]) continue;
                         const int i = row.token(i0 + e);
-                        add(is ? kept_term(code_of<T>(P::element(w, e), i)) : 0ull, is ? i / p.piece : 0);
+                        add(kept_term(code_of<T>(P::element(w, e), i)), i / p.piece);
                       }
                     });
         }
         __syncthreads();
+        for (int c = wave; c < p.pieces; c += kWaves) {
+          const int by = __builtin_amdgcn_readlane(down, c);
+          uint64_t v = 0;
+          if (by < 64)
+            for (int bin = lane + 16 * by; bin < chosen_bin; bin += 64)
+              v += shifted(((const uint64_t*)(records + c * p.record + kSumsAt))[bin - 16 * by],
+                           S - 40 + octave_of(bin));
+          v = wave_sum(v) + shifted(wave_sum(own[c * 64 + lane]), S - 40 + octave_of(chosen_bin));
+          if (lane == 0) kept[c] = v;
+        }
+        __syncthreads();
         // the first piece that passes the goal
         uint64_t mine_c = 0;
-        if (lane < p.pieces) mine_c = kept[lane] + shifted(kept[128 + lane], S - 40 + octave_of(chosen_bin));
+        if (lane < p.pieces) mine_c = kept[lane];
         const uint64_t up = wave_scan(mine_c);
         total = lane_of(up, 63);
         goal = share(set.u, total, false) + 1;
@@ -1188,13 +1212,13 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
           piece.place(w[a], s0 + a);
           const int i0 = piece.first(s0 + a);
           double sum_s = 0.0;
-          float top = -INFINITY;
+          uint32_t bits = 0;
 #pragma unroll
-          for (int e = 0; e < P::kPer; ++e) top = fmaxf(top, T::wide(P::element(w[a], e)));
-          if (__any(top >= least)) {
-#pragma unroll
-            for (int e = 0; e < P::kPer; ++e)
-              sum_s += kept_value(T::wide(P::element(w[a], e)), offset + piece.token(i0 + e));
+          for (int e = 0; e < P::kPer; ++e)
+            bits |= (uint32_t)(T::wide(P::element(w[a], e)) >= edge) << e;
+          for (; bits; bits &= bits - 1) {
+            const int e = __builtin_ctz(bits);
+            sum_s += kept_value(T::wide(P::any(w[a], e)), offset + piece.token(i0 + e));
           }
           sum_s = wave_sum(sum_s);
           if (lane == 0) parts[(s0 + a) * kWaves + wave] = in_units(sum_s, 0);
