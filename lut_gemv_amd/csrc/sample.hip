@@ -4,21 +4,30 @@
 // All three filters keep the first tokens of one order (value falling, index rising), so
 // a row's kept tokens are those before one border: a value, and among the tokens that
 // have it an index. Borders and the drawn token follow from sums of weights, and of
-// 100000 tokens whose sums are off by 2^-24 the wrong one is taken in 1 of 100 rows.
-// So weights are computed in 64 bits, 2^y = m 2^e from a table of 2^(i/32), which lies across the
-// LDS banks once, and a polynomial, and all sums are integers, exact and the same in any order: by value, m 2^40 in
-// bins of a sixteenth of an octave, where the bin tells e; in the order of the tokens,
-// 2^S m 2^e with S = 62 - log2(vocab). Tokens below 2^-63 of the largest weight count as none.
+// 100000 tokens whose sums are off by 2^-24 the wrong one is taken in 1 of 100 rows. So
+// weights are computed in 64 bits, 2^y = m 2^e with m from a table of 2^(i/32), which lies across
+// the LDS banks once, and a polynomial, and rounded once, to 41 bits. Their sums are
+//   by value   m 2^40 as integers, in bins of a sixteenth of an octave, where the bin tells e:
+//              exact, and the same in any order
+//   by place   over the up to 512 tokens of a part (a wave's word of a stripe) in 64-bit
+//              floating point, always in one order and exact where the weights are equal; parts
+//              are summed as integers, 2^S of the largest weight, S = min(50, 62 - log2(vocab))
+//   of a list  as integers, 2^50 of the largest weight
+// Tokens below 2^-63 of the largest weight count as none.
 //
 // chunk_kernel takes a piece of a row to each workgroup and holds it in registers: its
 // largest value, and relative to that (brought up to a whole octave, so that the
-// pieces' bins and integers are each other's but for shifts) what the row's settings ask for:
-// the sums of the bins (top_p, large top_k), the numbers of tokens in them (top_k), or the sums
-// by place (no filter). row_kernel joins them, finds the bin of the border, reads the row
-// once more for the tokens of this bin and the ones above, and ends on these in LDS where
-// they are few (a radix select by weight, on 64-bit codes of value and index, then on
-// the index); where they are many, the bins' sums say in which piece the drawn token lies,
-// and only that is weighed again.
+// pieces' bins and sums are each other's but for shifts) what the row's settings ask for:
+// the sums of the bins (top_p, large top_k), the numbers of tokens in them (top_k), or the
+// sums of the parts (no filter). row_kernel, a workgroup to each row, joins them, finds the bin
+// of the border, reads the row once more for the tokens of this bin and the ones above, and
+// ends on these in LDS where they are few (a radix select by weight, on codes of value
+// and index, then on the index); where they are many, the bins' sums say in which piece the
+// drawn token lies, and only that is weighed again.
+//
+// Measured (bf16, 256 rows of 131073, top_p; 67 MB, 10.5 us at a copy's rate): 87 us;
+// fp16, 1 row of 50272 28 to 31 us, 48 rows of 32000 of all kinds 34; fp32, 61 rows of 128001
+// without a filter 21. The kernels say what bounds each.
 #include <algorithm>
 #include <type_traits>
 
@@ -57,8 +66,8 @@ struct SampleParams {
   int64_t* tokens;
   float* logprobs;
   char* ws;  // [row][piece] of kRecord bytes
-  int64_t row_step, record;
-  int32_t rows, vocab, pieces, piece, parts, scale;  // parts: of a piece; scale: S
+  int64_t row_step;
+  int32_t vocab, pieces, piece, parts, scale;  // parts: of a piece; scale: S
 };
 
 struct F32 {
@@ -197,7 +206,7 @@ struct Scale {
     *a = __builtin_fma(f, p, 1.0);
     *b = steps[*k & (kSteps - 1)];
   }
-  // As integers: in its bin's sum, m 2^40, and by place, m 2^(S + e).
+  // In its bin's sum: m 2^40.
   static __device__ __forceinline__ uint64_t by_term(double a, double b) {
     constexpr double kUnit = 0x1p12;  // the last place of 2^12 + m is 2^-40
     return __builtin_bit_cast(uint64_t, __builtin_fma(a, b, kUnit)) - __builtin_bit_cast(uint64_t, kUnit);
@@ -207,7 +216,7 @@ struct Scale {
     factors(x, steps, k, &a, &b);
     return by_term(a, b);
   }
-  // As a number of 41 bits, of which part sums of equal weights are exact.
+  // In the sum of a part: m 2^e, m of 41 bits, so that sums of equal weights are exact.
   static __device__ __forceinline__ double by_value(double a, double b, int k) {
     constexpr double kUnit = 0x1p12;
     return __builtin_ldexp(__builtin_fma(a, b, kUnit) - kUnit, k >> 5);
@@ -373,6 +382,12 @@ struct Head {
 constexpr int kSumsAt = 64, kCountsAt = kSumsAt + kBins * 8, kPartsAt = kSumsAt;
 constexpr int kRecord = kCountsAt + kBins * 4;
 
+// Bound by instructions, for bins: 256 rows of 131073 37 us, of which about 20 a token, half of
+// them in 64 bits, take 25; their LDS additions alone take 30 (4.7 M cycles of bank
+// conflicts) and run beside them. Two or four tokens' table reads ahead of their additions: no
+// faster; 6, 8 or 16 pieces to a row: 40, 44 and 60 us. Without a filter (61 rows of 128001 in 32
+// bits) 15 us. A reference from the first tokens, raised where later ones pass it, in place of
+// the piece in registers: 91.
 template <class T>
 __global__ __launch_bounds__(kThreads, 8) void chunk_kernel(SampleParams p) {
   typedef Piece<T> P;
@@ -419,7 +434,7 @@ __global__ __launch_bounds__(kThreads, 8) void chunk_kernel(SampleParams p) {
   bad = __syncthreads_or(bad);
 #pragma unroll
   for (int v = 0; v < kWaves; ++v) most = fmaxf(most, waves[v]);
-  char* const record = p.ws + (r * p.pieces + c) * p.record;
+  char* const record = p.ws + (r * p.pieces + c) * kRecord;
   if (set.greedy()) {
     int least = INT32_MAX;
 #pragma unroll
@@ -590,6 +605,12 @@ __device__ __forceinline__ uint64_t select(RowShared& sh, uint64_t target, uint6
   return prefix;
 }
 
+// Bound by the latency of its steps, one row to a compute unit: 25 us for one row of 50272
+// (heads and settings 1.8, bins 2.4, their sums 1.5, the border's bin 0.9, the list's tokens 5, their
+// bins 1.6, the select 2.8, the kept sums of the pieces 2.7, the parts of one 2.7 and the token
+// in one 2.1), 50 for 256 rows of 131073, whose second reading takes 7 to 13 (at 9 to 5 TB/s)
+// and the weights of one piece 12. (A row in one workgroup from its first token on, one kernel:
+// 185.) Scratch memory costs a launch of it: 240 bytes a lane 13 us, the 28 that are left none.
 template <class T>
 __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
   typedef Piece<T> P;
@@ -600,10 +621,10 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
   const int64_t r = blockIdx.x;
   const Settings set(p, r);
-  const char* const records = p.ws + r * p.pieces * p.record;
+  const char* const records = p.ws + r * p.pieces * kRecord;
   // the pieces' heads, one to a lane
   Head head = {0.0, -INFINITY, 0, 0, 0};
-  if (lane < p.pieces) head = *(const Head*)(records + lane * p.record);
+  if (lane < p.pieces) head = *(const Head*)(records + lane * kRecord);
   if (t < kSteps) sh.steps[t] = exp2((double)t / kSteps);  // while they are under way
   float most = head.largest;
 #pragma unroll
@@ -680,7 +701,7 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
       const int at = min(i, all - 1), c = at / p.parts;
       const int by = __shfl(down, c, 64);  // by all lanes
       if (i >= all || by >= 64) return 0;
-      return in_units(((const double*)(records + c * p.record + kPartsAt))[at % p.parts], by);
+      return in_units(((const double*)(records + c * kRecord + kPartsAt))[at % p.parts], by);
     };
     uint64_t sum = 0;
     for (int j = 0; j < each; ++j) sum += part_at(t * each + j);
@@ -736,8 +757,8 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
         const int bin = max(t - 16 * __builtin_amdgcn_readlane(down, c), 0);
         v[j] = 0;
         n[j] = 0;
-        if (set.sums()) v[j] = ((const uint64_t*)(records + c * p.record + kSumsAt))[bin];
-        if (set.counts()) n[j] = ((const uint32_t*)(records + c * p.record + kCountsAt))[bin];
+        if (set.sums()) v[j] = ((const uint64_t*)(records + c * kRecord + kSumsAt))[bin];
+        if (set.counts()) n[j] = ((const uint32_t*)(records + c * kRecord + kCountsAt))[bin];
       }
 #pragma unroll
       for (int j = 0; j < kPieces; ++j) {
@@ -1178,7 +1199,7 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
           uint64_t v = 0;
           if (by < 64)
             for (int bin = lane + 16 * by; bin < chosen_bin; bin += 64)
-              v += shifted(((const uint64_t*)(records + c * p.record + kSumsAt))[bin - 16 * by],
+              v += shifted(((const uint64_t*)(records + c * kRecord + kSumsAt))[bin - 16 * by],
                            S - 40 + octave_of(bin));
           v = wave_sum(v) + shifted(wave_sum(own[c * 64 + lane]), S - 40 + octave_of(chosen_bin));
           if (lane == 0) kept[c] = v;
@@ -1278,7 +1299,7 @@ int check_sample(const lutgemm_sample* s) {
 
 struct SamplePlan {
   int pieces, piece, parts, slab;  // slab: rows of one launch
-  size_t record, ws_bytes;
+  size_t ws_bytes;
 };
 
 // Two workgroups of chunk_kernel run on a compute unit at a time. Rows are cut so that
@@ -1300,19 +1321,17 @@ SamplePlan plan(const lutgemm_sample* s) {
     r.pieces = pieces;
   }
   r.parts = (r.piece + 1 + per - 1) / per * kWaves;
-  r.record = kRecord;
   r.slab = std::max(1, std::min(s->rows, 4096 / r.pieces));
-  r.ws_bytes = s->rows ? (size_t)r.slab * r.pieces * r.record : 0;
+  r.ws_bytes = s->rows ? (size_t)r.slab * r.pieces * kRecord : 0;
   return r;
 }
 
 template <class T>
-int run_sample(SampleParams p, int slab, hipStream_t stream) {
-  const int rows = p.rows;
+int run_sample(SampleParams p, int rows, int slab, hipStream_t stream) {
   for (int r = 0; r < rows; r += slab) {
-    p.rows = rows - r < slab ? rows - r : slab;
-    int st = launch(chunk_kernel<T>, dim3((unsigned)(p.rows * p.pieces)), kThreads, p, stream);
-    if (!st) st = launch(row_kernel<T>, dim3((unsigned)p.rows), kThreads, p, stream);
+    const int n = rows - r < slab ? rows - r : slab;
+    int st = launch(chunk_kernel<T>, dim3((unsigned)(n * p.pieces)), kThreads, p, stream);
+    if (!st) st = launch(row_kernel<T>, dim3((unsigned)n), kThreads, p, stream);
     if (st) return st;
     p.logits = (const typename T::Raw*)p.logits + slab * p.row_step;
     p.u += slab;
@@ -1381,8 +1400,6 @@ extern "C" int lutgemm_sample_tokens(const lutgemm_sample* s, const void* d_logi
     p.logprobs = d_logprobs;
     p.ws = (char*)d_workspace;
     p.row_step = s->row_step;
-    p.record = (int64_t)r.record;
-    p.rows = s->rows;
     p.vocab = s->vocab;
     p.pieces = r.pieces;
     p.piece = r.piece;
@@ -1391,9 +1408,9 @@ extern "C" int lutgemm_sample_tokens(const lutgemm_sample* s, const void* d_logi
     while ((1 << bits) < s->vocab) ++bits;
     p.scale = 62 - bits < 50 ? 62 - bits : 50;
     hipStream_t strm = (hipStream_t)stream;
-    if (s->type == LUTGEMM_F32) return run_sample<F32>(p, r.slab, strm);
-    if (s->type == LUTGEMM_F16) return run_sample<Logit16<serve::F16>>(p, r.slab, strm);
-    return run_sample<Logit16<serve::BF16>>(p, r.slab, strm);
+    if (s->type == LUTGEMM_F32) return run_sample<F32>(p, s->rows, r.slab, strm);
+    if (s->type == LUTGEMM_F16) return run_sample<Logit16<serve::F16>>(p, s->rows, r.slab, strm);
+    return run_sample<Logit16<serve::BF16>>(p, s->rows, r.slab, strm);
   } catch (...) {
     return LUTGEMM_ERR_INTERNAL;
   }

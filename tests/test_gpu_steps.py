@@ -296,6 +296,24 @@ def test_shared_repeats_graphs_and_streams():
     assert torch.equal(here, other)
 
 
+def test_shared_group_starts_outside_and_sequences_without_rows():
+    """Starts are brought into [0, seqs]; sequences and groups without new tokens take no rows."""
+    b = Shared(F16, 8, 2, 64, 16, [33, 40, 17], [-3, 2, 4, 1 << 30], [9, 20, 33, 4, 50, 7], [1, 0, 0, 0, 30, 1], seed=27)
+    b.starts = [0, 2, 4, 6]
+    b.check(b.run(), "starts outside")
+    b.check(b.run(max_q=1), "starts outside, all said to be single tokens")
+
+
+@pytest.mark.parametrize("heads,kv_heads,dim", [(8, 1, 128), (2, 2, 64)])
+def test_shared_uneven_groups(heads, kv_heads, dim):
+    """Groups of a few rows beside one of many: the rows a group are an average."""
+    news = [1] * 9 + [2] + [1] * 40
+    starts = [0, 1, 2, 3, 4, 5, 6, 7, 8, 9, 50]
+    b = Shared(BF16, heads, kv_heads, dim, 16, [20 + 31 * i for i in range(10)], starts, [3 + (11 * i) % 70 for i in range(50)],
+               news, seed=29)
+    b.check(b.run(), f"{heads}/{kv_heads}x{dim}")
+
+
 def test_shared_nothing_to_do():
     b = Shared(F16, 4, 2, 64, 16, [20], [0, 3], [3, 2, 5], [1, 1, 1], seed=25)
     b.q = b.q[:0]
@@ -454,6 +472,30 @@ def test_tables_in_place_and_replayed():
         change = [int(-wl[s]) if rng.random() < 0.1 else int(rng.integers(-1, 3)) for s in range(seqs)]
         dc.copy_(_int(change))
         want = plain.tables(change, wl, wt, page, seqs, wr, wf)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert [g.tolist() for g in got] == list(want)
+        assert dt.tolist() == wt and dr.tolist() == wr
+        wl, wf = want[2], want[4]
+
+
+@pytest.mark.parametrize("tokens", [4000, 9000])
+def test_tables_of_prompts_replayed(tokens):
+    """Both ways of writing rows, captured: replays read the lengths and the ring anew."""
+    page, seqs = 16, 12
+    dl, dc, df = _int([0] * seqs), _int([0] * seqs), _int([0, 700])
+    dt, dr = torch.full((seqs, 100), -1, dtype=torch.int32, device=DEV), _int(list(range(700)))
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        got = lg.batch_tables(dc, dl, dt, page, tokens, dr, df, in_place=True)
+    wt, wr, wl, wf = dt.tolist(), dr.tolist(), [0] * seqs, [0, 700]
+    rng = np.random.default_rng(3)
+    for step in range(8):
+        change = [-wl[s] if (s + step) % 3 == 0 else int(rng.integers(1, 900)) for s in range(seqs)]
+        dc.copy_(_int(change))
+        want = plain.tables(change, wl, wt, page, tokens, wr, wf)
         graph.replay()
         torch.cuda.synchronize()
         assert [g.tolist() for g in got] == list(want)
@@ -625,6 +667,39 @@ def test_sample_flat_and_steep(dtype, top_p):
     _sample_check(x, u, top_p=[top_p] * rows)
     _sample_check(x, u, top_p=[top_p] * rows, top_k=[40000] * rows)
     _sample_check(x, u, [0.7] * rows, top_p=[top_p] * rows, min_p=[0.01] * rows)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("k", [2047, 2048, 2049, 4096, 4097, 20000])
+def test_sample_large_top_k(dtype, k):
+    """About where a list ends, with borders among equal values and all filters together."""
+    rows, vocab = 8, 30001
+    x = torch.from_numpy(_logits(rows, vocab, k)).to(dtype)
+    x[5] = torch.arange(vocab).remainder(9).to(dtype) / 8
+    x[6, 2100:] = -INF
+    x[7] = 1.5
+    u = [(i + 0.5) / rows for i in range(rows)]
+    _sample_check(x, u, top_k=[k] * rows)
+    _sample_check(x, u, [1.4] * rows, [k] * rows, [0.95] * rows)
+    _sample_check(x, u, [0.8] * rows, [k] * rows, None, [0.003] * rows)
+    _sample_check(x, u, [1.1] * rows, [k] * rows, [0.9] * rows, [0.001] * rows)
+
+
+def test_sample_more_rows_than_a_launch_takes():
+    """Rows beyond what the workspace holds at a time: the same inputs give the same results."""
+    rows, period, vocab = 3000, 100, 50272
+    base = torch.from_numpy(_logits(period, vocab, 13)).to(BF16)
+    x = base.to(DEV).repeat(rows // period, 1)
+    rng = np.random.default_rng(13)
+    u = np.tile(rng.random(period).astype(np.float32).clip(0, 1 - 2.0 ** -24), rows // period).tolist()
+    p = [1.0 if r % period < 50 else 0.9 for r in range(rows)]
+    k = [40 if r % period % 7 == 0 else 0 for r in range(rows)]
+    t = [0.0 if r % period == 3 else 0.9 for r in range(rows)]
+    got = lg.sample_tokens(x, _int(u, F32), _int(t, F32), _int(k), _int(p, F32))
+    for g in got:
+        assert torch.equal(g, g[:period].repeat(rows // period))
+    want = _sample_check(base, u[:period], t[:period], k[:period], p[:period])
+    assert got[0][:period].tolist() == want
 
 
 def test_sample_strided_and_unaligned_rows():
