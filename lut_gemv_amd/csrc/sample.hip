@@ -25,9 +25,9 @@
 // and index, then on the index); where they are many, the bins' sums say in which piece the
 // drawn token lies, and only that is weighed again.
 //
-// Measured (bf16, 256 rows of 131073, top_p; 67 MB, 10.5 us at a copy's rate): 87 us;
-// fp16, 1 row of 50272 28 to 31 us, 48 rows of 32000 of all kinds 34; fp32, 61 rows of 128001
-// without a filter 21. The kernels say what bounds each.
+// Measured (bf16, 256 rows of 131073, top_p; 67 MB, 10 us at a streaming read's rate): 80 us;
+// fp16, 1 row of 50272 26 us, 48 rows of 32000 of all kinds 32; fp32, 61 rows of 128001
+// without a filter 20. The kernels say what bounds each.
 #include <algorithm>
 #include <type_traits>
 
@@ -354,11 +354,15 @@ struct Settings {
   int top_k;
   bool bad, by_count, by_weight, by_least;
   __device__ __forceinline__ Settings(const SampleParams& p, int64_t r) {
+    // arrays that are not given are read as u: loads under a condition wait for one another
+    auto or_u = [&](const float* a) { return a ? a : p.u; };
+    const float t = or_u(p.temperature)[r], tp = or_u(p.top_p)[r], mp = or_u(p.min_p)[r];
+    const int32_t tk = (p.top_k ? p.top_k : (const int32_t*)p.u)[r];
     u = p.u[r];
-    temperature = p.temperature ? p.temperature[r] : 1.f;
-    top_p = p.top_p ? p.top_p[r] : 1.f;
-    min_p = p.min_p ? p.min_p[r] : 0.f;
-    top_k = p.top_k ? p.top_k[r] : 0;
+    temperature = p.temperature ? t : 1.f;
+    top_p = p.top_p ? tp : 1.f;
+    min_p = p.min_p ? mp : 0.f;
+    top_k = p.top_k ? tk : 0;
     bad = !(u >= 0.f && u < 1.f) || !(temperature >= 0.f && temperature < INFINITY) ||
           top_p != top_p || min_p != min_p;
     by_count = top_k > 0 && top_k < p.vocab;
@@ -506,15 +510,14 @@ __global__ __launch_bounds__(kThreads, 8) void chunk_kernel(SampleParams p) {
 
 struct RowShared {
   double steps[kSteps];   // first: across the banks once
-  uint64_t list[kList];   // codes; or the parts' sums
-  uint64_t inside[kList]; // codes of the border's bin
+  uint64_t list[kList];   // indices, codes, the pieces' lanes' sums or the parts' sums
   uint64_t sums[2][256];
   uint64_t counts[2][256];
   uint64_t qwaves[kWaves];
   uint32_t waves[kWaves];
   uint64_t found_sum, found_code, found_rest, ones, zeros;
   int32_t found, found_count;
-  uint32_t above, within;  // tokens of the lists
+  uint32_t listed;        // tokens of the list
 };
 
 // The first code, of those that `members` hands to its argument with a value (at least 1)
@@ -605,12 +608,13 @@ __device__ __forceinline__ uint64_t select(RowShared& sh, uint64_t target, uint6
   return prefix;
 }
 
-// Bound by the latency of its steps, one row to a compute unit: 25 us for one row of 50272
-// (heads and settings 1.8, bins 2.4, their sums 1.5, the border's bin 0.9, the list's tokens 5, their
-// bins 1.6, the select 2.8, the kept sums of the pieces 2.7, the parts of one 2.7 and the token
-// in one 2.1), 50 for 256 rows of 131073, whose second reading takes 7 to 13 (at 9 to 5 TB/s)
-// and the weights of one piece 12. (A row in one workgroup from its first token on, one kernel:
-// 185.) Scratch memory costs a launch of it: 240 bytes a lane 13 us, the 28 that are left none.
+// Bound by the latency of its steps, one row to a compute unit: 14 to 27 us for one row of 50272
+// (heads and settings 1.8, bins 2.5, their sums 0.8, the border's bin 0.9, the list's tokens 5.4, their
+// values 0.6, the select 2.8, the kept sums of the pieces 2.7, the parts of one 2.8, the token
+// in one 2.9), 47 for 256 rows of 131073, whose second reading takes 7 to 13 (9 to 5 TB/s, by
+// how many tokens it lists) and the weights of one piece 12. (A row in one workgroup from its
+// first token on, one kernel: 185.) Scratch memory costs a launch of it: 240 bytes a lane 13 us,
+// the 20 to 36 that are left none that shows.
 template <class T>
 __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
   typedef Piece<T> P;
@@ -620,11 +624,10 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
   fetch(p);
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
   const int64_t r = blockIdx.x;
-  const Settings set(p, r);
   const char* const records = p.ws + r * p.pieces * kRecord;
   // the pieces' heads, one to a lane
-  Head head = {0.0, -INFINITY, 0, 0, 0};
-  if (lane < p.pieces) head = *(const Head*)(records + lane * kRecord);
+  Head head = *(const Head*)(records + min(lane, p.pieces - 1) * kRecord);
+  const Settings set(p, r);
   if (t < kSteps) sh.steps[t] = exp2((double)t / kSteps);  // while they are under way
   float most = head.largest;
 #pragma unroll
@@ -738,10 +741,8 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
     // the row's first words are under way while the bins are joined
     u4v first[kAhead];
     auto first_words = [&](u4v (&w)[kAhead]) __attribute__((always_inline)) {
-      const int stripes = row.wave_stripes();
 #pragma unroll
-      for (int a = 0; a < kAhead; ++a)
-        if (a < stripes) w[a] = row.load(a);
+      for (int a = 0; a < kAhead; ++a) w[a] = row.load(a);
     };
     first_words(first);
     // the bins of all pieces: sums in their own octave's unit and in 2^S
@@ -822,9 +823,10 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
       for (int s0 = 0; s0 < stripes; s0 += kAhead) {
 #pragma unroll
         for (int a = 0; a < kAhead; ++a) {
-          if (s0 + a >= stripes) continue;
+          // loads behind the row's end give zeros: under a condition each is waited for at once
           u4v now = w[a];
-          if (s0 + a + kAhead < stripes) w[a] = row.load(s0 + a + kAhead);
+          w[a] = row.load(s0 + a + kAhead);
+          if (s0 + a >= stripes) continue;
           row.place(now, s0 + a);
           bool in[P::kPer], some = false;
 #pragma unroll
@@ -858,16 +860,21 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
         }
       });
     };
-    // their indices into a list; *n: how many there are, also where the list ends before
-    auto collect = [&](u4v (&first)[kAhead], float least, float limit, uint32_t* list, uint32_t* n) {
+    // The list's tokens, each thread's: their codes, ~0 for none, and bins; whole: all had room.
+    uint64_t code[kMine];
+    int code_bin[kMine];
+    bool whole = false;
+    // The tokens from `least` to `limit`: by their indices first, where the words are read.
+    auto gather = [&](u4v (&first)[kAhead], float least, float limit) __attribute__((always_inline)) {
+      uint32_t* const list = (uint32_t*)sh.list;
       __syncthreads();
-      if (t == 0) *n = 0;
+      if (t == 0) sh.listed = 0;
       __syncthreads();
       words_from(first, least, limit, [&](const u4v&, const bool (&in)[P::kPer], int i0) {
         uint32_t count = 0, at = 0;
 #pragma unroll
         for (int e = 0; e < P::kPer; ++e) count += __popcll(__ballot(in[e]));
-        if (lane == 0) at = atomicAdd(n, count);
+        if (lane == 0) at = atomicAdd(&sh.listed, count);
         uint32_t bits = bits_of(in);
         at = __builtin_amdgcn_readfirstlane(at);
         if (at + count > kList) return;
@@ -879,51 +886,41 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
         }
       });
       __syncthreads();
+      const uint32_t n = sh.listed;
+      whole = n <= kList;
+#pragma unroll
+      for (int j = 0; j < kMine; ++j) {
+        const uint32_t i = t + j * kThreads;
+        code[j] = ~0ull;
+        code_bin[j] = kBins;
+        if (i < n && whole) {  // read again: codes written by the collecting lanes 3 us more
+          uint64_t ignored;
+          const Raw raw = logits[list[i]];
+          code[j] = code_of<T>(raw, (int)list[i]);
+          code_bin[j] = bin_at(raw, &ignored);
+        }
+      }
     };
     auto raw_of = [&](uint64_t code) {  // the bits of a code's value
       const uint32_t key = ~(uint32_t)(code >> kIndexBits) & kKeyAll;
       constexpr uint32_t sign = 1u << (T::kKeyBits - 1);
       return (Raw)(key & sign ? key & (sign - 1) : ~key & kKeyAll);
     };
-    // The tokens of a bin into `inside`, those of the bins before it into `list`: by value
-    // first, which may take some of the next bins.
-    auto gather = [&](u4v (&first)[kAhead], int bin, bool before_too) {
-      collect(first, least_of(bin), before_too ? INFINITY : most_of(bin), (uint32_t*)sh.list, &sh.above);
-      const uint32_t n = sh.above;
-      uint64_t mine[kMine];
+    // Of a list that was written as codes.
+    auto take_list = [&]() __attribute__((always_inline)) {
+      __syncthreads();
+      const uint32_t n = sh.listed;
+      whole = n <= kList;
 #pragma unroll
       for (int j = 0; j < kMine; ++j) {
         const uint32_t i = t + j * kThreads;
-        mine[j] = ~0ull;
-        if (i < n && n <= kList) {  // read again: by the collecting lanes 3 us more
-          const uint32_t at = ((const uint32_t*)sh.list)[i];
-          mine[j] = code_of<T>(logits[at], (int)at);
-        }
+        code[j] = i < n && whole ? sh.list[i] : ~0ull;
       }
-      __syncthreads();
-      if (t == 0) {
-        sh.within = n <= kList ? 0 : n;
-        sh.above = n <= kList ? 0 : n;
-      }
-      __syncthreads();
-      if (n > kList) return;
-#pragma unroll
-      for (int j = 0; j < kMine; ++j) {
-        uint64_t ignored;
-        const int b = mine[j] == ~0ull ? kBins : bin_at(raw_of(mine[j]), &ignored);
-        const uint64_t in = __ballot(b == bin), above = __ballot(b < bin);
-        uint32_t at = 0, to = 0;
-        if (lane == 0 && in) at = atomicAdd(&sh.within, (uint32_t)__popcll(in));
-        if (lane == 0 && above) to = atomicAdd(&sh.above, (uint32_t)__popcll(above));
-        const uint64_t below = (1ull << lane) - 1;
-        if (b == bin) sh.inside[lane_of(at, 0) + __popcll(in & below)] = mine[j];
-        if (b < bin) sh.list[lane_of(to, 0) + __popcll(above & below)] = mine[j];
-      }
-      __syncthreads();
+      return whole;
     };
     // the border inside a bin: the code up to which its tokens' number or sum (in the
-    // bin's unit) reaches `need`; after gather(bin, .)
-    auto border_in = [&](int bin, bool weights, uint64_t need, uint64_t* before) {
+    // bin's unit) reaches `need`; after its tokens were gathered
+    auto border_in = [&](int bin, bool weights, uint64_t need, uint64_t* before) __attribute__((always_inline)) {
       if (need < 1) need = 1;
       // a value between two bins may be rounded into the other here: without any, the largest alone
       auto or_largest = [&](uint64_t code) {
@@ -931,14 +928,12 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
         if constexpr (T::kKeyBits == 16) raw = T::one(most);
         return code ? code : code_of<T>((Raw)raw, (1 << kIndexBits) - 1);
       };
-      if (sh.within <= kList) {
-        uint64_t code[kMine], value[kMine];
+      if (whole) {
+        uint64_t value[kMine];
 #pragma unroll
         for (int j = 0; j < kMine; ++j) {
-          const int i = t + j * kThreads;
           value[j] = 0;
-          if (i >= (int)sh.within) continue;
-          code[j] = sh.inside[i];
+          if (code_bin[j] != bin) continue;
           value[j] = 1;
           if (weights) bin_at(raw_of(code[j]), &value[j]);
         }
@@ -968,34 +963,25 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
       const double w = scale.weight((double)x, sh.steps, &k);
       return bin_of(k) < kBins && w >= at_least;
     };
-    // the tokens from `least` on that have this weight into the list, `above` of them if they fit
-    auto collect_counted = [&](float least, double at_least) {
+    // the tokens from `least` on that `takes` says into the list, as codes
+    auto collect = [&](float least, auto takes) __attribute__((always_inline)) {
       __syncthreads();
-      if (t == 0) sh.above = sh.within = 0;
+      if (t == 0) sh.listed = 0;
       __syncthreads();
       each_from(least, INFINITY, [&](Raw raw, int i) {
-        if (sh.above > kList || !counted(T::wide(raw), at_least)) return;
-        const uint32_t at = atomicAdd(&sh.above, 1u);
+        if (sh.listed > kList || !takes(raw, i)) return;
+        const uint32_t at = atomicAdd(&sh.listed, 1u);
         if (at < kList) sh.list[at] = code_of<T>(raw, i);
       });
-      __syncthreads();
+      return take_list();
+    };
+    auto collect_counted = [&](float least, double at_least) __attribute__((always_inline)) {
+      return collect(least, [&](Raw raw, int) { return counted(T::wide(raw), at_least); });
     };
     uint64_t border = ~0ull;  // kept: codes up to it
-    bool listed = false;      // the kept tokens are among the list's first `members`
-    int members = 0;
+    bool listed = false;      // the kept tokens are among the list's
     int last_bin = kBins - 1;  // no kept token is behind this bin
-    int chosen_bin = -1;      // the border is in this bin, of which `inside` has the tokens
-    // puts `inside` behind the list, if both have room
-    auto join_lists = [&] {
-      const uint32_t n = sh.above + sh.within;
-      const bool fits = sh.above <= kList && sh.within <= kList && n <= kList;
-      if (fits) {
-        for (uint32_t i = t; i < sh.within; i += kThreads) sh.list[sh.above + i] = sh.inside[i];
-        members = (int)n;
-      }
-      __syncthreads();
-      return fits;
-    };
+    int chosen_bin = -1;      // the border is in this bin, whose tokens were gathered
     uint64_t available = all_sum;  // what top_p takes its part of
     if (set.by_count) {
       const uint32_t k = (uint32_t)set.top_k;
@@ -1004,33 +990,19 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
         sh.found_sum = upto - mine;
       });
       if (bin == kBins) {  // fewer have weight: all of these
-        if (set.few()) {
-          collect_counted(least_of(kBins - 1), 0.0);
-          listed = join_lists();
-        }
+        if (set.few()) listed = collect_counted(least_of(kBins - 1), 0.0);
       } else {
         last_bin = bin;
         const uint64_t rest = (uint64_t)(set.top_k - sh.found_count);
         const uint64_t ahead = sh.found_sum;
-        gather(first, bin, set.few());
-        listed = set.few() && join_lists();
+        gather(first, least_of(bin), set.few() ? INFINITY : most_of(bin));
+        listed = set.few() && whole;
         if (!listed) {
           uint64_t before;
           border = border_in(bin, false, rest, &before);
           chosen_bin = bin;
           if (set.few()) {  // of the bin only those up to the border
-            __syncthreads();
-            if (t == 0) sh.above = 0;
-            __syncthreads();
-            each_from(least_of(bin), INFINITY, [&](Raw raw, int i) {
-              const uint64_t code = code_of<T>(raw, i);
-              if (code > border) return;
-              const uint32_t at = atomicAdd(&sh.above, 1u);
-              if (at < kList) sh.list[at] = code;
-            });
-            __syncthreads();
-            listed = true;
-            members = (int)min(sh.above, (uint32_t)kList);
+            listed = collect(least_of(bin), [&](Raw raw, int i) { return code_of<T>(raw, i) <= border; });
           } else {
             // the sum of what is kept: by weight up to the border's code
             uint64_t kept = 0;
@@ -1044,9 +1016,10 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
           }
         } else {
           uint64_t before;
-          const int n = members;
           border = select(sh, (uint64_t)set.top_k, &before, [&](auto f) {
-            for (int i = t; i < n; i += kThreads) f(sh.list[i], 1);
+#pragma unroll
+            for (int j = 0; j < kMine; ++j)
+              if (code_bin[j] <= bin) f(code[j], 1);
           });
         }
       }
@@ -1064,7 +1037,7 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
       const uint64_t ahead = sh.found_sum;
       const bool small = sh.found_count;
       if (set.by_count) first_words(first);
-      gather(first, bin, small);
+      gather(first, least_of(bin), small ? INFINITY : most_of(bin));
       const int by = 40 - octave_of(bin) - S;  // from 2^S to the bin's unit
       const uint64_t missing = target > ahead ? target - ahead : 1;
       const uint64_t need = by >= 0 ? shifted(missing, by) : (missing + (1ull << -by) - 1) >> -by;
@@ -1074,15 +1047,14 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
         border = second;
         chosen_bin = bin;
       }
-      listed = small && join_lists();
+      listed = small && whole;
     }
     float least = least_of(last_bin);
     if (set.by_least) {
       const double bins = 17.0 - 16.0 * log2(floor_weight);  // the top is less than an octave higher
       if (bins < (double)last_bin) least = least_of(bins);
       if (!listed && !set.by_count && !set.by_weight) {
-        collect_counted(least, least_weight);
-        listed = join_lists();
+        listed = collect_counted(least, least_weight);
       }
     }
     // the weight of a token of at least `least` if it is kept, as a part sums it
@@ -1099,14 +1071,11 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
     };
     if (listed) {
       unit = kListUnit;
-      uint64_t code[kMine], weight[kMine], sum = 0;
-      __syncthreads();
+      uint64_t weight[kMine], sum = 0;
 #pragma unroll
       for (int j = 0; j < kMine; ++j) {
-        const int i = t + j * kThreads;
-        code[j] = i < members ? sh.list[i] : ~0ull;
         weight[j] = 0;
-        if (i < members && code[j] <= border && counted(T::wide(raw_of(code[j])), least_weight))
+        if (code[j] <= border && code[j] != ~0ull && counted(T::wide(raw_of(code[j])), least_weight))
           weight[j] = scale.listed((double)T::wide(raw_of(code[j])), sh.steps);
         sum += weight[j];
       }
@@ -1175,13 +1144,11 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
           uint64_t term = 0;
           return code <= border && bin_at(raw_of(code), &term) == chosen_bin ? term : 0ull;
         };
-        if (sh.within <= kList) {
-          for (int i0 = 0; i0 < (int)sh.within; i0 += kThreads) {
-            const uint64_t code = i0 + t < (int)sh.within ? sh.inside[i0 + t] : ~0ull;
-            const bool is = code != ~0ull;
-            add(is ? kept_term(code) : 0ull,
-                is ? (int)(code & ((1u << kIndexBits) - 1)) / p.piece : 0);
-          }
+        if (whole) {
+#pragma unroll
+          for (int j = 0; j < kMine; ++j)
+            if (code_bin[j] == chosen_bin)
+              add(kept_term(code[j]), (int)(code[j] & ((1u << kIndexBits) - 1)) / p.piece);
         } else {
           each_word(least_of(chosen_bin), most_of(chosen_bin),
                     [&](const u4v& w, const bool (&in)[P::kPer], int i0) {
@@ -1218,15 +1185,15 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
         piece = P(logits + offset, min(p.piece, p.vocab - offset));
       }
       __syncthreads();
-      uint64_t* const parts = sh.list;  // list and inside: 2 kList
+      uint64_t* const parts = sh.list;
+      static_assert(kMostTokens / (64 * 4) <= kList, "a word to each part of a row");
       const int stripes = piece.wave_stripes(), all = piece.stripes() * kWaves;
       if (lane == 0)  // of the last stripe, in which the wave may have no tokens
         parts[(piece.stripes() - 1) * kWaves + wave] = 0;
       for (int s0 = 0; s0 < stripes; s0 += kAhead) {
         u4v w[kAhead];
 #pragma unroll
-        for (int a = 0; a < kAhead; ++a)
-          if (s0 + a < stripes) w[a] = piece.load(s0 + a);
+        for (int a = 0; a < kAhead; ++a) w[a] = piece.load(s0 + a);
 #pragma unroll
         for (int a = 0; a < kAhead; ++a) {
           if (s0 + a >= stripes) continue;
