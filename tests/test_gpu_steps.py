@@ -314,6 +314,22 @@ def test_shared_uneven_groups(heads, kv_heads, dim):
     b.check(b.run(), f"{heads}/{kv_heads}x{dim}")
 
 
+@pytest.mark.parametrize("news", [[1, 1, 1], [30, 1, 140]])
+def test_shared_far_pages(news):
+    """Pages more than 2^32 bytes, and 2^31 elements, into the cache, prefixes' and own."""
+    pages = (1 << 31) // (64 * 2 * 128) + 40
+    k, v = (torch.zeros((pages, 64, 2, 128), dtype=F16, device=DEV) for _ in range(2))
+    assert k.numel() > 1 << 31
+    b = Shared(F16, 8, 2, 128, 64, [200], [0, 3], [30, 65, 150], news, seed=31)
+    for table in (b.prefix_table, b.page_table):
+        for at in (table >= 0).nonzero().tolist():
+            near = int(table[tuple(at)])
+            table[tuple(at)] = pages - 1 - near
+            k[pages - 1 - near], v[pages - 1 - near] = b.k_pages[near], b.v_pages[near]
+    b.k_pages, b.v_pages = k, v
+    b.check(b.run(), "far pages")
+
+
 def test_shared_nothing_to_do():
     b = Shared(F16, 4, 2, 64, 16, [20], [0, 3], [3, 2, 5], [1, 1, 1], seed=25)
     b.q = b.q[:0]
@@ -743,6 +759,63 @@ def test_sample_repeats_graphs_and_streams():
     here = lg.sample_tokens(x, u, t, top_p=p)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(here, other))
+
+
+def test_sample_rows_far_apart():
+    """Rows that begin more than 2^32 bytes, and 2^31 elements, into the logits."""
+    vocab = 131073
+    x = torch.from_numpy(_logits(5, vocab, 14)).to(BF16)
+    dev = torch.zeros((4 * 4100 + 1, vocab), dtype=BF16, device=DEV)
+    assert dev.numel() > 1 << 31
+    far = dev[::4100]
+    far.copy_(x)
+    u = [0.1, 0.3, 0.5, 0.7, 0.9]
+    _sample_check(x, u, top_p=[0.9, 0.8, 0.7, 1.0, 0.95], logits=far)
+    _sample_check(x, u, [0.0, 1.0, 0.0, 1.0, 0.0], logits=far)
+
+
+def test_two_graphs_replayed_at_once():
+    """Graphs of all three operators on two streams at a time share nothing."""
+    b = Shared(BF16, 16, 2, 128, 32, [900], [0, 6], [20, 300, 7, 64, 65, 1], [1, 40, 1, 3, 1, 1], seed=33)
+    x = torch.from_numpy(_logits(50, 32000, 15)).to(F16).to(DEV)
+    change, lens = _int([3] * 2000), _int([17] * 2000)
+    ring, free = _int(list(range(6000))), _int([5, 4000])
+
+    def work(i):
+        table = torch.arange(8000, dtype=torch.int32, device=DEV).view(2000, 4)
+        u = torch.linspace(0.1 * i, 0.5 + 0.1 * i, 50, device=DEV)
+        got = lg.sample_tokens(x, u, top_p=torch.full((50,), 0.9, device=DEV))
+        return (b.run(), *got, *lg.batch_tables(change, lens, table, 16, 6000 + i, ring, free), table)
+
+    want = [work(i) for i in range(2)]
+    streams, graphs = [torch.cuda.Stream() for _ in range(2)], []
+    torch.cuda.synchronize()
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=streams[i]):
+            out = work(i)
+        graphs.append((g, out))
+    for _ in range(3):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                graphs[i][0].replay()
+        torch.cuda.synchronize()
+        for (_, out), w in zip(graphs, want):
+            assert all(torch.equal(a, b) for a, b in zip(out, w))
+
+
+def test_results_under_inference_mode():
+    x = torch.from_numpy(_logits(3, 100, 16)).to(F16).to(DEV)
+    u = _int([0.2, 0.5, 0.8], F32)
+    want = lg.sample_tokens(x, u)
+    table = _int([[0, 1], [2, 3]])
+    with torch.inference_mode():
+        tokens, logprobs = lg.sample_tokens(x, u)
+        got = lg.batch_tables(_int([1, 2]), _int([3, 4]), table, 4, 3)
+        assert torch.equal(tokens + 1, want[0] + 1) and torch.equal(logprobs * 2, want[1] * 2)
+        assert got[0].tolist() == [3, 4, 5] and got[1].tolist() == [3, 12, 13]
+        got[0].add_(1)
+    assert tokens.is_inference() and got[3].tolist() == [0, 1, 3] and got[0].tolist() == [4, 5, 6]
 
 
 def test_sample_follows_the_distribution():
