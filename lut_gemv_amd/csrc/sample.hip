@@ -943,6 +943,8 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
             if (value[j]) f(code[j], value[j]);
         }));
       }
+      // more than the list takes, of nearly equal logits: the row again for each byte (256 rows of
+      // 131073: 250 us at a temperature of 20, 630 if all are equal)
       const float least = least_of(bin), limit = most_of(bin);
       return or_largest(select(sh, need, before, [&](auto f) {
         each_from(least, limit, [&](Raw raw, int i) {
