@@ -1128,7 +1128,7 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
       P piece = row;
       int offset = 0;
       uint64_t ahead = 0, goal = 0;
-      const bool by_bins = chosen_bin >= 0 && set.sums() && !set.by_least;
+      bool by_bins = chosen_bin >= 0 && set.sums() && !set.by_least;
       if (by_bins) {
         // of each piece the sum of what is kept: the border's own tokens are added by themselves, each
         // lane to a word of its own (a wave's by piece 4 us more, all to one word 6), then
@@ -1186,40 +1186,53 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
         offset = c * p.piece;
         piece = P(logits + offset, min(p.piece, p.vocab - offset));
       }
-      __syncthreads();
       uint64_t* const parts = sh.list;
       static_assert(kMostTokens / (64 * 4) <= kList, "a word to each part of a row");
-      const int stripes = piece.wave_stripes(), all = piece.stripes() * kWaves;
-      if (lane == 0)  // of the last stripe, in which the wave may have no tokens
-        parts[(piece.stripes() - 1) * kWaves + wave] = 0;
-      for (int s0 = 0; s0 < stripes; s0 += kAhead) {
-        u4v w[kAhead];
+      // The parts' sums of the piece. Those of bins and of parts are rounded each by themselves: where
+      // u is among the last places of the total, a piece can have a sum by its bins and none by its
+      // parts. Then the parts of the whole row say, of which the largest token's has a sum.
+      uint64_t sum_t, up, here;
+      int all, each;
+      for (;;) {
+        __syncthreads();
+        const int stripes = piece.wave_stripes();
+        all = piece.stripes() * kWaves;
+        if (lane == 0)  // of the last stripe, in which the wave may have no tokens
+          parts[(piece.stripes() - 1) * kWaves + wave] = 0;
+        for (int s0 = 0; s0 < stripes; s0 += kAhead) {
+          u4v w[kAhead];
 #pragma unroll
-        for (int a = 0; a < kAhead; ++a) w[a] = piece.load(s0 + a);
+          for (int a = 0; a < kAhead; ++a) w[a] = piece.load(s0 + a);
 #pragma unroll
-        for (int a = 0; a < kAhead; ++a) {
-          if (s0 + a >= stripes) continue;
-          piece.place(w[a], s0 + a);
-          const int i0 = piece.first(s0 + a);
-          double sum_s = 0.0;
-          uint32_t bits = 0;
+          for (int a = 0; a < kAhead; ++a) {
+            if (s0 + a >= stripes) continue;
+            piece.place(w[a], s0 + a);
+            const int i0 = piece.first(s0 + a);
+            double sum_s = 0.0;
+            uint32_t bits = 0;
 #pragma unroll
-          for (int e = 0; e < P::kPer; ++e)
-            bits |= (uint32_t)(T::wide(P::element(w[a], e)) >= edge) << e;
-          for (; bits; bits &= bits - 1) {
-            const int e = __builtin_ctz(bits);
-            sum_s += kept_value(T::wide(P::any(w[a], e)), offset + piece.token(i0 + e));
+            for (int e = 0; e < P::kPer; ++e)
+              bits |= (uint32_t)(T::wide(P::element(w[a], e)) >= edge) << e;
+            for (; bits; bits &= bits - 1) {
+              const int e = __builtin_ctz(bits);
+              sum_s += kept_value(T::wide(P::any(w[a], e)), offset + piece.token(i0 + e));
+            }
+            sum_s = wave_sum(sum_s);
+            if (lane == 0) parts[(s0 + a) * kWaves + wave] = in_units(sum_s, 0);
           }
-          sum_s = wave_sum(sum_s);
-          if (lane == 0) parts[(s0 + a) * kWaves + wave] = in_units(sum_s, 0);
         }
+        __syncthreads();
+        each = (all + kThreads - 1) / kThreads;
+        sum_t = 0;
+        for (int j = 0; j < each; ++j)
+          if (t * each + j < all) sum_t += parts[t * each + j];
+        up = block_scan(sum_t, sh.qwaves, &here);
+        if (here || !by_bins) break;
+        by_bins = false;
+        piece = row;
+        offset = 0;
+        ahead = 0;
       }
-      __syncthreads();
-      const int each = (all + kThreads - 1) / kThreads;
-      uint64_t sum_t = 0, here;
-      for (int j = 0; j < each; ++j)
-        if (t * each + j < all) sum_t += parts[t * each + j];
-      const uint64_t up = block_scan(sum_t, sh.qwaves, &here);
       if (!by_bins) {
         total = here;
         goal = share(set.u, total, false) + 1;

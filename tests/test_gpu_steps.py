@@ -985,3 +985,87 @@ def test_decode_rate_counts_prefix_and_head():
     read = st.bytes_per_step() + (60 + 3 * 41) * 2 * 4096 * 2 + nb + 2 * na + 2 * 3 * 32000
     r = st.time_tokens(tokens=2, warmup=1)
     assert r["GBps"] == pytest.approx(read / (r["ms_per_step"] * 1e-3) / 1e9, rel=1e-9)
+
+
+def _sample_rows(x, u, temperature=None, top_k=None, top_p=None, min_p=None):
+    """Every row's draw by the definition, also next to a border: a token that the filters keep, up to
+    which the kept weights sum to more than u times their total, but for _margin of it. What the
+    last call's results held is no answer: the memory is filled before."""
+    rows, vocab = x.shape
+    near = _margin(vocab)
+    dev = [None if a is None else _int(a, t) for a, t in ((temperature, F32), (top_k, torch.int32), (top_p, F32),
+                                                         (min_p, F32))]
+    d, du, out = x.to(DEV), _int(u, F32), _int([-7] * rows, torch.int64)
+    last = torch.full((12 * rows,), 0xFF, dtype=torch.uint8, device=DEV)
+    torch.cuda.synchronize()
+    del last
+    tokens, logprobs = lg.sample_tokens(d, du, *dev, out=out)
+    tokens, logprobs, rounded = tokens.tolist(), logprobs.tolist(), x.double().numpy()
+    for r in range(rows):
+        t = 1.0 if temperature is None else float(np.float32(temperature[r]))
+        order = np.argsort(-rounded[r], kind="stable")
+        w = np.exp((rounded[r][order] - rounded[r][order[0]]) / t)
+        sure = np.ones(vocab, bool)      # kept wherever the borders lie within the margin
+        if top_k is not None and top_k[r] > 0:
+            w[top_k[r]:] = 0
+        maybe = w > 0
+        if top_p is not None and top_p[r] < 1:
+            before = (np.cumsum(w) - w) / w.sum()
+            p = float(np.float32(top_p[r]))
+            sure &= before < p - near
+            maybe &= before < p + near
+        if min_p is not None and min_p[r] > 0:
+            least = min(float(np.float32(min_p[r])), 1.0)
+            sure &= w >= least * (1 + 2.0 ** -40)
+            maybe &= w >= least * (1 - 2.0 ** -40)
+        sure[0] = maybe[0] = True
+        sure &= maybe
+        kept, most = np.zeros(vocab), np.zeros(vocab)
+        kept[order], most[order] = w * sure, w * maybe
+        loose = (most.sum() - kept.sum()) / kept.sum() + near
+        token = tokens[r]
+        assert 0 <= token < vocab and most[token] > 0, (r, token)
+        upto = np.cumsum(most) / most.sum()
+        below = upto[token] - most[token] / most.sum()
+        assert below - loose <= u[r] <= upto[token] + loose, (r, token, below, upto[token], u[r])
+        logprob = np.log(most[token] / most.sum())
+        assert abs(logprobs[r] - logprob) <= 2.0 ** -24 * abs(logprob) + 2 * loose, (r, logprobs[r], logprob)
+    return tokens
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows", [1, 11])
+def test_sample_small_parts_of_a_large_top_k(dtype, rows):
+    """One token has nearly all weight, and u is among the last places of the total: the first
+    pieces' tokens have a sum together, but none that their parts, 64 words of 16 bytes each, would
+    be rounded to. A row is answered whatever the sums of its pieces and its parts are."""
+    vocab = 131072                       # sums in units of 2^-45 of the largest weight
+    part = 64 * (4 if dtype == F32 else 8)
+    x = torch.full((rows, vocab), -INF, dtype=dtype)
+    for r in range(rows):
+        x[r, vocab - 1] = r / 8
+        light = np.log((0.1 + 0.03 * r) * 2.0 ** -45) + r / 8
+        x[r, part + r:16384:part] = light                # no part of these has half a unit
+        x[r, 65536 + 20 * np.arange(3000)] = light       # many in each part
+    for u in (0.0, 2.0 ** -45, 2.0 ** -40, 0.5):
+        for k in (2049, 2500, 100000):
+            _sample_rows(x, [u] * rows, top_k=[k] * rows)
+            _sample_rows(x, [u] * rows, top_k=[k] * rows, top_p=[1 - 2.0 ** -24] * rows)
+            _sample_rows(x, [u] * rows, top_p=[1 - 2.0 ** -24] * rows)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("vocab", [50272, 131073])
+def test_sample_peaked_rows_at_the_ends(dtype, vocab):
+    """u at and next to 0 and 1 on rows whose weights span all that is counted."""
+    rows = 6
+    rng = np.random.default_rng(vocab)
+    x = -rng.exponential(1, (rows, vocab)) * 2.0 ** np.arange(rows)[:, None] - 5.0 * np.arange(rows)[::-1, None]
+    x[rng.random((rows, vocab)) < 0.3] = -INF
+    x[np.arange(rows), rng.integers(0, vocab, rows)] = 1.0
+    x = torch.from_numpy(x).to(dtype)
+    for u in (0.0, 1e-45, 2.0 ** -50, 2.0 ** -44, 2.0 ** -30, 1 - 2.0 ** -24):
+        for more in (dict(), dict(top_k=[7] * rows), dict(top_k=[2048] * rows), dict(top_k=[2500] * rows),
+                     dict(top_k=[20000] * rows, top_p=[0.9999] * rows), dict(top_p=[0.97] * rows),
+                     dict(top_p=[1 - 2.0 ** -24] * rows)):
+            _sample_rows(x, [u] * rows, **more)
