@@ -246,9 +246,9 @@ __device__ __forceinline__ uint64_t shifted(uint64_t v, int by) {
   return by >= 64 || by <= -64 ? 0 : by >= 0 ? v << by : v >> -by;
 }
 
-// The largest whole number of at most a * v, a in [0, 1); `up`: the smallest of at least.
+// The largest whole number of at most a * v, a in [0, 1) or -0; `up`: the smallest of at least.
 __device__ __forceinline__ uint64_t share(float a, uint64_t v, bool up) {
-  const uint32_t bits = __builtin_bit_cast(uint32_t, a);
+  const uint32_t bits = __builtin_bit_cast(uint32_t, a) & 0x7FFFFFFF;
   const int e = (int)(bits >> 23);
   const uint64_t m = e ? (bits & 0x7FFFFF) | 0x800000 : bits & 0x7FFFFF;
   const int down = 150 - (e ? e : 1);  // a = m 2^-down

@@ -1069,3 +1069,18 @@ def test_sample_peaked_rows_at_the_ends(dtype, vocab):
                      dict(top_k=[20000] * rows, top_p=[0.9999] * rows), dict(top_p=[0.97] * rows),
                      dict(top_p=[1 - 2.0 ** -24] * rows)):
             _sample_rows(x, [u] * rows, **more)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+def test_sample_u_of_minus_zero(dtype):
+    """-0 is 0: the first kept token."""
+    rows, vocab = 3, 9001
+    x = torch.from_numpy(_logits(rows, vocab, 11)).to(dtype)
+    x[0, 4000:] = -INF       # the last parts are empty
+    x[1, :5000] = -INF
+    for more in (dict(), dict(top_k=[9] * rows), dict(top_k=[3000] * rows), dict(top_p=[0.9] * rows),
+                 dict(temperature=[0.0] * rows),
+                 dict(top_k=[2500] * rows, top_p=[0.99] * rows, min_p=[0.001] * rows)):
+        got = _sample_check(x, [-0.0] * rows, **more)
+        assert got == _sample_check(x, [0.0] * rows, **more)
+        assert min(got) >= 0 and got[1] >= 5000
