@@ -738,6 +738,7 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
            return Scale::by_value(a, b, k);
          });
   } else {
+    __syncthreads();  // the steps are written: with min_p alone nothing else waits before they are read
     // the row's first words are under way while the bins are joined
     u4v first[kAhead];
     auto first_words = [&](u4v (&w)[kAhead]) __attribute__((always_inline)) {

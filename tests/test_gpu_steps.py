@@ -1084,3 +1084,20 @@ def test_sample_u_of_minus_zero(dtype):
         got = _sample_check(x, [-0.0] * rows, **more)
         assert got == _sample_check(x, [0.0] * rows, **more)
         assert min(got) >= 0 and got[1] >= 5000
+
+
+@pytest.mark.parametrize("dtype", [F16, F32])
+def test_sample_min_p_alone_after_other_kernels(dtype):
+    """The table of steps is written before any wave reads it, whatever the call before has left in
+    the compute units' LDS."""
+    rows, vocab = 600, 4001
+    x = torch.from_numpy(_logits(rows, vocab, 12)).to(dtype)
+    u = np.random.default_rng(4).random(rows).astype(np.float32).clip(0, 1 - 2.0 ** -24).tolist()
+    m = np.random.default_rng(5).uniform(0.0005, 0.3, rows).tolist()
+    b = Shared(F16, 32, 4, 128, 64, [2000], [0, 64], [70] * 64, [1] * 64, seed=31)
+    b.run()
+    first = _sample_check(x, u, min_p=m)
+    for _ in range(3):
+        b.run()
+        assert _sample_check(x, u, min_p=m) == first
+    assert _sample_check(x, [-0.0] * rows, min_p=m) == _sample_check(x, [0.0] * rows, min_p=m)
