@@ -1101,3 +1101,33 @@ def test_sample_min_p_alone_after_other_kernels(dtype):
         b.run()
         assert _sample_check(x, u, min_p=m) == first
     assert _sample_check(x, [-0.0] * rows, min_p=m) == _sample_check(x, [0.0] * rows, min_p=m)
+
+
+@pytest.mark.parametrize("low", ["prefix", "own"])
+@pytest.mark.parametrize("news", [[1, 1], [40, 1]])
+def test_shared_part_of_minus_infinity_beside_finite_scores(news, low):
+    """A part all of whose scores are minus infinity has no weight beside a finite one: the row is
+    that of the other keys alone. The other rows see finite scores in all parts."""
+    b = Shared(BF16, 2, 2, 64, 16, [600], [0, 2], [40, 3], news, seed=21)
+    b.q[:, :, 0] = 0
+    low_key = -1e30
+    b.q[0, :, 0] = 1e20
+    own = b.page_table[:, :3][b.page_table[:, :3] >= 0].long()
+    for which, pages, held in (("prefix", b.prefix_table[0, :38].long(), b.kv[:1]), ("own", own, b.kv[1:])):
+        b.k_pages[pages, :, :, 0] = low_key if which == low else 0
+        for k, _ in held:
+            k[:, :, 0] = low_key if which == low else 0
+    out = b.run()                         # the product is -1e50: minus infinity in fp32
+    n = 40 - news[0] + 1                  # keys that the first row sees
+    k, v = (_np(t) for t in (b.kv[1] if low == "prefix" else b.kv[0]))
+    if low == "prefix":
+        k, v = k[:n], v[:n]
+    want, bound = plain.attention(_np(b.q[:1]), k, v, 1, len(k), 64 ** -0.5, 0, U[BF16])
+    got = _np(out[:1])
+    assert np.isfinite(got).all() and (np.abs(got - want) <= bound).all()
+    for s in range(2):
+        at = sum(news[:s])
+        want, bound = b.want(s)
+        skip = 1 if s == 0 else 0
+        got = _np(out[at:at + news[s]])
+        assert (np.abs(got - want) <= bound)[skip:].all(), s
