@@ -4,9 +4,11 @@
 // Integers only, a few megabytes at most: bound by latency. scan_kernel, one workgroup,
 // walks the sequences a workgroup's width at a time with running sums of new rows, of pages
 // taken and of pages given back; a sequence's rows and pages then follow from its sums alone.
-// Sums saturate at 2^30, above every limit that they are compared with. Up to kFewRows rows
-// it also writes the rows, those of a few tokens by the sequence's own thread; more
-// are fill_kernel's, whose workgroups look for the sequences of their rows.
+// Sums saturate at 2^30 + 2^29: above every limit that they are compared with, also less a
+// sequence's own pages (2^30 at most; a ring has fewer than 2^29), and an int with a thread's
+// number added. Up to kFewRows rows it also writes the rows, those of a few tokens by the
+// sequence's own thread; more are fill_kernel's, whose workgroups look for the sequences of
+// their rows.
 #include "serve.h"
 
 namespace lutgemm {
@@ -18,7 +20,7 @@ constexpr int kFill = 256;       // threads of fill_kernel
 constexpr int kFillRows = 512;   // rows of one of its workgroups
 constexpr int kFewRows = 4096;   // that scan_kernel writes itself
 constexpr int kOwnRows = 4;      // of a sequence, by its own thread
-constexpr uint32_t kFull = 1u << 30;
+constexpr uint32_t kFull = 3u << 29;
 
 struct TablesParams {
   const int32_t* change;
@@ -187,9 +189,11 @@ __global__ __launch_bounds__(Threads) void scan_kernel(TablesParams p) {
     // pages given back, a wave to a sequence at a time
     for (uint64_t givers = __ballot(back > 0); givers; givers &= givers - 1) {
       const int from = __builtin_ctzll(givers);
-      const int count = __builtin_amdgcn_readlane((int)back, from);
+      const int all_back = __builtin_amdgcn_readlane((int)back, from);
       const uint32_t at = (uint32_t)__builtin_amdgcn_readlane((int)(end.given - back), from);
-      const int first = __builtin_amdgcn_readlane(held, from) - count;
+      const int first = __builtin_amdgcn_readlane(held, from) - all_back;
+      if (at >= room) break;  // no room for these, nor for those behind
+      const int count = min(all_back, (int)(room - at));
       const int32_t* row = p.table + (int64_t)(s0 + (int)(threadIdx.x & ~63u) + from) * p.table_stride;
       constexpr int kTogether = 8;  // reads under way
       for (int j0 = lane; j0 < count; j0 += 64 * kTogether) {
@@ -199,7 +203,7 @@ __global__ __launch_bounds__(Threads) void scan_kernel(TablesParams p) {
 #pragma unroll
         for (int k = 0; k < kTogether; ++k) {
           const uint32_t nth = at + (uint32_t)(j0 + 64 * k);
-          if (j0 + 64 * k < count && nth < room) p.ring[around(behind, nth, p.capacity)] = id[k];
+          if (j0 + 64 * k < count) p.ring[around(behind, nth, p.capacity)] = id[k];
         }
       }
     }

@@ -1131,3 +1131,24 @@ def test_shared_part_of_minus_infinity_beside_finite_scores(news, low):
         skip = 1 if s == 0 else 0
         got = _np(out[at:at + news[s]])
         assert (np.abs(got - want) <= bound)[skip:].all(), s
+
+
+def test_tables_of_more_pages_back_than_are_counted():
+    """Two sequences give back 2^30 pages each, the second far behind what the ring takes: the ring
+    gets the first pages of the first alone. (Their rows of the table are 8 GB.)"""
+    width, capacity = 1 << 30, 1000
+    table = torch.empty((2, width), dtype=torch.int32, device=DEV)
+    table[:, :2000] = torch.arange(4000, dtype=torch.int32, device=DEV).view(2, 2000)
+    ring = torch.full((capacity,), -1, dtype=torch.int32, device=DEV)
+    lens = _int([width, width])
+    got = lg.batch_tables(_int([-width, -width]), lens, table, 1, 0, ring, _int([300, 10]))
+    assert got[2].tolist() == [0, 0] and got[4].tolist() == [300, capacity]
+    want = [-1] * capacity
+    for i in range(capacity - 10):
+        want[(310 + i) % capacity] = i
+    assert ring.tolist() == want
+    # the second keeps its first pages, the first ends: the ring takes what there is room for
+    ring.fill_(-1)
+    got = lg.batch_tables(_int([-5, -width + 7]), _int([12, width]), table, 1, 0, ring, _int([0, 0]))
+    assert got[2].tolist() == [7, 7] and got[4].tolist() == [0, capacity]
+    assert ring.tolist() == list(range(7, 12)) + list(range(2007, 2007 + capacity - 5))
