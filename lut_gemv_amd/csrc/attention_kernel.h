@@ -18,7 +18,13 @@
 //
 // The weights are rounded to the element type for the second product, their sum is not:
 // outputs are 1.2 to 1.4 times as far from 64 bits as with weights in fp32. Pairs of numbers
-// would double that product's matrix instructions, which bound many_rows.
+// would double that product's matrix instructions, which bound many_rows. few_rows has time
+// for them, but a weight in two parts, of which the second may be zero, times an infinity
+// is no sum, so infinities have to be looked for in every tile. Both sides of that, over
+// shared prefixes (rms error of fp16 outputs; time): 2 sequences on 512 keys 1.8e-5 in
+// 11.4 to 11.7 us and with pairs 1.5e-5 in 11.9 to 12.2, 40 in 5 groups 7.8e-6 in 99.1 and
+// 5.6e-6 in 99.5, 64 on 32768 keys 112.5 us and 114.3. Not taken: rows have the same rounding
+// whichever body has them.
 //
 // Two bodies, chosen per sequence by its rows (tokens x group):
 //   few_rows   up to 16 rows, memory-bound: each wave streams its own 32-key tiles
