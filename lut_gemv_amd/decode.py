@@ -26,7 +26,8 @@ What is modelled and what is not:
   * with ``room`` > 0 the cache has room for at least so many steps, in whole pages: each
     step's page tables, slots and positions are made on the GPU from the lengths, and a
     replayed step goes on where the one before ended, until the room is full (then its
-    rows are left as they were).
+    rows are left as they were). Steps are timed from the context on, each kernel's anew,
+    and only as many as there is room for.
     By default every step appends the same token;
   * with ``sample`` the step ends with a product of the vocabulary's size and the draw of
     the next tokens; the token drawn is not the next step's input, which stays synthetic;
@@ -108,6 +109,12 @@ def weight_bytes_per_step(model: str, q: int = 3, g: int = 128,
         nb, na, _ = packed_sizes(p.N, p.K, q, g, False)
         tot += nb + 2 * na
     return tot * (full_layers if layers is None else int(layers))
+
+
+def room_steps(context: int, prefix: int, room: int, page_size: int) -> int:
+    """Steps that a cache with room holds behind the context: whole pages of every sequence."""
+    at = context - prefix
+    return -(-(at + room) // page_size) * page_size - at
 
 
 class DecodeStack:
@@ -222,6 +229,9 @@ class DecodeStack:
             self.offsets = torch.full((self.m,), self.prefix, dtype=torch.int32, device=self.device)
             self.kv_lens = torch.full((self.m,), at, dtype=torch.int32, device=self.device)
             self.page_size = page_size
+            self.steps = room_steps(self.context, self.prefix, self.room, page_size)
+            self.moving = (self.kv_lens, self.page_table, self.free_pages, self.free_range)
+            self.begin = tuple(t.clone() for t in self.moving)
             self.q_starts = None
         else:
             self.positions = torch.full((self.m,), self.context, dtype=torch.int64, device=self.device)
@@ -252,11 +262,12 @@ class DecodeStack:
         """Packed weight bytes every decode step reads (bits + scales, all layers)."""
         return weight_bytes_per_step(self.model, self.q, self.g, self.layers)
 
-    def cache_bytes_per_step(self) -> int:
-        """Bytes of keys and values that one decode step's attention reads (all layers)."""
+    def cache_bytes_per_step(self, ahead=0):
+        """Bytes of keys and values that one decode step's attention reads (all layers), `ahead`
+        steps behind the first one."""
         if not self.context:
             return 0
-        keys = self.prefix + self.m * (self.context - self.prefix + 1)
+        keys = self.prefix + self.m * (self.context - self.prefix + 1 + ahead)
         return self.layers * keys * 2 * self.heads * HEAD_DIM * 2
 
     def head_bytes_per_step(self) -> int:
@@ -272,10 +283,10 @@ class DecodeStack:
         return sum(2 * used * a.shape[1] * (p.K + p.N)
                    for lw in self.lora for p in self.projs for a in lw[p.name][:1])
 
-    def read_bytes_per_step(self) -> int:
-        """All that one decode step reads: packed weights, cache, adapters and head (with
-        ``room``, the cache as it is before the first step)."""
-        return (self.bytes_per_step() + self.cache_bytes_per_step()
+    def read_bytes_per_step(self, ahead=0):
+        """All that one decode step reads: packed weights, cache, adapters and head, `ahead`
+        steps behind the first one."""
+        return (self.bytes_per_step() + self.cache_bytes_per_step(ahead)
                 + self.adapter_bytes_per_step() + self.head_bytes_per_step())
 
     # ------------------------------------------------------------ one token
@@ -364,13 +375,23 @@ class DecodeStack:
         self.graph, self.graph_kernel = g, kernel
         return g
 
+    def restart(self):
+        """With ``room``: the lengths, tables and free pages as before the first step."""
+        for t, first in zip(self.moving, self.begin):
+            t.copy_(first)
+
     def time_tokens(self, kernel: str = "lut", tokens: int = 20, warmup: int = 5) -> dict:
         """Time of one decode step (one token for each of the m sequences),
         replaying the captured step graph `tokens` times. The rate is that of all
-        that the step reads."""
+        that the step reads, with ``room`` on average: the steps begin at the context, and
+        more than the room holds are refused."""
         import torch
+        if self.room and warmup + tokens > self.steps:
+            raise ValueError(f"the cache has room for {self.steps} steps, not for {warmup} + {tokens}")
         if self.graph is None or self.graph_kernel != kernel:
             self.capture(kernel)
+        if self.room:
+            self.restart()
         for _ in range(warmup):
             self.graph.replay()
         torch.cuda.synchronize()
@@ -383,9 +404,10 @@ class DecodeStack:
         torch.cuda.synchronize()
         wall = (time.perf_counter() - t0) * 1e3 / tokens
         ms = e0.elapsed_time(e1) / tokens
+        ahead = warmup + (tokens - 1) / 2 if self.room else 0   # of the timed steps on average
         return {"kernel": kernel, "ms_per_step": ms, "wall_ms_per_step": wall,
                 "tokens_per_s": self.m / (ms * 1e-3),
-                "GBps": self.read_bytes_per_step() / (ms * 1e-3) / 1e9}
+                "GBps": self.read_bytes_per_step(ahead) / (ms * 1e-3) / 1e9}
 
     def time_projection(self, name: str, kernel: str = "lut", reps: int = 10,
                         warmup: int = 3) -> dict:
@@ -448,12 +470,16 @@ def main(argv=None) -> int:
     ap.add_argument("--prefix", type=int, default=0,
                     help="of the context, the keys that all sequences share")
     ap.add_argument("--room", type=int, default=0,
-                    help="steps for which the cache has room, tables made on the GPU; 0: every step "
-                         "appends the same token")
+                    help="steps for which the cache has room (at least warmup + tokens), tables made on the "
+                         "GPU; 0: every step appends the same token")
     ap.add_argument("--sample", action="store_true", help="end the step with the head and the draw of tokens")
     ap.add_argument("--breakdown", action="store_true",
                     help="also time each projection on its own (us per GEMV)")
     a = ap.parse_args(argv)
+    if a.room > 0:
+        steps = room_steps(a.context, a.prefix, a.room, a.page_size)
+        if a.warmup + a.tokens > steps:
+            ap.error(f"--room {a.room} holds {steps} steps, not --warmup {a.warmup} and --tokens {a.tokens}")
 
     import torch
     if not torch.cuda.is_available():

@@ -1152,3 +1152,25 @@ def test_tables_of_more_pages_back_than_are_counted():
     got = lg.batch_tables(_int([-5, -width + 7]), _int([12, width]), table, 1, 0, ring, _int([0, 0]))
     assert got[2].tolist() == [7, 7] and got[4].tolist() == [0, capacity]
     assert ring.tolist() == list(range(7, 12)) + list(range(2007, 2007 + capacity - 5))
+
+
+def test_decode_times_steps_from_the_context_on():
+    """With room each kernel's timed steps begin at the context, none is behind the room's end, and
+    the rate counts the keys that they read."""
+    from lut_gemv_amd import decode
+    st = decode.DecodeStack("llama7b", layers=1, q=2, g=128, m=3, device=DEV, page_size=16, context=100, prefix=60,
+                            room=9)
+    assert st.steps == 24                    # 40 own keys and 24 more in four pages
+    tables = []
+    for kernel in ("lut", "dequant", "lut"):
+        for tokens, warmup in ((20, 4), (3, 0)):
+            r = st.time_tokens(kernel, tokens, warmup)
+            assert st.kv_lens.tolist() == [40 + warmup + tokens] * 3
+            assert st.positions.tolist() == [99 + warmup + tokens] * 3
+            keys = 60 + 3 * (41 + warmup + (tokens - 1) / 2)
+            read = st.bytes_per_step() + keys * 2 * 4096 * 2
+            assert r["GBps"] == pytest.approx(read / (r["ms_per_step"] * 1e-3) / 1e9, rel=1e-9)
+        tables.append(st.page_table.tolist())
+    assert tables[0] == tables[1] == tables[2]
+    with pytest.raises(ValueError, match="room for 24 steps"):
+        st.time_tokens("lut", 20, 5)

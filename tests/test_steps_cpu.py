@@ -268,3 +268,18 @@ def test_decode_stack_arguments():
                dict(context=10, room=-1)):
         with pytest.raises(ValueError, match="prefix must be"):
             decode.DecodeStack("llama7b", layers=1, device="cpu", **kw)
+
+
+@pytest.mark.parametrize("context,prefix,room,page,steps", [(100, 70, 6, 16, 18), (100, 100, 1, 16, 16), (64, 0, 64, 64, 64),
+                                                            (1024, 0, 8, 16, 16)])
+def test_decode_times_only_steps_that_have_room(context, prefix, room, page, steps):
+    """A step without room attends over nothing and would be timed as a fast one."""
+    from lut_gemv_amd import decode
+    assert decode.room_steps(context, prefix, room, page) == steps
+    st = object.__new__(decode.DecodeStack)
+    st.room, st.steps = room, steps
+    with pytest.raises(ValueError, match=f"room for {steps} steps"):
+        st.time_tokens(tokens=steps, warmup=1)
+    args = [f"--context={context}", f"--prefix={prefix}", f"--room={room}", f"--page-size={page}", "--model=llama7b"]
+    with pytest.raises(SystemExit):
+        decode.main([*args, f"--tokens={steps - 4}", "--warmup=5"])
