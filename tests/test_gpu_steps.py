@@ -1174,3 +1174,36 @@ def test_decode_times_steps_from_the_context_on():
     assert tables[0] == tables[1] == tables[2]
     with pytest.raises(ValueError, match="room for 24 steps"):
         st.time_tokens("lut", 20, 5)
+
+
+def test_readme_step_behind_a_prefix():
+    """The step of the use example: rotated by positions behind the prefix, a request on a shared prefix
+    has the results of one whose table holds the prefix itself."""
+    rng = torch.Generator().manual_seed(8)
+    heads, kv_heads, dim, page, prefix, own, pages = 8, 2, 128, 64, 150, 21, 12
+    rope = lg.rotary_table(positions=512, rotary=dim, device=DEV)
+    k, v = (torch.randn((pages, page, kv_heads, dim), generator=rng).to(F16).to(DEV) for _ in range(2))
+    qkv = torch.randn((1, (heads + 2 * kv_heads) * dim), generator=rng).to(F16).to(DEV)
+    ring = torch.arange(6, pages, dtype=torch.int32, device=DEV)
+    # its own keys behind a prefix of whole pages: 128 keys in pages 0 and 1, 22 + 21 in page 2
+    shared, table = 2 * page, _int([[2, -1, -1]])
+    at = prefix - shared + own
+    positions, slots, kv_lens, q_starts, _ = lg.batch_tables(
+        _int([1]), _int([at]), table, page_size=page, tokens=1, free_pages=ring, free_range=_int([0, 6]),
+        offsets=_int([shared]))
+    assert positions.tolist() == [prefix + own] and slots.tolist() == [2 * page + at]
+    q = lg.qk_norm_rotate(qkv, heads, kv_heads, positions, rope, k_pages=k, v_pages=v, slots=slots)
+    o = lg.shared_prefix_attention(q, k, v, _int([[0, 1]]), _int([shared]), table, kv_lens, q_starts)
+    whole = _int([[0, 1, 2, -1]])
+    k2, v2 = k.clone(), v.clone()
+    k2[2, at], v2[2, at] = 0, 0
+    positions, slots, kv_lens, q_starts, _ = lg.batch_tables(
+        _int([1]), _int([prefix + own]), whole, page_size=page, tokens=1, free_pages=ring.clone(),
+        free_range=_int([0, 6]))
+    q2 = lg.qk_norm_rotate(qkv, heads, kv_heads, positions, rope, k_pages=k2, v_pages=v2, slots=slots)
+    assert torch.equal(q, q2) and torch.equal(k, k2) and torch.equal(v, v2)
+    n = prefix + own + 1
+    ks, vs = (_np(t[:3]).reshape(-1, kv_heads, dim)[:n] for t in (k, v))
+    want, bound = plain.attention(_np(q), ks, vs, 1, n, dim ** -0.5, 0, U[F16])
+    for got in (o, lg.paged_attention(q2, k2, v2, whole, kv_lens, q_starts)):
+        assert (np.abs(_np(got) - want) <= bound).all()
