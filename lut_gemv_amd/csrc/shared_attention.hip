@@ -5,9 +5,9 @@
 // with its own maximum and sum, so the prefix is one more sequence for the bodies of
 // attention_kernel.h: its rows are the new tokens of the whole group, all of which see all
 // of its keys. Its keys are read once for 128 rows, not once for each sequence. One
-// launch runs the prefixes' row tiles (many_rows), then the own keys of chunks (many_rows) and
-// of single tokens (few_rows); all leave their parts in the workspace, and
-// join_kernel brings each row's to one maximum.
+// launch runs the prefixes of small groups (few_rows), the row tiles of others (many_rows),
+// then the own keys of chunks (many_rows) and of single tokens (few_rows); all leave their
+// parts in the workspace, and join_kernel brings each row's to one maximum.
 //
 // Measured (keys of 128, prefix of 32768, 64 sequences with 450 keys of their own on average, 64
 // heads of 8, bf16): 69 G multiplications and additions, 57 us at a large matrix product's
@@ -25,8 +25,9 @@ struct SharedParams : AttnParams {
   const int32_t* group_starts;
   int64_t prefix_stride, prefix_at;  // prefix_at: where the prefixes' part rows begin
   int32_t groups, prefix_keys, prefix_tiles, prefix_splits, prefix_chunk;
-  int32_t prefix_few;     // groups of up to so many rows are few_rows': all or none
-  int32_t blocks[3];      // workgroups of the prefixes, of many_rows and of few_rows
+  int32_t prefix_few;     // groups of up to so many rows are few_rows'
+  int32_t blocks[4];      // workgroups of the prefixes' few_rows, their many_rows, the own keys'
+                          // many_rows and few_rows
 };
 
 // A sequence's own keys. Part row of split s: (s * tokens + token) * heads + head.
@@ -80,12 +81,13 @@ struct PrefixView {
   static __device__ __forceinline__ int64_t many_at(const SharedParams& p) { return p.prefix_at; }
 };
 
-// Which bodies a launch has: the prefixes' one (or none), and whether single tokens and
-// chunks are among the own keys. A kernel of all of them at once is slower at each (64
-// sequences on 32768 keys 146 us, so 106). Bound by the matrix cores where a group has many rows
+// Which bodies a launch has: the prefixes' (one, none, or both where groups of few rows may
+// stand beside larger ones), and whether single tokens and chunks are among the own keys. A
+// kernel of all of them at once is slower at each (64 sequences on 32768 keys 146 us, so
+// 106). Bound by the matrix cores where a group has many rows
 // (the prefix alone of those 64: 94 us, 730 TFLOP/s of many_rows on 14 parts of 2341 keys, whose
 // beginnings and ends it pays 14 times), by the reading where it has few.
-enum { kNoPrefix, kManyPrefix, kFewPrefix };
+enum { kNoPrefix, kManyPrefix, kFewPrefix, kBothPrefixes };
 
 template <class T, int D, int Prefix, bool Few, bool Many>
 __global__ __launch_bounds__(kThreads, 2) void shared_kernel(SharedParams p) {
@@ -95,22 +97,26 @@ __global__ __launch_bounds__(kThreads, 2) void shared_kernel(SharedParams p) {
   fetch(p);
   auto region = [&](int w) { return w == 0 ? keys0 : w == 1 ? vals0 : w == 2 ? keys1 : vals1; };
   int block = blockIdx.x;
-  if constexpr (Prefix != kNoPrefix) {
+  if constexpr (Prefix == kFewPrefix || Prefix == kBothPrefixes) {
     if (block < p.blocks[0]) {
-      if constexpr (Prefix == kFewPrefix)
-        few_rows<PrefixView, T, D, kThreads / 64>(p, block, region, shared);
-      else
-        many_rows<PrefixView, T, D>(p, block, keys0, vals0, keys1, vals1, shared.marks);
+      few_rows<PrefixView, T, D, kThreads / 64>(p, block, region, shared);
       return;
     }
     block -= p.blocks[0];
   }
-  if constexpr (Many) {
+  if constexpr (Prefix == kManyPrefix || Prefix == kBothPrefixes) {
     if (block < p.blocks[1]) {
-      many_rows<OwnView, T, D>(p, block, keys0, vals0, keys1, vals1, shared.marks);
+      many_rows<PrefixView, T, D>(p, block, keys0, vals0, keys1, vals1, shared.marks);
       return;
     }
     block -= p.blocks[1];
+  }
+  if constexpr (Many) {
+    if (block < p.blocks[2]) {
+      many_rows<OwnView, T, D>(p, block, keys0, vals0, keys1, vals1, shared.marks);
+      return;
+    }
+    block -= p.blocks[2];
   }
   if constexpr (Few) few_rows<OwnView, T, D, kThreads / 64>(p, block, region, shared);
 }
@@ -216,18 +222,24 @@ int check_shared(const lutgemm_shared* a) {
   return LUTGEMM_OK;
 }
 
+// A launch has fewer workgroups: below 2^32 threads along each axis of its grid.
+constexpr int64_t kMostBlocks = (int64_t)1 << 23;
+
 // Workgroups that run at a time: two to a compute unit. (Heads of 64 have room for three, and for four
 // in 128 registers: 40 sequences in 5 groups 104 and 111 to 118 us, so 100.)
 constexpr int64_t kSlots = 512;
 
 struct SharedPlan {
-  bool few, many, prefix_few;
+  bool few, many;
+  int prefix;  // which kernel
   int splits[3], chunk[3];  // of few_rows, many_rows and the prefixes
   int64_t tiles, prefix_tiles;
   int64_t rows, part_rows;
-  int64_t blocks[3];  // workgroups of the prefixes, of many_rows and of few_rows
+  int64_t blocks[4];  // as SharedParams'
   size_t ws_bytes;
 };
+
+int64_t grid_of(const SharedPlan& r) { return r.blocks[0] + r.blocks[1] + r.blocks[2] + r.blocks[3]; }
 
 // Cuts `keys` keys of `base` row tiles into the number of parts that takes least time on
 // `slots` workgroups at once, where a part costs as much as `more` keys besides its own.
@@ -258,16 +270,26 @@ SharedPlan plan(const lutgemm_shared* s) {
   r.many = max_q * group > kFewRows;
   r.few = !r.many || (a->seqs > 1 && group <= kFewRows);
   r.tiles = r.many ? a->tokens * group / kManyRows + a->seqs : 0;
-  // A group of up to sixteen rows to a key head (on average: few_rows takes more in turns) reads
-  // its prefix as a single token does: 16 rows on heads of 64 57 us so and 59 by row tiles of
-  // 128, on heads of 128 97 and 101; 32 rows 43 and 40, 68 and 62.
-  r.prefix_few = s->groups && (a->tokens + s->groups - 1) / s->groups * group <= kFewRows;
-  r.prefix_tiles = s->groups ? s->groups == 1 ? (a->tokens * group + kManyRows - 1) / kManyRows
-                                              : a->tokens * group / kManyRows + s->groups
-                             : 0;
+  // A group of up to sixteen rows to a key head reads its prefix as a single token does: 16 rows on
+  // heads of 64 57 us so and 59 by row tiles of 128, on heads of 128 97 and 101, 16 on 16000 keys in
+  // 16 groups 178 and 237; 32 rows 43 and 40, 68 and 62. Where few rows are the mean, each group goes
+  // by its own: 512 rows beside 63 groups of 8 on 4096 keys 143 us, all by few_rows 1420, all by
+  // row tiles 150. Even batches pay up to 4% for workgroups that find no tile (63 groups of 8 rows
+  // 92 to 94 us, with one of 16 99 to 103). Where more are the mean, all go by row tiles.
+  const int64_t rows = a->tokens * group;
+  const bool small = s->groups && (a->tokens + s->groups - 1) / s->groups * group <= kFewRows;
+  r.prefix = !s->groups ? kNoPrefix : !small ? kManyPrefix
+             : s->groups > 1 && rows > kFewRows ? kBothPrefixes : kFewPrefix;
+  // the row tiles of groups of more rows; of more than 64 groups row_tile gives one more to each
+  r.prefix_tiles = r.prefix == kManyPrefix
+                       ? s->groups == 1 ? (rows + kManyRows - 1) / kManyRows : rows / kManyRows + s->groups
+                   : r.prefix == kBothPrefixes
+                       ? rows / kManyRows + (s->groups > 64 ? s->groups
+                                                            : std::min<int64_t>(s->groups, rows / (kFewRows + 1)))
+                       : 0;
   const int64_t few = (int64_t)a->seqs * a->kv_heads;
   const int64_t many = (a->tokens * group / kManyRows + (a->seqs + 1) / 2) * a->kv_heads;
-  const int64_t shared_tiles = r.prefix_few       ? s->groups
+  const int64_t shared_tiles = small            ? s->groups
                                : s->groups == 1 ? r.prefix_tiles
                                                 : a->tokens * group / kManyRows + (s->groups + 1) / 2;
   const int64_t shared = shared_tiles * a->kv_heads;
@@ -277,23 +299,27 @@ SharedPlan plan(const lutgemm_shared* s) {
   // own keys to run beside them (64 sequences on 32768 keys, 64 heads of 8: 14 parts 112 to
   // 116 us, 16, which fill the slots, 119 to 122, 8, which fill half of them, 118). Both
   // in turn from the start was slower: the tiles then end late (125 to 146 us).
-  cut_keys(prefix, shared, r.many || r.prefix_few ? kSlots : kSlots / 8 * 7, 256, &r.splits[2],
-           &r.chunk[2]);
+  cut_keys(prefix, shared, r.many || small ? kSlots : kSlots / 8 * 7, 256, &r.splits[2], &r.chunk[2]);
   if (!r.few) r.splits[0] = 0;
   if (!r.many) r.splits[1] = 0;
   if (!s->groups) r.splits[2] = 0;
   r.rows = a->tokens * a->heads;
   r.part_rows = (std::max(r.splits[0], r.splits[1]) + r.splits[2]) * r.rows;
   r.ws_bytes = (size_t)r.part_rows * (size_t)(a->head_dim + 2) * sizeof(float);
-  r.blocks[0] = (r.prefix_few ? s->groups : r.prefix_tiles) * a->kv_heads * r.splits[2];
-  r.blocks[1] = r.tiles * a->kv_heads * r.splits[1];
-  r.blocks[2] = few * r.splits[0];
+  r.blocks[0] = small ? (int64_t)s->groups * a->kv_heads * r.splits[2] : 0;
+  r.blocks[1] = r.prefix_tiles * a->kv_heads * r.splits[2];
+  r.blocks[2] = r.tiles * a->kv_heads * r.splits[1];
+  r.blocks[3] = few * r.splits[0];
+  if (r.prefix == kBothPrefixes && grid_of(r) >= kMostBlocks) {  // by few_rows all fit, or none
+    r.prefix = kFewPrefix;
+    r.blocks[1] = 0;
+  }
   return r;
 }
 
 template <class T, int D, int Prefix>
 int launch_shared(const SharedPlan& r, const SharedParams& p, hipStream_t stream) {
-  const dim3 grid((unsigned)(r.blocks[0] + r.blocks[1] + r.blocks[2]));
+  const dim3 grid((unsigned)grid_of(r));
   if (r.few && r.many) return launch(shared_kernel<T, D, Prefix, true, true>, grid, kThreads, p, stream);
   if (r.many) return launch(shared_kernel<T, D, Prefix, false, true>, grid, kThreads, p, stream);
   return launch(shared_kernel<T, D, Prefix, true, false>, grid, kThreads, p, stream);
@@ -303,9 +329,10 @@ template <class T, int D>
 int run_shared(const SharedPlan& r, const SharedParams& p, hipStream_t stream) {
   constexpr int kRows = kThreads / (D / 4);
   const int64_t joins = (int64_t)p.tokens * ((p.heads + kRows - 1) / kRows);
-  const int st = !r.blocks[0] ? launch_shared<T, D, kNoPrefix>(r, p, stream)
-                 : r.prefix_few ? launch_shared<T, D, kFewPrefix>(r, p, stream)
-                                : launch_shared<T, D, kManyPrefix>(r, p, stream);
+  const int st = r.prefix == kNoPrefix       ? launch_shared<T, D, kNoPrefix>(r, p, stream)
+                 : r.prefix == kManyPrefix ? launch_shared<T, D, kManyPrefix>(r, p, stream)
+                 : r.prefix == kFewPrefix  ? launch_shared<T, D, kFewPrefix>(r, p, stream)
+                                           : launch_shared<T, D, kBothPrefixes>(r, p, stream);
   return st ? st : launch(join_kernel<T, D>, dim3((unsigned)joins), kThreads, p, stream);
 }
 
@@ -342,10 +369,7 @@ extern "C" int lutgemm_shared_attention(const lutgemm_shared* s, const void* d_q
         !aligned(d_prefix_table, 4) || !aligned(d_prefix_lens, 4) || !aligned(d_group_starts, 4))
       return LUTGEMM_ERR_ALIGN;
     const SharedPlan r = plan(s);
-    // a launch has fewer than 2^32 threads along each axis of its grid
-    constexpr int64_t kMost = (int64_t)1 << 24;
-    if (r.blocks[0] + r.blocks[1] + r.blocks[2] >= kMost / 2 ||
-        a->tokens * ((a->heads + 7) / 8) >= kMost)
+    if (grid_of(r) >= kMostBlocks || a->tokens * ((a->heads + 7) / 8) >= 2 * kMostBlocks)
       return LUTGEMM_ERR_SHAPE;
     if (!d_workspace) return LUTGEMM_ERR_NULL;
     if (workspace_bytes < r.ws_bytes) return LUTGEMM_ERR_BUFFER;
@@ -397,8 +421,8 @@ extern "C" int lutgemm_shared_attention(const lutgemm_shared* s, const void* d_q
     p.prefix_chunk = r.chunk[2];
     p.groups = s->groups;
     p.prefix_tiles = (int32_t)r.prefix_tiles;
-    p.prefix_few = r.prefix_few ? 0x7FFFFFFF : 0;
-    for (int i = 0; i < 3; ++i) p.blocks[i] = (int32_t)r.blocks[i];
+    p.prefix_few = r.prefix == kManyPrefix ? 0 : r.prefix == kFewPrefix ? 0x7FFFFFFF : kFewRows;
+    for (int i = 0; i < 4; ++i) p.blocks[i] = (int32_t)r.blocks[i];
     p.few_rows = !r.many ? 0x7FFFFFFF : r.few ? kFewRows : 0;
     p.tiles = (int32_t)r.tiles;
     p.scale2 = a->scale * 1.4426950408889634f;

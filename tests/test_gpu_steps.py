@@ -1207,3 +1207,57 @@ def test_readme_step_behind_a_prefix():
     want, bound = plain.attention(_np(q), ks, vs, 1, n, dim ** -0.5, 0, U[F16])
     for got in (o, lg.paged_attention(q2, k2, v2, whole, kv_lens, q_starts)):
         assert (np.abs(_np(got) - want) <= bound).all()
+
+
+@pytest.mark.parametrize("dtype,heads,kv_heads,dim", [(BF16, 16, 2, 128), (F16, 4, 4, 64)])
+@pytest.mark.parametrize("small", [9, 63, 64, 90])
+@pytest.mark.parametrize("at", ["first", "middle", "last"])
+def test_shared_large_group_among_small_ones(small, at, dtype, heads, kv_heads, dim):
+    """A group of many rows beside groups of one token, and chunks among them: each group by its
+    own rows, however many there are on average."""
+    large = 5 * small // (heads // kv_heads) + 20 // (heads // kv_heads)
+    sizes = [1] * small
+    sizes.insert(dict(first=0, middle=small // 2, last=small)[at], large)
+    starts = [0, *np.cumsum(sizes).tolist()]
+    seqs = starts[-1]
+    rng = np.random.default_rng(small)
+    for chunks in (False, True):
+        news = [23 if chunks and s == seqs // 2 else 1 for s in range(seqs)]
+        lens = [n + int(x) for n, x in zip(news, rng.integers(0, 40, seqs))]
+        b = Shared(dtype, heads, kv_heads, dim, 16, [int(x) for x in rng.integers(0, 200, len(sizes))], starts, lens, news,
+                   seed=small)
+        b.check(b.run(), f"{large} among {small}, chunks {chunks}")
+        b.check(b.run(max_q=max(news), max_kv=70, max_prefix=200), "with hints")
+
+
+def test_shared_time_of_a_large_group_among_small_ones():
+    """One call takes about as long as one of the large group and one of the small ones: were the
+    large group read as single tokens are, 16 rows at a time, it would take ten times that."""
+    gen = torch.Generator(device=DEV).manual_seed(0)
+
+    def call(sizes):
+        groups, seqs, pages = len(sizes), sum(sizes), 64
+        total = groups * pages + 2 * seqs
+        k, v = (torch.empty((total, 64, 4, 128), dtype=BF16, device=DEV).normal_(generator=gen) for _ in range(2))
+        ids = torch.arange(total, dtype=torch.int32, device=DEV)
+        q = torch.empty((seqs, 32, 128), dtype=BF16, device=DEV).normal_(generator=gen)
+        a = (q, k, v, ids[:groups * pages].view(groups, pages), _int([4096] * groups),
+             ids[groups * pages:].view(seqs, 2), _int([100] * seqs), None, _int([0, *np.cumsum(sizes).tolist()]))
+        return lambda: lg.shared_prefix_attention(*a, max_q=1, max_kv=100, max_prefix=4096)
+
+    def least(f):
+        times = []
+        for _ in range(12):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            for _ in range(5):
+                f()
+            b.record()
+            torch.cuda.synchronize()
+            times.append(a.elapsed_time(b) / 5)
+        return min(times)
+
+    apart = least(call([64])) + least(call([1] * 63))
+    together = least(call([64] + [1] * 63))
+    _say(f"apart {apart * 1e3:.0f} us, together {together * 1e3:.0f} us")
+    assert together < 3 * apart

@@ -283,3 +283,13 @@ def test_decode_times_only_steps_that_have_room(context, prefix, room, page, ste
     args = [f"--context={context}", f"--prefix={prefix}", f"--room={room}", f"--page-size={page}", "--model=llama7b"]
     with pytest.raises(SystemExit):
         decode.main([*args, f"--tokens={steps - 4}", "--warmup=5"])
+
+
+@pytest.mark.parametrize("count", [700000, (1 << 20) - 1])
+def test_shared_many_groups_fit_a_launch(count):
+    """Groups of one token: workgroups for larger ones among them are left out where they would make
+    the launch too large (the missing workspace is found behind that)."""
+    assert _shared(type=1, seqs=count, tokens=count, groups=count, heads=4, kv_heads=4, max_q=1, max_kv=16, max_prefix=16,
+                   ws=None) == NULL
+    assert _shared(type=1, seqs=count, tokens=count, groups=count, heads=8, kv_heads=8, max_q=1, max_kv=16, max_prefix=16,
+                   ws=None) == SHAPE
