@@ -738,7 +738,6 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
            return Scale::by_value(a, b, k);
          });
   } else {
-    __syncthreads();  // the steps are written: with min_p alone nothing else waits before they are read
     // the row's first words are under way while the bins are joined
     u4v first[kAhead];
     auto first_words = [&](u4v (&w)[kAhead]) __attribute__((always_inline)) {
@@ -955,6 +954,7 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
       }));
     };
 
+    if (set.by_least) __syncthreads();  // with min_p alone nothing has waited yet for the steps
     const double floor_weight =  // of what min_p keeps
         set.by_least ? (double)(set.min_p < 1.f ? set.min_p : 1.f) : 0.0;
     int k;
