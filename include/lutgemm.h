@@ -590,7 +590,7 @@ int lutgemm_batch_tables(const lutgemm_tables* t, const int32_t* d_change, const
  * 2^-63 count as having none, and no top_k or top_p border is looked for among them.
  *   d_logits  [rows][vocab] of type F16, BF16 or F32, rows row_step elements apart; -infinity:
  *             the token is never drawn
- *   d_u       fp32 [rows] in [0, 1)     d_temperature, d_top_p, d_min_p  fp32 [rows] or
+ *   d_u       fp32 [rows] in [0, 1), -0 as 0   d_temperature, d_top_p, d_min_p  fp32 [rows] or
  *   NULL: 1, 1, 0                       d_top_k  int32 [rows] or NULL: 0
  *   d_tokens  int64 [rows]              d_logprobs  fp32 [rows] or NULL
  *   d_workspace  at least lutgemm_sample_tokens_workspace bytes (50 MB at most); as for attention

@@ -26,8 +26,9 @@
 // drawn token lies, and only that is weighed again.
 //
 // Measured (bf16, 256 rows of 131073, top_p; 67 MB, 10 us at a streaming read's rate): 80 us;
-// fp16, 1 row of 50272 26 us, 48 rows of 32000 of all kinds 32; fp32, 61 rows of 128001
-// without a filter 20. The kernels say what bounds each.
+// fp16, 1 row of 50272 27 us, 48 rows of 32000 of all kinds 31; fp32, 61 rows of 128001
+// without a filter 20. The kernels say what bounds each; their own times are a trace's, in which
+// the two of a call sum to up to 4 us more than calls in a row take.
 #include <algorithm>
 #include <type_traits>
 
@@ -386,11 +387,12 @@ struct Head {
 constexpr int kSumsAt = 64, kCountsAt = kSumsAt + kBins * 8, kPartsAt = kSumsAt;
 constexpr int kRecord = kCountsAt + kBins * 4;
 
-// Bound by instructions, for bins: 256 rows of 131073 37 us, of which about 20 a token, half of
-// them in 64 bits, take 25; their LDS additions alone take 30 (4.7 M cycles of bank
-// conflicts) and run beside them. Two or four tokens' table reads ahead of their additions: no
+// Bound by instructions, for bins: 256 rows of 131073 37 us, of which 29 vector instructions a
+// token, some of them in 64 bits, take 25; their LDS additions alone take 30 (4.7 M cycles of
+// bank conflicts) and run beside them. Two or four tokens' table reads ahead of their additions: no
 // faster; 6, 8 or 16 pieces to a row: 40, 44 and 60 us. Without a filter (61 rows of 128001 in 32
-// bits) 15 us. A reference from the first tokens, raised where later ones pass it, in place of
+// bits) 15 us: 5 of reading, then 9 of 43 instructions a token, which cannot begin before the
+// piece's largest value is known. A reference from the first tokens, raised where later ones pass it, in place of
 // the piece in registers: 91.
 template <class T>
 __global__ __launch_bounds__(kThreads, 8) void chunk_kernel(SampleParams p) {
@@ -944,7 +946,7 @@ __global__ __launch_bounds__(kThreads) void row_kernel(SampleParams p) {
         }));
       }
       // more than the list takes, of nearly equal logits: the row again for each byte (256 rows of
-      // 131073: 250 us at a temperature of 20, 630 if all are equal)
+      // 131073: 320 us at a temperature of 20, 620 if all are equal)
       const float least = least_of(bin), limit = most_of(bin);
       return or_largest(select(sh, need, before, [&](auto f) {
         each_from(least, limit, [&](Raw raw, int i) {

@@ -12,8 +12,10 @@
 // Measured (keys of 128, prefix of 32768, 64 sequences with 450 keys of their own on average, 64
 // heads of 8, bf16): 69 G multiplications and additions, 57 us at a large matrix product's
 // rate, take 105 and the join 10. 40 sequences in 5 groups on 4099 keys (32 heads of 64, fp16):
-// 470 MB, 70 us at a copy's rate, take 95 to 100. 8 chunks of 253 tokens on 16384 keys (32 heads
-// of 8, bf16): 348 us at the product's rate, take 430 to 470 by the machine's clock.
+// 470 MB, 70 us at a copy's rate, take 95 and the join 5. 8 chunks of 253 tokens on 16384 keys (32
+// heads of 8, bf16): 348 us at the product's rate, take 438 to 473 by the machine's clock and the
+// join 29. (Kernels by themselves, in a trace; calls in a row take 107 to 117, 98 to 100 and 432
+// to 457 us.)
 #include "attention_kernel.h"
 
 namespace lutgemm {

@@ -123,8 +123,9 @@ __device__ __forceinline__ void write_row(const TablesParams& p, int s, int row,
 }
 
 // Bound by latency: the lengths' reads, two barriers a turn, the table's and the ring's entries behind
-// them. One sequence 2.8 us, 400 of which 20 are chunks 7.2; 34 prompts of 5800 tokens each,
-// whose rows are fill_kernel's, 4.1.
+// them. One sequence 2.8 to 3.0 us; 400, of which 9 end and 31 take keys back, 6.8 to 7.2 (a wave's
+// sequences that give pages back wait for one another, a read and a write each); 64 chunks beside 96
+// single tokens, whose rows are fill_kernel's, 4.0.
 template <int Threads>
 __global__ __launch_bounds__(Threads) void scan_kernel(TablesParams p) {
   __shared__ Sums waves[2][Threads / 64];
@@ -260,7 +261,7 @@ __device__ __forceinline__ int owner(const TablesParams& p, int row, int lane) {
   return lo;
 }
 
-// Bound by its beginning (the search, 2 us) and its writes: 196608 rows, 3.1 MB, 5.6 us.
+// Bound by its beginning (the search, 2 us) and its writes: 196608 rows, 3.1 MB, 5.1 to 5.6 us.
 __global__ __launch_bounds__(kFill) void fill_kernel(TablesParams p) {
   __shared__ int32_t starts[kFillRows + 1];
   fetch(p);
